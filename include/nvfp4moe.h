@@ -45,6 +45,18 @@
  *     pitch = round_up(K/2, 128) bytes; scales in 512-byte atoms, one per (128-row block
  *     rb, 64-element k-step s) at byte ((rb * K/64) + s) * 512, and inside an atom row m
  *     (0..127) scale kk (0..3) at byte (m % 32) * 16 + (m / 32) * 4 + kk.
+ *   MXFP4 matrices [B][R][K] (B matrices of R rows, K a multiple of 32): codes uint8
+ *     [B][R][K/2], element 2i in the low nibble and 2i+1 in the high nibble; one scale byte
+ *     s (E8M0) per 32 elements of a row; the value of an element is E2M1(code) * 2^(s-127),
+ *     s = 255 is NaN.  Scale layouts (moe_sf_layout): canonical [B][R][K/32]; tiled, the
+ *     grouped product's operand layout: [B][ceil(R/128)][ceil(K/128)] atoms of 512 bytes, one
+ *     per 128 rows x 4 scales, inside an atom row m (0..127) scale kk (0..3) at byte
+ *     (m % 32) * 16 + (m / 32) * 4 + kk.  The scales of K blocks past K are 0; those of rows
+ *     past R are not used.
+ *   Sorted rows (moe_dispatch): the kept (token, expert) pairs grouped by local expert, in
+ *     ascending pair index p = t*k + j inside a group, each group starting on a multiple of
+ *     row_align (1: no padding; 128: what moe_grouped_gemm_mxfp4 reads).  There is no shared
+ *     group.  inv[p] is pair p's row (-1: dropped), perm_src[r] row r's pair (-1: none).
  */
 #ifndef NVFP4MOE_H
 #define NVFP4MOE_H
@@ -87,13 +99,35 @@ typedef enum {
     MOE_GS_DEQUANT = 1      /* a dequantisation multiplier m: value = code * sf * m */
 } moe_gs_convention;
 
+/* Element types of the operators that take a dtype. */
+typedef enum {
+    MOE_BF16 = 0,
+    MOE_FP16 = 1,
+    MOE_FP32 = 2
+} moe_dtype;
+
+/* Where the scale bytes of an MXFP4 matrix lie (see "MXFP4 matrices" above). */
+typedef enum {
+    MOE_SF_CANONICAL = 0,
+    MOE_SF_TILED = 1
+} moe_sf_layout;
+
+/* The block scale 2^e of moe_quant_mxfp4, for m the largest magnitude of the block. */
+typedef enum {
+    MOE_MX_FLOOR = 0,       /* e = floor(log2 m) - 2: m may pass 6 * 2^e and saturate */
+    MOE_MX_CEIL = 1         /* the least e with m <= 6 * 2^e: nothing saturates */
+} moe_mx_rule;
+
 /* Device status bits (moe_get_status's *bits). */
 #define MOE_DEV_BAD_EXPERT_ID  0x1u   /* a top-k id outside [0, num_experts): pair dropped */
 #define MOE_DEV_WAIT_TIMEOUT   0x2u   /* a pipeline wait ran out: that tile was abandoned */
 #define MOE_DEV_ROWS_OVERFLOW  0x4u   /* padded rows exceeded capacity: pairs dropped */
 #define MOE_DEV_BAD_INDEX      0x8u   /* library built with MOE_DEBUG only: a padded-row or
                                          pair index read from a buffer was out of range; the
-                                         access was skipped */
+                                         access was skipped.  moe_grouped_gemm_mxfp4 (every
+                                         build): a group's rows do not start on a multiple of
+                                         128 or do not lie within rows_cap; the group was
+                                         skipped */
 
 typedef struct {
     int32_t hidden;               /* H: multiple of 128 */
@@ -382,6 +416,130 @@ MOE_API moe_status moe_forward_buffers(moe_handle h, void* ws_d, int32_t T, int3
  * MOE_ERR_DEVICE_STATUS (other bits set).
  * Passage: none; the device status word of this library (the pages have no counterpart). */
 MOE_API moe_status moe_get_status(moe_handle h, void* ws_d, moe_stream_t stream, uint32_t* bits);
+
+/* ---- Tokens sorted by expert, and back, with their gradients.  No handle: sizes are
+ * arguments, and the rows carry any of the moe_dtype types.  A row that belongs to no pair is
+ * neither written nor read.  T, k, H: tokens, routed experts per token (1..32), elements per
+ * row; x_stride, out_stride etc.: elements between consecutive token rows (>= H); sorted rows
+ * are contiguous [rows_cap][H].  Sums are taken in fp32 in ascending j and rounded once.
+ * Rows whose size, stride and addresses are multiples of 16 bytes move in 16-byte pieces,
+ * others element by element.  Inputs and outputs must not overlap. */
+
+/* Rows that hold every pair however the T tokens route among num_local experts (0 for
+ * arguments out of range).
+ * Passage: none; sizing of the sorted rows (the pages have no counterpart). */
+MOE_API int32_t moe_dispatch_rows_capacity(int32_t T, int32_t k, int32_t num_local,
+                                           int32_t row_align);
+
+/* Dispatch: the maps, then rows_d[inv[p]] = x[p / k] for every kept pair.
+ *   topk_ids_d [T*k]: pair p is kept iff 0 <= id - local_off < num_local (an id outside
+ *     [0, num_experts) is dropped and sets MOE_DEV_BAD_EXPERT_ID in *status_d);
+ *   counts_d [num_local], offsets_d [num_local + 1]: rows and first row of each group, the
+ *     last offset the total; perm_src_d [rows_cap] and inv_d [T*k] as above.  A pair whose row
+ *     would pass rows_cap is dropped (inv -1) and sets MOE_DEV_ROWS_OVERFLOW; counts and
+ *     offsets keep counting it;
+ *   x_d and rows_d both NULL: the maps alone.
+ * num_experts and num_local up to 1024; row_align a power of two up to 128; status_d nullable.
+ * Passage: [EP] (tokens reach the local experts of the shard, grouped by expert); rows in
+ * bf16/fp16/fp32 for training are an addition of this library. */
+MOE_API moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
+                                const int32_t* topk_ids_d, int32_t T, int32_t k, int32_t H,
+                                int32_t num_experts, int32_t local_off, int32_t num_local,
+                                int32_t row_align, int32_t rows_cap, int32_t* counts_d,
+                                int32_t* offsets_d, int32_t* perm_src_d, int32_t* inv_d,
+                                void* rows_d, uint32_t* status_d, moe_stream_t stream);
+
+/* The gradient of dispatch: dx[t] = sum_j drows[inv[t*k + j]] over the kept pairs of t (zero
+ * when none is kept).  An inv outside [0, rows_cap) counts as dropped.
+ * Passage: none; training is an addition of this library (the pages serve only). */
+MOE_API moe_status moe_dispatch_backward(const void* drows_d, int32_t dtype,
+                                         const int32_t* inv_d, int32_t T, int32_t k, int32_t H,
+                                         int32_t rows_cap, void* dx_d, int64_t dx_stride,
+                                         moe_stream_t stream);
+
+/* Combine with the routing weights applied: out[t] = sum_j w[t*k + j] y[inv[t*k + j]] over the
+ * kept pairs of t (zero when none is kept); w_d fp32 [T][k].  (moe_combine adds rows that the
+ * down product has weighted already.)  An inv outside [0, rows_cap) counts as dropped.
+ * Passage: [EP] (each local expert's output, weighted by its routing weight, enters the
+ * shard's partial sum). */
+MOE_API moe_status moe_combine_weighted(const void* y_d, int32_t dtype, const int32_t* inv_d,
+                                        const float* w_d, int32_t T, int32_t k, int32_t H,
+                                        int32_t rows_cap, void* out_d, int64_t out_stride,
+                                        moe_stream_t stream);
+
+/* The gradient of combine: dy[inv[p]] = w[p] dout[t] (rows of y's dtype; rows that no pair has
+ * are not written) and dw[p] = <dout[t], y[inv[p]]> in fp32 (0 for a dropped pair).  dy_d or
+ * dw_d may be NULL (that gradient is not computed); y_d may be NULL when dw_d is.
+ * Passage: none; training is an addition of this library (the pages serve only). */
+MOE_API moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_stride,
+                                        const void* y_d, const int32_t* inv_d,
+                                        const float* w_d, int32_t T, int32_t k, int32_t H,
+                                        int32_t rows_cap, void* dy_d, float* dw_d,
+                                        moe_stream_t stream);
+
+/* ---- MXFP4: quantisation, scale layout, grouped product (see "MXFP4 matrices" above). */
+
+/* Bytes of the scales of an MXFP4 matrix [batch][rows][cols] in a layout (0 for arguments out
+ * of range).
+ * Passage: none; buffer sizing of this library (the pages have no counterpart). */
+MOE_API size_t moe_mxfp4_scale_bytes(int32_t batch, int32_t rows, int32_t cols,
+                                     int32_t sf_layout);
+
+/* MXFP4 quantiser of x [batch][rows][cols] (row_stride, batch_stride in elements, the columns
+ * contiguous).  transpose 0: the MXFP4 matrix [batch][rows][cols], cols % 32 == 0; transpose
+ * 1: that of each matrix's transpose, [batch][cols][rows], rows % 32 == 0.  A block's scale is
+ * 2^e, e by scale_rule (moe_mx_rule) clamped to [-127, 127]; an element is x 2^-e rounded to
+ * the nearest E2M1 value, ties to the even code, saturating at 6 (the sign of a value that
+ * rounds to zero is kept).  A block of zeros has scale byte 0; a block with a NaN or an
+ * infinity has scale byte 255 and codes 0.
+ *   perm_src_d (nullable; batch 1, transpose 0): rows r with perm_src[r] < 0 are skipped and
+ *     their outputs left as they are (the padding of sorted rows);
+ *   values_d (nullable): receives the values that the codes stand for, in x's dtype, contiguous
+ *     in the output's shape (a quantise-dequantise pass).
+ * Passage: [CK] (packed FP4 codes with block scales); the MX block form is an addition of this
+ * library. */
+MOE_API moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_t rows,
+                                   int32_t cols, int64_t row_stride, int64_t batch_stride,
+                                   int32_t transpose, int32_t scale_rule,
+                                   const int32_t* perm_src_d, uint8_t* codes_d, uint8_t* sf_d,
+                                   int32_t sf_layout, void* values_d, moe_stream_t stream);
+
+/* Canonical scales [batch][rows][cols/32] (a checkpoint's) -> the tiled layout, the scales of
+ * rows past `rows` zero.
+ * Passage: [CK] (the MMA tile layout of a checkpoint's block scales); MXFP4 is an addition of
+ * this library. */
+MOE_API moe_status moe_mxfp4_tile_scales(const uint8_t* sf_d, int32_t batch, int32_t rows,
+                                         int32_t cols, uint8_t* sf_tiled_d,
+                                         moe_stream_t stream);
+
+/* Bytes of workspace with which moe_grouped_gemm_mxfp4 may split the contraction of a product
+ * of these sizes (at most 32 MiB; 0 for arguments out of range).
+ * Passage: none; workspace sizing of this library (the pages have no counterpart). */
+MOE_API size_t moe_mxfp4_workspace_size(int32_t rows_cap, int32_t num_groups, int32_t N,
+                                        int32_t K);
+
+/* Grouped MXFP4 product: for group g and its rows r (offsets[g] <= r < offsets[g] + counts[g]),
+ *   out[r][n] = sum_i A[r][i] W_g[n][i],  n < N, accumulated in fp32, rounded once to out_dtype.
+ * a_codes_d [rows_cap][K/2] with tiled scales a_sf_d; w_codes_d [num_groups][N][K/2] with tiled
+ * scales w_sf_d; out_d [rows_cap][out_stride >= N].  offsets_d [g] must be a multiple of 128
+ * (row_align 128) and the group must lie within rows_cap, else the group is skipped and
+ * MOE_DEV_BAD_INDEX set; counts_d and offsets_d both NULL: one group, of all rows_cap rows.
+ * Rows outside every group are not written, and what their codes and scales hold is of no
+ * effect.  The gradient with respect to A is the same product of the output's gradient with
+ * the transposed matrices (moe_quant_mxfp4, transpose 1).
+ * K a multiple of 32; num_groups 1..1024; codes 16-byte aligned, scales 16-byte aligned.
+ * ws_d (nullable, 256-byte aligned): lets products with few rows split their contraction over
+ * more of the GPU; the parts are added in a fixed order.  It must not be used by another call
+ * that may run at the same time.
+ * Passage: [CK] and [EP] (the grouped FP4 products of the local experts); the MX block form is
+ * an addition of this library. */
+MOE_API moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_d,
+                                          int32_t rows_cap, const int32_t* counts_d,
+                                          const int32_t* offsets_d, int32_t num_groups,
+                                          const uint8_t* w_codes_d, const uint8_t* w_sf_d,
+                                          int32_t N, int32_t K, void* out_d, int32_t out_dtype,
+                                          int64_t out_stride, void* ws_d, size_t ws_bytes,
+                                          uint32_t* status_d, moe_stream_t stream);
 
 /* Self-test of the failure path of the pipelines' bounded waits: one thread waits, with the
  * same bounded wait the kernels use, on an mbarrier phase that nothing completes, so the

@@ -21,6 +21,9 @@ MOE_TILING_AUTO, MOE_TILING_ROWS, MOE_TILING_TOKENS, MOE_TILING_PAIRS, MOE_TILIN
     0, 1, 2, 3, 4
 MOE_DEV_BAD_EXPERT_ID, MOE_DEV_WAIT_TIMEOUT, MOE_DEV_ROWS_OVERFLOW = 1, 2, 4
 MOE_DEV_BAD_INDEX = 8
+MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
+MOE_SF_CANONICAL, MOE_SF_TILED = 0, 1
+MOE_MX_FLOOR, MOE_MX_CEIL = 0, 1
 
 
 class moe_config(C.Structure):
@@ -41,6 +44,7 @@ class moe_weights(C.Structure):
 
 _V = C.c_void_p
 _I = C.c_int32
+_L = C.c_int64
 _SZ = C.c_size_t
 
 # name -> (restype, argtypes); the list mirrors include/nvfp4moe.h
@@ -68,6 +72,17 @@ SIGNATURES = {
     "moe_get_status": (C.c_int, [_V, _V, _V, C.POINTER(C.c_uint32)]),
     "moe_status_string": (C.c_char_p, [C.c_int]),
     "moe_selftest_bounded_wait": (C.c_int, [_V, C.c_uint64, _V]),
+    "moe_dispatch_rows_capacity": (_I, [_I] * 4),
+    "moe_dispatch": (C.c_int, [_V, _I, _L, _V] + [_I] * 8 + [_V] * 7),
+    "moe_dispatch_backward": (C.c_int, [_V, _I, _V] + [_I] * 4 + [_V, _L, _V]),
+    "moe_combine_weighted": (C.c_int, [_V, _I, _V, _V] + [_I] * 4 + [_V, _L, _V]),
+    "moe_combine_backward": (C.c_int, [_V, _I, _L, _V, _V, _V] + [_I] * 4 + [_V, _V, _V]),
+    "moe_mxfp4_scale_bytes": (_SZ, [_I] * 4),
+    "moe_quant_mxfp4": (C.c_int, [_V] + [_I] * 4 + [_L, _L, _I, _I, _V, _V, _V, _I, _V, _V]),
+    "moe_mxfp4_tile_scales": (C.c_int, [_V, _I, _I, _I, _V, _V]),
+    "moe_mxfp4_workspace_size": (_SZ, [_I] * 4),
+    "moe_grouped_gemm_mxfp4": (C.c_int, [_V, _V, _I, _V, _V, _I, _V, _V, _I, _I, _V, _I, _L, _V,
+                                         _SZ, _V, _V]),
 }
 
 _lib = None
@@ -262,6 +277,154 @@ def moe_get_status(h, ws, stream=None):
     bits = C.c_uint32(0)
     st = load().moe_get_status(h, _p(ws), _stream(stream), C.byref(bits))
     return st, bits.value
+
+
+# ---------------------------------------------------------------- operators without a handle
+# Element types come from the tensors (int16 tensors are bf16 bit patterns, as above), sizes from
+# their shapes; a tensor whose type, shape or strides do not fit raises MoEError before the call.
+
+def _dtype(t):
+    import torch
+    global _DTYPES
+    if _DTYPES is None:
+        _DTYPES = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_FP16,
+                   torch.float32: MOE_FP32}
+    return _DTYPES.get(t.dtype, -1)
+
+
+_DTYPES = None
+
+
+def _need(ok, where):
+    if not ok:
+        raise MoEError(MOE_ERR_INVALID, where)
+
+
+def _rows_ok(t, H):
+    """Token rows [T][H]: the elements of a row contiguous, rows at any stride."""
+    return t.dim() == 2 and t.shape[1] == H and (H == 1 or t.stride(1) == 1)
+
+
+def moe_dispatch_rows_capacity(T, k, num_local, row_align):
+    return load().moe_dispatch_rows_capacity(T, k, num_local, row_align)
+
+
+def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, counts, offsets,
+                 perm_src, inv, rows, status=None, stream=None):
+    """x [T, H] (None: the maps alone, rows None too), topk_ids int32 [T, k]; outputs counts
+    [num_local], offsets [num_local + 1], perm_src [rows_cap], inv [T * k] (all int32), rows
+    [rows_cap, H]; status: an int32 word that errors found on the device are or-ed into."""
+    T, k = topk_ids.shape
+    cap = perm_src.numel()
+    _need(topk_ids.is_contiguous() and topk_ids.element_size() == 4 and inv.numel() == T * k and
+          counts.numel() == num_local and offsets.numel() == num_local + 1 and
+          (x is None) == (rows is None), "moe_dispatch")
+    H, xs, dt = 1, 1, MOE_BF16
+    if x is not None:
+        H, xs, dt = x.shape[1], x.stride(0), _dtype(x)
+        _need(x.shape[0] == T and _rows_ok(x, H) and dt == _dtype(rows) and
+              rows.shape == (cap, H) and rows.is_contiguous(), "moe_dispatch")
+    _check(load().moe_dispatch(_p(x), dt, xs, _p(topk_ids), T, k, H, num_experts, local_off,
+                               num_local, row_align, cap, _p(counts), _p(offsets), _p(perm_src),
+                               _p(inv), _p(rows), _p(status), _stream(stream)), "moe_dispatch")
+
+
+def moe_dispatch_backward(drows, inv, k, dx, stream=None):
+    """drows [rows_cap, H], inv int32 [T * k] -> dx [T, H]."""
+    T, H = dx.shape
+    _need(_rows_ok(dx, H) and drows.shape[1] == H and drows.is_contiguous() and
+          _dtype(drows) == _dtype(dx) and inv.numel() == T * k and inv.is_contiguous(),
+          "moe_dispatch_backward")
+    _check(load().moe_dispatch_backward(_p(drows), _dtype(dx), _p(inv), T, k, H, drows.shape[0],
+                                        _p(dx), dx.stride(0), _stream(stream)),
+           "moe_dispatch_backward")
+
+
+def moe_combine_weighted(y, inv, w, out, stream=None):
+    """y [rows_cap, H], inv int32 [T * k], w float32 [T, k] -> out [T, H]."""
+    (T, k), H = w.shape, out.shape[1]
+    _need(out.shape[0] == T and _rows_ok(out, H) and y.shape[1] == H and y.is_contiguous() and
+          _dtype(y) == _dtype(out) and inv.numel() == T * k and inv.is_contiguous() and
+          w.is_contiguous() and _dtype(w) == MOE_FP32, "moe_combine_weighted")
+    _check(load().moe_combine_weighted(_p(y), _dtype(y), _p(inv), _p(w), T, k, H, y.shape[0],
+                                       _p(out), out.stride(0), _stream(stream)),
+           "moe_combine_weighted")
+
+
+def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
+    """dout [T, H], y [rows_cap, H], inv int32 [T * k], w float32 [T, k] -> dy [rows_cap, H] and
+    dw float32 [T, k]; dy or dw may be None (and y with dw)."""
+    (T, k), H = w.shape, dout.shape[1]
+    _need(dout.shape[0] == T and _rows_ok(dout, H) and inv.numel() == T * k and
+          inv.is_contiguous() and w.is_contiguous() and _dtype(w) == MOE_FP32,
+          "moe_combine_backward")
+    cap = None
+    for t in (y, dy):
+        if t is not None:
+            _need(t.shape[1] == H and t.is_contiguous() and _dtype(t) == _dtype(dout) and
+                  cap in (None, t.shape[0]), "moe_combine_backward")
+            cap = t.shape[0]
+    if dw is not None:
+        _need(dw.numel() == T * k and dw.is_contiguous() and _dtype(dw) == MOE_FP32 and
+              y is not None, "moe_combine_backward")
+    _check(load().moe_combine_backward(_p(dout), _dtype(dout), dout.stride(0), _p(y), _p(inv),
+                                       _p(w), T, k, H, cap or 0, _p(dy), _p(dw),
+                                       _stream(stream)), "moe_combine_backward")
+
+
+def moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout):
+    return load().moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout)
+
+
+def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_FLOOR,
+                    perm_src=None, values=None, stream=None):
+    """x [rows, cols] or [batch, rows, cols] (columns contiguous); codes uint8, sf uint8 and values
+    (x's type) hold the MXFP4 matrix, or with transpose that of each matrix's transpose."""
+    B = x.shape[0] if x.dim() == 3 else 1
+    R, Cc = x.shape[-2:]
+    n = B * R * Cc
+    _need(x.dim() in (2, 3) and (Cc == 1 or x.stride(-1) == 1) and codes.numel() * 2 == n and
+          codes.is_contiguous() and
+          sf.numel() == moe_mxfp4_scale_bytes(B, *((Cc, R) if transpose else (R, Cc)),
+                                              sf_layout) and sf.is_contiguous() and
+          (perm_src is None or (perm_src.numel() == R and perm_src.element_size() == 4)) and
+          (values is None or (values.numel() == n and values.is_contiguous() and
+                              _dtype(values) == _dtype(x))), "moe_quant_mxfp4")
+    _check(load().moe_quant_mxfp4(_p(x), _dtype(x), B, R, Cc, x.stride(-2),
+                                  x.stride(0) if x.dim() == 3 else 0, int(bool(transpose)),
+                                  scale_rule, _p(perm_src), _p(codes), _p(sf), sf_layout,
+                                  _p(values), _stream(stream)), "moe_quant_mxfp4")
+
+
+def moe_mxfp4_tile_scales(sf, batch, rows, cols, sf_tiled, stream=None):
+    _need(sf.numel() == moe_mxfp4_scale_bytes(batch, rows, cols, MOE_SF_CANONICAL) and
+          sf_tiled.numel() == moe_mxfp4_scale_bytes(batch, rows, cols, MOE_SF_TILED) and
+          sf.is_contiguous() and sf_tiled.is_contiguous(), "moe_mxfp4_tile_scales")
+    _check(load().moe_mxfp4_tile_scales(_p(sf), batch, rows, cols, _p(sf_tiled),
+                                        _stream(stream)), "moe_mxfp4_tile_scales")
+
+
+def moe_mxfp4_workspace_size(rows_cap, num_groups, N, K):
+    return load().moe_mxfp4_workspace_size(rows_cap, num_groups, N, K)
+
+
+def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, ws=None,
+                           status=None, stream=None):
+    """a_codes [rows_cap, K/2], w_codes [num_groups, N, K/2] (uint8) with tiled scales; counts and
+    offsets int32 (both None: one group, all rows); out [rows_cap, N]."""
+    (G, N, K2), cap = w_codes.shape, a_codes.shape[0]
+    _need(a_codes.shape[1] == K2 and a_codes.is_contiguous() and w_codes.is_contiguous() and
+          a_codes.element_size() == 1 and w_codes.element_size() == 1 and
+          a_sf.numel() == moe_mxfp4_scale_bytes(1, cap, 2 * K2, MOE_SF_TILED) and
+          w_sf.numel() == moe_mxfp4_scale_bytes(G, N, 2 * K2, MOE_SF_TILED) and
+          out.shape[0] == cap and _rows_ok(out, N) and (counts is None) == (offsets is None) and
+          (counts is None or (counts.numel() == G and offsets.numel() >= G)),
+          "moe_grouped_gemm_mxfp4")
+    _check(load().moe_grouped_gemm_mxfp4(
+        _p(a_codes), _p(a_sf), cap, _p(counts), _p(offsets), G, _p(w_codes), _p(w_sf), N, 2 * K2,
+        _p(out), _dtype(out), out.stride(0), _p(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream(stream)),
+        "moe_grouped_gemm_mxfp4")
 
 
 from .layer import MoELayer, make_config  # noqa: E402,F401

@@ -1,0 +1,330 @@
+// C ABI of the operators that need no handle: tokens sorted by expert and back with their
+// gradients, MXFP4 quantisation and the grouped MXFP4 product.  Argument checks and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "host.cuh"
+
+using namespace moe;
+
+namespace {
+
+int elem_bytes(int dtype) { return dtype == MOE_FP32 ? 4 : 2; }
+
+bool dtype_ok(int dtype) { return dtype == MOE_BF16 || dtype == MOE_FP16 || dtype == MOE_FP32; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Whether a tensor of rows can be moved in 16-byte pieces.
+bool rows_vec(const void* p, int64_t row_bytes, int64_t stride_bytes)
+{
+    return aligned16(p) && row_bytes % 16 == 0 && stride_bytes % 16 == 0;
+}
+
+int num_sms()
+{
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+unsigned blocks_for(int64_t work, int per_block, int per_sm)
+{
+    const int64_t want = (work + per_block - 1) / per_block;
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)num_sms() * per_sm));
+}
+
+// T, k, H and rows_cap of the sorted-row calls.
+moe_status check_rows(int dtype, int T, int k, int H, int rows_cap)
+{
+    if (!dtype_ok(dtype) || T < 0 || k < 1 || H < 1 || rows_cap < 0) return MOE_ERR_INVALID;
+    if (k > kMaxTopK || (int64_t)T * k > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+bool align_ok(int a) { return a >= 1 && a <= 128 && (a & (a - 1)) == 0; }
+
+// combine (w given) and dispatch's gradient (w null)
+moe_status combine_rows(const void* y_d, int32_t dtype, const int32_t* inv_d, const float* w_d,
+                        int32_t T, int32_t k, int32_t H, int32_t rows_cap, void* out_d,
+                        int64_t out_stride, moe_stream_t stream)
+{
+    const moe_status st = check_rows(dtype, T, k, H, rows_cap);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    if (!inv_d || !out_d || (rows_cap && !y_d) || (T > 1 && out_stride < H))
+        return MOE_ERR_INVALID;
+    const int es = elem_bytes(dtype);
+    const bool vec = rows_vec(out_d, (int64_t)H * es, T > 1 ? out_stride * es : 0) && aligned16(y_d);
+    CombineArgs a = {};
+    a.y = y_d;
+    a.inv = inv_d;
+    a.w = w_d;
+    a.T = T;
+    a.k = k;
+    a.H = H;
+    a.rows_cap = rows_cap;
+    a.out = out_d;
+    a.out_stride = out_stride;
+    const int64_t n = (int64_t)T * (vec ? (int64_t)H * es / 16 : H);
+    return launch(combine_rows_kernel_for(dtype, vec), dim3(blocks_for(n, 256, 16)), dim3(256), 0,
+                  reinterpret_cast<cudaStream_t>(stream), false, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t moe_dispatch_rows_capacity(int32_t T, int32_t k, int32_t num_local, int32_t row_align)
+{
+    if (T < 0 || k < 1 || k > kMaxTopK || num_local < 0 || num_local > kMaxExperts ||
+        !align_ok(row_align))
+        return 0;
+    const int64_t P = (int64_t)T * k, a = row_align;
+    const int64_t rows = (P + std::min<int64_t>(num_local, P) * (a - 1) + a - 1) / a * a;
+    return rows > 0x7fffffff ? 0 : (int32_t)rows;
+}
+
+moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
+                        const int32_t* topk_ids_d, int32_t T, int32_t k, int32_t H,
+                        int32_t num_experts, int32_t local_off, int32_t num_local,
+                        int32_t row_align, int32_t rows_cap, int32_t* counts_d,
+                        int32_t* offsets_d, int32_t* perm_src_d, int32_t* inv_d, void* rows_d,
+                        uint32_t* status_d, moe_stream_t stream)
+{
+    const NvtxRange nvtx_range("moe_dispatch");
+    if (!x_d != !rows_d) return MOE_ERR_INVALID;
+    const moe_status st = check_rows(x_d ? dtype : MOE_BF16, T, k, x_d ? H : 1, rows_cap);
+    if (st != MOE_OK) return st;
+    if (num_experts < 1 || local_off < 0 || num_local < 0 || !align_ok(row_align) ||
+        (int64_t)local_off + num_local > num_experts || k > num_experts)
+        return MOE_ERR_INVALID;
+    if (x_d && T > 1 && x_stride < H) return MOE_ERR_INVALID;
+    if (!offsets_d || (num_local && !counts_d) || (T && (!topk_ids_d || !inv_d)) ||
+        (rows_cap && !perm_src_d))
+        return MOE_ERR_INVALID;
+    const int64_t P = (int64_t)T * k;
+    if (num_experts > kMaxExperts || P + (int64_t)num_local * (row_align - 1) > 0x7fffffff)
+        return MOE_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+    SortArgs a = {};
+    a.ids = topk_ids_d;
+    a.P = (int)P;
+    a.E = num_experts;
+    a.off = local_off;
+    a.El = num_local;
+    a.align = row_align;
+    a.rows_cap = rows_cap;
+    a.counts = counts_d;
+    a.offsets = offsets_d;
+    a.perm_src = perm_src_d;
+    a.inv = inv_d;
+    a.status = status_d;
+    const int blocks = P <= 1024 ? 1 : kSortBlocks;
+    a.segment = (int)((P + (int64_t)blocks * 32 * 32 - 1) / ((int64_t)blocks * 32 * 32) * 32);
+    if (cudaFuncSetAttribute(sort_pairs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)sort_smem(kMaxExperts)) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sort_smem(num_local);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, sort_pairs_kernel, a) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!x_d || T == 0 || rows_cap == 0 || num_local == 0) return MOE_OK;
+
+    const int es = elem_bytes(dtype);
+    const bool vec = rows_vec(x_d, (int64_t)H * es, T > 1 ? x_stride * es : 0) && aligned16(rows_d);
+    const int unit = vec ? 16 : es;
+    DispatchArgs d = {};
+    d.x = x_d;
+    d.x_stride = x_stride * es / unit;
+    d.inv = inv_d;
+    d.T = T;
+    d.k = k;
+    d.units = (int)((int64_t)H * es / unit);
+    d.rows_cap = rows_cap;
+    d.rows = rows_d;
+    const int64_t runs = (int64_t)T * ceil_div(d.units, 128);
+    return launch(dispatch_rows_kernel_for(unit), dim3(blocks_for(runs, 8, 8)), dim3(256), 0, s,
+                  false, d);
+}
+
+moe_status moe_dispatch_backward(const void* drows_d, int32_t dtype, const int32_t* inv_d,
+                                 int32_t T, int32_t k, int32_t H, int32_t rows_cap, void* dx_d,
+                                 int64_t dx_stride, moe_stream_t stream)
+{
+    const NvtxRange nvtx_range("moe_dispatch_backward");
+    return combine_rows(drows_d, dtype, inv_d, nullptr, T, k, H, rows_cap, dx_d, dx_stride, stream);
+}
+
+moe_status moe_combine_weighted(const void* y_d, int32_t dtype, const int32_t* inv_d,
+                                const float* w_d, int32_t T, int32_t k, int32_t H,
+                                int32_t rows_cap, void* out_d, int64_t out_stride,
+                                moe_stream_t stream)
+{
+    const NvtxRange nvtx_range("moe_combine_weighted");
+    if (T > 0 && !w_d) return MOE_ERR_INVALID;
+    return combine_rows(y_d, dtype, inv_d, w_d, T, k, H, rows_cap, out_d, out_stride, stream);
+}
+
+moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_stride,
+                                const void* y_d, const int32_t* inv_d, const float* w_d,
+                                int32_t T, int32_t k, int32_t H, int32_t rows_cap, void* dy_d,
+                                float* dw_d, moe_stream_t stream)
+{
+    const NvtxRange nvtx_range("moe_combine_backward");
+    const moe_status st = check_rows(dtype, T, k, H, rows_cap);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    if (!dout_d || !inv_d || !w_d || (!dy_d && !dw_d) || (dw_d && rows_cap && !y_d) ||
+        (T > 1 && dout_stride < H))
+        return MOE_ERR_INVALID;
+    const int es = elem_bytes(dtype);
+    const bool vec = rows_vec(dout_d, (int64_t)H * es, T > 1 ? dout_stride * es : 0) &&
+                     (!dw_d || aligned16(y_d)) && (!dy_d || aligned16(dy_d));
+    CombineBackArgs a = {};
+    a.dout = dout_d;
+    a.dout_stride = dout_stride;
+    a.y = y_d;
+    a.inv = inv_d;
+    a.w = w_d;
+    a.T = T;
+    a.k = k;
+    a.H = H;
+    a.rows_cap = rows_cap;
+    a.dy = dy_d;
+    a.dw = dw_d;
+    return launch(combine_back_kernel_for(dtype, vec), dim3(blocks_for(T, 1, 8)),
+                  dim3(kCombineBackThreads), 0, reinterpret_cast<cudaStream_t>(stream), false, a);
+}
+
+size_t moe_mxfp4_scale_bytes(int32_t batch, int32_t rows, int32_t cols, int32_t sf_layout)
+{
+    if (batch < 0 || rows < 0 || cols <= 0 || cols % 32 ||
+        (sf_layout != MOE_SF_CANONICAL && sf_layout != MOE_SF_TILED))
+        return 0;
+    const size_t blocks = (size_t)cols / 32;
+    if (sf_layout == MOE_SF_CANONICAL) return (size_t)batch * rows * blocks;
+    return (size_t)batch * (((size_t)rows + 127) / 128) * ((blocks + 3) / 4) * 512;
+}
+
+moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_t rows,
+                           int32_t cols, int64_t row_stride, int64_t batch_stride,
+                           int32_t transpose, int32_t scale_rule, const int32_t* perm_src_d,
+                           uint8_t* codes_d, uint8_t* sf_d, int32_t sf_layout, void* values_d,
+                           moe_stream_t stream)
+{
+    const NvtxRange nvtx_range("moe_quant_mxfp4");
+    if (!dtype_ok(dtype) || batch < 0 || rows < 0 || cols < 1) return MOE_ERR_INVALID;
+    if (transpose != 0 && transpose != 1) return MOE_ERR_INVALID;
+    if (scale_rule != MOE_MX_FLOOR && scale_rule != MOE_MX_CEIL) return MOE_ERR_INVALID;
+    if (sf_layout != MOE_SF_CANONICAL && sf_layout != MOE_SF_TILED) return MOE_ERR_INVALID;
+    if (perm_src_d && (transpose || batch != 1)) return MOE_ERR_INVALID;
+    if ((transpose ? rows : cols) % 32) return MOE_ERR_UNSUPPORTED;
+    if (batch == 0 || rows == 0) return MOE_OK;
+    if (!x_d || !codes_d || !sf_d || (rows > 1 && row_stride < cols) ||
+        (batch > 1 && batch_stride < 0))
+        return MOE_ERR_INVALID;
+    if (!aligned16(codes_d) || (values_d && !aligned16(values_d))) return MOE_ERR_INVALID;
+    MxQuantArgs a = {};
+    a.x = x_d;
+    a.row_stride = row_stride;
+    a.batch_stride = batch_stride;
+    a.batch = batch;
+    a.rows = rows;
+    a.cols = cols;
+    a.rule = scale_rule;
+    a.perm_src = perm_src_d;
+    a.codes = codes_d;
+    a.sf = sf_d;
+    a.layout = sf_layout;
+    a.values = values_d;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (transpose) {
+        const int64_t n = (int64_t)batch * (rows / 32) * cols;
+        return launch(mx_quant_transposed_kernel_for(dtype), dim3(blocks_for(n, 128, 16)),
+                      dim3(128), 0, s, false, a);
+    }
+    const int es = elem_bytes(dtype);
+    const bool vec = rows_vec(x_d, (int64_t)cols * es, rows > 1 ? row_stride * es : 0) &&
+                     (batch == 1 || batch_stride * es % 16 == 0);
+    const int64_t n = (int64_t)batch * rows * (cols / 8);
+    return launch(mx_quant_kernel_for(dtype, vec), dim3(blocks_for(n, 256, 8)), dim3(256), 0, s,
+                  false, a);
+}
+
+moe_status moe_mxfp4_tile_scales(const uint8_t* sf_d, int32_t batch, int32_t rows, int32_t cols,
+                                 uint8_t* sf_tiled_d, moe_stream_t stream)
+{
+    const NvtxRange nvtx_range("moe_mxfp4_tile_scales");
+    if (batch < 0 || rows < 0 || cols < 1) return MOE_ERR_INVALID;
+    if (cols % 32) return MOE_ERR_UNSUPPORTED;
+    if (batch == 0 || rows == 0) return MOE_OK;
+    if (!sf_d || !sf_tiled_d || !aligned16(sf_tiled_d)) return MOE_ERR_INVALID;
+    const int64_t n = (int64_t)moe_mxfp4_scale_bytes(batch, rows, cols, MOE_SF_TILED) / 4;
+    return launch(mx_tile_scales_kernel, dim3(blocks_for(n, 256, 16)), dim3(256), 0,
+                  reinterpret_cast<cudaStream_t>(stream), false, sf_d, batch, rows, cols / 32,
+                  sf_tiled_d);
+}
+
+size_t moe_mxfp4_workspace_size(int32_t rows_cap, int32_t num_groups, int32_t N, int32_t K)
+{
+    if (rows_cap < 0 || num_groups < 1 || num_groups > kMaxExperts || N < 1 || K < 32 || K % 32)
+        return 0;
+    return 32u << 20;
+}
+
+moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_d,
+                                  int32_t rows_cap, const int32_t* counts_d,
+                                  const int32_t* offsets_d, int32_t num_groups,
+                                  const uint8_t* w_codes_d, const uint8_t* w_sf_d, int32_t N,
+                                  int32_t K, void* out_d, int32_t out_dtype, int64_t out_stride,
+                                  void* ws_d, size_t ws_bytes, uint32_t* status_d,
+                                  moe_stream_t stream)
+{
+    const NvtxRange nvtx_range("moe_grouped_gemm_mxfp4");
+    if (!dtype_ok(out_dtype) || rows_cap < 0 || num_groups < 1 || N < 1 || K < 1 ||
+        !counts_d != !offsets_d || (!counts_d && num_groups != 1))
+        return MOE_ERR_INVALID;
+    if (K % 32 || num_groups > kMaxExperts || (int64_t)num_groups * N > 0x7fffffff)
+        return MOE_ERR_UNSUPPORTED;
+    if (rows_cap == 0) return MOE_OK;
+    if (!a_codes_d || !a_sf_d || !w_codes_d || !w_sf_d || !out_d ||
+        (rows_cap > 1 && out_stride < N))
+        return MOE_ERR_INVALID;
+    if (!aligned16(a_codes_d) || !aligned16(a_sf_d) || !aligned16(w_codes_d) || !aligned16(w_sf_d) ||
+        (reinterpret_cast<uintptr_t>(out_d) % elem_bytes(out_dtype)) != 0 ||
+        (reinterpret_cast<uintptr_t>(ws_d) & 255) != 0 || (ws_bytes && !ws_d))
+        return MOE_ERR_INVALID;
+    MxGemmArgs a = {};
+    a.a_codes = a_codes_d;
+    a.a_sf = a_sf_d;
+    a.rows_cap = rows_cap;
+    a.counts = counts_d;
+    a.offsets = offsets_d;
+    a.G = num_groups;
+    a.w_codes = w_codes_d;
+    a.w_sf = w_sf_d;
+    a.N = N;
+    a.K = K;
+    a.out = out_d;
+    a.out_stride = out_stride;
+    a.status = status_d;
+    return launch(mx_gemm_kernel_for(out_dtype),
+                  dim3(ceil_div(N, 64), std::min(ceil_div(rows_cap, 32), 65535)), dim3(256), 0,
+                  reinterpret_cast<cudaStream_t>(stream), false, a);
+}
+
+}  // extern "C"

@@ -1,0 +1,388 @@
+// Tokens sorted by expert and back, with their gradients: the sort of the routed (token, expert)
+// pairs, the row scatter (dispatch), the weighted row gather (combine, and dispatch's gradient)
+// and combine's gradient.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kernels.cuh"
+
+namespace moe {
+
+// ------------------------------------------------------------------ element types
+
+// Pieces of a row: 16 bytes (kVec elements) when rows allow it, else one element.
+template <typename T>
+struct Elem;
+
+template <>
+struct Elem<__nv_bfloat16> {
+    static constexpr int kVec = 8;
+    static __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+};
+
+template <>
+struct Elem<__half> {
+    static constexpr int kVec = 8;
+    static __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+};
+
+template <>
+struct Elem<float> {
+    static constexpr int kVec = 4;
+    static __device__ __forceinline__ float to_f32(float v) { return v; }
+    static __device__ __forceinline__ float from_f32(float v) { return v; }
+};
+
+// A piece of V elements of type T (V = kVec: one 16-byte access; V = 1: one element).
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Piece {
+    T v[V];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Piece<T, V>& p, float (&f)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = Elem<T>::to_f32(p.v[i]);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Piece<T, V> pack(const float (&f)[V])
+{
+    Piece<T, V> p;
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.v[i] = Elem<T>::from_f32(f[i]);
+    return p;
+}
+
+// ------------------------------------------------------------------ the sort
+
+// One thread block cluster sorts all P pairs: a stable counting sort in one launch.  Every warp
+// of the cluster owns a contiguous segment of the pairs and a table of counts by expert in
+// shared memory.  Pass 1 counts the segments (32 pairs at a time: lanes of equal expert found
+// with one match instruction, their first lane adds their number, so no atomics).  Prefix sums
+// over the block's warps, over the cluster's blocks (read through distributed shared memory) and
+// over the experts (group sizes rounded up to row_align) turn the tables into the row of each
+// segment's first pair of each expert.  Pass 2 walks the segments again: a pair's row is its
+// table entry plus the number of lower lanes of equal expert, the first lane moves the entry on.
+__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32_t rank)
+{
+    uint32_t v;
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\t"
+        "mapa.shared::cluster.u32 ra, %1, %2;\n\t"
+        "ld.shared::cluster.u32 %0, [ra];\n\t}"
+        : "=r"(v)
+        : "r"(smem_u32(local)), "r"(rank)
+        : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a)
+{
+    extern __shared__ uint32_t s_tab[];  // [32 warps][El]
+    __shared__ uint32_t s_tot[kMaxExperts];
+    __shared__ uint32_t s_off[kMaxExperts + 1];
+    __shared__ uint32_t s_cnt[kMaxExperts];
+    __shared__ uint32_t s_warp[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = blockIdx.x, nblk = gridDim.x;
+    const int El = a.El;
+    uint32_t* tab = s_tab + (size_t)warp * El;
+    for (int e = lane; e < El; e += 32) tab[e] = 0;
+    __syncwarp();
+    const int64_t p0 = min((int64_t)a.P, ((int64_t)rank * 32 + warp) * a.segment);
+    const int64_t p1 = min((int64_t)a.P, p0 + a.segment);
+    auto local_expert = [&](int64_t p, bool count_bad) {
+        if (p >= p1) return -1;
+        const int id = a.ids[p];
+        if (id < 0 || id >= a.E) {
+            if (count_bad) set_status(a.status, MOE_DEV_BAD_EXPERT_ID);
+            return -1;
+        }
+        const int le = id - a.off;
+        return (le >= 0 && le < El) ? le : -1;
+    };
+    for (int64_t p = p0; p < p1; p += 32) {
+        const int le = local_expert(p + lane, true);
+        const uint32_t same = __match_any_sync(0xffffffffu, le);
+        if (le >= 0 && lane == __ffs(same) - 1) tab[le] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // exclusive prefix over the block's warps, a thread per expert
+    for (int e = tid; e < El; e += kSortThreads) {
+        uint32_t run = 0;
+        for (int w = 0; w < 32; ++w) {
+            const uint32_t c = s_tab[(size_t)w * El + e];
+            s_tab[(size_t)w * El + e] = run;
+            run += c;
+        }
+        s_tot[e] = run;
+    }
+    cluster_sync();
+    // pairs of each expert in the blocks before this one, and in all of them
+    uint32_t before = 0, all = 0;
+    if (tid < El)
+        for (int b = 0; b < nblk; ++b) {
+            const uint32_t c = b == rank ? s_tot[tid] : ld_cluster_u32(&s_tot[tid], b);
+            if (b < rank) before += c;
+            all += c;
+        }
+    // first row of each group: exclusive scan of the counts rounded up
+    const uint32_t padded = (all + a.align - 1) / a.align * a.align;
+    uint32_t x = padded;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t v = s_warp[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        s_warp[lane] = v;
+    }
+    __syncthreads();
+    const uint32_t first = x - padded + (warp ? s_warp[warp - 1] : 0);
+    if (tid < El) {
+        s_off[tid] = first;
+        s_cnt[tid] = all;
+        if (tid == El - 1) s_off[El] = first + padded;
+        for (int w = 0; w < 32; ++w) s_tab[(size_t)w * El + tid] += first + before;
+    }
+    if (El == 0 && tid == 0) s_off[0] = 0;
+    __syncthreads();
+    if (rank == 0) {
+        for (int e = tid; e <= El; e += kSortThreads) a.offsets[e] = (int32_t)s_off[e];
+        for (int e = tid; e < El; e += kSortThreads) a.counts[e] = (int32_t)s_cnt[e];
+        if (tid == 0 && s_off[El] > (uint32_t)a.rows_cap) {
+            // rows past the capacity: only padding may fall there
+            for (int e = 0; e < El; ++e)
+                if (s_cnt[e] && s_off[e] + s_cnt[e] > (uint32_t)a.rows_cap)
+                    set_status(a.status, MOE_DEV_ROWS_OVERFLOW);
+        }
+    }
+    // the pairs' rows
+    for (int64_t p = p0; p < p1; p += 32) {
+        const int le = local_expert(p + lane, false);
+        const uint32_t same = __match_any_sync(0xffffffffu, le);
+        int row = -1;
+        if (le >= 0) {
+            const uint32_t r = tab[le] + __popc(same & ((1u << lane) - 1u));
+            if (r < (uint32_t)a.rows_cap) row = (int)r;
+        }
+        __syncwarp();
+        if (le >= 0 && lane == __ffs(same) - 1) tab[le] += __popc(same);
+        __syncwarp();
+        if (p + lane < p1) {
+            a.inv[p + lane] = row;
+            if (row >= 0) a.perm_src[row] = (int32_t)(p + lane);
+        }
+    }
+    // rows of no pair
+    const uint32_t cap = (uint32_t)a.rows_cap;
+    for (int g = rank * 32 + warp; g < El; g += nblk * 32) {
+        const uint32_t r1 = min(s_off[g + 1], cap);
+        for (uint32_t r = s_off[g] + s_cnt[g] + lane; r < r1; r += 32) a.perm_src[r] = -1;
+    }
+    for (uint32_t r = s_off[El] + (uint32_t)rank * kSortThreads + tid; r < cap;
+         r += (uint32_t)nblk * kSortThreads)
+        a.perm_src[r] = -1;
+    cluster_sync();  // no block leaves while another may read its totals
+}
+
+// ------------------------------------------------------------------ dispatch
+
+// rows[inv[t k + j]] = x[t]: a warp takes a run of pieces of one token and stores it to each of
+// the token's rows, so x is read once.
+template <typename U>
+__global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchArgs a)
+{
+    constexpr int kRun = 4;  // pieces per lane
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+    const int runs = (a.units + 32 * kRun - 1) / (32 * kRun);
+    const U* x = static_cast<const U*>(a.x);
+    U* rows = static_cast<U*>(a.rows);
+    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+         i < (int64_t)a.T * runs; i += warps) {
+        const int64_t t = i / runs;
+        const int u0 = (int)(i % runs) * 32 * kRun + lane;
+        U v[kRun];
+#pragma unroll
+        for (int r = 0; r < kRun; ++r)
+            if (u0 + 32 * r < a.units) v[r] = x[t * a.x_stride + u0 + 32 * r];
+        for (int j = 0; j < a.k; ++j) {
+            const int row = a.inv[t * a.k + j];
+            if ((uint32_t)row >= (uint32_t)a.rows_cap) continue;
+#pragma unroll
+            for (int r = 0; r < kRun; ++r)
+                if (u0 + 32 * r < a.units) rows[(int64_t)row * a.units + u0 + 32 * r] = v[r];
+        }
+    }
+}
+
+DispatchKernel dispatch_rows_kernel_for(int unit_bytes)
+{
+    switch (unit_bytes) {
+        case 16: return dispatch_rows_kernel<uint4>;
+        case 4: return dispatch_rows_kernel<uint32_t>;
+        default: return dispatch_rows_kernel<uint16_t>;
+    }
+}
+
+// ------------------------------------------------------------------ combine
+
+// out[t] = sum_j w[t, j] rows[inv[t k + j]] (w null: 1): a thread per piece of a token, the loads
+// of up to eight rows in flight, fp32 sums in ascending j.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
+{
+    const int units = a.H / V;
+    const int64_t n = (int64_t)a.T * units;
+    const T* y = static_cast<const T*>(a.y);
+    T* out = static_cast<T*>(a.out);
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = i / units;
+        const int u = (int)(i % units);
+        float acc[V] = {};
+        for (int j0 = 0; j0 < a.k; j0 += 8) {
+            Piece<T, V> p[8];
+            float w[8];
+            bool live[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                live[j] = false;
+                if (j0 + j < a.k) {
+                    const int row = a.inv[t * a.k + j0 + j];
+                    live[j] = (uint32_t)row < (uint32_t)a.rows_cap;
+                    if (live[j]) {
+                        p[j] = *reinterpret_cast<const Piece<T, V>*>(y + (int64_t)row * a.H +
+                                                                     (int64_t)u * V);
+                        w[j] = a.w ? a.w[t * a.k + j0 + j] : 1.0f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (live[j]) {
+                    float f[V];
+                    unpack(p[j], f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(w[j], f[e], acc[e]);
+                }
+        }
+        *reinterpret_cast<Piece<T, V>*>(out + t * a.out_stride + (int64_t)u * V) = pack<T, V>(acc);
+    }
+}
+
+CombineKernel combine_rows_kernel_for(int dtype, bool vec)
+{
+    switch (dtype) {
+        case MOE_BF16:
+            return vec ? combine_rows_kernel<__nv_bfloat16, 8> : combine_rows_kernel<__nv_bfloat16, 1>;
+        case MOE_FP16: return vec ? combine_rows_kernel<__half, 8> : combine_rows_kernel<__half, 1>;
+        default: return vec ? combine_rows_kernel<float, 4> : combine_rows_kernel<float, 1>;
+    }
+}
+
+// ------------------------------------------------------------------ combine's gradient
+
+// A block per token: dy rows = w dout, and the k dot products <dout, y row>, eight rows at a
+// time, reduced over the block.
+template <typename T, int V>
+__global__ void __launch_bounds__(kCombineBackThreads) combine_back_kernel(CombineBackArgs a)
+{
+    __shared__ float s_dot[kCombineBackThreads / 32][8];
+    const int units = a.H / V;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T* dout = static_cast<const T*>(a.dout);
+    const T* y = static_cast<const T*>(a.y);
+    T* dy = static_cast<T*>(a.dy);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        for (int j0 = 0; j0 < a.k; j0 += 8) {
+            int row[8];
+            float w[8], dot[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dot[j] = 0.0f;
+                w[j] = 0.0f;
+                row[j] = -1;
+                if (j0 + j < a.k) {
+                    const int r = a.inv[t * a.k + j0 + j];
+                    if ((uint32_t)r < (uint32_t)a.rows_cap) {
+                        row[j] = r;
+                        w[j] = a.w[t * a.k + j0 + j];
+                    }
+                }
+            }
+            for (int u = threadIdx.x; u < units; u += kCombineBackThreads) {
+                float d[V];
+                unpack(*reinterpret_cast<const Piece<T, V>*>(dout + t * a.dout_stride +
+                                                             (int64_t)u * V), d);
+                Piece<T, V> p[8];
+                if (a.dw) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (row[j] >= 0)
+                            p[j] = *reinterpret_cast<const Piece<T, V>*>(
+                                y + (int64_t)row[j] * a.H + (int64_t)u * V);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (row[j] < 0) continue;
+                    if (a.dw) {
+                        float f[V];
+                        unpack(p[j], f);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
+                    }
+                    if (dy) {
+                        float g[V];
+#pragma unroll
+                        for (int e = 0; e < V; ++e) g[e] = w[j] * d[e];
+                        *reinterpret_cast<Piece<T, V>*>(dy + (int64_t)row[j] * a.H +
+                                                        (int64_t)u * V) = pack<T, V>(g);
+                    }
+                }
+            }
+            if (a.dw) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+                        dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+                    if (lane == 0) s_dot[warp][j] = dot[j];
+                }
+                __syncthreads();
+                if (threadIdx.x < 8 && j0 + (int)threadIdx.x < a.k) {
+                    float sum = 0.0f;
+                    for (int q = 0; q < kCombineBackThreads / 32; ++q) sum += s_dot[q][threadIdx.x];
+                    a.dw[t * a.k + j0 + threadIdx.x] = sum;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+CombineBackKernel combine_back_kernel_for(int dtype, bool vec)
+{
+    switch (dtype) {
+        case MOE_BF16:
+            return vec ? combine_back_kernel<__nv_bfloat16, 8> : combine_back_kernel<__nv_bfloat16, 1>;
+        case MOE_FP16: return vec ? combine_back_kernel<__half, 8> : combine_back_kernel<__half, 1>;
+        default: return vec ? combine_back_kernel<float, 4> : combine_back_kernel<float, 1>;
+    }
+}
+
+}  // namespace moe

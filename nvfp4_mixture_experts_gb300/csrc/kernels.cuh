@@ -318,4 +318,105 @@ FusedGemvKernel gemv_w4a16_fused_kernel_ptr();
 size_t gemv_w4a16_fused_smem(int H, int tok_rows, int slots, int list_cap);
 int gemv_w4a16_fused_slots(int H, int tok_rows, int list_cap);
 
+// ---- dispatch.cu: tokens sorted by expert and back, and their gradients
+constexpr int kSortThreads = 1024;
+constexpr int kSortBlocks = 8;       // blocks of the sort's cluster at most (the portable size)
+struct SortArgs {
+    const int32_t* ids;   // [P]
+    int P;                // T * k
+    int segment;          // pairs per warp of the cluster (a multiple of 32)
+    int E, off, El;       // experts; the shard's first, and how many
+    int align;            // groups start on multiples of it
+    int rows_cap;
+    int32_t* counts;      // [El]
+    int32_t* offsets;     // [El + 1]
+    int32_t* perm_src;    // [rows_cap]
+    int32_t* inv;         // [P]
+    uint32_t* status;     // nullable
+};
+__global__ void sort_pairs_kernel(SortArgs args);
+inline size_t sort_smem(int El) { return (size_t)32 * El * 4; }
+
+struct DispatchArgs {
+    const void* x;
+    int64_t x_stride;     // in units
+    const int32_t* inv;
+    int T, k;
+    int units;            // units (16, 4 or 2 bytes) per row
+    int rows_cap;
+    void* rows;
+};
+using DispatchKernel = void (*)(DispatchArgs);
+DispatchKernel dispatch_rows_kernel_for(int unit_bytes);
+
+struct CombineArgs {
+    const void* y;
+    const int32_t* inv;
+    const float* w;       // nullable: 1
+    int T, k, H, rows_cap;
+    void* out;
+    int64_t out_stride;   // in elements
+};
+using CombineKernel = void (*)(CombineArgs);
+// vec: every row starts on 16 bytes and is a whole number of 16-byte pieces
+CombineKernel combine_rows_kernel_for(int dtype, bool vec);
+
+constexpr int kCombineBackThreads = 256;
+struct CombineBackArgs {
+    const void* dout;
+    int64_t dout_stride;  // in elements
+    const void* y;        // nullable when dw is
+    const int32_t* inv;
+    const float* w;
+    int T, k, H, rows_cap;
+    void* dy;             // nullable
+    float* dw;            // nullable
+};
+using CombineBackKernel = void (*)(CombineBackArgs);
+CombineBackKernel combine_back_kernel_for(int dtype, bool vec);
+
+// ---- mxfp4.cu: MXFP4 quantisation and scale layouts
+struct MxQuantArgs {
+    const void* x;
+    int64_t row_stride, batch_stride;  // in elements
+    int batch, rows, cols;             // of x
+    int rule;                          // moe_mx_rule
+    const int32_t* perm_src;           // nullable: rows with a negative entry are skipped
+    uint8_t* codes;
+    uint8_t* sf;
+    int layout;                        // moe_sf_layout
+    void* values;                      // nullable
+};
+using MxQuantKernel = void (*)(MxQuantArgs);
+MxQuantKernel mx_quant_kernel_for(int dtype, bool vec);
+MxQuantKernel mx_quant_transposed_kernel_for(int dtype);
+__global__ void mx_tile_scales_kernel(const uint8_t* sf, int batch, int rows, int blocks,
+                                      uint8_t* tiled);
+
+// Byte of scale block kb of row r (of matrix b) in the tiled layout; RB row blocks of 128 and KA
+// atoms of four blocks per matrix.
+__host__ __device__ __forceinline__ size_t mx_sf_tiled(int64_t b, int RB, int KA, int r, int kb)
+{
+    return (size_t)(((b * RB + (r >> 7)) * KA + (kb >> 2)) * 512 + (r & 31) * 16 +
+                    ((r >> 5) & 3) * 4 + (kb & 3));
+}
+
+// ---- gemm_mxfp4.cu: the grouped MXFP4 product
+struct MxGemmArgs {
+    const uint8_t* a_codes;
+    const uint8_t* a_sf;
+    int rows_cap;
+    const int32_t* counts;   // nullable (with offsets): one group of rows_cap rows
+    const int32_t* offsets;
+    int G;
+    const uint8_t* w_codes;
+    const uint8_t* w_sf;
+    int N, K;
+    void* out;
+    int64_t out_stride;
+    uint32_t* status;
+};
+using MxGemmKernel = void (*)(MxGemmArgs);
+MxGemmKernel mx_gemm_kernel_for(int out_dtype);
+
 }  // namespace moe
