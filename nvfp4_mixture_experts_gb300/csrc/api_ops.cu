@@ -308,23 +308,39 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
         (reinterpret_cast<uintptr_t>(out_d) % elem_bytes(out_dtype)) != 0 ||
         (reinterpret_cast<uintptr_t>(ws_d) & 255) != 0 || (ws_bytes && !ws_d))
         return MOE_ERR_INVALID;
+    const int KA = (K / 32 + 3) / 4, es = elem_bytes(out_dtype);
+    CUtensorMap tmW, tmT, tmT16, tmSW, tmST;
+    constexpr auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, U32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+    constexpr auto SW = CU_TENSOR_MAP_SWIZZLE_128B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if (!make_tmap_3d(&tmW, w_codes_d, U8, K / 2, N, num_groups, K / 2, 128, 128, SW) ||
+        !make_tmap(&tmT, a_codes_d, U8, K / 2, rows_cap, K / 2, 128, 128, SW) ||
+        !make_tmap(&tmT16, a_codes_d, U8, K / 2, rows_cap, K / 2, 128, 16, SW) ||
+        !make_tmap(&tmSW, w_sf_d, U32, KA * 128, (uint64_t)num_groups * ceil_div(N, 128), KA * 512,
+                   256, 1, NOSW) ||
+        !make_tmap(&tmST, a_sf_d, U32, KA * 128, ceil_div(rows_cap, 128), KA * 512, 256, 1, NOSW))
+        return MOE_ERR_CUDA;
     MxGemmArgs a = {};
-    a.a_codes = a_codes_d;
-    a.a_sf = a_sf_d;
     a.rows_cap = rows_cap;
     a.counts = counts_d;
     a.offsets = offsets_d;
     a.G = num_groups;
-    a.w_codes = w_codes_d;
-    a.w_sf = w_sf_d;
     a.N = N;
     a.K = K;
     a.out = out_d;
     a.out_stride = out_stride;
+    a.vec = rows_vec(out_d, (int64_t)N * es, rows_cap > 1 ? out_stride * es : 0);
     a.status = status_d;
-    return launch(mx_gemm_kernel_for(out_dtype),
-                  dim3(ceil_div(N, 64), std::min(ceil_div(rows_cap, 32), 65535)), dim3(256), 0,
-                  reinterpret_cast<cudaStream_t>(stream), false, a);
+    const MxGemmKernel kern = gemm_mxfp4_kernel_for(out_dtype);
+    const int smem = gemm_mxfp4_smem(num_groups, es);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    // at most this many tiles, however the rows fall into groups
+    const int64_t tiles = std::min<int64_t>(num_groups + rows_cap / kMxTileRows, ceil_div(rows_cap, 128)) *
+                          ceil_div(N, 256);
+    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms() / 2));
+    return launch_pairs(kern, dim3(2 * pairs), dim3(kMxThreads), smem,
+                        reinterpret_cast<cudaStream_t>(stream), false, tmW, tmT, tmT16, tmSW, tmST, a);
 }
 
 }  // extern "C"

@@ -1,4 +1,24 @@
-// The grouped MXFP4 product: out[r][n] = sum_i A[r][i] W_g[n][i] over the rows r of each group g.
+// The grouped MXFP4 product on CTA pairs: out[r][n] = sum_i A[r][i] W_g[n][i] over the rows r of
+// each group g.
+//
+// One tile is 256 weight rows (the MMA's M side: 128 in each CTA of the pair) by up to 256 rows of
+// one group (its N side, in steps of 32: a group costs round_up(rows, 32) columns, where rows on
+// the M side would cost a multiple of 128), the whole contraction in order, so nothing is summed
+// across tiles and results do not depend on the schedule.  tcgen05.mma.cta_group::2 with
+// kind::mxf4 multiplies E2M1 operands from shared memory under UE8M0 scales (one per 32 elements)
+// from TMEM.  Each CTA loads its own 128 weight rows and half of the group's rows, so a
+// 256-element k-stage brings 35 KB through each SM for 128 x 256 x 256 multiply-adds: half of
+// what a CTA by itself would need for its half of the tile.
+//
+// Warp roles (both CTAs unless said): warp 0 issues the TMA loads of its CTA's operands and
+// scales, all counted on the leader's stage barrier; warp 1 of the leader (cluster rank 0) copies
+// each stage's scales to TMEM (tcgen05.cp, in order with the MMAs) and issues the MMAs; warps
+// 2..9 read the accumulator (lane = weight row, column = group row), transpose it through shared
+// memory and store 64-byte (16-bit types) or 128-byte (fp32) pieces of the output rows.
+//
+// TMEM (512 columns): two accumulators, of the even tiles at column 0 upwards, of the odd tiles
+// ending at column 448; two slots of a stage's scales in columns 448..511.  Two tiles of together
+// up to 448 columns overlap freely: the next tile's MMAs run while one is read out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -8,92 +28,427 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ float e2m1_f32(uint32_t c)
+constexpr int kW = 16384;                    // a stage's weight rows of one CTA: 128 x 128 bytes
+constexpr int kT = 16384;                    // up to 128 group rows of one CTA
+constexpr int kScW = 1024, kScT = 2048;      // scale atoms: 2 k-atoms x (1 | 2) row blocks
+static_assert(kW + kT + kScW + kScT == kMxStageBytes, "stage layout");
+constexpr int kAccEnd = 448;                 // TMEM columns of accumulators; scales above
+
+struct Ctl {
+    uint64_t full[kMxStages], empty[kMxStages], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort_flag, zero;
+};
+static_assert(sizeof(Ctl) <= kMxCtlBytes, "control block");
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
 {
-    const uint32_t m = c & 7u;
-    const float v = m < 2 ? 0.5f * (float)m : (float)(2 + (m & 1)) * (float)(1 << (m >> 1)) * 0.25f;
-    return (c & 8u) ? -v : v;
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
 }
 
-__device__ __forceinline__ float mx_scale(uint32_t s)
+// Tensor loads of a CTA pair: the bytes may be counted on the barrier of either CTA (bar is a
+// shared::cluster address).
+__device__ __forceinline__ void tma_pair_2d(void* dst, const CUtensorMap* m, uint32_t bar,
+                                            int32_t x, int32_t y, uint64_t policy)
 {
-    return s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s == 0 ? 0x400000u : s << 23);
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
 }
 
-__device__ __forceinline__ void store_out(float v, __nv_bfloat16* o) { *o = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void store_out(float v, __half* o) { *o = __float2half_rn(v); }
-__device__ __forceinline__ void store_out(float v, float* o) { *o = v; }
-
-}  // namespace
-
-// A block per (32 rows of a group, 64 columns), 32 contraction elements at a time decoded into
-// shared memory; a thread sums 8 outputs.
-template <typename T>
-__global__ void __launch_bounds__(256) mx_gemm_kernel(MxGemmArgs a)
+__device__ __forceinline__ void tma_pair_3d(void* dst, const CUtensorMap* m, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z, uint64_t policy)
 {
-    __shared__ float sA[32][33], sW[64][33];
-    const int n0 = blockIdx.x * 64, KA = ((a.K >> 5) + 3) >> 2, NB = (a.N + 127) >> 7;
-    for (int64_t r0 = (int64_t)blockIdx.y * 32; r0 < a.rows_cap; r0 += (int64_t)gridDim.y * 32) {
-        int g = 0;
-        int64_t end = a.rows_cap;
-        if (a.offsets) {
-            int lo = 0, hi = a.G - 1;  // the last group that starts at or before r0
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (a.offsets[mid] <= r0) lo = mid;
-                else hi = mid - 1;
-            }
-            g = lo;
-            const int64_t first = a.offsets[g], cnt = a.counts[g];
-            end = first + cnt;
-            if (cnt > 0 && (first < 0 || (first & 127) || end > a.rows_cap)) {
-                if (threadIdx.x == 0) set_status(a.status, MOE_DEV_BAD_INDEX);
-                continue;
-            }
-            if (r0 < first || r0 >= end) continue;
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+
+// One 512-byte scale atom of each CTA's shared memory into its own TMEM (as tc_cp_sf, for a pair).
+__device__ __forceinline__ void tc_cp_sf_pair(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+                 : "memory");
+}
+
+// Instruction descriptor of kind::mxf4: E2M1 x E2M1, UE8M0 scales, fp32 accumulation, both
+// operands K-major; the scale ids (which two of the four bytes of a scale column a K = 64 step
+// uses) are added per step.
+__device__ __forceinline__ uint32_t idesc_mxf4(int M, int N)
+{
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(M >> 7) << 27);
+}
+
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_taddr, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t sfa_taddr,
+                                                 uint32_t sfb_taddr, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_taddr),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_taddr), "r"(sfb_taddr), "r"(accumulate)
+        : "memory");
+}
+
+// What a tile covers.  Tiles run over the groups' token tiles (256 group rows), and inside one
+// over the 256-row weight tiles, so that tiles in flight at a time share their group rows in L2.
+struct Tile {
+    int g, n0;       // group; first weight row
+    int rows, row0;  // group rows of the tile (1..256); first row of the tile in A
+    int nt;          // columns of the MMA: rows rounded up to 32
+};
+
+struct Groups {
+    const int32_t* start;   // [G + 1] first token tile of each group
+    const int32_t* counts;  // [G] rows (0 for a skipped group)
+    const int32_t* first;   // [G] first row
+    int G, NB;
+};
+
+// The tile of index t; g is the group of an earlier tile of the warp (the search goes on from it).
+// All lanes of a warp.
+__device__ __forceinline__ Tile find_tile(const Groups& gs, int t, int& g)
+{
+    const int lane = threadIdx.x & 31;
+    const int tt = t / gs.NB;
+    for (;;) {
+        const int i = g + 1 + lane;
+        const uint32_t past = __ballot_sync(0xffffffffu, i >= gs.G || gs.start[i] > tt);
+        if (past) {
+            g += __ffs(past) - 1;
+            break;
         }
-        const int m = threadIdx.x & 31, nq = threadIdx.x >> 5;
-        float acc[8] = {};
-        for (int kb = 0; kb < a.K / 32; ++kb) {
-            for (int i = threadIdx.x; i < 96 * 16; i += 256) {
-                const int row = i >> 4, byte = i & 15;
-                uint32_t c = 0;
-                float s = 0.0f;
-                if (row < 32) {
-                    if (r0 + row < end) {
-                        c = a.a_codes[(r0 + row) * (a.K / 2) + kb * 16 + byte];
-                        s = mx_scale(a.a_sf[mx_sf_tiled(0, 0, KA, (int)(r0 + row), kb)]);
-                    }
-                } else if (n0 + row - 32 < a.N) {
-                    const int n = n0 + row - 32;
-                    c = a.w_codes[((int64_t)g * a.N + n) * (a.K / 2) + kb * 16 + byte];
-                    s = mx_scale(a.w_sf[mx_sf_tiled(g, NB, KA, n, kb)]);
-                }
-                float* d = row < 32 ? sA[row] : sW[row - 32];
-                d[2 * byte] = e2m1_f32(c & 15u) * s;
-                d[2 * byte + 1] = e2m1_f32(c >> 4) * s;
-            }
-            __syncthreads();
-            for (int i = 0; i < 32; ++i) {
-                const float x = sA[m][i];
+        g += 32;
+    }
+    Tile ti;
+    ti.g = g;
+    ti.n0 = (t - tt * gs.NB) * 256;
+    const int r = (tt - gs.start[g]) * kMxTileRows;
+    ti.rows = min(kMxTileRows, gs.counts[g] - r);
+    ti.row0 = gs.first[g] + r;
+    ti.nt = (ti.rows + 31) & ~31;
+    return ti;
+}
+
+// Token tiles of the groups and their exclusive prefix, in shared memory (all threads; ends with
+// __syncthreads).  A group whose rows do not start on a multiple of 128 or leave the capacity is
+// flagged and gets none.
+__device__ __forceinline__ Groups load_groups(const MxGemmArgs& a, int32_t* sm, int32_t* s_warp)
+{
+    const int G = a.G, nthr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t* start = sm;
+    int32_t* cnt = start + G + 1;
+    int32_t* first = cnt + G;
+    for (int g = tid; g < G; g += nthr) {
+        int64_t c = a.counts ? a.counts[g] : a.rows_cap, o = a.offsets ? a.offsets[g] : 0;
+        if (c > 0 && (o < 0 || (o & 127) || o + c > a.rows_cap)) {
+            set_status(a.status, MOE_DEV_BAD_INDEX);
+            c = 0;
+        }
+        cnt[g] = (int32_t)max(c, (int64_t)0);
+        first[g] = (int32_t)o;
+    }
+    __syncthreads();
+    const int per = (G + nthr - 1) / nthr;
+    const int g0 = min(G, tid * per), g1 = min(G, g0 + per);
+    int sum = 0;
+    for (int g = g0; g < g1; ++g) sum += (cnt[g] + kMxTileRows - 1) / kMxTileRows;
+    int v = sum;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] = fmaf(x, sW[nq * 8 + q][i], acc[q]);
-            }
-            __syncthreads();
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += y;
+    }
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    int pre = v - sum;
+    for (int w = 0; w < warp; ++w) pre += s_warp[w];
+    for (int g = g0; g < g1; ++g) {
+        start[g] = pre;
+        pre += (cnt[g] + kMxTileRows - 1) / kMxTileRows;
+    }
+    if (tid == nthr - 1) start[G] = pre;
+    __syncthreads();
+    return Groups{start, cnt, first, G, (a.N + 255) / 256};
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort)
+{
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  volatile int* abort)
+{
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_cluster(bar, parity, abort) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+__device__ __forceinline__ void put(float v, __nv_bfloat16* o) { *o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(float v, __half* o) { *o = __float2half_rn(v); }
+__device__ __forceinline__ void put(float v, float* o) { *o = v; }
+
+// Stores 32 group rows (registers) x 32 weight rows (lanes) of the accumulator: lane l holds
+// output column n0 + l of rows row0 .. row0 + live - 1.  vec: through the warp's staging buffer as
+// 16-byte pieces along the output rows; else element by element.
+template <typename T>
+__device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t (&r)[32], T* stage,
+                                            int64_t row0, int live, int n0, int lane)
+{
+    T* out = static_cast<T*>(a.out);
+    if (a.vec) {
+        constexpr int kPer = 16 / (int)sizeof(T);   // elements of a piece
+        constexpr int kLanes = 32 / kPer;           // lanes per row
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) put(__uint_as_float(r[j]), stage + j * 32 + lane);
+        __syncwarp();
+        const int n = n0 + (lane % kLanes) * kPer;
+        if (n < a.N) {
+#pragma unroll
+            for (int j = lane / kLanes; j < 32; j += 32 / kLanes)
+                if (j < live)
+                    *reinterpret_cast<uint4*>(out + (row0 + j) * a.out_stride + n) =
+                        *reinterpret_cast<const uint4*>(stage + j * 32 + (lane % kLanes) * kPer);
         }
-        if (r0 + m < end)
-            for (int q = 0; q < 8; ++q)
-                if (n0 + nq * 8 + q < a.N)
-                    store_out(acc[q], static_cast<T*>(a.out) + (r0 + m) * a.out_stride + n0 + nq * 8 + q);
+    } else if (n0 + lane < a.N) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < live) put(__uint_as_float(r[j]), out + (row0 + j) * a.out_stride + n0 + lane);
     }
 }
 
-MxGemmKernel mx_gemm_kernel_for(int out_dtype)
+}  // namespace
+
+template <typename T>
+__global__ void __launch_bounds__(kMxThreads, 1)
+    gemm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
+                      const __grid_constant__ CUtensorMap tmT16,
+                      const __grid_constant__ CUtensorMap tmSW,
+                      const __grid_constant__ CUtensorMap tmST, MxGemmArgs args)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+    uint8_t* staging = stages + kMxStages * kMxStageBytes;
+    Ctl& ctl = *reinterpret_cast<Ctl*>(staging + kMxEpiWarps * 32 * 32 * sizeof(T));
+    int32_t* tables = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(&ctl) + kMxCtlBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int KB = (args.K + 255) / 256;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMxStages; ++s) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl.acc_full[b], 1);
+            mbar_init(&ctl.acc_empty[b], 2 * kMxEpiWarps);  // both CTAs' (the leader's barrier)
+        }
+        mbar_init(&ctl.drain, 1);
+        ctl.abort_flag = ctl.zero = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmT);
+        prefetch_tmap(&tmT16);
+        prefetch_tmap(&tmSW);
+        prefetch_tmap(&tmST);
+    }
+    if (warp == 1) tmem_alloc_pair(&ctl.tmem, 512);
+    const Groups gs = load_groups(args, tables, reinterpret_cast<int32_t*>(staging));
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any arrives across the pair
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    const int ntiles = gs.start[gs.G] * gs.NB;
+    volatile int* abort = &ctl.abort_flag;
+
+    if (warp == 0) {
+        const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
+        int stage = 0, g = 0;
+        uint32_t phase = 0, issued = 0, issued_par = 0;
+        bool ok = true;
+        for (int t = pair; t < ntiles && ok; t += npairs) {
+            const Tile ti = find_tile(gs, t, g);
+            const int half = ti.nt >> 1;                    // group rows of this CTA
+            const int trow = ti.row0 + (int)rank * half, wrow = ti.n0 + (int)rank * 128;
+            const int nsc = ti.nt > 128 ? 2 : 1;            // row blocks of group-row scales
+            const uint32_t bytes = 2u * (kW + kScW + half * 128 + nsc * 1024);
+            const int wb = ti.g * ((args.N + 127) >> 7) + (wrow >> 7);
+            for (int kb = 0; kb < KB; ++kb) {
+                if (!warp_wait(&ctl.empty[stage], phase ^ 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    uint8_t* sW = stages + stage * kMxStageBytes;
+                    uint8_t* sT = sW + kW;
+                    uint8_t* sSW = sT + kT;
+                    uint8_t* sST = sSW + kScW;
+                    const uint32_t bar = cluster_addr(&ctl.full[stage], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[stage], bytes);
+                    tma_pair_3d(sW, &tmW, bar, kb * 128, wrow, ti.g, pol_w);
+                    tma_pair_2d(sSW, &tmSW, bar, kb * 256, wb, pol_w);
+                    if (half == 128) {
+                        tma_pair_2d(sT, &tmT, bar, kb * 128, trow, pol_t);
+                    } else {
+                        for (int i = 0; i < half; i += 16)
+                            tma_pair_2d(sT + i * 128, &tmT16, bar, kb * 128, trow + i, pol_t);
+                    }
+                    for (int i = 0; i < nsc; ++i)
+                        tma_pair_2d(sST + i * 1024, &tmST, bar, kb * 256, (ti.row0 >> 7) + i, pol_t);
+                }
+                issued |= 1u << stage;
+                issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == kMxStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (lane == 0) {
+            if (!ok) {
+                set_status(args.status, MOE_DEV_WAIT_TIMEOUT);
+                *abort = 1;
+            }
+            if (rank == 0)  // both CTAs' copies in flight land before either exits
+                for (int s = 0; s < kMxStages; ++s)
+                    if ((issued >> s) & 1u)
+                        mbar_wait(&ctl.full[s], (issued_par >> s) & 1u, &ctl.zero);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            int stage = 0, it = 0, g = 0, prev_nt = 0;
+            uint32_t phase = 0, slot = 0;
+            bool ok = true;
+            for (int t = pair; t < ntiles && ok; t += npairs, ++it) {
+                const Tile ti = find_tile(gs, t, g);
+                const int buf = it & 1;
+                // the accumulator's last user has been read out; so has the previous tile's where
+                // the two overlap
+                ok = warp_wait_cluster(&ctl.acc_empty[buf], ((it >> 1) & 1) ^ 1u, abort);
+                if (ok && it && ti.nt + prev_nt > kAccEnd)
+                    ok = warp_wait_cluster(&ctl.acc_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort);
+                if (!ok) break;
+                prev_nt = ti.nt;
+                tc_fence_after();
+                const uint32_t d_t = tmem + (buf ? kAccEnd - ti.nt : 0);
+                const uint32_t idesc = idesc_mxf4(256, ti.nt);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!warp_wait_cluster(&ctl.full[stage], phase, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t sW = smem_u32(stages + stage * kMxStageBytes);
+                        const uint32_t sT = sW + kW, sSW = sT + kT, sST = sSW + kScW;
+                        const uint32_t sc = tmem + kAccEnd + slot * 32;
+                        const int nk = min(4, (args.K - kb * 256 + 63) >> 6);
+                        for (int ka = 0; ka < (nk + 1) >> 1; ++ka) {
+                            tc_cp_sf_pair(sc + 4 * ka, sdesc_sf(sSW + 512 * ka));
+                            tc_cp_sf_pair(sc + 8 + 8 * ka, sdesc_sf(sST + 512 * ka));
+                            if (ti.nt > 128)
+                                tc_cp_sf_pair(sc + 12 + 8 * ka, sdesc_sf(sST + 1024 + 512 * ka));
+                        }
+                        const uint64_t ad = sdesc_sw128(sW), bd = sdesc_sw128(sT);
+                        for (int j = 0; j < nk; ++j) {
+                            const uint32_t id = (uint32_t)(j & 1) * 2u;
+                            tc_mma_mxf4_pair(d_t, ad + 2 * j, bd + 2 * j,
+                                             idesc | (id << 4) | (id << 29), sc + 4 * (j >> 1),
+                                             sc + 8 + 8 * (j >> 1), (kb | j) != 0);
+                        }
+                        tc_commit_pair(&ctl.empty[stage], 3);
+                    }
+                    __syncwarp();
+                    slot ^= 1u;
+                    if (++stage == kMxStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (lane == 0) tc_commit_pair(&ctl.acc_full[buf], 3);
+                __syncwarp();
+            }
+            if (lane == 0) {
+                if (!ok) {
+                    set_status(args.status, MOE_DEV_WAIT_TIMEOUT);
+                    *abort = 1;
+                }
+                tc_commit_pair(&ctl.drain, 1);  // every MMA issued above is complete after this
+                mbar_wait(&ctl.drain, 0, &ctl.zero);
+            }
+            __syncwarp();
+        }
+    } else {
+        const int q = warp & 3, h = (warp - 2) >> 2;  // TMEM lane quarter; which 32-row chunks
+        T* stage = reinterpret_cast<T*>(staging) + (warp - 2) * 32 * 32;
+        int it = 0, g = 0;
+        for (int t = pair; t < ntiles; t += npairs, ++it) {
+            const Tile ti = find_tile(gs, t, g);
+            const int buf = it & 1;
+            if (!warp_wait(&ctl.acc_full[buf], (it >> 1) & 1, abort)) {
+                if (lane == 0) {
+                    set_status(args.status, MOE_DEV_WAIT_TIMEOUT);
+                    *abort = 1;
+                }
+                break;
+            }
+            tc_fence_after();
+            const uint32_t acc = tmem + (buf ? kAccEnd - ti.nt : 0) + ((uint32_t)(q * 32) << 16);
+            const int nch = ti.nt >> 5;
+            uint32_t r[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (h + 2 * i < nch) tmem_ld32(acc + 32 * (h + 2 * i), r[i]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(&ctl.acc_empty[buf], 0);
+            const int n0 = ti.n0 + (int)rank * 128 + 32 * q;
+            if (n0 < args.N) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 32 * (h + 2 * i);
+                    if (c < ti.nt)
+                        store_chunk<T>(args, r[i], stage, (int64_t)ti.row0 + c, ti.rows - c, n0, lane);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the leader's MMAs have read this CTA's memory; both CTAs leave together
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+MxGemmKernel gemm_mxfp4_kernel_for(int out_dtype)
 {
     switch (out_dtype) {
-        case MOE_BF16: return mx_gemm_kernel<__nv_bfloat16>;
-        case MOE_FP16: return mx_gemm_kernel<__half>;
-        default: return mx_gemm_kernel<float>;
+        case MOE_BF16: return gemm_mxfp4_kernel<__nv_bfloat16>;
+        case MOE_FP16: return gemm_mxfp4_kernel<__half>;
+        default: return gemm_mxfp4_kernel<float>;
     }
 }
 

@@ -69,6 +69,22 @@ inline bool make_tmap(CUtensorMap* m, const void* base, CUtensorMapDataType dtyp
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D tensor map: matrices of rows of row_bytes, row_bytes * rows apart; boxes of one matrix.
+inline bool make_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dtype,
+                         uint64_t inner, uint64_t rows, uint64_t matrices, uint64_t row_bytes,
+                         uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc || rows == 0 || matrices == 0) return false;
+    const cuuint64_t dims[3] = {inner, rows, matrices};
+    const cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
+    const cuuint32_t box[3] = {box_inner, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, dtype, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }

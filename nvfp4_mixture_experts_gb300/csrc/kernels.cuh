@@ -401,22 +401,30 @@ __host__ __device__ __forceinline__ size_t mx_sf_tiled(int64_t b, int RB, int KA
                     ((r >> 5) & 3) * 4 + (kb & 3));
 }
 
-// ---- gemm_mxfp4.cu: the grouped MXFP4 product
+// ---- gemm_mxfp4.cu: the grouped MXFP4 product on CTA pairs
 struct MxGemmArgs {
-    const uint8_t* a_codes;
-    const uint8_t* a_sf;
     int rows_cap;
     const int32_t* counts;   // nullable (with offsets): one group of rows_cap rows
     const int32_t* offsets;
-    int G;
-    const uint8_t* w_codes;
-    const uint8_t* w_sf;
-    int N, K;
+    int G, N, K;
     void* out;
     int64_t out_stride;
+    int vec;                 // the output rows may be stored in 16-byte pieces
     uint32_t* status;
 };
-using MxGemmKernel = void (*)(MxGemmArgs);
-MxGemmKernel mx_gemm_kernel_for(int out_dtype);
+constexpr int kMxTileRows = 256;     // group rows per tile at most
+constexpr int kMxEpiWarps = 8;
+constexpr int kMxThreads = (2 + kMxEpiWarps) * 32;
+constexpr int kMxStages = 5;
+constexpr int kMxStageBytes = 16384 + 16384 + 1024 + 2048;
+constexpr int kMxCtlBytes = 256;
+inline int gemm_mxfp4_smem(int G, int out_bytes)
+{
+    return 1024 + kMxStages * kMxStageBytes + kMxEpiWarps * 32 * 32 * out_bytes + kMxCtlBytes +
+           4 * (3 * G + 1);
+}
+using MxGemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
+                              MxGemmArgs);
+MxGemmKernel gemm_mxfp4_kernel_for(int out_dtype);
 
 }  // namespace moe
