@@ -310,11 +310,11 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
         return MOE_ERR_INVALID;
     const int KA = (K / 32 + 3) / 4, es = elem_bytes(out_dtype);
     CUtensorMap tmW, tmT, tmT16, tmSW, tmST;
-    constexpr auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, U32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+    constexpr auto U32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
     constexpr auto SW = CU_TENSOR_MAP_SWIZZLE_128B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
-    if (!make_tmap_3d(&tmW, w_codes_d, U8, K / 2, N, num_groups, K / 2, 128, 128, SW) ||
-        !make_tmap(&tmT, a_codes_d, U8, K / 2, rows_cap, K / 2, 128, 128, SW) ||
-        !make_tmap(&tmT16, a_codes_d, U8, K / 2, rows_cap, K / 2, 128, 16, SW) ||
+    if (!make_tmap_3d(&tmW, w_codes_d, U32, K / 8, N, num_groups, K / 2, 32, 128, SW) ||
+        !make_tmap(&tmT, a_codes_d, U32, K / 8, rows_cap, K / 2, 32, 128, SW) ||
+        !make_tmap(&tmT16, a_codes_d, U32, K / 8, rows_cap, K / 2, 32, 16, SW) ||
         !make_tmap(&tmSW, w_sf_d, U32, KA * 128, (uint64_t)num_groups * ceil_div(N, 128), KA * 512,
                    256, 1, NOSW) ||
         !make_tmap(&tmST, a_sf_d, U32, KA * 128, ceil_div(rows_cap, 128), KA * 512, 256, 1, NOSW))

@@ -16,7 +16,7 @@
 // 2..9 read the accumulator (lane = weight row, column = group row), transpose it through shared
 // memory and store 64-byte (16-bit types) or 128-byte (fp32) pieces of the output rows.
 //
-// TMEM (512 columns): two accumulators, of the even tiles at column 0 upwards, of the odd tiles
+// TMEM (all 512 columns, so the allocation starts at column 0): two accumulators, of the even tiles at column 0 upwards, of the odd tiles
 // ending at column 448; two slots of a stage's scales in columns 448..511.  Two tiles of together
 // up to 448 columns overlap freely: the next tile's MMAs run while one is read out.
 #include <cuda_bf16.h>
@@ -40,6 +40,19 @@ struct Ctl {
     int abort_flag, zero;
 };
 static_assert(sizeof(Ctl) <= kMxCtlBytes, "control block");
+
+// One lane of a converged warp, the same one each time: the compiler knows that code under it runs
+// in one thread, so the operands of the TMA and tcgen05 instructions stay in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
 
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
 {
@@ -188,13 +201,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort)
-{
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait_cluster(bar, parity, abort) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
+// A place in the ring of stages: the n-th k-stage of the CTA.
+struct Ring {
+    uint32_t stage, phase;
+    __device__ __forceinline__ explicit Ring(uint32_t n)
+        : stage(n % kMxStages), phase((n / kMxStages) & 1u)
+    {
+    }
+    __device__ __forceinline__ void next()
+    {
+        if (++stage == kMxStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 __device__ __forceinline__ void put(float v, __nv_bfloat16* o) { *o = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(float v, __half* o) { *o = __float2half_rn(v); }
@@ -275,120 +296,123 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before any arrives across the pair
     tc_fence_after();
-    const uint32_t tmem = ctl.tmem;
     const int ntiles = gs.start[gs.G] * gs.NB;
     volatile int* abort = &ctl.abort_flag;
 
     if (warp == 0) {
         const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
-        int stage = 0, g = 0;
-        uint32_t phase = 0, issued = 0, issued_par = 0;
+        const uint32_t full0 = cluster_addr(&ctl.full[0], 0);  // the leader's barriers
+        int g = 0;
+        uint32_t n = 0, done = 0;  // k-stages of the earlier tiles; issued so far
         bool ok = true;
-        for (int t = pair; t < ntiles && ok; t += npairs) {
+        for (int t = pair; t < ntiles && ok; t += npairs, n += KB) {
             const Tile ti = find_tile(gs, t, g);
-            const int half = ti.nt >> 1;                    // group rows of this CTA
-            const int trow = ti.row0 + (int)rank * half, wrow = ti.n0 + (int)rank * 128;
-            const int nsc = ti.nt > 128 ? 2 : 1;            // row blocks of group-row scales
-            const uint32_t bytes = 2u * (kW + kScW + half * 128 + nsc * 1024);
-            const int wb = ti.g * ((args.N + 127) >> 7) + (wrow >> 7);
-            for (int kb = 0; kb < KB; ++kb) {
-                if (!warp_wait(&ctl.empty[stage], phase ^ 1u, abort)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    uint8_t* sW = stages + stage * kMxStageBytes;
+            if (elect_one()) {
+                const int half = ti.nt >> 1;                    // group rows of this CTA
+                const int trow = ti.row0 + (int)rank * half, wrow = ti.n0 + (int)rank * 128;
+                const int nsc = ti.nt > 128 ? 2 : 1;            // row blocks of group-row scales
+                const uint32_t bytes = 2u * (kW + kScW + half * 128 + nsc * 1024);
+                const int wb = ti.g * ((args.N + 127) >> 7) + (wrow >> 7), tb = ti.row0 >> 7;
+                Ring ring(n);
+                for (int kb = 0; kb < KB; ++kb, ring.next()) {
+                    if (!mbar_wait(&ctl.empty[ring.stage], ring.phase ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sW = stages + ring.stage * kMxStageBytes;
                     uint8_t* sT = sW + kW;
                     uint8_t* sSW = sT + kT;
                     uint8_t* sST = sSW + kScW;
-                    const uint32_t bar = cluster_addr(&ctl.full[stage], 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[stage], bytes);
-                    tma_pair_3d(sW, &tmW, bar, kb * 128, wrow, ti.g, pol_w);
+                    const uint32_t bar = full0 + ring.stage * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[ring.stage], bytes);
+                    tma_pair_3d(sW, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
                     tma_pair_2d(sSW, &tmSW, bar, kb * 256, wb, pol_w);
                     if (half == 128) {
-                        tma_pair_2d(sT, &tmT, bar, kb * 128, trow, pol_t);
+                        tma_pair_2d(sT, &tmT, bar, kb * 32, trow, pol_t);
                     } else {
                         for (int i = 0; i < half; i += 16)
-                            tma_pair_2d(sT + i * 128, &tmT16, bar, kb * 128, trow + i, pol_t);
+                            tma_pair_2d(sT + i * 128, &tmT16, bar, kb * 32, trow + i, pol_t);
                     }
-                    for (int i = 0; i < nsc; ++i)
-                        tma_pair_2d(sST + i * 1024, &tmST, bar, kb * 256, (ti.row0 >> 7) + i, pol_t);
-                }
-                issued |= 1u << stage;
-                issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-                if (++stage == kMxStages) {
-                    stage = 0;
-                    phase ^= 1u;
+                    tma_pair_2d(sST, &tmST, bar, kb * 256, tb, pol_t);
+                    if (nsc == 2) tma_pair_2d(sST + 1024, &tmST, bar, kb * 256, tb + 1, pol_t);
+                    done = n + kb + 1;
                 }
             }
+            ok = __all_sync(0xffffffffu, ok);
         }
-        if (lane == 0) {
+        if (elect_one()) {
             if (!ok) {
                 set_status(args.status, MOE_DEV_WAIT_TIMEOUT);
                 *abort = 1;
             }
             if (rank == 0)  // both CTAs' copies in flight land before either exits
-                for (int s = 0; s < kMxStages; ++s)
-                    if ((issued >> s) & 1u)
-                        mbar_wait(&ctl.full[s], (issued_par >> s) & 1u, &ctl.zero);
+                for (uint32_t i = done > kMxStages ? done - kMxStages : 0; i < done; ++i) {
+                    const Ring r(i);
+                    mbar_wait(&ctl.full[r.stage], r.phase, &ctl.zero);
+                }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            int stage = 0, it = 0, g = 0, prev_nt = 0;
-            uint32_t phase = 0, slot = 0;
+            const uint32_t s0 = smem_u32(stages);
+            const uint64_t w0 = sdesc_sw128(s0), t0 = sdesc_sw128(s0 + kW);
+            const uint64_t cw0 = sdesc_sf(s0 + kW + kT), ct0 = sdesc_sf(s0 + kW + kT + kScW);
+            int it = 0, g = 0, prev_nt = 0;
+            uint32_t n = 0;  // k-stages of the earlier tiles
             bool ok = true;
-            for (int t = pair; t < ntiles && ok; t += npairs, ++it) {
+            for (int t = pair; t < ntiles && ok; t += npairs, ++it, n += KB) {
                 const Tile ti = find_tile(gs, t, g);
-                const int buf = it & 1;
-                // the accumulator's last user has been read out; so has the previous tile's where
-                // the two overlap
-                ok = warp_wait_cluster(&ctl.acc_empty[buf], ((it >> 1) & 1) ^ 1u, abort);
-                if (ok && it && ti.nt + prev_nt > kAccEnd)
-                    ok = warp_wait_cluster(&ctl.acc_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort);
-                if (!ok) break;
-                prev_nt = ti.nt;
-                tc_fence_after();
-                const uint32_t d_t = tmem + (buf ? kAccEnd - ti.nt : 0);
-                const uint32_t idesc = idesc_mxf4(256, ti.nt);
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!warp_wait_cluster(&ctl.full[stage], phase, abort)) {
-                        ok = false;
-                        break;
-                    }
+                if (elect_one()) {
+                    const int buf = it & 1;
+                    // the accumulator's last user has been read out; so has the previous tile's
+                    // where the two overlap
+                    ok = mbar_wait_cluster(&ctl.acc_empty[buf], ((it >> 1) & 1) ^ 1u, abort);
+                    if (ok && it && ti.nt + prev_nt > kAccEnd)
+                        ok = mbar_wait_cluster(&ctl.acc_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort);
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t sW = smem_u32(stages + stage * kMxStageBytes);
-                        const uint32_t sT = sW + kW, sSW = sT + kT, sST = sSW + kScW;
-                        const uint32_t sc = tmem + kAccEnd + slot * 32;
-                        const int nk = min(4, (args.K - kb * 256 + 63) >> 6);
-                        for (int ka = 0; ka < (nk + 1) >> 1; ++ka) {
-                            tc_cp_sf_pair(sc + 4 * ka, sdesc_sf(sSW + 512 * ka));
-                            tc_cp_sf_pair(sc + 8 + 8 * ka, sdesc_sf(sST + 512 * ka));
-                            if (ti.nt > 128)
-                                tc_cp_sf_pair(sc + 12 + 8 * ka, sdesc_sf(sST + 1024 + 512 * ka));
+                    const uint32_t d_t = buf ? kAccEnd - ti.nt : 0;
+                    const uint32_t idesc = idesc_mxf4(256, ti.nt), idesc2 = idesc | (2u << 4) | (2u << 29);
+                    const bool two = ti.nt > 128;  // row blocks of group-row scales
+                    Ring ring(n);
+                    for (int kb = 0; kb < KB && ok; ++kb, ring.next()) {
+                        ok = mbar_wait(&ctl.full[ring.stage], ring.phase, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t o = ring.stage * (kMxStageBytes >> 4);  // descriptor units
+                        const uint64_t w = w0 + o, tk = t0 + o, cw = cw0 + o, ct = ct0 + o;
+                        const uint32_t sc = kAccEnd + ((n + kb) & 1u) * 32;
+                        const int left = args.K - kb * 256;
+                        if (left >= 256) {
+                            tc_cp_sf_pair(sc, cw);
+                            tc_cp_sf_pair(sc + 8, ct);
+                            if (two) tc_cp_sf_pair(sc + 12, ct + 64);
+                            tc_cp_sf_pair(sc + 4, cw + 32);
+                            tc_cp_sf_pair(sc + 16, ct + 32);
+                            if (two) tc_cp_sf_pair(sc + 20, ct + 96);
+                            tc_mma_mxf4_pair(d_t, w, tk, idesc, sc, sc + 8, kb != 0);
+                            tc_mma_mxf4_pair(d_t, w + 2, tk + 2, idesc2, sc, sc + 8, 1);
+                            tc_mma_mxf4_pair(d_t, w + 4, tk + 4, idesc, sc + 4, sc + 16, 1);
+                            tc_mma_mxf4_pair(d_t, w + 6, tk + 6, idesc2, sc + 4, sc + 16, 1);
+                        } else {  // the last k-stage: K = 64 steps that hold any of it
+                            for (int j = 0; 64 * j < left; ++j) {
+                                const int ka = j >> 1;
+                                if (!(j & 1)) {
+                                    tc_cp_sf_pair(sc + 4 * ka, cw + 32 * ka);
+                                    tc_cp_sf_pair(sc + 8 + 8 * ka, ct + 32 * ka);
+                                    if (two) tc_cp_sf_pair(sc + 12 + 8 * ka, ct + 64 + 32 * ka);
+                                }
+                                tc_mma_mxf4_pair(d_t, w + 2 * j, tk + 2 * j, (j & 1) ? idesc2 : idesc,
+                                                 sc + 4 * ka, sc + 8 + 8 * ka, (kb | j) != 0);
+                            }
                         }
-                        const uint64_t ad = sdesc_sw128(sW), bd = sdesc_sw128(sT);
-                        for (int j = 0; j < nk; ++j) {
-                            const uint32_t id = (uint32_t)(j & 1) * 2u;
-                            tc_mma_mxf4_pair(d_t, ad + 2 * j, bd + 2 * j,
-                                             idesc | (id << 4) | (id << 29), sc + 4 * (j >> 1),
-                                             sc + 8 + 8 * (j >> 1), (kb | j) != 0);
-                        }
-                        tc_commit_pair(&ctl.empty[stage], 3);
+                        tc_commit_pair(&ctl.empty[ring.stage], 3);
                     }
-                    __syncwarp();
-                    slot ^= 1u;
-                    if (++stage == kMxStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    if (ok) tc_commit_pair(&ctl.acc_full[buf], 3);
                 }
-                if (!ok) break;
-                if (lane == 0) tc_commit_pair(&ctl.acc_full[buf], 3);
-                __syncwarp();
+                prev_nt = ti.nt;
+                ok = __all_sync(0xffffffffu, ok);
             }
-            if (lane == 0) {
+            if (elect_one()) {  // the thread that issued the MMAs
                 if (!ok) {
                     set_status(args.status, MOE_DEV_WAIT_TIMEOUT);
                     *abort = 1;
@@ -413,7 +437,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t acc = tmem + (buf ? kAccEnd - ti.nt : 0) + ((uint32_t)(q * 32) << 16);
+            const uint32_t acc = (buf ? kAccEnd - ti.nt : 0) + ((uint32_t)(q * 32) << 16);
             const int nch = ti.nt >> 5;
             uint32_t r[4][32];
 #pragma unroll
@@ -439,7 +463,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     cluster_sync();  // the leader's MMAs have read this CTA's memory; both CTAs leave together
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 512);
+        tmem_dealloc_pair(ctl.tmem, 512);
     }
 }
 
