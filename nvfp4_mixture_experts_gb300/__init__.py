@@ -132,14 +132,22 @@ def _check(status, where):
 
 def _p(t):
     """Device pointer of a torch tensor (or None)."""
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_cuda = None  # torch._C, bound at the first call
 
 
 def _stream(stream):
+    """The handle of a torch stream, of an integer, or (None) of the current stream."""
     if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        global _cuda
+        if _cuda is None:
+            import torch
+            torch.cuda.current_stream()  # the CUDA context exists
+            _cuda = torch._C
+        return _cuda._cuda_getCurrentRawStream(_cuda._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 # ---------------------------------------------------------------- C entry points
@@ -283,16 +291,21 @@ def moe_get_status(h, ws, stream=None):
 # Element types come from the tensors (int16 tensors are bf16 bit patterns, as above), sizes from
 # their shapes; a tensor whose type, shape or strides do not fit raises MoEError before the call.
 
+class _Dtypes(dict):
+    """torch dtype -> moe_dtype (-1: none), filled at the first look-up."""
+
+    def __missing__(self, key):
+        import torch
+        self.update({torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_FP16,
+                     torch.float32: MOE_FP32})
+        return self.setdefault(key, -1)
+
+
+_DTYPES = _Dtypes()
+
+
 def _dtype(t):
-    import torch
-    global _DTYPES
-    if _DTYPES is None:
-        _DTYPES = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_FP16,
-                   torch.float32: MOE_FP32}
-    return _DTYPES.get(t.dtype, -1)
-
-
-_DTYPES = None
+    return _DTYPES[t.dtype]
 
 
 def _need(ok, where):

@@ -45,6 +45,15 @@ moe_status check_rows(int dtype, int T, int k, int H, int rows_cap)
     return MOE_OK;
 }
 
+// Raises a kernel's limit of dynamic shared memory where the default (48 KB with the static part,
+// up to 17 KB here) does not do.
+bool allow_smem(const void* kern, size_t bytes)
+{
+    return bytes <= 31 * 1024 ||
+           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+               cudaSuccess;
+}
+
 bool align_ok(int a) { return a >= 1 && a <= 128 && (a & (a - 1)) == 0; }
 
 // combine (w given) and dispatch's gradient (w null)
@@ -71,7 +80,7 @@ moe_status combine_rows(const void* y_d, int32_t dtype, const int32_t* inv_d, co
     a.out_stride = out_stride;
     const int64_t n = (int64_t)T * (vec ? (int64_t)H * es / 16 : H);
     return launch(combine_rows_kernel_for(dtype, vec), dim3(blocks_for(n, 256, 16)), dim3(256), 0,
-                  reinterpret_cast<cudaStream_t>(stream), false, a);
+                  reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
 }  // namespace
@@ -124,41 +133,36 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
     a.perm_src = perm_src_d;
     a.inv = inv_d;
     a.status = status_d;
-    const int blocks = P <= 1024 ? 1 : kSortBlocks;
-    a.segment = (int)((P + (int64_t)blocks * 32 * 32 - 1) / ((int64_t)blocks * 32 * 32) * 32);
-    if (cudaFuncSetAttribute(sort_pairs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)sort_smem(kMaxExperts)) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = sort_smem(num_local);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = blocks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, sort_pairs_kernel, a) != cudaSuccess) return MOE_ERR_CUDA;
-    if (!x_d || T == 0 || rows_cap == 0 || num_local == 0) return MOE_OK;
-
-    const int es = elem_bytes(dtype);
-    const bool vec = rows_vec(x_d, (int64_t)H * es, T > 1 ? x_stride * es : 0) && aligned16(rows_d);
-    const int unit = vec ? 16 : es;
     DispatchArgs d = {};
-    d.x = x_d;
-    d.x_stride = x_stride * es / unit;
-    d.inv = inv_d;
-    d.T = T;
-    d.k = k;
-    d.units = (int)((int64_t)H * es / unit);
-    d.rows_cap = rows_cap;
-    d.rows = rows_d;
-    const int64_t runs = (int64_t)T * ceil_div(d.units, 128);
-    return launch(dispatch_rows_kernel_for(unit), dim3(blocks_for(runs, 8, 8)), dim3(256), 0, s,
-                  false, d);
+    int unit = 16;
+    if (x_d) {
+        const int es = elem_bytes(dtype);
+        if (!rows_vec(x_d, (int64_t)H * es, T > 1 ? x_stride * es : 0) || !aligned16(rows_d)) unit = es;
+        d.x = x_d;
+        d.x_stride = x_stride * es / unit;
+        d.inv = inv_d;
+        d.T = T;
+        d.k = k;
+        d.units = (int)((int64_t)H * es / unit);
+        d.rows_cap = rows_cap;
+        d.rows = rows_d;
+    }
+    const bool small = P <= kSmallPairs;
+    a.segment = small ? 32 : ceil_div((int)((P + 31) / 32), kSortBlocks * 32) * 32;
+    const size_t smem = sort_smem(num_local, small ? ceil_div((int)P, 32) : 32);
+    if (small) {
+        const DispatchSmallKernel kern = dispatch_small_kernel_for(unit);
+        if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return MOE_ERR_CUDA;
+        const int blocks = std::max(1, x_d ? std::min(T, num_sms()) : 1);
+        return launch(kern, dim3(blocks), dim3(kSortThreads), smem, s, true, a, d);
+    }
+    if (!allow_smem(reinterpret_cast<const void*>(sort_pairs_kernel), smem)) return MOE_ERR_CUDA;
+    const moe_status sorted = launch_cluster(sort_pairs_kernel, kSortBlocks, dim3(kSortBlocks),
+                                             dim3(kSortThreads), smem, s, true, a);
+    if (sorted != MOE_OK || !x_d || rows_cap == 0 || num_local == 0) return sorted;
+    const int64_t runs = (int64_t)T * ceil_div(d.units, kDispatchRun);
+    return launch(dispatch_rows_kernel_for(unit), dim3(blocks_for(runs, 8, 16)), dim3(256), 0, s,
+                  true, d);
 }
 
 moe_status moe_dispatch_backward(const void* drows_d, int32_t dtype, const int32_t* inv_d,
@@ -207,7 +211,7 @@ moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_
     a.dy = dy_d;
     a.dw = dw_d;
     return launch(combine_back_kernel_for(dtype, vec), dim3(blocks_for(T, 1, 8)),
-                  dim3(kCombineBackThreads), 0, reinterpret_cast<cudaStream_t>(stream), false, a);
+                  dim3(kCombineBackThreads), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
 size_t moe_mxfp4_scale_bytes(int32_t batch, int32_t rows, int32_t cols, int32_t sf_layout)

@@ -59,14 +59,25 @@ __device__ __forceinline__ Piece<T, V> pack(const float (&f)[V])
 
 // ------------------------------------------------------------------ the sort
 
-// One thread block cluster sorts all P pairs: a stable counting sort in one launch.  Every warp
-// of the cluster owns a contiguous segment of the pairs and a table of counts by expert in
-// shared memory.  Pass 1 counts the segments (32 pairs at a time: lanes of equal expert found
-// with one match instruction, their first lane adds their number, so no atomics).  Prefix sums
-// over the block's warps, over the cluster's blocks (read through distributed shared memory) and
-// over the experts (group sizes rounded up to row_align) turn the tables into the row of each
-// segment's first pair of each expert.  Pass 2 walks the segments again: a pair's row is its
-// table entry plus the number of lower lanes of equal expert, the first lane moves the entry on.
+// A stable counting sort.  Every warp that takes part owns a contiguous segment of the pairs and a
+// table of counts by expert in shared memory.  Pass 1 counts the segments (32 pairs at a time: lanes
+// of equal expert found with one match instruction, their first lane adds their number, so no
+// atomics).  Prefix sums over the block's warps, over the blocks and over the experts (group
+// sizes rounded up to row_align) turn the tables into the row of each segment's first pair of each
+// expert.  Pass 2 walks the segments again: a pair's row is its table entry plus the number of
+// lower lanes of equal expert, and the first lane moves the entry on.
+//
+// Up to kSmallPairs pairs one block does it alone, in the launch that also moves the rows, every
+// block of which sorts for itself (a few hundred cycles, less than a launch); more are shared out
+// over the blocks of one thread block cluster, which read each other's totals through distributed
+// shared memory.
+struct SortShared {
+    uint32_t tot[kMaxExperts];       // this block's pairs of each expert
+    uint32_t off[kMaxExperts + 1];   // first row of each group
+    uint32_t cnt[kMaxExperts];
+    uint32_t warp[32];
+};
+
 __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32_t rank)
 {
     uint32_t v;
@@ -80,99 +91,113 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32
     return v;
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a)
+constexpr int kSortHold = 8;  // batches of 32 ids that a lane keeps in registers between the passes
+
+// Sorts with the `nw` first warps of each of `nblk` blocks (rank: this one's place).  calls
+// emit(pair, row) for this block's pairs (row -1: dropped); leaves off and cnt in sh.  tab:
+// [nw][El].  Ends with a block barrier for nblk 1; for more the caller ends with cluster_sync.
+template <typename Emit>
+__device__ __forceinline__ void sort_core(const SortArgs& a, SortShared& sh, uint32_t* tabs, int rank,
+                                          int nblk, int nw, bool flag, Emit emit)
 {
-    extern __shared__ uint32_t s_tab[];  // [32 warps][El]
-    __shared__ uint32_t s_tot[kMaxExperts];
-    __shared__ uint32_t s_off[kMaxExperts + 1];
-    __shared__ uint32_t s_cnt[kMaxExperts];
-    __shared__ uint32_t s_warp[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = blockIdx.x, nblk = gridDim.x;
     const int El = a.El;
-    uint32_t* tab = s_tab + (size_t)warp * El;
-    for (int e = lane; e < El; e += 32) tab[e] = 0;
-    __syncwarp();
-    const int64_t p0 = min((int64_t)a.P, ((int64_t)rank * 32 + warp) * a.segment);
-    const int64_t p1 = min((int64_t)a.P, p0 + a.segment);
-    auto local_expert = [&](int64_t p, bool count_bad) {
-        if (p >= p1) return -1;
-        const int id = a.ids[p];
+    uint32_t* tab = tabs + (size_t)warp * El;
+    const bool works = warp < nw;
+    const int64_t p0 = min((int64_t)a.P, ((int64_t)rank * nw + warp) * a.segment);
+    const int64_t p1 = works ? min((int64_t)a.P, p0 + a.segment) : p0;
+    auto local_expert = [&](int id, bool in) {
+        if (!in) return -1;
         if (id < 0 || id >= a.E) {
-            if (count_bad) set_status(a.status, MOE_DEV_BAD_EXPERT_ID);
+            if (flag) set_status(a.status, MOE_DEV_BAD_EXPERT_ID);
             return -1;
         }
         const int le = id - a.off;
         return (le >= 0 && le < El) ? le : -1;
     };
-    for (int64_t p = p0; p < p1; p += 32) {
-        const int le = local_expert(p + lane, true);
+    int held[kSortHold];  // the first batches' ids, loaded together
+#pragma unroll
+    for (int i = 0; i < kSortHold; ++i) {
+        const int64_t p = p0 + 32 * i + lane;
+        held[i] = p < p1 ? a.ids[p] : 0;
+    }
+    if (works)
+        for (int e = lane; e < El; e += 32) tab[e] = 0;
+    __syncwarp();
+    auto count = [&](int le) {
         const uint32_t same = __match_any_sync(0xffffffffu, le);
         if (le >= 0 && lane == __ffs(same) - 1) tab[le] += __popc(same);
         __syncwarp();
+    };
+#pragma unroll
+    for (int i = 0; i < kSortHold; ++i) {
+        if (p0 + 32 * i >= p1) break;
+        held[i] = local_expert(held[i], p0 + 32 * i + lane < p1);
+        count(held[i]);
     }
+    for (int64_t p = p0 + 32 * kSortHold; p < p1; p += 32)
+        count(local_expert(p + lane < p1 ? a.ids[p + lane] : 0, p + lane < p1));
     __syncthreads();
     // exclusive prefix over the block's warps, a thread per expert
     for (int e = tid; e < El; e += kSortThreads) {
         uint32_t run = 0;
-        for (int w = 0; w < 32; ++w) {
-            const uint32_t c = s_tab[(size_t)w * El + e];
-            s_tab[(size_t)w * El + e] = run;
+#pragma unroll 8
+        for (int w = 0; w < nw; ++w) {
+            const uint32_t c = tabs[(size_t)w * El + e];
+            tabs[(size_t)w * El + e] = run;
             run += c;
         }
-        s_tot[e] = run;
+        sh.tot[e] = run;
     }
-    cluster_sync();
     // pairs of each expert in the blocks before this one, and in all of them
     uint32_t before = 0, all = 0;
-    if (tid < El)
-        for (int b = 0; b < nblk; ++b) {
-            const uint32_t c = b == rank ? s_tot[tid] : ld_cluster_u32(&s_tot[tid], b);
-            if (b < rank) before += c;
-            all += c;
+    if (nblk > 1) {
+        cluster_sync();
+        if (tid < El) {
+            uint32_t c[kSortBlocks];
+#pragma unroll
+            for (int b = 0; b < kSortBlocks; ++b)
+                c[b] = b >= nblk ? 0u : ld_cluster_u32(&sh.tot[tid], b);
+#pragma unroll
+            for (int b = 0; b < kSortBlocks; ++b) {
+                if (b < rank) before += c[b];
+                all += c[b];
+            }
         }
+    } else if (tid < El) {
+        all = sh.tot[tid];
+    }
     // first row of each group: exclusive scan of the counts rounded up
-    const uint32_t padded = (all + a.align - 1) / a.align * a.align;
+    const uint32_t padded = (all + a.align - 1) & ~(uint32_t)(a.align - 1);
     uint32_t x = padded;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) s_warp[warp] = x;
+    if (lane == 31) sh.warp[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        uint32_t v = s_warp[lane];
+        uint32_t v = sh.warp[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += y;
         }
-        s_warp[lane] = v;
+        sh.warp[lane] = v;
     }
     __syncthreads();
-    const uint32_t first = x - padded + (warp ? s_warp[warp - 1] : 0);
+    const uint32_t first = x - padded + (warp ? sh.warp[warp - 1] : 0);
     if (tid < El) {
-        s_off[tid] = first;
-        s_cnt[tid] = all;
-        if (tid == El - 1) s_off[El] = first + padded;
-        for (int w = 0; w < 32; ++w) s_tab[(size_t)w * El + tid] += first + before;
+        sh.off[tid] = first;
+        sh.cnt[tid] = all;
+        if (tid == El - 1) sh.off[El] = first + padded;
+#pragma unroll 8
+        for (int w = 0; w < nw; ++w) tabs[(size_t)w * El + tid] += first + before;
     }
-    if (El == 0 && tid == 0) s_off[0] = 0;
+    if (El == 0 && tid == 0) sh.off[0] = 0;
     __syncthreads();
-    if (rank == 0) {
-        for (int e = tid; e <= El; e += kSortThreads) a.offsets[e] = (int32_t)s_off[e];
-        for (int e = tid; e < El; e += kSortThreads) a.counts[e] = (int32_t)s_cnt[e];
-        if (tid == 0 && s_off[El] > (uint32_t)a.rows_cap) {
-            // rows past the capacity: only padding may fall there
-            for (int e = 0; e < El; ++e)
-                if (s_cnt[e] && s_off[e] + s_cnt[e] > (uint32_t)a.rows_cap)
-                    set_status(a.status, MOE_DEV_ROWS_OVERFLOW);
-        }
-    }
-    // the pairs' rows
-    for (int64_t p = p0; p < p1; p += 32) {
-        const int le = local_expert(p + lane, false);
+    auto place = [&](int64_t p, int le) {
         const uint32_t same = __match_any_sync(0xffffffffu, le);
         int row = -1;
         if (le >= 0) {
@@ -182,21 +207,106 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a)
         __syncwarp();
         if (le >= 0 && lane == __ffs(same) - 1) tab[le] += __popc(same);
         __syncwarp();
-        if (p + lane < p1) {
-            a.inv[p + lane] = row;
-            if (row >= 0) a.perm_src[row] = (int32_t)(p + lane);
-        }
+        if (p + lane < p1) emit((int32_t)(p + lane), row);
+    };
+#pragma unroll
+    for (int i = 0; i < kSortHold; ++i) {
+        if (p0 + 32 * i >= p1) break;
+        place(p0 + 32 * i, held[i]);
     }
-    // rows of no pair
+    for (int64_t p = p0 + 32 * kSortHold; p < p1; p += 32) {
+        const int id = p + lane < p1 ? a.ids[p + lane] : 0;
+        const int le = id - a.off;
+        place(p, p + lane < p1 && id >= 0 && id < a.E && le >= 0 && le < El ? le : -1);
+    }
+}
+
+// counts, offsets and the overflow flag (one block of the launch).
+__device__ __forceinline__ void sort_write_groups(const SortArgs& a, const SortShared& sh)
+{
+    const int tid = threadIdx.x;
+    for (int e = tid; e <= a.El; e += kSortThreads) a.offsets[e] = (int32_t)sh.off[e];
+    for (int e = tid; e < a.El; e += kSortThreads) {
+        a.counts[e] = (int32_t)sh.cnt[e];
+        // rows past the capacity (padding alone may fall there)
+        if (sh.cnt[e] && sh.off[e] + sh.cnt[e] > (uint32_t)a.rows_cap)
+            set_status(a.status, MOE_DEV_ROWS_OVERFLOW);
+    }
+}
+
+// perm_src of the rows of no pair, shared out over the launch's blocks.
+__device__ __forceinline__ void sort_write_padding(const SortArgs& a, const SortShared& sh, int rank,
+                                                   int nblk)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t cap = (uint32_t)a.rows_cap;
-    for (int g = rank * 32 + warp; g < El; g += nblk * 32) {
-        const uint32_t r1 = min(s_off[g + 1], cap);
-        for (uint32_t r = s_off[g] + s_cnt[g] + lane; r < r1; r += 32) a.perm_src[r] = -1;
+    for (int g = rank * 32 + warp; g < a.El; g += nblk * 32) {
+        const uint32_t r1 = min(sh.off[g + 1], cap);
+        for (uint32_t r = sh.off[g] + sh.cnt[g] + lane; r < r1; r += 32) a.perm_src[r] = -1;
     }
-    for (uint32_t r = s_off[El] + (uint32_t)rank * kSortThreads + tid; r < cap;
+    for (uint32_t r = sh.off[a.El] + (uint32_t)rank * kSortThreads + tid; r < cap;
          r += (uint32_t)nblk * kSortThreads)
         a.perm_src[r] = -1;
-    cluster_sync();  // no block leaves while another may read its totals
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ uint32_t s_tab[];  // [32 warps][El]
+    __shared__ SortShared sh;
+    const int rank = blockIdx.x, nblk = gridDim.x;
+    sort_core(a, sh, s_tab, rank, nblk, 32, true, [&](int32_t p, int row) {
+        a.inv[p] = row;
+        if (row >= 0) a.perm_src[row] = p;
+    });
+    if (rank == 0) sort_write_groups(a, sh);
+    sort_write_padding(a, sh, rank, nblk);
+    if (nblk > 1) cluster_sync();  // no block leaves while another may read its totals
+}
+
+// The sort of up to kSmallPairs pairs and the rows' move (rows null: none) in one launch: every
+// block sorts all pairs into shared memory and moves its share of the tokens.
+template <typename U>
+__global__ void __launch_bounds__(kSortThreads) dispatch_small_kernel(SortArgs a, DispatchArgs d)
+{
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ uint32_t s_tab[];  // [warps that hold pairs][El]
+    __shared__ SortShared sh;
+    __shared__ int32_t s_row[kSmallPairs];
+    const int rank = blockIdx.x, nblk = gridDim.x;
+    sort_core(a, sh, s_tab, 0, 1, (a.P + 31) >> 5, rank == 0, [&](int32_t p, int row) {
+        s_row[p] = row;
+        if (rank == 0) {
+            a.inv[p] = row;
+            if (row >= 0) a.perm_src[row] = p;
+        }
+    });
+    __syncthreads();
+    if (d.rows) {
+        const U* x = static_cast<const U*>(d.x);
+        U* rows = static_cast<U*>(d.rows);
+        for (int t = rank; t < d.T; t += nblk)
+            for (int u = threadIdx.x; u < d.units; u += kSortThreads) {
+                const U v = x[t * d.x_stride + u];
+                for (int j = 0; j < d.k; ++j) {
+                    const int row = s_row[t * d.k + j];
+                    if (row >= 0) rows[(int64_t)row * d.units + u] = v;
+                }
+            }
+    }
+    if (rank == 0) sort_write_groups(a, sh);
+    sort_write_padding(a, sh, rank, nblk);
+}
+
+DispatchSmallKernel dispatch_small_kernel_for(int unit_bytes)
+{
+    switch (unit_bytes) {
+        case 16: return dispatch_small_kernel<uint4>;
+        case 4: return dispatch_small_kernel<uint32_t>;
+        default: return dispatch_small_kernel<uint16_t>;
+    }
 }
 
 // ------------------------------------------------------------------ dispatch
@@ -206,7 +316,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a)
 template <typename U>
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchArgs a)
 {
-    constexpr int kRun = 4;  // pieces per lane
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kRun = 8;  // pieces per lane
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
     const int runs = (a.units + 32 * kRun - 1) / (32 * kRun);
@@ -246,6 +358,8 @@ DispatchKernel dispatch_rows_kernel_for(int unit_bytes)
 template <typename T, int V>
 __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
 {
+    pdl_wait();
+    pdl_trigger();
     const int units = a.H / V;
     const int64_t n = (int64_t)a.T * units;
     const T* y = static_cast<const T*>(a.y);
@@ -302,6 +416,8 @@ CombineKernel combine_rows_kernel_for(int dtype, bool vec)
 template <typename T, int V>
 __global__ void __launch_bounds__(kCombineBackThreads) combine_back_kernel(CombineBackArgs a)
 {
+    pdl_wait();
+    pdl_trigger();
     __shared__ float s_dot[kCombineBackThreads / 32][8];
     const int units = a.H / V;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -139,10 +139,10 @@ moe_status launch_coop(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
                : MOE_ERR_CUDA;
 }
 
-// As launch, for a kernel whose blocks run as clusters of two (CTA pairs).
+// As launch, for a kernel whose blocks run as clusters of `blocks`.
 template <typename... KArgs, typename... Args>
-moe_status launch_pairs(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                        bool pdl, Args... args)
+moe_status launch_cluster(void (*kern)(KArgs...), int blocks, dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t s, bool pdl, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -151,7 +151,7 @@ moe_status launch_pairs(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sm
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -161,6 +161,14 @@ moe_status launch_pairs(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sm
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+// As launch, for a kernel whose blocks run as CTA pairs.
+template <typename... KArgs, typename... Args>
+moe_status launch_pairs(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                        bool pdl, Args... args)
+{
+    return launch_cluster(kern, 2, grid, block, smem, s, pdl, args...);
 }
 
 }  // namespace

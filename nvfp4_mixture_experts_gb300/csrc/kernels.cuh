@@ -335,7 +335,7 @@ struct SortArgs {
     uint32_t* status;     // nullable
 };
 __global__ void sort_pairs_kernel(SortArgs args);
-inline size_t sort_smem(int El) { return (size_t)32 * El * 4; }
+inline size_t sort_smem(int El, int warps) { return (size_t)warps * El * 4; }
 
 struct DispatchArgs {
     const void* x;
@@ -346,6 +346,10 @@ struct DispatchArgs {
     int rows_cap;
     void* rows;
 };
+constexpr int kSmallPairs = 1024;  // a pair per thread of one block
+using DispatchSmallKernel = void (*)(SortArgs, DispatchArgs);
+DispatchSmallKernel dispatch_small_kernel_for(int unit_bytes);
+constexpr int kDispatchRun = 8 * 32;  // pieces that a warp moves at a time
 using DispatchKernel = void (*)(DispatchArgs);
 DispatchKernel dispatch_rows_kernel_for(int unit_bytes);
 
