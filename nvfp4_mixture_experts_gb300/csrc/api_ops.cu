@@ -257,16 +257,16 @@ moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_
     a.values = values_d;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (transpose) {
-        const int64_t n = (int64_t)batch * (rows / 32) * cols;
-        return launch(mx_quant_transposed_kernel_for(dtype), dim3(blocks_for(n, 128, 16)),
-                      dim3(128), 0, s, false, a);
+        const int64_t tiles = (int64_t)batch * ceil_div(rows, 128) * ceil_div(cols, 64);
+        return launch(mx_quant_transposed_kernel_for(dtype), dim3(blocks_for(tiles, 1, 16)),
+                      dim3(256), 0, s, true, a);
     }
     const int es = elem_bytes(dtype);
     const bool vec = rows_vec(x_d, (int64_t)cols * es, rows > 1 ? row_stride * es : 0) &&
                      (batch == 1 || batch_stride * es % 16 == 0);
-    const int64_t n = (int64_t)batch * rows * (cols / 8);
-    return launch(mx_quant_kernel_for(dtype, vec), dim3(blocks_for(n, 256, 8)), dim3(256), 0, s,
-                  false, a);
+    const int64_t items = (int64_t)batch * rows * ceil_div(cols / 8, kMxQuantRun);
+    return launch(mx_quant_kernel_for(dtype, vec), dim3(blocks_for(items, 8, 16)), dim3(256), 0, s,
+                  true, a);
 }
 
 moe_status moe_mxfp4_tile_scales(const uint8_t* sf_d, int32_t batch, int32_t rows, int32_t cols,

@@ -4,65 +4,77 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kernels.cuh"
 
 namespace moe {
 
 // ------------------------------------------------------------------ element types
 
-// Pieces of a row: 16 bytes (kVec elements) when rows allow it, else one element.
+// A piece of a row of elements of type T: 16 bytes (V elements, held as a uint4) where the rows
+// allow it, else one element (V = 1).  fp32 values in, fp32 values out; rounding to nearest even.
+template <typename T, int V>
+struct Piece {
+    uint4 raw;
+    __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = raw; }
+    __device__ __forceinline__ void unpack(float (&f)[V]) const
+    {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (V == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else if constexpr (kIsHalf) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ void pack(const float (&f)[V])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (V == 4) {
+                w[i] = __float_as_uint(f[i]);
+            } else if constexpr (kIsHalf) {
+                const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        raw = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static constexpr bool kIsHalf = std::is_same<T, __half>::value;
+};
+
 template <typename T>
-struct Elem;
-
-template <>
-struct Elem<__nv_bfloat16> {
-    static constexpr int kVec = 8;
-    static __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-    static __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+struct Piece<T, 1> {
+    T raw;
+    __device__ __forceinline__ void load(const T* p) { raw = *p; }
+    __device__ __forceinline__ void store(T* p) const { *p = raw; }
+    __device__ __forceinline__ void unpack(float (&f)[1]) const { f[0] = (float)raw; }
+    __device__ __forceinline__ void pack(const float (&f)[1])
+    {
+        if constexpr (std::is_same<T, __half>::value) raw = __float2half_rn(f[0]);
+        else if constexpr (std::is_same<T, float>::value) raw = f[0];
+        else raw = __float2bfloat16_rn(f[0]);
+    }
 };
-
-template <>
-struct Elem<__half> {
-    static constexpr int kVec = 8;
-    static __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-    static __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
-};
-
-template <>
-struct Elem<float> {
-    static constexpr int kVec = 4;
-    static __device__ __forceinline__ float to_f32(float v) { return v; }
-    static __device__ __forceinline__ float from_f32(float v) { return v; }
-};
-
-// A piece of V elements of type T (V = kVec: one 16-byte access; V = 1: one element).
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Piece {
-    T v[V];
-};
-
-template <typename T, int V>
-__device__ __forceinline__ void unpack(const Piece<T, V>& p, float (&f)[V])
-{
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = Elem<T>::to_f32(p.v[i]);
-}
-
-template <typename T, int V>
-__device__ __forceinline__ Piece<T, V> pack(const float (&f)[V])
-{
-    Piece<T, V> p;
-#pragma unroll
-    for (int i = 0; i < V; ++i) p.v[i] = Elem<T>::from_f32(f[i]);
-    return p;
-}
 
 // ------------------------------------------------------------------ the sort
 
 // A stable counting sort.  Every warp that takes part owns a contiguous segment of the pairs and a
 // table of counts by expert in shared memory.  Pass 1 counts the segments (32 pairs at a time: lanes
-// of equal expert found with one match instruction, their first lane adds their number, so no
-// atomics).  Prefix sums over the block's warps, over the blocks and over the experts (group
+// of equal expert found with votes, their first lane adds their number, so no atomics).  Prefix sums over the block's warps, over the blocks and over the experts (group
 // sizes rounded up to row_align) turn the tables into the row of each segment's first pair of each
 // expert.  Pass 2 walks the segments again: a pair's row is its table entry plus the number of
 // lower lanes of equal expert, and the first lane moves the entry on.
@@ -91,7 +103,21 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* local, uint32
     return v;
 }
 
-constexpr int kSortHold = 8;  // batches of 32 ids that a lane keeps in registers between the passes
+constexpr int kSortHold = 8;  // batches of 32 pairs that a warp keeps in registers between passes
+
+// The lanes of the warp whose le (-1 .. El - 1) equals this lane's: one vote per bit of the
+// numbers 0 .. El (a match instruction takes some 230 cycles on 32 different values, a vote a few).
+__device__ __forceinline__ uint32_t equal_lanes(int le, int bits)
+{
+    const uint32_t key = (uint32_t)(le + 1);
+    uint32_t same = 0xffffffffu;
+    for (int i = 0; i < bits; ++i) {
+        const bool set = (key >> i) & 1u;
+        const uint32_t vote = __ballot_sync(0xffffffffu, set);
+        same &= set ? vote : ~vote;
+    }
+    return same;
+}
 
 // Sorts with the `nw` first warps of each of `nblk` blocks (rank: this one's place).  calls
 // emit(pair, row) for this block's pairs (row -1: dropped); leaves off and cnt in sh.  tab:
@@ -124,16 +150,19 @@ __device__ __forceinline__ void sort_core(const SortArgs& a, SortShared& sh, uin
     if (works)
         for (int e = lane; e < El; e += 32) tab[e] = 0;
     __syncwarp();
+    const int bits = 32 - __clz(El);
     auto count = [&](int le) {
-        const uint32_t same = __match_any_sync(0xffffffffu, le);
+        const uint32_t same = equal_lanes(le, bits);
         if (le >= 0 && lane == __ffs(same) - 1) tab[le] += __popc(same);
         __syncwarp();
+        return same;
     };
+    uint32_t same[kSortHold];
 #pragma unroll
     for (int i = 0; i < kSortHold; ++i) {
         if (p0 + 32 * i >= p1) break;
         held[i] = local_expert(held[i], p0 + 32 * i + lane < p1);
-        count(held[i]);
+        same[i] = count(held[i]);
     }
     for (int64_t p = p0 + 32 * kSortHold; p < p1; p += 32)
         count(local_expert(p + lane < p1 ? a.ids[p + lane] : 0, p + lane < p1));
@@ -197,8 +226,7 @@ __device__ __forceinline__ void sort_core(const SortArgs& a, SortShared& sh, uin
     }
     if (El == 0 && tid == 0) sh.off[0] = 0;
     __syncthreads();
-    auto place = [&](int64_t p, int le) {
-        const uint32_t same = __match_any_sync(0xffffffffu, le);
+    auto place = [&](int64_t p, int le, uint32_t same) {
         int row = -1;
         if (le >= 0) {
             const uint32_t r = tab[le] + __popc(same & ((1u << lane) - 1u));
@@ -212,12 +240,13 @@ __device__ __forceinline__ void sort_core(const SortArgs& a, SortShared& sh, uin
 #pragma unroll
     for (int i = 0; i < kSortHold; ++i) {
         if (p0 + 32 * i >= p1) break;
-        place(p0 + 32 * i, held[i]);
+        place(p0 + 32 * i, held[i], same[i]);
     }
     for (int64_t p = p0 + 32 * kSortHold; p < p1; p += 32) {
         const int id = p + lane < p1 ? a.ids[p + lane] : 0;
-        const int le = id - a.off;
-        place(p, p + lane < p1 && id >= 0 && id < a.E && le >= 0 && le < El ? le : -1);
+        const int off = id - a.off;
+        const int le = p + lane < p1 && id >= 0 && id < a.E && off >= 0 && off < El ? off : -1;
+        place(p, le, equal_lanes(le, bits));
     }
 }
 
@@ -380,8 +409,7 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
                     const int row = a.inv[t * a.k + j0 + j];
                     live[j] = (uint32_t)row < (uint32_t)a.rows_cap;
                     if (live[j]) {
-                        p[j] = *reinterpret_cast<const Piece<T, V>*>(y + (int64_t)row * a.H +
-                                                                     (int64_t)u * V);
+                        p[j].load(y + (int64_t)row * a.H + (int64_t)u * V);
                         w[j] = a.w ? a.w[t * a.k + j0 + j] : 1.0f;
                     }
                 }
@@ -390,12 +418,14 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
             for (int j = 0; j < 8; ++j)
                 if (live[j]) {
                     float f[V];
-                    unpack(p[j], f);
+                    p[j].unpack(f);
 #pragma unroll
                     for (int e = 0; e < V; ++e) acc[e] = fmaf(w[j], f[e], acc[e]);
                 }
         }
-        *reinterpret_cast<Piece<T, V>*>(out + t * a.out_stride + (int64_t)u * V) = pack<T, V>(acc);
+        Piece<T, V> sum;
+        sum.pack(acc);
+        sum.store(out + t * a.out_stride + (int64_t)u * V);
     }
 }
 
@@ -442,23 +472,22 @@ __global__ void __launch_bounds__(kCombineBackThreads) combine_back_kernel(Combi
                 }
             }
             for (int u = threadIdx.x; u < units; u += kCombineBackThreads) {
-                float d[V];
-                unpack(*reinterpret_cast<const Piece<T, V>*>(dout + t * a.dout_stride +
-                                                             (int64_t)u * V), d);
-                Piece<T, V> p[8];
+                Piece<T, V> pd, p[8];
+                pd.load(dout + t * a.dout_stride + (int64_t)u * V);
                 if (a.dw) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (row[j] >= 0)
-                            p[j] = *reinterpret_cast<const Piece<T, V>*>(
-                                y + (int64_t)row[j] * a.H + (int64_t)u * V);
+                            p[j].load(y + (int64_t)row[j] * a.H + (int64_t)u * V);
                 }
+                float d[V];
+                pd.unpack(d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     if (row[j] < 0) continue;
                     if (a.dw) {
                         float f[V];
-                        unpack(p[j], f);
+                        p[j].unpack(f);
 #pragma unroll
                         for (int e = 0; e < V; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
                     }
@@ -466,8 +495,9 @@ __global__ void __launch_bounds__(kCombineBackThreads) combine_back_kernel(Combi
                         float g[V];
 #pragma unroll
                         for (int e = 0; e < V; ++e) g[e] = w[j] * d[e];
-                        *reinterpret_cast<Piece<T, V>*>(dy + (int64_t)row[j] * a.H +
-                                                        (int64_t)u * V) = pack<T, V>(g);
+                        Piece<T, V> pg;
+                        pg.pack(g);
+                        pg.store(dy + (int64_t)row[j] * a.H + (int64_t)u * V);
                     }
                 }
             }

@@ -391,6 +391,7 @@ struct MxQuantArgs {
     int layout;                        // moe_sf_layout
     void* values;                      // nullable
 };
+constexpr int kMxQuantRun = 4 * 32;   // eights of a row that a warp takes at a time
 using MxQuantKernel = void (*)(MxQuantArgs);
 MxQuantKernel mx_quant_kernel_for(int dtype, bool vec);
 MxQuantKernel mx_quant_transposed_kernel_for(int dtype);
