@@ -287,7 +287,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a)
     const int rank = blockIdx.x, nblk = gridDim.x;
     sort_core(a, sh, s_tab, rank, nblk, 32, true, [&](int32_t p, int row) {
         a.inv[p] = row;
-        if (row >= 0) a.perm_src[row] = p;
+        // scattered words, 32 sectors a warp: left to the kernel that moves the rows, where all
+        // of the GPU shares them, if one follows
+        if (row >= 0 && !a.rows_follow) a.perm_src[row] = p;
     });
     if (rank == 0) sort_write_groups(a, sh);
     sort_write_padding(a, sh, rank, nblk);
@@ -364,6 +366,7 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchArgs a)
         for (int j = 0; j < a.k; ++j) {
             const int row = a.inv[t * a.k + j];
             if ((uint32_t)row >= (uint32_t)a.rows_cap) continue;
+            if (u0 == 0) a.perm_src[row] = (int32_t)(t * a.k + j);
 #pragma unroll
             for (int r = 0; r < kRun; ++r)
                 if (u0 + 32 * r < a.units) rows[(int64_t)row * a.units + u0 + 32 * r] = v[r];
@@ -382,50 +385,65 @@ DispatchKernel dispatch_rows_kernel_for(int unit_bytes)
 
 // ------------------------------------------------------------------ combine
 
-// out[t] = sum_j w[t, j] rows[inv[t k + j]] (w null: 1): a thread per piece of a token, the loads
-// of up to eight rows in flight, fp32 sums in ascending j.
+// out[t] = sum_j w[t, j] rows[inv[t k + j]] (w null: 1): a warp takes kCombineRun pieces of a token,
+// the rows and weights of the token's pairs held by its lanes, the loads of eight rows in flight;
+// fp32 sums in ascending j.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    const int units = a.H / V;
-    const int64_t n = (int64_t)a.T * units;
+    constexpr int kPer = kCombineRun / 32;
+    const int lane = threadIdx.x & 31;
+    const int units = a.H / V, runs = (units + kCombineRun - 1) / kCombineRun;
+    const int64_t items = (int64_t)a.T * runs, step = (int64_t)gridDim.x * (blockDim.x >> 5);
     const T* y = static_cast<const T*>(a.y);
     T* out = static_cast<T*>(a.out);
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-         i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t t = i / units;
-        const int u = (int)(i % units);
-        float acc[V] = {};
+    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < items; i += step) {
+        const int64_t t = i / runs;
+        const int u0 = (int)(i - t * runs) * kCombineRun + lane;
+        int my_row = -1;
+        float my_w = 1.0f;
+        if (lane < a.k) {
+            my_row = a.inv[t * a.k + lane];
+            if ((uint32_t)my_row >= (uint32_t)a.rows_cap) my_row = -1;
+            if (a.w) my_w = a.w[t * a.k + lane];
+        }
+        float acc[kPer][V] = {};
         for (int j0 = 0; j0 < a.k; j0 += 8) {
-            Piece<T, V> p[8];
-            float w[8];
-            bool live[8];
+            Piece<T, V> p[8][kPer];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                live[j] = false;
-                if (j0 + j < a.k) {
-                    const int row = a.inv[t * a.k + j0 + j];
-                    live[j] = (uint32_t)row < (uint32_t)a.rows_cap;
-                    if (live[j]) {
-                        p[j].load(y + (int64_t)row * a.H + (int64_t)u * V);
-                        w[j] = a.w ? a.w[t * a.k + j0 + j] : 1.0f;
-                    }
+                const int row = __shfl_sync(0xffffffffu, my_row, j0 + j);  // -1 past k
+                if (row >= 0) {
+#pragma unroll
+                    for (int q = 0; q < kPer; ++q)
+                        if (u0 + 32 * q < units)
+                            p[j][q].load(y + (int64_t)row * a.H + (int64_t)(u0 + 32 * q) * V);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (live[j]) {
-                    float f[V];
-                    p[j].unpack(f);
+            for (int j = 0; j < 8; ++j) {
+                const int row = __shfl_sync(0xffffffffu, my_row, j0 + j);
+                const float w = __shfl_sync(0xffffffffu, my_w, j0 + j);
+                if (row >= 0) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) acc[e] = fmaf(w[j], f[e], acc[e]);
+                    for (int q = 0; q < kPer; ++q) {
+                        float f[V];
+                        p[j][q].unpack(f);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) acc[q][e] = fmaf(w, f[e], acc[q][e]);
+                    }
                 }
+            }
         }
-        Piece<T, V> sum;
-        sum.pack(acc);
-        sum.store(out + t * a.out_stride + (int64_t)u * V);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+            if (u0 + 32 * q < units) {
+                Piece<T, V> sum;
+                sum.pack(acc[q]);
+                sum.store(out + t * a.out_stride + (int64_t)(u0 + 32 * q) * V);
+            }
     }
 }
 
@@ -441,14 +459,14 @@ CombineKernel combine_rows_kernel_for(int dtype, bool vec)
 
 // ------------------------------------------------------------------ combine's gradient
 
-// A block per token: dy rows = w dout, and the k dot products <dout, y row>, eight rows at a
-// time, reduced over the block.
-template <typename T, int V>
-__global__ void __launch_bounds__(kCombineBackThreads) combine_back_kernel(CombineBackArgs a)
+// A block of W warps per token: dy rows = w dout, and the k dot products <dout, y row>, eight rows
+// at a time, reduced over the block.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(32 * W) combine_back_kernel(CombineBackArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    __shared__ float s_dot[kCombineBackThreads / 32][8];
+    __shared__ float s_dot[W][8];
     const int units = a.H / V;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T* dout = static_cast<const T*>(a.dout);
@@ -471,14 +489,13 @@ __global__ void __launch_bounds__(kCombineBackThreads) combine_back_kernel(Combi
                     }
                 }
             }
-            for (int u = threadIdx.x; u < units; u += kCombineBackThreads) {
+            for (int u = threadIdx.x; u < units; u += 32 * W) {
                 Piece<T, V> pd, p[8];
                 pd.load(dout + t * a.dout_stride + (int64_t)u * V);
                 if (a.dw) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (row[j] >= 0)
-                            p[j].load(y + (int64_t)row[j] * a.H + (int64_t)u * V);
+                        if (row[j] >= 0) p[j].load(y + (int64_t)row[j] * a.H + (int64_t)u * V);
                 }
                 float d[V];
                 pd.unpack(d);
@@ -512,7 +529,7 @@ __global__ void __launch_bounds__(kCombineBackThreads) combine_back_kernel(Combi
                 __syncthreads();
                 if (threadIdx.x < 8 && j0 + (int)threadIdx.x < a.k) {
                     float sum = 0.0f;
-                    for (int q = 0; q < kCombineBackThreads / 32; ++q) sum += s_dot[q][threadIdx.x];
+                    for (int q = 0; q < W; ++q) sum += s_dot[q][threadIdx.x];
                     a.dw[t * a.k + j0 + threadIdx.x] = sum;
                 }
                 __syncthreads();
@@ -521,13 +538,23 @@ __global__ void __launch_bounds__(kCombineBackThreads) combine_back_kernel(Combi
     }
 }
 
-CombineBackKernel combine_back_kernel_for(int dtype, bool vec)
+template <typename T, int V>
+static CombineBackKernel combine_back_of(int warps)
+{
+    switch (warps) {
+        case 2: return combine_back_kernel<T, V, 2>;
+        case 4: return combine_back_kernel<T, V, 4>;
+        default: return combine_back_kernel<T, V, 8>;
+    }
+}
+
+CombineBackKernel combine_back_kernel_for(int dtype, bool vec, int warps)
 {
     switch (dtype) {
         case MOE_BF16:
-            return vec ? combine_back_kernel<__nv_bfloat16, 8> : combine_back_kernel<__nv_bfloat16, 1>;
-        case MOE_FP16: return vec ? combine_back_kernel<__half, 8> : combine_back_kernel<__half, 1>;
-        default: return vec ? combine_back_kernel<float, 4> : combine_back_kernel<float, 1>;
+            return vec ? combine_back_of<__nv_bfloat16, 8>(warps) : combine_back_of<__nv_bfloat16, 1>(warps);
+        case MOE_FP16: return vec ? combine_back_of<__half, 8>(warps) : combine_back_of<__half, 1>(warps);
+        default: return vec ? combine_back_of<float, 4>(warps) : combine_back_of<float, 1>(warps);
     }
 }
 

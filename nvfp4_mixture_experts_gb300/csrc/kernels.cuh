@@ -333,6 +333,7 @@ struct SortArgs {
     int32_t* perm_src;    // [rows_cap]
     int32_t* inv;         // [P]
     uint32_t* status;     // nullable
+    int rows_follow;      // perm_src of the pairs' rows is written by dispatch_rows_kernel
 };
 __global__ void sort_pairs_kernel(SortArgs args);
 inline size_t sort_smem(int El, int warps) { return (size_t)warps * El * 4; }
@@ -344,6 +345,7 @@ struct DispatchArgs {
     int T, k;
     int units;            // units (16, 4 or 2 bytes) per row
     int rows_cap;
+    int32_t* perm_src;
     void* rows;
 };
 constexpr int kSmallPairs = 1024;  // a pair per thread of one block
@@ -361,11 +363,11 @@ struct CombineArgs {
     void* out;
     int64_t out_stride;   // in elements
 };
+constexpr int kCombineRun = 2 * 32;   // pieces of a token that a warp takes at a time
 using CombineKernel = void (*)(CombineArgs);
 // vec: every row starts on 16 bytes and is a whole number of 16-byte pieces
 CombineKernel combine_rows_kernel_for(int dtype, bool vec);
 
-constexpr int kCombineBackThreads = 256;
 struct CombineBackArgs {
     const void* dout;
     int64_t dout_stride;  // in elements
@@ -377,7 +379,7 @@ struct CombineBackArgs {
     float* dw;            // nullable
 };
 using CombineBackKernel = void (*)(CombineBackArgs);
-CombineBackKernel combine_back_kernel_for(int dtype, bool vec);
+CombineBackKernel combine_back_kernel_for(int dtype, bool vec, int warps);
 
 // ---- mxfp4.cu: MXFP4 quantisation and scale layouts
 struct MxQuantArgs {
