@@ -345,7 +345,7 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
     a.status = status_d;
     const MxGemmKernel kern = gemm_mxfp4_kernel_for(out_dtype);
     const int smem = gemm_mxfp4_smem(num_groups, es);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
     // at most this many tiles, however the rows fall into groups
@@ -353,7 +353,7 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
                           ceil_div(N, 256);
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms() / 2));
     return launch_pairs(kern, dim3(2 * pairs), dim3(kMxThreads), smem,
-                        reinterpret_cast<cudaStream_t>(stream), false, tmW, tmT, tmT16, tmSW, tmST, a);
+                        reinterpret_cast<cudaStream_t>(stream), true, tmW, tmT, tmT16, tmSW, tmST, a);
 }
 
 }  // extern "C"

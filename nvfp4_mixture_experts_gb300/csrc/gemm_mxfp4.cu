@@ -13,8 +13,9 @@
 // Warp roles (both CTAs unless said): warp 0 issues the TMA loads of its CTA's operands and
 // scales, all counted on the leader's stage barrier; warp 1 of the leader (cluster rank 0) copies
 // each stage's scales to TMEM (tcgen05.cp, in order with the MMAs) and issues the MMAs; warps
-// 2..9 read the accumulator (lane = weight row, column = group row), transpose it through shared
-// memory and store 64-byte (16-bit types) or 128-byte (fp32) pieces of the output rows.
+// 2..9 read the accumulator (lane = weight row, column = group row) into registers, which frees it
+// for the MMAs, transpose it through shared memory and store 64-byte (16-bit types) or 128-byte
+// (fp32) pieces of the output rows.
 //
 // TMEM (all 512 columns, so the allocation starts at column 0): two accumulators, of the even tiles at column 0 upwards, of the odd tiles
 // ending at column 448; two slots of a stage's scales in columns 448..511.  Two tiles of together
@@ -28,14 +29,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kW = 16384;                    // a stage's weight rows of one CTA: 128 x 128 bytes
-constexpr int kT = 16384;                    // up to 128 group rows of one CTA
-constexpr int kScW = 1024, kScT = 2048;      // scale atoms: 2 k-atoms x (1 | 2) row blocks
-static_assert(kW + kT + kScW + kScT == kMxStageBytes, "stage layout");
 constexpr int kAccEnd = 448;                 // TMEM columns of accumulators; scales above
 
 struct Ctl {
-    uint64_t full[kMxStages], empty[kMxStages], acc_full[2], acc_empty[2], drain;
+    uint64_t full[kMxMaxStages], empty[kMxMaxStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort_flag, zero;
 };
@@ -59,6 +56,16 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
     uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
+}
+
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Tensor loads of a CTA pair: the bytes may be counted on the barrier of either CTA (bar is a
@@ -125,23 +132,19 @@ struct Groups {
     const int32_t* counts;  // [G] rows (0 for a skipped group)
     const int32_t* first;   // [G] first row
     int G, NB;
+    int most;               // rows of the largest group
 };
 
-// The tile of index t; g is the group of an earlier tile of the warp (the search goes on from it).
-// All lanes of a warp.
-__device__ __forceinline__ Tile find_tile(const Groups& gs, int t, int& g)
+// The tile of index t (all lanes of a warp).  Its group, the last one that starts at or before the
+// token tile, is found in two votes: the 32 groups it is among, then the one.
+__device__ __forceinline__ Tile find_tile(const Groups& gs, int t)
 {
     const int lane = threadIdx.x & 31;
     const int tt = t / gs.NB;
-    for (;;) {
-        const int i = g + 1 + lane;
-        const uint32_t past = __ballot_sync(0xffffffffu, i >= gs.G || gs.start[i] > tt);
-        if (past) {
-            g += __ffs(past) - 1;
-            break;
-        }
-        g += 32;
-    }
+    const int c = lane * 32;
+    const int coarse = (__popc(__ballot_sync(0xffffffffu, c < gs.G && gs.start[c] <= tt)) - 1) * 32;
+    const int f = coarse + lane;
+    const int g = coarse + __popc(__ballot_sync(0xffffffffu, f < gs.G && gs.start[f] <= tt)) - 1;
     Tile ti;
     ti.g = g;
     ti.n0 = (t - tt * gs.NB) * 256;
@@ -157,41 +160,58 @@ __device__ __forceinline__ Tile find_tile(const Groups& gs, int t, int& g)
 // flagged and gets none.
 __device__ __forceinline__ Groups load_groups(const MxGemmArgs& a, int32_t* sm, int32_t* s_warp)
 {
-    const int G = a.G, nthr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kPer = (kMaxExperts + kMxThreads - 1) / kMxThreads;  // groups of a thread at most
+    const int G = a.G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int32_t* start = sm;
     int32_t* cnt = start + G + 1;
     int32_t* first = cnt + G;
-    for (int g = tid; g < G; g += nthr) {
-        int64_t c = a.counts ? a.counts[g] : a.rows_cap, o = a.offsets ? a.offsets[g] : 0;
-        if (c > 0 && (o < 0 || (o & 127) || o + c > a.rows_cap)) {
-            set_status(a.status, MOE_DEV_BAD_INDEX);
-            c = 0;
-        }
-        cnt[g] = (int32_t)max(c, (int64_t)0);
-        first[g] = (int32_t)o;
+    const int per = (G + kMxThreads - 1) / kMxThreads, g0 = tid * per;
+    int c[kPer], o[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const bool in = i < per && g0 + i < G;
+        c[i] = !in ? 0 : a.counts ? a.counts[g0 + i] : a.rows_cap;
+        o[i] = in && a.offsets ? a.offsets[g0 + i] : 0;
     }
-    __syncthreads();
-    const int per = (G + nthr - 1) / nthr;
-    const int g0 = min(G, tid * per), g1 = min(G, g0 + per);
-    int sum = 0;
-    for (int g = g0; g < g1; ++g) sum += (cnt[g] + kMxTileRows - 1) / kMxTileRows;
+    int sum = 0, most = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (c[i] > 0 && (o[i] < 0 || (o[i] & 127) || (int64_t)o[i] + c[i] > a.rows_cap)) {
+            set_status(a.status, MOE_DEV_BAD_INDEX);
+            c[i] = 0;
+        }
+        c[i] = max(c[i], 0);
+        most = max(most, c[i]);
+        sum += (c[i] + kMxTileRows - 1) / kMxTileRows;
+    }
     int v = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, v, d);
         if (lane >= d) v += y;
     }
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 31) s_warp[warp] = v;
+    if (lane == 0) s_warp[32 + warp] = most;
     __syncthreads();
+    constexpr int kWarps = kMxThreads / 32;
     int pre = v - sum;
-    for (int w = 0; w < warp; ++w) pre += s_warp[w];
-    for (int g = g0; g < g1; ++g) {
-        start[g] = pre;
-        pre += (cnt[g] + kMxTileRows - 1) / kMxTileRows;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) pre += s_warp[w];
+        most = max(most, s_warp[32 + w]);
     }
-    if (tid == nthr - 1) start[G] = pre;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (i < per && g0 + i < G) {
+            start[g0 + i] = pre;
+            cnt[g0 + i] = c[i];
+            first[g0 + i] = o[i];
+            pre += (c[i] + kMxTileRows - 1) / kMxTileRows;
+        }
+    if (tid == kMxThreads - 1) start[G] = pre;  // (no groups of its own, or the last ones)
     __syncthreads();
-    return Groups{start, cnt, first, G, (a.N + 255) / 256};
+    return Groups{start, cnt, first, G, (a.N + 255) / 256, most};
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort)
@@ -201,53 +221,122 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-// A place in the ring of stages: the n-th k-stage of the CTA.
-struct Ring {
-    uint32_t stage, phase;
-    __device__ __forceinline__ explicit Ring(uint32_t n)
-        : stage(n % kMxStages), phase((n / kMxStages) & 1u)
+// The ring of k-stages in shared memory.  Where no group has more than 64 rows a stage holds 32
+// group rows per CTA and one row block of scales instead of 128 and two, and eight of them fit
+// instead of five: with few tiles the loads in flight bound the product (one token's gate_up,
+// 16 k-stages a tile: 8 stages 350 -> 220 cycles a k-stage).
+struct Stages {
+    uint8_t* base;
+    int n;                                   // stages
+    uint32_t bytes, t, sw, st;               // of a stage; offsets of its parts (weights at 0)
+    __device__ __forceinline__ Stages(uint8_t* p, bool small) : base(p)
     {
+        n = small ? kMxMaxStages : kMxStages;
+        bytes = small ? kMxSmallStageBytes : kMxStageBytes;
+        t = 16384;
+        sw = t + (small ? 4096 : 16384);
+        st = sw + 1024;
     }
-    __device__ __forceinline__ void next()
+};
+
+struct Place {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n)
     {
-        if (++stage == kMxStages) {
+        if (++stage == n) {
             stage = 0;
             phase ^= 1u;
         }
     }
 };
 
-__device__ __forceinline__ void put(float v, __nv_bfloat16* o) { *o = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(float v, __half* o) { *o = __float2half_rn(v); }
-__device__ __forceinline__ void put(float v, float* o) { *o = v; }
-
-// Stores 32 group rows (registers) x 32 weight rows (lanes) of the accumulator: lane l holds
-// output column n0 + l of rows row0 .. row0 + live - 1.  vec: through the warp's staging buffer as
-// 16-byte pieces along the output rows; else element by element.
-template <typename T>
-__device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t (&r)[32], T* stage,
-                                            int64_t row0, int live, int n0, int lane)
+// Each thread of the warp reads 2 x 16 lanes x 32 columns of TMEM from taddr: register 4 i + e of
+// half h holds lane 16 h + l / 4 + 8 (e / 2), column 8 i + 2 (l % 4) + e % 2 (l: the thread's lane).
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32])
 {
-    T* out = static_cast<T*>(a.out);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t* q = r + 16 * h;
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]),
+              "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]),
+              "=r"(q[13]), "=r"(q[14]), "=r"(q[15])
+            : "r"(taddr + ((uint32_t)(16 * h) << 16))
+            : "memory");
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A chunk of the accumulator: 32 weight rows (TMEM lanes) x 32 group rows (columns).
+template <typename T>
+__device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[32])
+{
+    if constexpr (sizeof(T) == 2) tmem_ld_frag(taddr, r);
+    else tmem_ld32(taddr, r);
+}
+
+// Stores a chunk: output columns n0 .. n0 + 31 of the `live` first of 32 rows, out pointing at the
+// first row.  The chunk is transposed through the warp's staging buffer (16-bit types: 8 x 8
+// matrices stored transposed; fp32: a word per lane and row), then leaves as 16-byte pieces along
+// the output rows, or (vec false) element by element.
+template <typename T>
+__device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t (&r)[32],
+                                            uint8_t* stage, T* out, int live, int n0, int lane)
+{
+    constexpr int kPitch = mx_epi_pitch((int)sizeof(T));  // bytes of a staged row
+    __syncwarp();
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t at = smem_u32(stage) + (lane & 7) * kPitch + (lane >> 3) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t m[4];  // features 8 m .. 8 m + 7 of rows 8 i .. 8 i + 7
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const int e = 16 * (f >> 1) + 4 * i + 2 * (f & 1);
+                m[f] = pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]), T());
+            }
+            asm volatile(
+                "stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                    at + 8 * i * kPitch),
+                "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
+                : "memory");
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            *reinterpret_cast<uint32_t*>(stage + j * kPitch + 4 * lane) = r[j];
+    }
+    __syncwarp();
     if (a.vec) {
         constexpr int kPer = 16 / (int)sizeof(T);   // elements of a piece
         constexpr int kLanes = 32 / kPer;           // lanes per row
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) put(__uint_as_float(r[j]), stage + j * 32 + lane);
-        __syncwarp();
         const int n = n0 + (lane % kLanes) * kPer;
         if (n < a.N) {
+            T* o = out + (lane / kLanes) * a.out_stride + n;
+            const uint8_t* st = stage + (lane / kLanes) * kPitch + (lane % kLanes) * 16;
 #pragma unroll
-            for (int j = lane / kLanes; j < 32; j += 32 / kLanes)
-                if (j < live)
-                    *reinterpret_cast<uint4*>(out + (row0 + j) * a.out_stride + n) =
-                        *reinterpret_cast<const uint4*>(stage + j * 32 + (lane % kLanes) * kPer);
+            for (int j = 0; j < 32; j += 32 / kLanes)
+                if (j + lane / kLanes < live)
+                    *reinterpret_cast<uint4*>(o + j * a.out_stride) =
+                        *reinterpret_cast<const uint4*>(st + j * kPitch);
         }
     } else if (n0 + lane < a.N) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < live) put(__uint_as_float(r[j]), out + (row0 + j) * a.out_stride + n0 + lane);
+        T* o = out + n0 + lane;
+        for (int j = 0; j < live && j < 32; ++j)
+            o[j * a.out_stride] = reinterpret_cast<const T*>(stage + j * kPitch)[lane];
     }
 }
 
@@ -261,17 +350,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                       const __grid_constant__ CUtensorMap tmST, MxGemmArgs args)
 {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* stages = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-    uint8_t* staging = stages + kMxStages * kMxStageBytes;
-    Ctl& ctl = *reinterpret_cast<Ctl*>(staging + kMxEpiWarps * 32 * 32 * sizeof(T));
+    uint8_t* ring = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+    uint8_t* staging = ring + kMxRingBytes;
+    Ctl& ctl = *reinterpret_cast<Ctl*>(staging + kMxEpiWarps * 32 * mx_epi_pitch((int)sizeof(T)));
     int32_t* tables = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(&ctl) + kMxCtlBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int KB = (args.K + 255) / 256;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kMxStages; ++s) {
+    if (warp == 0 && elect_one()) {
+        for (int s = 0; s < kMxMaxStages; ++s) {
             mbar_init(&ctl.full[s], 1);
             mbar_init(&ctl.empty[s], 1);
         }
@@ -282,60 +371,59 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         mbar_init(&ctl.drain, 1);
         ctl.abort_flag = ctl.zero = 0;
         fence_barrier_init();
-    }
-    if (warp == 0 && lane == 0) {
         prefetch_tmap(&tmW);
         prefetch_tmap(&tmT);
         prefetch_tmap(&tmT16);
         prefetch_tmap(&tmSW);
         prefetch_tmap(&tmST);
     }
+    __syncwarp();
     if (warp == 1) tmem_alloc_pair(&ctl.tmem, 512);
-    const Groups gs = load_groups(args, tables, reinterpret_cast<int32_t*>(staging));
     tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // both CTAs' barriers exist before any arrives across the pair
+    cluster_arrive();  // this CTA's barriers exist and its TMEM is allocated
+    pdl_wait();
+    pdl_trigger();
+    const Groups gs = load_groups(args, tables, reinterpret_cast<int32_t*>(staging));
+    cluster_wait();    // ... and the peer's
     tc_fence_after();
     const int ntiles = gs.start[gs.G] * gs.NB;
+    const Stages sg(ring, gs.most <= 64);
     volatile int* abort = &ctl.abort_flag;
 
     if (warp == 0) {
         const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
         const uint32_t full0 = cluster_addr(&ctl.full[0], 0);  // the leader's barriers
-        int g = 0;
-        uint32_t n = 0, done = 0;  // k-stages of the earlier tiles; issued so far
+        Place at;               // (the elected lane's)
+        int issued = 0;         // stages with a copy of this CTA, the last one before `at`
         bool ok = true;
-        for (int t = pair; t < ntiles && ok; t += npairs, n += KB) {
-            const Tile ti = find_tile(gs, t, g);
+        for (int t = pair; t < ntiles && ok; t += npairs) {
+            const Tile ti = find_tile(gs, t);
             if (elect_one()) {
                 const int half = ti.nt >> 1;                    // group rows of this CTA
                 const int trow = ti.row0 + (int)rank * half, wrow = ti.n0 + (int)rank * 128;
                 const int nsc = ti.nt > 128 ? 2 : 1;            // row blocks of group-row scales
-                const uint32_t bytes = 2u * (kW + kScW + half * 128 + nsc * 1024);
+                const uint32_t bytes = 2u * (16384 + 1024 + half * 128 + nsc * 1024);
                 const int wb = ti.g * ((args.N + 127) >> 7) + (wrow >> 7), tb = ti.row0 >> 7;
-                Ring ring(n);
-                for (int kb = 0; kb < KB; ++kb, ring.next()) {
-                    if (!mbar_wait(&ctl.empty[ring.stage], ring.phase ^ 1u, abort)) {
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!mbar_wait(&ctl.empty[at.stage], at.phase ^ 1u, abort)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* sW = stages + ring.stage * kMxStageBytes;
-                    uint8_t* sT = sW + kW;
-                    uint8_t* sSW = sT + kT;
-                    uint8_t* sST = sSW + kScW;
-                    const uint32_t bar = full0 + ring.stage * 8;
-                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[ring.stage], bytes);
-                    tma_pair_3d(sW, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
-                    tma_pair_2d(sSW, &tmSW, bar, kb * 256, wb, pol_w);
+                    uint8_t* p = sg.base + at.stage * sg.bytes;
+                    const uint32_t bar = full0 + at.stage * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at.stage], bytes);
+                    tma_pair_3d(p, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
+                    tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
                     if (half == 128) {
-                        tma_pair_2d(sT, &tmT, bar, kb * 32, trow, pol_t);
+                        tma_pair_2d(p + sg.t, &tmT, bar, kb * 32, trow, pol_t);
                     } else {
                         for (int i = 0; i < half; i += 16)
-                            tma_pair_2d(sT + i * 128, &tmT16, bar, kb * 32, trow + i, pol_t);
+                            tma_pair_2d(p + sg.t + i * 128, &tmT16, bar, kb * 32, trow + i, pol_t);
                     }
-                    tma_pair_2d(sST, &tmST, bar, kb * 256, tb, pol_t);
-                    if (nsc == 2) tma_pair_2d(sST + 1024, &tmST, bar, kb * 256, tb + 1, pol_t);
-                    done = n + kb + 1;
+                    tma_pair_2d(p + sg.st, &tmST, bar, kb * 256, tb, pol_t);
+                    if (nsc == 2) tma_pair_2d(p + sg.st + 1024, &tmST, bar, kb * 256, tb + 1, pol_t);
+                    issued = min(issued + 1, sg.n);
+                    at.next(sg.n);
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -346,22 +434,26 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 *abort = 1;
             }
             if (rank == 0)  // both CTAs' copies in flight land before either exits
-                for (uint32_t i = done > kMxStages ? done - kMxStages : 0; i < done; ++i) {
-                    const Ring r(i);
-                    mbar_wait(&ctl.full[r.stage], r.phase, &ctl.zero);
+                for (; issued > 0; --issued) {
+                    if (--at.stage < 0) {
+                        at.stage = sg.n - 1;
+                        at.phase ^= 1u;
+                    }
+                    mbar_wait(&ctl.full[at.stage], at.phase, &ctl.zero);
                 }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            const uint32_t s0 = smem_u32(stages);
-            const uint64_t w0 = sdesc_sw128(s0), t0 = sdesc_sw128(s0 + kW);
-            const uint64_t cw0 = sdesc_sf(s0 + kW + kT), ct0 = sdesc_sf(s0 + kW + kT + kScW);
-            int it = 0, g = 0, prev_nt = 0;
-            uint32_t n = 0;  // k-stages of the earlier tiles
+            const uint32_t s0 = smem_u32(sg.base);
+            const uint64_t w0 = sdesc_sw128(s0), t0 = sdesc_sw128(s0 + sg.t);
+            const uint64_t cw0 = sdesc_sf(s0 + sg.sw), ct0 = sdesc_sf(s0 + sg.st);
+            int it = 0, prev_nt = 0;
+            uint32_t slot = 0;
+            Place at;  // (the elected lane's)
             bool ok = true;
-            for (int t = pair; t < ntiles && ok; t += npairs, ++it, n += KB) {
-                const Tile ti = find_tile(gs, t, g);
+            for (int t = pair; t < ntiles && ok; t += npairs, ++it) {
+                const Tile ti = find_tile(gs, t);
                 if (elect_one()) {
                     const int buf = it & 1;
                     // the accumulator's last user has been read out; so has the previous tile's
@@ -373,14 +465,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                     const uint32_t d_t = buf ? kAccEnd - ti.nt : 0;
                     const uint32_t idesc = idesc_mxf4(256, ti.nt), idesc2 = idesc | (2u << 4) | (2u << 29);
                     const bool two = ti.nt > 128;  // row blocks of group-row scales
-                    Ring ring(n);
-                    for (int kb = 0; kb < KB && ok; ++kb, ring.next()) {
-                        ok = mbar_wait(&ctl.full[ring.stage], ring.phase, abort);
+                    for (int kb = 0; kb < KB && ok; ++kb) {
+                        ok = mbar_wait(&ctl.full[at.stage], at.phase, abort);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t o = ring.stage * (kMxStageBytes >> 4);  // descriptor units
+                        const uint32_t o = at.stage * (sg.bytes >> 4);  // descriptor units
                         const uint64_t w = w0 + o, tk = t0 + o, cw = cw0 + o, ct = ct0 + o;
-                        const uint32_t sc = kAccEnd + ((n + kb) & 1u) * 32;
+                        const uint32_t sc = kAccEnd + slot;
                         const int left = args.K - kb * 256;
                         if (left >= 256) {
                             tc_cp_sf_pair(sc, cw);
@@ -405,7 +496,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                                                  sc + 4 * ka, sc + 8 + 8 * ka, (kb | j) != 0);
                             }
                         }
-                        tc_commit_pair(&ctl.empty[ring.stage], 3);
+                        tc_commit_pair(&ctl.empty[at.stage], 3);
+                        slot ^= 32u;
+                        at.next(sg.n);
                     }
                     if (ok) tc_commit_pair(&ctl.acc_full[buf], 3);
                 }
@@ -424,10 +517,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
     } else {
         const int q = warp & 3, h = (warp - 2) >> 2;  // TMEM lane quarter; which 32-row chunks
-        T* stage = reinterpret_cast<T*>(staging) + (warp - 2) * 32 * 32;
-        int it = 0, g = 0;
+        uint8_t* stage = staging + (warp - 2) * 32 * mx_epi_pitch((int)sizeof(T));
+        int it = 0;
         for (int t = pair; t < ntiles; t += npairs, ++it) {
-            const Tile ti = find_tile(gs, t, g);
+            const Tile ti = find_tile(gs, t);
             const int buf = it & 1;
             if (!warp_wait(&ctl.acc_full[buf], (it >> 1) & 1, abort)) {
                 if (lane == 0) {
@@ -442,18 +535,19 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             uint32_t r[4][32];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (h + 2 * i < nch) tmem_ld32(acc + 32 * (h + 2 * i), r[i]);
+                if (h + 2 * i < nch) load_chunk<T>(acc + 32 * (h + 2 * i), r[i]);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(&ctl.acc_empty[buf], 0);
             const int n0 = ti.n0 + (int)rank * 128 + 32 * q;
             if (n0 < args.N) {
+                T* out = static_cast<T*>(args.out) + (int64_t)ti.row0 * args.out_stride;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = 32 * (h + 2 * i);
                     if (c < ti.nt)
-                        store_chunk<T>(args, r[i], stage, (int64_t)ti.row0 + c, ti.rows - c, n0, lane);
+                        store_chunk<T>(args, r[i], stage, out + c * args.out_stride, ti.rows - c, n0, lane);
                 }
             }
         }

@@ -422,12 +422,19 @@ struct MxGemmArgs {
 constexpr int kMxTileRows = 256;     // group rows per tile at most
 constexpr int kMxEpiWarps = 8;
 constexpr int kMxThreads = (2 + kMxEpiWarps) * 32;
-constexpr int kMxStages = 5;
-constexpr int kMxStageBytes = 16384 + 16384 + 1024 + 2048;
+// stages of weight rows 16 KB, group rows 16 KB (small: 4 KB), weight scales 1 KB, group-row scales
+// 2 KB (small: 1 KB)
+constexpr int kMxStages = 5, kMxStageBytes = 16384 + 16384 + 1024 + 2048;
+constexpr int kMxMaxStages = 8, kMxSmallStageBytes = 16384 + 4096 + 1024 + 1024;
+constexpr int kMxRingBytes = kMxMaxStages * kMxSmallStageBytes;
+static_assert(kMxStages * kMxStageBytes <= kMxRingBytes, "both geometries fit the ring");
 constexpr int kMxCtlBytes = 256;
+// bytes of a staged output row of 32 elements: 16-bit types padded so that the rows of an 8 x 8
+// matrix fall into different banks
+__host__ __device__ constexpr int mx_epi_pitch(int out_bytes) { return out_bytes == 2 ? 80 : 128; }
 inline int gemm_mxfp4_smem(int G, int out_bytes)
 {
-    return 1024 + kMxStages * kMxStageBytes + kMxEpiWarps * 32 * 32 * out_bytes + kMxCtlBytes +
+    return 1024 + kMxRingBytes + kMxEpiWarps * 32 * mx_epi_pitch(out_bytes) + kMxCtlBytes +
            4 * (3 * G + 1);
 }
 using MxGemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
