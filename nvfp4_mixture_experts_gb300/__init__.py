@@ -313,6 +313,13 @@ def _need(ok, where):
         raise MoEError(MOE_ERR_INVALID, where)
 
 
+def _sf_bytes(batch, rows, blocks, sf_layout):
+    """moe_mxfp4_scale_bytes for `blocks` scales a row (the calls below check sizes often)."""
+    if sf_layout == MOE_SF_TILED:
+        return batch * ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512
+    return batch * rows * blocks
+
+
 def _rows_ok(t, H):
     """Token rows [T][H]: the elements of a row contiguous, rows at any stride."""
     return t.dim() == 2 and t.shape[1] == H and (H == 1 or t.stride(1) == 1)
@@ -332,14 +339,16 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
     _need(topk_ids.is_contiguous() and topk_ids.element_size() == 4 and inv.numel() == T * k and
           counts.numel() == num_local and offsets.numel() == num_local + 1 and
           (x is None) == (rows is None), "moe_dispatch")
-    H, xs, dt = 1, 1, MOE_BF16
+    H, stride, dt = 1, (1, 1), MOE_BF16
     if x is not None:
-        H, xs, dt = x.shape[1], x.stride(0), _dtype(x)
-        _need(x.shape[0] == T and _rows_ok(x, H) and dt == _dtype(rows) and
+        Tx, H = x.shape
+        stride, dt = x.stride(), _dtype(x)
+        _need(Tx == T and (H == 1 or stride[1] == 1) and dt == _dtype(rows) and
               rows.shape == (cap, H) and rows.is_contiguous(), "moe_dispatch")
-    _check(load().moe_dispatch(_p(x), dt, xs, _p(topk_ids), T, k, H, num_experts, local_off,
-                               num_local, row_align, cap, _p(counts), _p(offsets), _p(perm_src),
-                               _p(inv), _p(rows), _p(status), _stream(stream)), "moe_dispatch")
+    _check(load().moe_dispatch(_p(x), dt, stride[0], topk_ids.data_ptr(), T, k, H, num_experts,
+                               local_off, num_local, row_align, cap, counts.data_ptr(),
+                               offsets.data_ptr(), perm_src.data_ptr(), inv.data_ptr(), _p(rows),
+                               _p(status), _stream(stream)), "moe_dispatch")
 
 
 def moe_dispatch_backward(drows, inv, k, dx, stream=None):
@@ -393,20 +402,22 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
                     perm_src=None, values=None, stream=None):
     """x [rows, cols] or [batch, rows, cols] (columns contiguous); codes uint8, sf uint8 and values
     (x's type) hold the MXFP4 matrix, or with transpose that of each matrix's transpose."""
-    B = x.shape[0] if x.dim() == 3 else 1
-    R, Cc = x.shape[-2:]
-    n = B * R * Cc
-    _need(x.dim() in (2, 3) and (Cc == 1 or x.stride(-1) == 1) and codes.numel() * 2 == n and
-          codes.is_contiguous() and
-          sf.numel() == moe_mxfp4_scale_bytes(B, *((Cc, R) if transpose else (R, Cc)),
-                                              sf_layout) and sf.is_contiguous() and
+    shape, stride = x.shape, x.stride()
+    _need(len(shape) in (2, 3), "moe_quant_mxfp4")
+    B, bs = (shape[0], stride[0]) if len(shape) == 3 else (1, 0)
+    R, Cc = shape[-2], shape[-1]
+    n, dt = B * R * Cc, _dtype(x)
+    _need((Cc == 1 or stride[-1] == 1) and codes.numel() * 2 == n and codes.is_contiguous() and
+          sf.is_contiguous() and
+          sf.numel() == (_sf_bytes(B, Cc, R >> 5, sf_layout) if transpose else
+                         _sf_bytes(B, R, Cc >> 5, sf_layout)) and
           (perm_src is None or (perm_src.numel() == R and perm_src.element_size() == 4)) and
           (values is None or (values.numel() == n and values.is_contiguous() and
-                              _dtype(values) == _dtype(x))), "moe_quant_mxfp4")
-    _check(load().moe_quant_mxfp4(_p(x), _dtype(x), B, R, Cc, x.stride(-2),
-                                  x.stride(0) if x.dim() == 3 else 0, int(bool(transpose)),
-                                  scale_rule, _p(perm_src), _p(codes), _p(sf), sf_layout,
-                                  _p(values), _stream(stream)), "moe_quant_mxfp4")
+                              _dtype(values) == dt)), "moe_quant_mxfp4")
+    _check(load().moe_quant_mxfp4(x.data_ptr(), dt, B, R, Cc, stride[-2], bs,
+                                  1 if transpose else 0, scale_rule, _p(perm_src),
+                                  codes.data_ptr(), sf.data_ptr(), sf_layout, _p(values),
+                                  _stream(stream)), "moe_quant_mxfp4")
 
 
 def moe_mxfp4_tile_scales(sf, batch, rows, cols, sf_tiled, stream=None):
@@ -425,17 +436,20 @@ def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, w
                            status=None, stream=None):
     """a_codes [rows_cap, K/2], w_codes [num_groups, N, K/2] (uint8) with tiled scales; counts and
     offsets int32 (both None: one group, all rows); out [rows_cap, N]."""
-    (G, N, K2), cap = w_codes.shape, a_codes.shape[0]
-    _need(a_codes.shape[1] == K2 and a_codes.is_contiguous() and w_codes.is_contiguous() and
+    G, N, K2 = w_codes.shape
+    cap, Ka = a_codes.shape
+    stride = out.stride()
+    _need(Ka == K2 and a_codes.is_contiguous() and w_codes.is_contiguous() and
           a_codes.element_size() == 1 and w_codes.element_size() == 1 and
-          a_sf.numel() == moe_mxfp4_scale_bytes(1, cap, 2 * K2, MOE_SF_TILED) and
-          w_sf.numel() == moe_mxfp4_scale_bytes(G, N, 2 * K2, MOE_SF_TILED) and
-          out.shape[0] == cap and _rows_ok(out, N) and (counts is None) == (offsets is None) and
+          a_sf.numel() == _sf_bytes(1, cap, K2 >> 4, MOE_SF_TILED) and
+          w_sf.numel() == _sf_bytes(G, N, K2 >> 4, MOE_SF_TILED) and
+          out.shape == (cap, N) and (N == 1 or stride[1] == 1) and
+          (counts is None) == (offsets is None) and
           (counts is None or (counts.numel() == G and offsets.numel() >= G)),
           "moe_grouped_gemm_mxfp4")
     _check(load().moe_grouped_gemm_mxfp4(
-        _p(a_codes), _p(a_sf), cap, _p(counts), _p(offsets), G, _p(w_codes), _p(w_sf), N, 2 * K2,
-        _p(out), _dtype(out), out.stride(0), _p(ws),
+        a_codes.data_ptr(), a_sf.data_ptr(), cap, _p(counts), _p(offsets), G, w_codes.data_ptr(),
+        w_sf.data_ptr(), N, 2 * K2, out.data_ptr(), _dtype(out), stride[0], _p(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream(stream)),
         "moe_grouped_gemm_mxfp4")
 

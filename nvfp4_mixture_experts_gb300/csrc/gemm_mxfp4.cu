@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     __syncwarp();
     if (warp == 1) tmem_alloc_pair(&ctl.tmem, 512);
     tc_fence_before();
+    const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
     cluster_arrive();  // this CTA's barriers exist and its TMEM is allocated
     pdl_wait();
     pdl_trigger();
@@ -391,7 +392,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     volatile int* abort = &ctl.abort_flag;
 
     if (warp == 0) {
-        const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
         const uint32_t full0 = cluster_addr(&ctl.full[0], 0);  // the leader's barriers
         Place at;               // (the elected lane's)
         int issued = 0;         // stages with a copy of this CTA, the last one before `at`
