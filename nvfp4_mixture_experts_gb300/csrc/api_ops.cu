@@ -274,6 +274,7 @@ moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_
     const bool vec = rows_vec(x_d, (int64_t)cols * es, rows > 1 ? row_stride * es : 0) &&
                      (batch == 1 || batch_stride * es % 16 == 0);
     const int64_t items = (int64_t)batch * rows * ceil_div(cols / 8, kMxQuantRun);
+    if (items > 0xffffffffll) return MOE_ERR_UNSUPPORTED;
     return launch(mx_quant_kernel_for(dtype, vec), dim3(blocks_for(items, 8, 16)), dim3(256), 0, s,
                   true, a);
 }

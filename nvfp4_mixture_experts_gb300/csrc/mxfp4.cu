@@ -2,6 +2,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kernels.cuh"
 
 namespace moe {
@@ -15,6 +17,105 @@ __device__ __forceinline__ void set_elem(__nv_bfloat16& d, float v) { d = __floa
 __device__ __forceinline__ void set_elem(__half& d, float v) { d = __float2half_rn(v); }
 __device__ __forceinline__ void set_elem(float& d, float v) { d = v; }
 
+// Eight elements of a row as raw words.
+template <typename T>
+struct Eight {
+    static constexpr int kWords = 2 * (int)sizeof(T);
+    uint32_t w[kWords];
+
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T* x)
+    {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int q = 0; q < kWords / 4; ++q) {
+                const uint4 v = reinterpret_cast<const uint4*>(x)[q];
+                w[4 * q] = v.x;
+                w[4 * q + 1] = v.y;
+                w[4 * q + 2] = v.z;
+                w[4 * q + 3] = v.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] = reinterpret_cast<const uint32_t*>(x)[q];
+        } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(x);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = h[2 * q] | (uint32_t)h[2 * q + 1] << 16;
+        }
+    }
+    // bits (as fp32) of the largest magnitude over the eights of four neighbouring lanes; 16-bit
+    // types compare two magnitudes at a time (their bits are ordered as they are)
+    __device__ __forceinline__ uint32_t amax4() const
+    {
+        uint32_t m = 0;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = max(m, w[q] & 0x7FFFFFFFu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = max_u16x2(m, w[q] & 0x7FFF7FFFu);
+            m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = max(m & 0xFFFFu, m >> 16);
+            if constexpr (std::is_same<T, __half>::value)
+                return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+            else return m << 16;
+        }
+    }
+    __device__ __forceinline__ void to_f32(float (&v)[8]) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(w[q]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (std::is_same<T, __half>::value) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
+                    v[2 * q] = f.x;
+                    v[2 * q + 1] = f.y;
+                } else {
+                    v[2 * q] = __uint_as_float(w[q] << 16);
+                    v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void from_f32(const float (&v)[8])
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(v[q]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (std::is_same<T, __half>::value) {
+                    const __half2 h = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
+                    w[q] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+                    w[q] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T* x) const  // 16-byte aligned
+    {
+#pragma unroll
+        for (int q = 0; q < kWords / 4; ++q)
+            reinterpret_cast<uint4*>(x)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
+    static __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+    {
+        uint32_t r;
+        asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+};
+
 // The scale byte of a block from the bits of its largest magnitude (the magnitudes' bits are
 // ordered as the magnitudes are, infinities and NaNs above every number): exponent field - 2, one
 // more under the ceil rule when the significand passes 1.5 (m = 1.5 * 2^(e+2) is 6 * 2^e), at
@@ -27,7 +128,8 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits, int rule)
     return (uint32_t)max(b, 0);
 }
 
-// 2^(127 - s): what elements of a block with scale byte s (0..253) are multiplied by.
+// 2^(127 - s): what elements of a block with scale byte s (0..253) are multiplied by (255: any
+// number; its codes are not used).
 __device__ __forceinline__ float mx_encode_scale(uint32_t s)
 {
     return __uint_as_float((254u - s) << 23);
@@ -90,70 +192,79 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
     const int lane = threadIdx.x & 31;
     const int units = a.cols >> 3;  // eights per row, a multiple of 4
     const int runs = (units + kMxQuantRun - 1) / kMxQuantRun;
-    const int64_t items = (int64_t)a.batch * a.rows * runs;
-    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < items; i += step) {
-        const int64_t row = i / runs;
-        const int u0 = (int)(i - row * runs) * kMxQuantRun + lane;
-        const int64_t b = a.batch == 1 ? 0 : row / a.rows;
-        const int r = (int)(row - b * a.rows);
-        if (a.perm_src && a.perm_src[r] < 0) continue;
-        const T* x = static_cast<const T*>(a.x) + b * a.batch_stride + r * a.row_stride;
-        alignas(16) T e[kPer][8];
+    const uint32_t items = (uint32_t)a.batch * a.rows * runs;  // (fits: checked by the caller)
+    const uint32_t step = gridDim.x * (blockDim.x >> 5);
+    const int blocks = units >> 2, RB = (a.rows + 127) >> 7, KA = (blocks + 3) >> 2;
+    struct Item {
+        uint32_t row;   // of all matrices
+        int b, r, u0;   // matrix, row in it, this lane's first eight
+        bool live;
+    };
+    // item i of the warp, and its elements; the next item's are loaded ahead of this one's work
+    auto fetch = [&](uint32_t i, Item& it, Eight<T>(&e)[kPer]) {
+        it.live = false;
+        if (i >= items) return;
+        it.row = i / (uint32_t)runs;
+        it.u0 = (int)(i - it.row * runs) * kMxQuantRun + lane;
+        it.b = a.batch == 1 ? 0 : (int)(it.row / (uint32_t)a.rows);
+        it.r = (int)(it.row - (uint32_t)it.b * a.rows);
+        it.live = !(a.perm_src && a.perm_src[it.r] < 0);
+        if (!it.live) return;
+        const T* x = static_cast<const T*>(a.x) + it.b * a.batch_stride + it.r * a.row_stride + it.u0 * 8;
+#pragma unroll
+        for (int p = 0; p < kPer; ++p)
+            if (it.u0 + 32 * p < units) e[p].template load<VEC>(x + 256 * p);
+    };
+    uint32_t i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    Item next;
+    Eight<T> ahead[kPer] = {};
+    fetch(i, next, ahead);
+    for (; i < items; i += step) {
+        const Item it = next;
+        Eight<T> e[kPer];
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) e[p] = ahead[p];
+        if (items - i > step) fetch(i + step, next, ahead);
+        if (!it.live) continue;
+        const int64_t at = (int64_t)it.row * units + it.u0;
+        uint32_t* codes_at = reinterpret_cast<uint32_t*>(a.codes) + at;
+        T* values_at = static_cast<T*>(a.values) + at * 8;
+        // the scale word of this lane's first block's atom (tiled), or its scale byte
+        const int kb = it.u0 >> 2;
+        uint8_t* sf_at = a.sf + (a.layout == MOE_SF_TILED ? mx_sf_tiled(it.b, RB, KA, it.r, kb)
+                                                          : (size_t)it.row * blocks + kb);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
-            const int u = u0 + 32 * p;
-            if (u < units) {
-                if constexpr (VEC) {
-#pragma unroll
-                    for (int q = 0; q < (int)sizeof(T) / 2; ++q)
-                        reinterpret_cast<uint4*>(e[p])[q] = reinterpret_cast<const uint4*>(x + (int64_t)u * 8)[q];
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) e[p][q] = x[(int64_t)u * 8 + q];
-                }
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-            const int u = u0 + 32 * p;
+            const int u = it.u0 + 32 * p;
             if (u - lane >= units) break;
-            const bool in = u < units;
-            float v[8];
-            uint32_t m = 0;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                v[q] = in ? elem_f32(e[p][q]) : 0.0f;
-                m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
-            }
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const uint32_t s = mx_scale_byte(m, a.rule);
+            const bool in = u < units;  // (a block's four lanes are in or out together)
+            const uint32_t s = mx_scale_byte(e[p].amax4(), a.rule);
             // the scales of four blocks (16 lanes) in one word
             uint32_t word = in ? s << (8 * ((lane >> 2) & 3)) : 0u;
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
             word |= __shfl_xor_sync(0xffffffffu, word, 8);
             if (!in) continue;
-            uint32_t codes = 0;
-            if (s != 255u) {
-                const float scale = mx_encode_scale(s);
+            float v[8];
+            e[p].to_f32(v);
+            const float scale = mx_encode_scale(s);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] *= scale;
-                codes = f32x8_to_e2m1(v);
+            for (int q = 0; q < 8; ++q) v[q] *= scale;
+            const uint32_t codes = s == 255u ? 0u : f32x8_to_e2m1(v);
+            codes_at[32 * p] = codes;
+            // 8 blocks, two atoms, per 32 eights; the bytes past the row's blocks are zero
+            if (a.layout == MOE_SF_TILED) {
+                if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(sf_at + 1024 * p) = word;
+            } else if ((lane & 3) == 0) {
+                sf_at[8 * p] = (uint8_t)s;
             }
-            const int64_t at = row * units + u;
-            reinterpret_cast<uint32_t*>(a.codes)[at] = codes;
-            if ((lane & 15) == 0) store_scales(a.sf, a.layout, b, a.rows, r, units >> 2, u >> 2, word);
             if (a.values) {
                 const float d = mx_decode_scale(s);
                 e2m1x8_to_f32(codes, v);
-                alignas(16) T o[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) set_elem(o[q], v[q] * d);
-#pragma unroll
-                for (int q = 0; q < (int)sizeof(T) / 2; ++q)
-                    reinterpret_cast<uint4*>(static_cast<T*>(a.values) + at * 8)[q] =
-                        reinterpret_cast<const uint4*>(o)[q];
+                for (int q = 0; q < 8; ++q) v[q] *= d;
+                Eight<T> o;
+                o.from_f32(v);
+                o.store(values_at + 256 * p);
             }
         }
     }
