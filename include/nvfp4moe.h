@@ -512,8 +512,8 @@ MOE_API moe_status moe_mxfp4_tile_scales(const uint8_t* sf_d, int32_t batch, int
                                          int32_t cols, uint8_t* sf_tiled_d,
                                          moe_stream_t stream);
 
-/* Bytes of workspace with which moe_grouped_gemm_mxfp4 may split the contraction of a product
- * of these sizes (at most 32 MiB; 0 for arguments out of range).
+/* Bytes of workspace that moe_grouped_gemm_mxfp4 needs for these sizes: 0, whatever they are (no
+ * product is split along its contraction, see the kernel), and never more than 32 MiB.
  * Passage: none; workspace sizing of this library (the pages have no counterpart). */
 MOE_API size_t moe_mxfp4_workspace_size(int32_t rows_cap, int32_t num_groups, int32_t N,
                                         int32_t K);
@@ -528,9 +528,8 @@ MOE_API size_t moe_mxfp4_workspace_size(int32_t rows_cap, int32_t num_groups, in
  * effect.  The gradient with respect to A is the same product of the output's gradient with
  * the transposed matrices (moe_quant_mxfp4, transpose 1).
  * K a multiple of 32; num_groups 1..1024; codes 16-byte aligned, scales 16-byte aligned.
- * ws_d (nullable, 256-byte aligned): lets products with few rows split their contraction over
- * more of the GPU; the parts are added in a fixed order.  It must not be used by another call
- * that may run at the same time.
+ * ws_d, ws_bytes: at least moe_mxfp4_workspace_size bytes, 256-byte aligned; NULL where that is
+ * 0.  It must not be used by another call that may run at the same time.
  * Passage: [CK] and [EP] (the grouped FP4 products of the local experts); the MX block form is
  * an addition of this library. */
 MOE_API moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_d,

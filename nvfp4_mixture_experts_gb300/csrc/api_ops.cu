@@ -295,9 +295,8 @@ moe_status moe_mxfp4_tile_scales(const uint8_t* sf_d, int32_t batch, int32_t row
 
 size_t moe_mxfp4_workspace_size(int32_t rows_cap, int32_t num_groups, int32_t N, int32_t K)
 {
-    if (rows_cap < 0 || num_groups < 1 || num_groups > kMaxExperts || N < 1 || K < 32 || K % 32)
-        return 0;
-    return 32u << 20;
+    (void)rows_cap, (void)num_groups, (void)N, (void)K;
+    return 0;
 }
 
 moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_d,

@@ -17,6 +17,11 @@
 // for the MMAs, transpose it through shared memory and store 64-byte (16-bit types) or 128-byte
 // (fp32) pieces of the output rows.
 //
+// No tile is split along its contraction, also where there are fewer tiles than pairs: a k-stage
+// of a lone tile takes some 220 cycles (its loads' latency over eight stages in flight), so 16 of
+// them cost less than 2 us, about what writing, counting and adding up parts would; one token's
+// gate_up (80 tiles, 45 MB of weights) is bound by memory already.
+//
 // TMEM (all 512 columns, so the allocation starts at column 0): two accumulators, of the even tiles at column 0 upwards, of the odd tiles
 // ending at column 448; two slots of a stage's scales in columns 448..511.  Two tiles of together
 // up to 448 columns overlap freely: the next tile's MMAs run while one is read out.
