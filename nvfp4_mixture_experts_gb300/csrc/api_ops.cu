@@ -17,6 +17,14 @@ bool dtype_ok(int dtype) { return dtype == MOE_BF16 || dtype == MOE_FP16 || dtyp
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Whether an address is a multiple of an element's size (null: yes).
+bool elem_aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// The largest power of two up to 16 that divides addresses, row sizes and strides (or-ed together).
+int largest_unit(uint64_t ored) { return (int)((ored | 16) & (~(ored | 16) + 1)); }
+
+uint64_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
 // Whether a tensor of rows can be moved in 16-byte pieces.
 bool rows_vec(const void* p, int64_t row_bytes, int64_t stride_bytes)
 {
@@ -41,7 +49,7 @@ unsigned blocks_for(int64_t work, int per_block, int per_sm)
 moe_status check_rows(int dtype, int T, int k, int H, int rows_cap)
 {
     if (!dtype_ok(dtype) || T < 0 || k < 1 || H < 1 || rows_cap < 0) return MOE_ERR_INVALID;
-    if (k > kMaxTopK || (int64_t)T * k > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+    if (k > kMaxTopK || (int64_t)T * k > 0x7fffffff || H > (1 << 28)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -64,10 +72,12 @@ moe_status combine_rows(const void* y_d, int32_t dtype, const int32_t* inv_d, co
     const moe_status st = check_rows(dtype, T, k, H, rows_cap);
     if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
-    if (!inv_d || !out_d || (rows_cap && !y_d) || (T > 1 && out_stride < H))
-        return MOE_ERR_INVALID;
     const int es = elem_bytes(dtype);
-    const bool vec = rows_vec(out_d, (int64_t)H * es, T > 1 ? out_stride * es : 0) && aligned16(y_d);
+    if (!inv_d || !out_d || (rows_cap && !y_d) || (T > 1 && out_stride < H) ||
+        !elem_aligned(y_d, es) || !elem_aligned(out_d, es))
+        return MOE_ERR_INVALID;
+    const int unit = largest_unit(addr(y_d) | addr(out_d) | (uint64_t)H * es |
+                                  (T > 1 ? (uint64_t)out_stride * es : 0));
     CombineArgs a = {};
     a.y = y_d;
     a.inv = inv_d;
@@ -78,9 +88,8 @@ moe_status combine_rows(const void* y_d, int32_t dtype, const int32_t* inv_d, co
     a.rows_cap = rows_cap;
     a.out = out_d;
     a.out_stride = out_stride;
-    const int units = vec ? (int)((int64_t)H * es / 16) : H;
-    const int64_t items = (int64_t)T * ceil_div(units, kCombineRun);
-    return launch(combine_rows_kernel_for(dtype, vec), dim3(blocks_for(items, 8, 16)), dim3(256), 0,
+    const int64_t items = (int64_t)T * ceil_div((int)((int64_t)H * es / unit), combine_run(unit));
+    return launch(combine_rows_kernel_for(dtype, unit), dim3(blocks_for(items, 8, 16)), dim3(256), 0,
                   reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
@@ -116,6 +125,8 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
     if (!offsets_d || (num_local && !counts_d) || (T && (!topk_ids_d || !inv_d)) ||
         (rows_cap && !perm_src_d))
         return MOE_ERR_INVALID;
+    if (x_d && (!elem_aligned(x_d, elem_bytes(dtype)) || !elem_aligned(rows_d, elem_bytes(dtype))))
+        return MOE_ERR_INVALID;
     const int64_t P = (int64_t)T * k;
     if (num_experts > kMaxExperts || P + (int64_t)num_local * (row_align - 1) > 0x7fffffff)
         return MOE_ERR_UNSUPPORTED;
@@ -138,7 +149,7 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
     int unit = 16;
     if (x_d) {
         const int es = elem_bytes(dtype);
-        if (!rows_vec(x_d, (int64_t)H * es, T > 1 ? x_stride * es : 0) || !aligned16(rows_d)) unit = es;
+        unit = largest_unit(addr(x_d) | addr(rows_d) | (uint64_t)H * es | (T > 1 ? (uint64_t)x_stride * es : 0));
         d.x = x_d;
         d.x_stride = x_stride * es / unit;
         d.inv = inv_d;
@@ -199,8 +210,10 @@ moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_
         (T > 1 && dout_stride < H))
         return MOE_ERR_INVALID;
     const int es = elem_bytes(dtype);
-    const bool vec = rows_vec(dout_d, (int64_t)H * es, T > 1 ? dout_stride * es : 0) &&
-                     (!dw_d || aligned16(y_d)) && (!dy_d || aligned16(dy_d));
+    if (!elem_aligned(dout_d, es) || !elem_aligned(y_d, es) || !elem_aligned(dy_d, es))
+        return MOE_ERR_INVALID;
+    const int unit = largest_unit(addr(dout_d) | (dw_d ? addr(y_d) : 0) | addr(dy_d) | (uint64_t)H * es |
+                                  (T > 1 ? (uint64_t)dout_stride * es : 0));
     CombineBackArgs a = {};
     a.dout = dout_d;
     a.dout_stride = dout_stride;
@@ -219,7 +232,7 @@ moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_
     // 76; 777 tokens x 1001 fp16: 10.3, 8.4, 9.4; 64 tokens x 4096: 6.7, 4.7, 3.8.
     int warps = 2;
     while (warps < 8 && (int64_t)T * warps < 16 * num_sms()) warps *= 2;
-    return launch(combine_back_kernel_for(dtype, vec, warps), dim3(blocks_for(T, 1, 64 / warps)),
+    return launch(combine_back_kernel_for(dtype, unit, warps), dim3(blocks_for(T, 1, 64 / warps)),
                   dim3(32 * warps), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
@@ -250,7 +263,9 @@ moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_
     if (!x_d || !codes_d || !sf_d || (rows > 1 && row_stride < cols) ||
         (batch > 1 && batch_stride < 0))
         return MOE_ERR_INVALID;
-    if (!aligned16(codes_d) || (values_d && !aligned16(values_d))) return MOE_ERR_INVALID;
+    if (!aligned16(codes_d) || (values_d && !aligned16(values_d)) ||
+        (sf_layout == MOE_SF_TILED && !aligned16(sf_d)) || !elem_aligned(x_d, elem_bytes(dtype)))
+        return MOE_ERR_INVALID;
     MxQuantArgs a = {};
     a.x = x_d;
     a.row_stride = row_stride;

@@ -12,61 +12,79 @@ namespace moe {
 
 // ------------------------------------------------------------------ element types
 
-// A piece of a row of elements of type T: 16 bytes (V elements, held as a uint4) where the rows
-// allow it, else one element (V = 1).  fp32 values in, fp32 values out; rounding to nearest even.
+// A piece of a row: V elements of type T in one access of B = V sizeof(T) bytes (16, 8, 4 or 2), the
+// largest that every row of the call's tensors is aligned to.  fp32 values in, fp32 values out;
+// rounding to nearest even.  (Rows of 4001 16-bit elements, aligned to nothing more, take 146 us
+// in combine where 4004, aligned to 8 bytes, take 92; reading 16-byte blocks around every piece and
+// shifting them into place was measured at 167, and at 600 against 239 in combine's gradient:
+// the blocks' registers cost more loads in flight than they save instructions.)
+template <int B>
+struct Word;
+template <>
+struct Word<16> { using type = uint4; };
+template <>
+struct Word<8> { using type = uint2; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<2> { using type = uint16_t; };
+
 template <typename T, int V>
 struct Piece {
-    uint4 raw;
-    __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = raw; }
+    typename Word<V * (int)sizeof(T)>::type raw;
+    using W = decltype(raw);
+    __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const W*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<W*>(p) = raw; }
     __device__ __forceinline__ void unpack(float (&f)[V]) const
     {
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        if constexpr (V == 1) {
+            T e;
+            *reinterpret_cast<W*>(&e) = raw;
+            f[0] = (float)e;
+        } else {
+            constexpr int N = V * (int)sizeof(T) / 4;
+            alignas(16) uint32_t w[N];
+            *reinterpret_cast<W*>(w) = raw;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (V == 4) {
-                f[i] = __uint_as_float(w[i]);
-            } else if constexpr (kIsHalf) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                f[2 * i] = v.x;
-                f[2 * i + 1] = v.y;
-            } else {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            for (int i = 0; i < N; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    f[i] = __uint_as_float(w[i]);
+                } else if constexpr (std::is_same<T, __half>::value) {
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                    f[2 * i] = v.x;
+                    f[2 * i + 1] = v.y;
+                } else {
+                    f[2 * i] = __uint_as_float(w[i] << 16);
+                    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                }
             }
         }
     }
     __device__ __forceinline__ void pack(const float (&f)[V])
     {
-        uint32_t w[4];
+        if constexpr (V == 1) {
+            T e;
+            if constexpr (std::is_same<T, __half>::value) e = __float2half_rn(f[0]);
+            else if constexpr (std::is_same<T, float>::value) e = f[0];
+            else e = __float2bfloat16_rn(f[0]);
+            raw = *reinterpret_cast<const W*>(&e);
+        } else {
+            constexpr int N = V * (int)sizeof(T) / 4;
+            alignas(16) uint32_t w[N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (V == 4) {
-                w[i] = __float_as_uint(f[i]);
-            } else if constexpr (kIsHalf) {
-                const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            } else {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int i = 0; i < N; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = __float_as_uint(f[i]);
+                } else if constexpr (std::is_same<T, __half>::value) {
+                    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
             }
+            raw = *reinterpret_cast<const W*>(w);
         }
-        raw = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    static constexpr bool kIsHalf = std::is_same<T, __half>::value;
-};
-
-template <typename T>
-struct Piece<T, 1> {
-    T raw;
-    __device__ __forceinline__ void load(const T* p) { raw = *p; }
-    __device__ __forceinline__ void store(T* p) const { *p = raw; }
-    __device__ __forceinline__ void unpack(float (&f)[1]) const { f[0] = (float)raw; }
-    __device__ __forceinline__ void pack(const float (&f)[1])
-    {
-        if constexpr (std::is_same<T, __half>::value) raw = __float2half_rn(f[0]);
-        else if constexpr (std::is_same<T, float>::value) raw = f[0];
-        else raw = __float2bfloat16_rn(f[0]);
     }
 };
 
@@ -74,9 +92,9 @@ struct Piece<T, 1> {
 
 // A stable counting sort.  Every warp that takes part owns a contiguous segment of the pairs and a
 // table of counts by expert in shared memory.  Pass 1 counts the segments (32 pairs at a time: lanes
-// of equal expert found with votes, their first lane adds their number, so no atomics).  Prefix sums over the block's warps, over the blocks and over the experts (group
-// sizes rounded up to row_align) turn the tables into the row of each segment's first pair of each
-// expert.  Pass 2 walks the segments again: a pair's row is its table entry plus the number of
+// of equal expert found with votes, their first lane adds their number, so no atomics).  Prefix sums
+// over the block's warps, over the blocks and over the experts (group sizes rounded up to
+// row_align) turn the tables into the row of each segment's first pair of each expert.  Pass 2 walks the segments again: a pair's row is its table entry plus the number of
 // lower lanes of equal expert, and the first lane moves the entry on.
 //
 // Up to kSmallPairs pairs one block does it alone, in the launch that also moves the rows, every
@@ -335,6 +353,7 @@ DispatchSmallKernel dispatch_small_kernel_for(int unit_bytes)
 {
     switch (unit_bytes) {
         case 16: return dispatch_small_kernel<uint4>;
+        case 8: return dispatch_small_kernel<uint2>;
         case 4: return dispatch_small_kernel<uint32_t>;
         default: return dispatch_small_kernel<uint16_t>;
     }
@@ -358,18 +377,26 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchArgs a)
     for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
          i < (int64_t)a.T * runs; i += warps) {
         const int64_t t = i / runs;
-        const int u0 = (int)(i % runs) * 32 * kRun + lane;
+        const int u0 = (int)(i - t * runs) * 32 * kRun + lane;
+        const U* from = x + t * a.x_stride + u0;
+        const bool full = u0 - lane + 32 * kRun <= a.units;
         U v[kRun];
 #pragma unroll
         for (int r = 0; r < kRun; ++r)
-            if (u0 + 32 * r < a.units) v[r] = x[t * a.x_stride + u0 + 32 * r];
+            if (full || u0 + 32 * r < a.units) v[r] = from[32 * r];
         for (int j = 0; j < a.k; ++j) {
             const int row = a.inv[t * a.k + j];
             if ((uint32_t)row >= (uint32_t)a.rows_cap) continue;
             if (u0 == 0) a.perm_src[row] = (int32_t)(t * a.k + j);
+            U* to = rows + (int64_t)row * a.units + u0;
+            if (full) {
 #pragma unroll
-            for (int r = 0; r < kRun; ++r)
-                if (u0 + 32 * r < a.units) rows[(int64_t)row * a.units + u0 + 32 * r] = v[r];
+                for (int r = 0; r < kRun; ++r) to[32 * r] = v[r];
+            } else {
+#pragma unroll
+                for (int r = 0; r < kRun; ++r)
+                    if (u0 + 32 * r < a.units) to[32 * r] = v[r];
+            }
         }
     }
 }
@@ -378,6 +405,7 @@ DispatchKernel dispatch_rows_kernel_for(int unit_bytes)
 {
     switch (unit_bytes) {
         case 16: return dispatch_rows_kernel<uint4>;
+        case 8: return dispatch_rows_kernel<uint2>;
         case 4: return dispatch_rows_kernel<uint32_t>;
         default: return dispatch_rows_kernel<uint16_t>;
     }
@@ -393,15 +421,16 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    constexpr int kPer = kCombineRun / 32;
+    constexpr int kPer = combine_run(V * (int)sizeof(T)) / 32;
     const int lane = threadIdx.x & 31;
-    const int units = a.H / V, runs = (units + kCombineRun - 1) / kCombineRun;
+    const int units = a.H / V, runs = (units + 32 * kPer - 1) / (32 * kPer);
     const int64_t items = (int64_t)a.T * runs, step = (int64_t)gridDim.x * (blockDim.x >> 5);
     const T* y = static_cast<const T*>(a.y);
     T* out = static_cast<T*>(a.out);
     for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < items; i += step) {
         const int64_t t = i / runs;
-        const int u0 = (int)(i - t * runs) * kCombineRun + lane;
+        const int u0 = (int)(i - t * runs) * 32 * kPer + lane;
+        const bool full = u0 - lane + 32 * kPer <= units;
         int my_row = -1;
         float my_w = 1.0f;
         if (lane < a.k) {
@@ -416,10 +445,15 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
             for (int j = 0; j < 8; ++j) {
                 const int row = __shfl_sync(0xffffffffu, my_row, j0 + j);  // -1 past k
                 if (row >= 0) {
+                    const T* from = y + (int64_t)row * a.H + (int64_t)u0 * V;
+                    if (full) {
 #pragma unroll
-                    for (int q = 0; q < kPer; ++q)
-                        if (u0 + 32 * q < units)
-                            p[j][q].load(y + (int64_t)row * a.H + (int64_t)(u0 + 32 * q) * V);
+                        for (int q = 0; q < kPer; ++q) p[j][q].load(from + 32 * V * q);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < kPer; ++q)
+                            if (u0 + 32 * q < units) p[j][q].load(from + 32 * V * q);
+                    }
                 }
             }
 #pragma unroll
@@ -437,23 +471,34 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
                 }
             }
         }
+        T* to = out + t * a.out_stride + (int64_t)u0 * V;
 #pragma unroll
         for (int q = 0; q < kPer; ++q)
-            if (u0 + 32 * q < units) {
+            if (full || u0 + 32 * q < units) {
                 Piece<T, V> sum;
                 sum.pack(acc[q]);
-                sum.store(out + t * a.out_stride + (int64_t)(u0 + 32 * q) * V);
+                sum.store(to + 32 * V * q);
             }
     }
 }
 
-CombineKernel combine_rows_kernel_for(int dtype, bool vec)
+template <typename T>
+static CombineKernel combine_rows_of(int unit)
+{
+    switch (unit / (int)sizeof(T)) {
+        case 8: if constexpr (sizeof(T) == 2) return combine_rows_kernel<T, 8>;
+        case 4: return combine_rows_kernel<T, 4>;
+        case 2: return combine_rows_kernel<T, 2>;
+        default: return combine_rows_kernel<T, 1>;
+    }
+}
+
+CombineKernel combine_rows_kernel_for(int dtype, int unit)
 {
     switch (dtype) {
-        case MOE_BF16:
-            return vec ? combine_rows_kernel<__nv_bfloat16, 8> : combine_rows_kernel<__nv_bfloat16, 1>;
-        case MOE_FP16: return vec ? combine_rows_kernel<__half, 8> : combine_rows_kernel<__half, 1>;
-        default: return vec ? combine_rows_kernel<float, 4> : combine_rows_kernel<float, 1>;
+        case MOE_BF16: return combine_rows_of<__nv_bfloat16>(unit);
+        case MOE_FP16: return combine_rows_of<__half>(unit);
+        default: return combine_rows_of<float>(unit);
     }
 }
 
@@ -489,32 +534,46 @@ __global__ void __launch_bounds__(32 * W) combine_back_kernel(CombineBackArgs a)
                     }
                 }
             }
-            for (int u = threadIdx.x; u < units; u += 32 * W) {
-                Piece<T, V> pd, p[8];
-                pd.load(dout + t * a.dout_stride + (int64_t)u * V);
+            constexpr int kPer = back_per(V * (int)sizeof(T));  // pieces of a row in flight
+            for (int u0 = threadIdx.x; u0 < units; u0 += 32 * W * kPer) {
+                const bool full = u0 - lane + 32 * W * (kPer - 1) + 31 < units;
+                Piece<T, V> pd[kPer], p[8][kPer];
+                const T* from = dout + t * a.dout_stride + (int64_t)u0 * V;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q)
+                    if (full || u0 + 32 * W * q < units) pd[q].load(from + 32 * W * V * q);
                 if (a.dw) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (row[j] >= 0) p[j].load(y + (int64_t)row[j] * a.H + (int64_t)u * V);
+                        if (row[j] >= 0) {
+                            const T* yr = y + (int64_t)row[j] * a.H + (int64_t)u0 * V;
+#pragma unroll
+                            for (int q = 0; q < kPer; ++q)
+                                if (full || u0 + 32 * W * q < units) p[j][q].load(yr + 32 * W * V * q);
+                        }
                 }
-                float d[V];
-                pd.unpack(d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (row[j] < 0) continue;
-                    if (a.dw) {
-                        float f[V];
-                        p[j].unpack(f);
+                for (int q = 0; q < kPer; ++q) {
+                    if (!full && u0 + 32 * W * q >= units) break;
+                    float d[V];
+                    pd[q].unpack(d);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
-                    }
-                    if (dy) {
-                        float g[V];
+                    for (int j = 0; j < 8; ++j) {
+                        if (row[j] < 0) continue;
+                        if (a.dw) {
+                            float f[V];
+                            p[j][q].unpack(f);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) g[e] = w[j] * d[e];
-                        Piece<T, V> pg;
-                        pg.pack(g);
-                        pg.store(dy + (int64_t)row[j] * a.H + (int64_t)u * V);
+                            for (int e = 0; e < V; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
+                        }
+                        if (dy) {
+                            float g[V];
+#pragma unroll
+                            for (int e = 0; e < V; ++e) g[e] = w[j] * d[e];
+                            Piece<T, V> pg;
+                            pg.pack(g);
+                            pg.store(dy + (int64_t)row[j] * a.H + (int64_t)(u0 + 32 * W * q) * V);
+                        }
                     }
                 }
             }
@@ -548,13 +607,23 @@ static CombineBackKernel combine_back_of(int warps)
     }
 }
 
-CombineBackKernel combine_back_kernel_for(int dtype, bool vec, int warps)
+template <typename T>
+static CombineBackKernel combine_back_unit(int unit, int warps)
+{
+    switch (unit / (int)sizeof(T)) {
+        case 8: if constexpr (sizeof(T) == 2) return combine_back_of<T, 8>(warps);
+        case 4: return combine_back_of<T, 4>(warps);
+        case 2: return combine_back_of<T, 2>(warps);
+        default: return combine_back_of<T, 1>(warps);
+    }
+}
+
+CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps)
 {
     switch (dtype) {
-        case MOE_BF16:
-            return vec ? combine_back_of<__nv_bfloat16, 8>(warps) : combine_back_of<__nv_bfloat16, 1>(warps);
-        case MOE_FP16: return vec ? combine_back_of<__half, 8>(warps) : combine_back_of<__half, 1>(warps);
-        default: return vec ? combine_back_of<float, 4>(warps) : combine_back_of<float, 1>(warps);
+        case MOE_BF16: return combine_back_unit<__nv_bfloat16>(unit, warps);
+        case MOE_FP16: return combine_back_unit<__half>(unit, warps);
+        default: return combine_back_unit<float>(unit, warps);
     }
 }
 

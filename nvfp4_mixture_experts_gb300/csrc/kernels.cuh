@@ -343,7 +343,7 @@ struct DispatchArgs {
     int64_t x_stride;     // in units
     const int32_t* inv;
     int T, k;
-    int units;            // units (16, 4 or 2 bytes) per row
+    int units;            // units (16, 8, 4 or 2 bytes) per row
     int rows_cap;
     int32_t* perm_src;
     void* rows;
@@ -363,11 +363,16 @@ struct CombineArgs {
     void* out;
     int64_t out_stride;   // in elements
 };
-constexpr int kCombineRun = 2 * 32;   // pieces of a token that a warp takes at a time
+// pieces (of `unit` bytes) of a token that a warp takes at a time: 64 registers of eight rows' pieces
+__host__ __device__ constexpr int combine_run(int unit)
+{
+    return 32 * (unit == 16 ? 2 : unit == 8 ? 4 : 8);
+}
 using CombineKernel = void (*)(CombineArgs);
-// vec: every row starts on 16 bytes and is a whole number of 16-byte pieces
-CombineKernel combine_rows_kernel_for(int dtype, bool vec);
+CombineKernel combine_rows_kernel_for(int dtype, int unit);
 
+// pieces of a row that a thread of combine's gradient loads together
+__host__ __device__ constexpr int back_per(int unit) { return unit == 16 ? 1 : unit == 8 ? 2 : 4; }
 struct CombineBackArgs {
     const void* dout;
     int64_t dout_stride;  // in elements
@@ -379,7 +384,7 @@ struct CombineBackArgs {
     float* dw;            // nullable
 };
 using CombineBackKernel = void (*)(CombineBackArgs);
-CombineBackKernel combine_back_kernel_for(int dtype, bool vec, int warps);
+CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps);
 
 // ---- mxfp4.cu: MXFP4 quantisation and scale layouts
 struct MxQuantArgs {

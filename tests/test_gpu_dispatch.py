@@ -105,6 +105,10 @@ ROWS = [  # T, H, E, k, off, El, align, ld, shift
     (64, 256, 16, 2, 0, 16, 128, 3, 0), (50, 520, 9, 9, 2, 2, 16, 8, 1),
     (300, 136, 32, 8, 0, 32, 4, 0, 0), (7, 2055, 40, 32, 0, 40, 1, 1, 0),
     (40, 64, 8, 8, 4, 0, 1, 0, 0), (200, 4104, 64, 4, 0, 64, 1, 0, 0),
+    # rows shorter than a piece, and every distance of rows from 16 bytes
+    (70, 3, 6, 2, 0, 6, 1, 0, 0), (9, 7, 6, 2, 0, 6, 2, 2, 1), (600, 5, 6, 2, 1, 4, 1, 0, 3),
+    (40, 4001, 16, 2, 0, 16, 1, 0, 0), (300, 1026, 16, 4, 0, 16, 1, 2, 0),
+    (130, 2300, 16, 8, 0, 16, 1, 0, 2), (20, 777, 12, 12, 0, 12, 1, 9, 5),
 ]
 
 

@@ -9,6 +9,7 @@ from nvfp4_mixture_experts_gb300 import build as moe_build
 
 P = C.c_void_p(4096)      # a well aligned address that nothing reads
 ODD = C.c_void_p(4104)
+BYTE = C.c_void_p(4097)   # no multiple of an element's size
 
 
 @pytest.fixture(scope="module")
@@ -39,18 +40,21 @@ INVALID = [
                                 dict(E=0), dict(off=-1), dict(El=9), dict(off=1), dict(align=3),
                                 dict(align=256), dict(align=0), dict(k=9), dict(x_stride=63),
                                 dict(x=None), dict(rows=None), dict(ids=None), dict(counts=None),
-                                dict(offsets=None), dict(perm=None), dict(inv=None)]),
+                                dict(offsets=None), dict(perm=None), dict(inv=None),
+                                dict(x=BYTE), dict(rows=BYTE)]),
     ("moe_dispatch_backward", {k: v for k, v in COMBINE.items() if k != "w"},
      [dict(dtype=-1), dict(T=-1), dict(k=0), dict(H=0), dict(inv=None), dict(out=None),
       dict(y=None), dict(out_stride=63)]),
     ("moe_combine_weighted", COMBINE, [dict(dtype=3), dict(w=None), dict(y=None), dict(inv=None),
-                                       dict(out=None), dict(out_stride=1), dict(cap=-1)]),
+                                       dict(out=None), dict(out_stride=1), dict(cap=-1),
+                                       dict(y=BYTE), dict(out=BYTE), dict(out=C.c_void_p(4098), dtype=2)]),
     ("moe_combine_backward", BACK, [dict(dtype=3), dict(dout=None), dict(inv=None), dict(w=None),
-                                    dict(dy=None, dw=None), dict(y=None), dict(stride=63)]),
+                                    dict(dy=None, dw=None), dict(y=None), dict(stride=63),
+                                    dict(dout=BYTE), dict(y=BYTE), dict(dy=BYTE)]),
     ("moe_quant_mxfp4", QUANT, [dict(dtype=3), dict(batch=-1), dict(rows=-1), dict(cols=0),
                                 dict(transpose=2), dict(rule=2), dict(layout=2), dict(x=None),
                                 dict(codes=None), dict(sf=None), dict(rs=63), dict(codes=ODD),
-                                dict(values=ODD), dict(perm=P, batch=2),
+                                dict(values=ODD), dict(x=BYTE), dict(sf=ODD), dict(perm=P, batch=2),
                                 dict(perm=P, transpose=1, rows=32)]),
     ("moe_grouped_gemm_mxfp4", GEMM,
      [dict(dtype=3), dict(cap=-1), dict(G=0), dict(N=0), dict(K=0), dict(counts=None),
