@@ -290,6 +290,7 @@ def moe_get_status(h, ws, stream=None):
 # ---------------------------------------------------------------- operators without a handle
 # Element types come from the tensors (int16 tensors are bf16 bit patterns, as above), sizes from
 # their shapes; a tensor whose type, shape or strides do not fit raises MoEError before the call.
+# (Small calls are bound by this side: each tensor's attributes are asked for once.)
 
 class _Dtypes(dict):
     """torch dtype -> moe_dtype (-1: none), filled at the first look-up."""
@@ -304,25 +305,15 @@ class _Dtypes(dict):
 _DTYPES = _Dtypes()
 
 
-def _dtype(t):
-    return _DTYPES[t.dtype]
-
-
-def _need(ok, where):
-    if not ok:
-        raise MoEError(MOE_ERR_INVALID, where)
+def _refuse(where):
+    raise MoEError(MOE_ERR_INVALID, where)
 
 
 def _sf_bytes(batch, rows, blocks, sf_layout):
-    """moe_mxfp4_scale_bytes for `blocks` scales a row (the calls below check sizes often)."""
+    """moe_mxfp4_scale_bytes for `blocks` scales a row."""
     if sf_layout == MOE_SF_TILED:
         return batch * ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512
     return batch * rows * blocks
-
-
-def _rows_ok(t, H):
-    """Token rows [T][H]: the elements of a row contiguous, rows at any stride."""
-    return t.dim() == 2 and t.shape[1] == H and (H == 1 or t.stride(1) == 1)
 
 
 def moe_dispatch_rows_capacity(T, k, num_local, row_align):
@@ -336,62 +327,85 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
     [rows_cap, H]; status: an int32 word that errors found on the device are or-ed into."""
     T, k = topk_ids.shape
     cap = perm_src.numel()
-    _need(topk_ids.is_contiguous() and topk_ids.element_size() == 4 and inv.numel() == T * k and
-          counts.numel() == num_local and offsets.numel() == num_local + 1 and
-          (x is None) == (rows is None), "moe_dispatch")
-    H, stride, dt = 1, (1, 1), MOE_BF16
+    if not (topk_ids.is_contiguous() and topk_ids.element_size() == 4 and
+            inv.numel() == T * k and counts.numel() == num_local and
+            offsets.numel() == num_local + 1 and (x is None) == (rows is None)):
+        _refuse("moe_dispatch")
+    H, xs, dt, px, pr = 1, 1, MOE_BF16, None, None
     if x is not None:
         Tx, H = x.shape
-        stride, dt = x.stride(), _dtype(x)
-        _need(Tx == T and (H == 1 or stride[1] == 1) and dt == _dtype(rows) and
-              rows.shape == (cap, H) and rows.is_contiguous(), "moe_dispatch")
-    _check(load().moe_dispatch(_p(x), dt, stride[0], topk_ids.data_ptr(), T, k, H, num_experts,
-                               local_off, num_local, row_align, cap, counts.data_ptr(),
-                               offsets.data_ptr(), perm_src.data_ptr(), inv.data_ptr(), _p(rows),
-                               _p(status), _stream(stream)), "moe_dispatch")
+        xs, one = x.stride()
+        dt = _DTYPES[x.dtype]
+        if not (Tx == T and (one == 1 or H == 1) and dt == _DTYPES[rows.dtype] and
+                rows.shape == (cap, H) and rows.is_contiguous()):
+            _refuse("moe_dispatch")
+        px, pr = x.data_ptr(), rows.data_ptr()
+    st = (_lib or load()).moe_dispatch(
+        px, dt, xs, topk_ids.data_ptr(), T, k, H, num_experts, local_off, num_local, row_align,
+        cap, counts.data_ptr(), offsets.data_ptr(), perm_src.data_ptr(), inv.data_ptr(), pr,
+        _p(status), _stream(stream))
+    if st:
+        _check(st, "moe_dispatch")
 
 
 def moe_dispatch_backward(drows, inv, k, dx, stream=None):
     """drows [rows_cap, H], inv int32 [T * k] -> dx [T, H]."""
     T, H = dx.shape
-    _need(_rows_ok(dx, H) and drows.shape[1] == H and drows.is_contiguous() and
-          _dtype(drows) == _dtype(dx) and inv.numel() == T * k and inv.is_contiguous(),
-          "moe_dispatch_backward")
-    _check(load().moe_dispatch_backward(_p(drows), _dtype(dx), _p(inv), T, k, H, drows.shape[0],
-                                        _p(dx), dx.stride(0), _stream(stream)),
-           "moe_dispatch_backward")
+    cap, Hr = drows.shape
+    xs, one = dx.stride()
+    dt = _DTYPES[dx.dtype]
+    if not (Hr == H and (one == 1 or H == 1) and drows.is_contiguous() and
+            _DTYPES[drows.dtype] == dt and inv.numel() == T * k and inv.is_contiguous()):
+        _refuse("moe_dispatch_backward")
+    st = (_lib or load()).moe_dispatch_backward(drows.data_ptr(), dt, inv.data_ptr(), T, k, H, cap,
+                                                dx.data_ptr(), xs, _stream(stream))
+    if st:
+        _check(st, "moe_dispatch_backward")
 
 
 def moe_combine_weighted(y, inv, w, out, stream=None):
     """y [rows_cap, H], inv int32 [T * k], w float32 [T, k] -> out [T, H]."""
-    (T, k), H = w.shape, out.shape[1]
-    _need(out.shape[0] == T and _rows_ok(out, H) and y.shape[1] == H and y.is_contiguous() and
-          _dtype(y) == _dtype(out) and inv.numel() == T * k and inv.is_contiguous() and
-          w.is_contiguous() and _dtype(w) == MOE_FP32, "moe_combine_weighted")
-    _check(load().moe_combine_weighted(_p(y), _dtype(y), _p(inv), _p(w), T, k, H, y.shape[0],
-                                       _p(out), out.stride(0), _stream(stream)),
-           "moe_combine_weighted")
+    T, k = w.shape
+    To, H = out.shape
+    cap, Hy = y.shape
+    xs, one = out.stride()
+    dt = _DTYPES[y.dtype]
+    if not (To == T and Hy == H and (one == 1 or H == 1) and y.is_contiguous() and
+            _DTYPES[out.dtype] == dt and inv.numel() == T * k and inv.is_contiguous() and
+            w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32):
+        _refuse("moe_combine_weighted")
+    st = (_lib or load()).moe_combine_weighted(y.data_ptr(), dt, inv.data_ptr(), w.data_ptr(), T, k,
+                                               H, cap, out.data_ptr(), xs, _stream(stream))
+    if st:
+        _check(st, "moe_combine_weighted")
 
 
 def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
     """dout [T, H], y [rows_cap, H], inv int32 [T * k], w float32 [T, k] -> dy [rows_cap, H] and
     dw float32 [T, k]; dy or dw may be None (and y with dw)."""
-    (T, k), H = w.shape, dout.shape[1]
-    _need(dout.shape[0] == T and _rows_ok(dout, H) and inv.numel() == T * k and
-          inv.is_contiguous() and w.is_contiguous() and _dtype(w) == MOE_FP32,
-          "moe_combine_backward")
+    T, k = w.shape
+    To, H = dout.shape
+    xs, one = dout.stride()
+    dt = _DTYPES[dout.dtype]
+    ok = (To == T and (one == 1 or H == 1) and inv.numel() == T * k and inv.is_contiguous() and
+          w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32)
     cap = None
     for t in (y, dy):
         if t is not None:
-            _need(t.shape[1] == H and t.is_contiguous() and _dtype(t) == _dtype(dout) and
-                  cap in (None, t.shape[0]), "moe_combine_backward")
-            cap = t.shape[0]
+            rows, Ht = t.shape
+            ok = (ok and Ht == H and t.is_contiguous() and _DTYPES[t.dtype] == dt and
+                  (cap is None or cap == rows))
+            cap = rows
     if dw is not None:
-        _need(dw.numel() == T * k and dw.is_contiguous() and _dtype(dw) == MOE_FP32 and
-              y is not None, "moe_combine_backward")
-    _check(load().moe_combine_backward(_p(dout), _dtype(dout), dout.stride(0), _p(y), _p(inv),
-                                       _p(w), T, k, H, cap or 0, _p(dy), _p(dw),
-                                       _stream(stream)), "moe_combine_backward")
+        ok = (ok and dw.numel() == T * k and dw.is_contiguous() and
+              _DTYPES[dw.dtype] == MOE_FP32 and y is not None)
+    if not ok:
+        _refuse("moe_combine_backward")
+    st = (_lib or load()).moe_combine_backward(dout.data_ptr(), dt, xs, _p(y), inv.data_ptr(),
+                                               w.data_ptr(), T, k, H, cap or 0, _p(dy), _p(dw),
+                                               _stream(stream))
+    if st:
+        _check(st, "moe_combine_backward")
 
 
 def moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout):
@@ -403,29 +417,36 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
     """x [rows, cols] or [batch, rows, cols] (columns contiguous); codes uint8, sf uint8 and values
     (x's type) hold the MXFP4 matrix, or with transpose that of each matrix's transpose."""
     shape, stride = x.shape, x.stride()
-    _need(len(shape) in (2, 3), "moe_quant_mxfp4")
-    B, bs = (shape[0], stride[0]) if len(shape) == 3 else (1, 0)
-    R, Cc = shape[-2], shape[-1]
-    n, dt = B * R * Cc, _dtype(x)
-    _need((Cc == 1 or stride[-1] == 1) and codes.numel() * 2 == n and codes.is_contiguous() and
-          sf.is_contiguous() and
-          sf.numel() == (_sf_bytes(B, Cc, R >> 5, sf_layout) if transpose else
-                         _sf_bytes(B, R, Cc >> 5, sf_layout)) and
-          (perm_src is None or (perm_src.numel() == R and perm_src.element_size() == 4)) and
-          (values is None or (values.numel() == n and values.is_contiguous() and
-                              _dtype(values) == dt)), "moe_quant_mxfp4")
-    _check(load().moe_quant_mxfp4(x.data_ptr(), dt, B, R, Cc, stride[-2], bs,
-                                  1 if transpose else 0, scale_rule, _p(perm_src),
-                                  codes.data_ptr(), sf.data_ptr(), sf_layout, _p(values),
-                                  _stream(stream)), "moe_quant_mxfp4")
+    if len(shape) == 3:
+        (B, R, Cc), (bs, rs, one) = shape, stride
+    elif len(shape) == 2:
+        (R, Cc), (rs, one) = shape, stride
+        B, bs = 1, 0
+    else:
+        _refuse("moe_quant_mxfp4")
+    n, dt = B * R * Cc, _DTYPES[x.dtype]
+    scales = _sf_bytes(B, Cc, R >> 5, sf_layout) if transpose else _sf_bytes(B, R, Cc >> 5, sf_layout)
+    if not ((one == 1 or Cc == 1) and codes.numel() * 2 == n and codes.is_contiguous() and
+            sf.numel() == scales and sf.is_contiguous() and
+            (perm_src is None or (perm_src.numel() == R and perm_src.element_size() == 4)) and
+            (values is None or (values.numel() == n and values.is_contiguous() and
+                                _DTYPES[values.dtype] == dt))):
+        _refuse("moe_quant_mxfp4")
+    st = (_lib or load()).moe_quant_mxfp4(x.data_ptr(), dt, B, R, Cc, rs, bs, 1 if transpose else 0,
+                                          scale_rule, _p(perm_src), codes.data_ptr(), sf.data_ptr(),
+                                          sf_layout, _p(values), _stream(stream))
+    if st:
+        _check(st, "moe_quant_mxfp4")
 
 
 def moe_mxfp4_tile_scales(sf, batch, rows, cols, sf_tiled, stream=None):
-    _need(sf.numel() == moe_mxfp4_scale_bytes(batch, rows, cols, MOE_SF_CANONICAL) and
-          sf_tiled.numel() == moe_mxfp4_scale_bytes(batch, rows, cols, MOE_SF_TILED) and
-          sf.is_contiguous() and sf_tiled.is_contiguous(), "moe_mxfp4_tile_scales")
-    _check(load().moe_mxfp4_tile_scales(_p(sf), batch, rows, cols, _p(sf_tiled),
-                                        _stream(stream)), "moe_mxfp4_tile_scales")
+    if not (sf.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_CANONICAL) and
+            sf_tiled.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_TILED) and
+            sf.is_contiguous() and sf_tiled.is_contiguous()):
+        _refuse("moe_mxfp4_tile_scales")
+    st = load().moe_mxfp4_tile_scales(_p(sf), batch, rows, cols, _p(sf_tiled), _stream(stream))
+    if st:
+        _check(st, "moe_mxfp4_tile_scales")
 
 
 def moe_mxfp4_workspace_size(rows_cap, num_groups, N, K):
@@ -438,20 +459,21 @@ def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, w
     offsets int32 (both None: one group, all rows); out [rows_cap, N]."""
     G, N, K2 = w_codes.shape
     cap, Ka = a_codes.shape
-    stride = out.stride()
-    _need(Ka == K2 and a_codes.is_contiguous() and w_codes.is_contiguous() and
-          a_codes.element_size() == 1 and w_codes.element_size() == 1 and
-          a_sf.numel() == _sf_bytes(1, cap, K2 >> 4, MOE_SF_TILED) and
-          w_sf.numel() == _sf_bytes(G, N, K2 >> 4, MOE_SF_TILED) and
-          out.shape == (cap, N) and (N == 1 or stride[1] == 1) and
-          (counts is None) == (offsets is None) and
-          (counts is None or (counts.numel() == G and offsets.numel() >= G)),
-          "moe_grouped_gemm_mxfp4")
-    _check(load().moe_grouped_gemm_mxfp4(
+    xs, one = out.stride()
+    if not (Ka == K2 and a_codes.is_contiguous() and w_codes.is_contiguous() and
+            a_codes.element_size() == 1 and w_codes.element_size() == 1 and
+            a_sf.numel() == _sf_bytes(1, cap, K2 >> 4, MOE_SF_TILED) and
+            w_sf.numel() == _sf_bytes(G, N, K2 >> 4, MOE_SF_TILED) and
+            out.shape == (cap, N) and (one == 1 or N == 1) and
+            (counts is None) == (offsets is None) and
+            (counts is None or (counts.numel() == G and offsets.numel() >= G))):
+        _refuse("moe_grouped_gemm_mxfp4")
+    st = (_lib or load()).moe_grouped_gemm_mxfp4(
         a_codes.data_ptr(), a_sf.data_ptr(), cap, _p(counts), _p(offsets), G, w_codes.data_ptr(),
-        w_sf.data_ptr(), N, 2 * K2, out.data_ptr(), _dtype(out), stride[0], _p(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream(stream)),
-        "moe_grouped_gemm_mxfp4")
+        w_sf.data_ptr(), N, 2 * K2, out.data_ptr(), _DTYPES[out.dtype], xs, _p(ws),
+        0 if ws is None else ws.nbytes, _p(status), _stream(stream))
+    if st:
+        _check(st, "moe_grouped_gemm_mxfp4")
 
 
 from .layer import MoELayer, make_config  # noqa: E402,F401
