@@ -359,7 +359,9 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
     a.vec = rows_vec(out_d, (int64_t)N * es, rows_cap > 1 ? out_stride * es : 0);
     a.status = status_d;
     const MxGemmKernel kern = gemm_mxfp4_kernel_for(out_dtype);
-    const int smem = gemm_mxfp4_smem(num_groups, es);
+    a.stages = kMxStages;
+    while (gemm_mxfp4_smem(a.stages, num_groups, es) > kSmemLimit) --a.stages;  // many groups: 5
+    const int smem = gemm_mxfp4_smem(a.stages, num_groups, es);
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
         return MOE_ERR_CUDA;

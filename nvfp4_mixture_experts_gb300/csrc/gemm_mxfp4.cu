@@ -227,16 +227,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // The ring of k-stages in shared memory.  Where no group has more than 64 rows a stage holds 32
-// group rows per CTA and one row block of scales instead of 128 and two, and eight of them fit
-// instead of five: with few tiles the loads in flight bound the product (one token's gate_up,
-// 16 k-stages a tile: 8 stages 350 -> 220 cycles a k-stage).
+// group rows per CTA and one row block of scales instead of 128 and two, and nine of them fit
+// instead of six: with few tiles the loads in flight bound the product (one token's gate_up,
+// 16 k-stages a tile: 5 stages 350 cycles a k-stage, 8 stages 220).
 struct Stages {
     uint8_t* base;
     int n;                                   // stages
     uint32_t bytes, t, sw, st;               // of a stage; offsets of its parts (weights at 0)
-    __device__ __forceinline__ Stages(uint8_t* p, bool small) : base(p)
+    __device__ __forceinline__ Stages(uint8_t* p, int big, bool small) : base(p)
     {
-        n = small ? kMxMaxStages : kMxStages;
+        n = small ? big * kMxStageBytes / kMxSmallStageBytes : big;
         bytes = small ? kMxSmallStageBytes : kMxStageBytes;
         t = 16384;
         sw = t + (small ? 4096 : 16384);
@@ -294,54 +294,60 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[32])
 }
 
 // Stores a chunk: output columns n0 .. n0 + 31 of the `live` first of 32 rows, out pointing at the
-// first row.  The chunk is transposed through the warp's staging buffer (16-bit types: 8 x 8
-// matrices stored transposed; fp32: a word per lane and row), then leaves as 16-byte pieces along
-// the output rows, or (vec false) element by element.
+// first row.  A few rows at a time the chunk is transposed through the warp's staging buffer
+// (16-bit types: 8 x 8 matrices stored transposed; fp32: a word per lane and row) and leaves as
+// 16-byte pieces along the output rows, or (vec false) element by element.
 template <typename T>
 __device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t (&r)[32],
                                             uint8_t* stage, T* out, int live, int n0, int lane)
 {
     constexpr int kPitch = mx_epi_pitch((int)sizeof(T));  // bytes of a staged row
-    __syncwarp();
-    if constexpr (sizeof(T) == 2) {
-        const uint32_t at = smem_u32(stage) + (lane & 7) * kPitch + (lane >> 3) * 16;
+    constexpr int kRows = mx_epi_rows((int)sizeof(T));    // rows staged at a time
+    constexpr int kPer = 16 / (int)sizeof(T);             // elements of a piece
+    constexpr int kLanes = 32 / kPer;                     // lanes per row
+    const int64_t stride = a.out_stride;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t m[4];  // features 8 m .. 8 m + 7 of rows 8 i .. 8 i + 7
+    for (int j0 = 0; j0 < 32; j0 += kRows) {
+        if (j0 >= live) break;
+        __syncwarp();
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t at = smem_u32(stage) + (lane & 7) * kPitch + (lane >> 3) * 16;
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const int e = 16 * (f >> 1) + 4 * i + 2 * (f & 1);
-                m[f] = pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]), T());
+            for (int i = j0 / 8; i < (j0 + kRows) / 8; ++i) {
+                uint32_t m[4];  // features 8 m .. 8 m + 7 of rows 8 i .. 8 i + 7
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int e = 16 * (f >> 1) + 4 * i + 2 * (f & 1);
+                    m[f] = pack2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]), T());
+                }
+                asm volatile(
+                    "stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                        at + (8 * i - j0) * kPitch),
+                    "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
+                    : "memory");
             }
-            asm volatile(
-                "stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                    at + 8 * i * kPitch),
-                "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3])
-                : "memory");
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            *reinterpret_cast<uint32_t*>(stage + j * kPitch + 4 * lane) = r[j];
-    }
-    __syncwarp();
-    if (a.vec) {
-        constexpr int kPer = 16 / (int)sizeof(T);   // elements of a piece
-        constexpr int kLanes = 32 / kPer;           // lanes per row
-        const int n = n0 + (lane % kLanes) * kPer;
-        if (n < a.N) {
-            T* o = out + (lane / kLanes) * a.out_stride + n;
-            const uint8_t* st = stage + (lane / kLanes) * kPitch + (lane % kLanes) * 16;
-#pragma unroll
-            for (int j = 0; j < 32; j += 32 / kLanes)
-                if (j + lane / kLanes < live)
-                    *reinterpret_cast<uint4*>(o + j * a.out_stride) =
-                        *reinterpret_cast<const uint4*>(st + j * kPitch);
+            for (int j = 0; j < kRows; ++j)
+                *reinterpret_cast<uint32_t*>(stage + j * kPitch + 4 * lane) = r[j0 + j];
         }
-    } else if (n0 + lane < a.N) {
-        T* o = out + n0 + lane;
-        for (int j = 0; j < live && j < 32; ++j)
-            o[j * a.out_stride] = reinterpret_cast<const T*>(stage + j * kPitch)[lane];
+        __syncwarp();
+        if (a.vec) {
+            const int n = n0 + (lane % kLanes) * kPer, jl = lane / kLanes;
+            if (n < a.N) {
+                T* o = out + (j0 + jl) * stride + n;
+                const uint8_t* st = stage + jl * kPitch + (lane % kLanes) * 16;
+#pragma unroll
+                for (int j = 0; j < kRows; j += 32 / kLanes)
+                    if (j0 + j + jl < live)
+                        *reinterpret_cast<uint4*>(o + j * stride) =
+                            *reinterpret_cast<const uint4*>(st + j * kPitch);
+            }
+        } else if (n0 + lane < a.N) {
+            T* o = out + j0 * stride + n0 + lane;
+            for (int j = 0; j < kRows && j0 + j < live; ++j)
+                o[j * stride] = reinterpret_cast<const T*>(stage + j * kPitch)[lane];
+        }
     }
 }
 
@@ -356,8 +362,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-    uint8_t* staging = ring + kMxRingBytes;
-    Ctl& ctl = *reinterpret_cast<Ctl*>(staging + kMxEpiWarps * 32 * mx_epi_pitch((int)sizeof(T)));
+    uint8_t* staging = ring + args.stages * kMxStageBytes;
+    Ctl& ctl = *reinterpret_cast<Ctl*>(staging + mx_epi_bytes((int)sizeof(T)));
     int32_t* tables = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(&ctl) + kMxCtlBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     cluster_wait();    // ... and the peer's
     tc_fence_after();
     const int ntiles = gs.start[gs.G] * gs.NB;
-    const Stages sg(ring, gs.most <= 64);
+    const Stages sg(ring, args.stages, gs.most <= 64);
     volatile int* abort = &ctl.abort_flag;
 
     if (warp == 0) {
@@ -522,7 +528,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
     } else {
         const int q = warp & 3, h = (warp - 2) >> 2;  // TMEM lane quarter; which 32-row chunks
-        uint8_t* stage = staging + (warp - 2) * 32 * mx_epi_pitch((int)sizeof(T));
+        uint8_t* stage = staging + (warp - 2) * (mx_epi_bytes((int)sizeof(T)) / kMxEpiWarps);
         int it = 0;
         for (int t = pair; t < ntiles; t += npairs, ++it) {
             const Tile ti = find_tile(gs, t);

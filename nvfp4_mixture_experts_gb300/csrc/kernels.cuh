@@ -422,6 +422,7 @@ struct MxGemmArgs {
     void* out;
     int64_t out_stride;
     int vec;                 // the output rows may be stored in 16-byte pieces
+    int stages;              // of kMxStageBytes
     uint32_t* status;
 };
 constexpr int kMxTileRows = 256;     // group rows per tile at most
@@ -429,18 +430,22 @@ constexpr int kMxEpiWarps = 8;
 constexpr int kMxThreads = (2 + kMxEpiWarps) * 32;
 // stages of weight rows 16 KB, group rows 16 KB (small: 4 KB), weight scales 1 KB, group-row scales
 // 2 KB (small: 1 KB)
-constexpr int kMxStages = 5, kMxStageBytes = 16384 + 16384 + 1024 + 2048;
-constexpr int kMxMaxStages = 8, kMxSmallStageBytes = 16384 + 4096 + 1024 + 1024;
-constexpr int kMxRingBytes = kMxMaxStages * kMxSmallStageBytes;
-static_assert(kMxStages * kMxStageBytes <= kMxRingBytes, "both geometries fit the ring");
+constexpr int kMxStageBytes = 16384 + 16384 + 1024 + 2048;
+constexpr int kMxSmallStageBytes = 16384 + 4096 + 1024 + 1024;
+constexpr int kMxStages = 6;                 // as many as fit beside the tables of 490 groups
+constexpr int kMxMaxStages = kMxStages * kMxStageBytes / kMxSmallStageBytes;
 constexpr int kMxCtlBytes = 256;
-// bytes of a staged output row of 32 elements: 16-bit types padded so that the rows of an 8 x 8
-// matrix fall into different banks
+// an epilogue warp's staging: rows of 32 elements, 16-bit types padded so that the rows of an
+// 8 x 8 matrix fall into different banks
 __host__ __device__ constexpr int mx_epi_pitch(int out_bytes) { return out_bytes == 2 ? 80 : 128; }
-inline int gemm_mxfp4_smem(int G, int out_bytes)
+__host__ __device__ constexpr int mx_epi_rows(int out_bytes) { return out_bytes == 2 ? 16 : 8; }
+__host__ __device__ constexpr int mx_epi_bytes(int out_bytes)
 {
-    return 1024 + kMxRingBytes + kMxEpiWarps * 32 * mx_epi_pitch(out_bytes) + kMxCtlBytes +
-           4 * (3 * G + 1);
+    return kMxEpiWarps * mx_epi_rows(out_bytes) * mx_epi_pitch(out_bytes);
+}
+inline int gemm_mxfp4_smem(int stages, int G, int out_bytes)
+{
+    return 1024 + stages * kMxStageBytes + mx_epi_bytes(out_bytes) + kMxCtlBytes + 4 * (3 * G + 1);
 }
 using MxGemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
                               MxGemmArgs);
