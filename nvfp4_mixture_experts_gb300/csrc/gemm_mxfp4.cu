@@ -293,25 +293,33 @@ __device__ __forceinline__ void load_chunk(uint32_t taddr, uint32_t (&r)[32])
     else tmem_ld32(taddr, r);
 }
 
-// Stores a chunk: output columns n0 .. n0 + 31 of the `live` first of 32 rows, out pointing at the
-// first row.  A few rows at a time the chunk is transposed through the warp's staging buffer
-// (16-bit types: 8 x 8 matrices stored transposed; fp32: a word per lane and row) and leaves as
-// 16-byte pieces along the output rows, or (vec false) element by element.
+// A barrier of the four epilogue warps of a group.
+__device__ __forceinline__ void group_sync(int group)
+{
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+
+// Stores the chunks of a group's four warps: columns n0 .. n0 + 127 (this warp holds the 32 from
+// 32 q) of the `live` first of 32 rows, out pointing at the first row.  A few rows at a time the
+// chunks are transposed into the group's staging buffer (16-bit types: 8 x 8 matrices stored
+// transposed; fp32: a word per lane and row) and leave as 16-byte pieces of whole 128-column rows
+// (256 or 512 contiguous bytes), or (vec false) element by element.
 template <typename T>
 __device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t (&r)[32],
-                                            uint8_t* stage, T* out, int live, int n0, int lane)
+                                            uint8_t* stage, T* out, int live, int n0, int q,
+                                            int group, int lane)
 {
     constexpr int kPitch = mx_epi_pitch((int)sizeof(T));  // bytes of a staged row
     constexpr int kRows = mx_epi_rows((int)sizeof(T));    // rows staged at a time
     constexpr int kPer = 16 / (int)sizeof(T);             // elements of a piece
-    constexpr int kLanes = 32 / kPer;                     // lanes per row
+    constexpr int kLanes = 128 / kPer;                    // pieces of a row
     const int64_t stride = a.out_stride;
 #pragma unroll
     for (int j0 = 0; j0 < 32; j0 += kRows) {
         if (j0 >= live) break;
-        __syncwarp();
+        group_sync(group);  // the buffer has been read
         if constexpr (sizeof(T) == 2) {
-            const uint32_t at = smem_u32(stage) + (lane & 7) * kPitch + (lane >> 3) * 16;
+            const uint32_t at = smem_u32(stage) + (lane & 7) * kPitch + q * 64 + (lane >> 3) * 16;
 #pragma unroll
             for (int i = j0 / 8; i < (j0 + kRows) / 8; ++i) {
                 uint32_t m[4];  // features 8 m .. 8 m + 7 of rows 8 i .. 8 i + 7
@@ -329,24 +337,25 @@ __device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t 
         } else {
 #pragma unroll
             for (int j = 0; j < kRows; ++j)
-                *reinterpret_cast<uint32_t*>(stage + j * kPitch + 4 * lane) = r[j0 + j];
+                *reinterpret_cast<uint32_t*>(stage + j * kPitch + 4 * (32 * q + lane)) = r[j0 + j];
         }
-        __syncwarp();
+        group_sync(group);
+        const int th = 32 * q + lane;  // thread of the group
         if (a.vec) {
-            const int n = n0 + (lane % kLanes) * kPer, jl = lane / kLanes;
+            const int n = n0 + (th % kLanes) * kPer, jl = th / kLanes;
             if (n < a.N) {
                 T* o = out + (j0 + jl) * stride + n;
-                const uint8_t* st = stage + jl * kPitch + (lane % kLanes) * 16;
+                const uint8_t* st = stage + jl * kPitch + (th % kLanes) * 16;
 #pragma unroll
-                for (int j = 0; j < kRows; j += 32 / kLanes)
+                for (int j = 0; j < kRows; j += 128 / kLanes)
                     if (j0 + j + jl < live)
                         *reinterpret_cast<uint4*>(o + j * stride) =
                             *reinterpret_cast<const uint4*>(st + j * kPitch);
             }
-        } else if (n0 + lane < a.N) {
-            T* o = out + j0 * stride + n0 + lane;
+        } else if (n0 + th < a.N) {
+            T* o = out + j0 * stride + n0 + th;
             for (int j = 0; j < kRows && j0 + j < live; ++j)
-                o[j * stride] = reinterpret_cast<const T*>(stage + j * kPitch)[lane];
+                o[j * stride] = reinterpret_cast<const T*>(stage + j * kPitch)[th];
         }
     }
 }
@@ -391,7 +400,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     __syncwarp();
     if (warp == 1) tmem_alloc_pair(&ctl.tmem, 512);
     tc_fence_before();
-    const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
+    // Group rows are read by every weight tile: kept in L2 (evicted first instead: 8192 tokens'
+    // gate_up 332 -> 402 us).  Weights pass once where groups have few rows (evicted first: 64
+    // tokens' gate_up 206 -> 201 us), but elsewhere neighbouring 128-byte pieces of their rows, which
+    // L2 fetches in pairs, must outlive a k-stage (normal: 8192 tokens' down 244 -> 226 us).
+    const uint64_t pol_first = policy_evict_first(), pol_normal = policy_evict_normal();
+    const uint64_t pol_t = policy_evict_last();
     cluster_arrive();  // this CTA's barriers exist and its TMEM is allocated
     pdl_wait();
     pdl_trigger();
@@ -403,6 +417,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     volatile int* abort = &ctl.abort_flag;
 
     if (warp == 0) {
+        const uint64_t pol_w = gs.most <= 64 ? pol_first : pol_normal;
         const uint32_t full0 = cluster_addr(&ctl.full[0], 0);  // the leader's barriers
         Place at;               // (the elected lane's)
         int issued = 0;         // stages with a copy of this CTA, the last one before `at`
@@ -528,7 +543,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
     } else {
         const int q = warp & 3, h = (warp - 2) >> 2;  // TMEM lane quarter; which 32-row chunks
-        uint8_t* stage = staging + (warp - 2) * (mx_epi_bytes((int)sizeof(T)) / kMxEpiWarps);
+        uint8_t* stage = staging + h * (mx_epi_bytes((int)sizeof(T)) / 2);
         int it = 0;
         for (int t = pair; t < ntiles; t += npairs, ++it) {
             const Tile ti = find_tile(gs, t);
@@ -551,14 +566,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(&ctl.acc_empty[buf], 0);
-            const int n0 = ti.n0 + (int)rank * 128 + 32 * q;
+            const int n0 = ti.n0 + (int)rank * 128;
             if (n0 < args.N) {
                 T* out = static_cast<T*>(args.out) + (int64_t)ti.row0 * args.out_stride;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = 32 * (h + 2 * i);
                     if (c < ti.nt)
-                        store_chunk<T>(args, r[i], stage, out + c * args.out_stride, ti.rows - c, n0, lane);
+                        store_chunk<T>(args, r[i], stage, out + c * args.out_stride, ti.rows - c, n0, q, h,
+                                       lane);
                 }
             }
         }

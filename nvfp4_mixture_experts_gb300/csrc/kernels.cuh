@@ -435,13 +435,13 @@ constexpr int kMxSmallStageBytes = 16384 + 4096 + 1024 + 1024;
 constexpr int kMxStages = 6;                 // as many as fit beside the tables of 490 groups
 constexpr int kMxMaxStages = kMxStages * kMxStageBytes / kMxSmallStageBytes;
 constexpr int kMxCtlBytes = 256;
-// an epilogue warp's staging: rows of 32 elements, 16-bit types padded so that the rows of an
-// 8 x 8 matrix fall into different banks
-__host__ __device__ constexpr int mx_epi_pitch(int out_bytes) { return out_bytes == 2 ? 80 : 128; }
+// Staging of the output: two groups of four epilogue warps, each with rows of 128 elements (padded
+// so that the rows of an 8 x 8 matrix fall into different banks)
+__host__ __device__ constexpr int mx_epi_pitch(int out_bytes) { return 128 * out_bytes + 16; }
 __host__ __device__ constexpr int mx_epi_rows(int out_bytes) { return out_bytes == 2 ? 16 : 8; }
 __host__ __device__ constexpr int mx_epi_bytes(int out_bytes)
 {
-    return kMxEpiWarps * mx_epi_rows(out_bytes) * mx_epi_pitch(out_bytes);
+    return 2 * mx_epi_rows(out_bytes) * mx_epi_pitch(out_bytes);
 }
 inline int gemm_mxfp4_smem(int stages, int G, int out_bytes)
 {
