@@ -280,12 +280,15 @@ moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_
     a.layout = sf_layout;
     a.values = values_d;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (transpose) {
-        const int64_t tiles = (int64_t)batch * ceil_div(rows, 128) * ceil_div(cols, 64);
-        return launch(mx_quant_transposed_kernel_for(dtype), dim3(blocks_for(tiles, 1, 16)),
-                      dim3(256), 0, s, true, a);
-    }
     const int es = elem_bytes(dtype);
+    if (transpose) {
+        const int64_t tiles = (int64_t)batch * ceil_div(rows, 128) * ceil_div(cols, mx_transposed_cols(es));
+        // 16-bit types: two neighbouring columns are one aligned word in every row
+        const bool words = addr(x_d) % 4 == 0 && row_stride % 2 == 0 && (batch == 1 || batch_stride % 2 == 0);
+        const MxQuantKernel kern = mx_quant_transposed_kernel_for(dtype, words);
+        if (!allow_smem(reinterpret_cast<const void*>(kern), mx_transposed_smem(es))) return MOE_ERR_CUDA;
+        return launch(kern, dim3(blocks_for(tiles, 1, 16)), dim3(256), mx_transposed_smem(es), s, true, a);
+    }
     const bool vec = rows_vec(x_d, (int64_t)cols * es, rows > 1 ? row_stride * es : 0) &&
                      (batch == 1 || batch_stride * es % 16 == 0);
     const int64_t items = (int64_t)batch * rows * ceil_div(cols / 8, kMxQuantRun);

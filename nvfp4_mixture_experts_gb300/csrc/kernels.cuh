@@ -401,7 +401,13 @@ struct MxQuantArgs {
 constexpr int kMxQuantRun = 4 * 32;   // eights of a row that a warp takes at a time
 using MxQuantKernel = void (*)(MxQuantArgs);
 MxQuantKernel mx_quant_kernel_for(int dtype, bool vec);
-MxQuantKernel mx_quant_transposed_kernel_for(int dtype);
+MxQuantKernel mx_quant_transposed_kernel_for(int dtype, bool words);
+// columns of a tile of the transposing quantiser, and its shared memory
+constexpr int mx_transposed_cols(int elem_bytes) { return 256 / elem_bytes; }
+constexpr int mx_transposed_smem(int elem_bytes)
+{
+    return mx_transposed_cols(elem_bytes) * ((128 + 16 / elem_bytes) * elem_bytes + 80 + 4);
+}
 __global__ void mx_tile_scales_kernel(const uint8_t* sf, int batch, int rows, int blocks,
                                       uint8_t* tiled);
 

@@ -10,13 +10,6 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ float elem_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float elem_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float elem_f32(float v) { return v; }
-__device__ __forceinline__ void set_elem(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void set_elem(__half& d, float v) { d = __float2half_rn(v); }
-__device__ __forceinline__ void set_elem(float& d, float v) { d = v; }
-
 // Eight elements of a row as raw words.
 template <typename T>
 struct Eight {
@@ -59,11 +52,15 @@ struct Eight {
             for (int q = 0; q < 4; ++q) m = max_u16x2(m, w[q] & 0x7FFF7FFFu);
             m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            m = max(m & 0xFFFFu, m >> 16);
-            if constexpr (std::is_same<T, __half>::value)
-                return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
-            else return m << 16;
+            return bits16_f32(max(m & 0xFFFFu, m >> 16));
         }
+    }
+    // the bits, as fp32, of a 16-bit element's value
+    static __device__ __forceinline__ uint32_t bits16_f32(uint32_t h)
+    {
+        if constexpr (std::is_same<T, __half>::value)
+            return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
+        else return h << 16;
     }
     __device__ __forceinline__ void to_f32(float (&v)[8]) const
     {
@@ -281,24 +278,27 @@ MxQuantKernel mx_quant_kernel_for(int dtype, bool vec)
 
 // ------------------------------------------------------------------ a matrix's transpose
 
-// A block of threads per tile of 128 rows x 64 columns, a thread per (column, 32 rows), whose
-// block of 32 of the transposed row is its own: the loads run along the rows of x (lanes =
-// columns).  The transposed rows go out through shared memory, 128 elements (64 code bytes) of a
-// row at a time; a row's four scale bytes are one word.
-template <typename T>
+// A block of threads per tile of 128 rows x 64 columns (128 of 16-bit types), a thread per 32 rows
+// of a column (of two neighbouring columns, loaded as one word where WORDS says that they are
+// aligned), whose blocks of 32 of the transposed rows are its own: the loads run along the rows of
+// x (lanes = columns).  The transposed rows go out through shared memory, 128 elements (64 code
+// bytes) of a row at a time; a row's four scale bytes are one word.
+template <typename T, bool WORDS>
 __global__ void __launch_bounds__(256) mx_quant_transposed_kernel(MxQuantArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    constexpr int kCols = 64;
+    constexpr int kPer = 4 / (int)sizeof(T);           // columns of a thread
+    constexpr int kCols = 64 * kPer;
     constexpr int kPitch = 128 + 16 / (int)sizeof(T);  // elements; 16-byte accesses of neighbouring
                                                        // columns fall into different banks
-    __shared__ alignas(16) T s_val[kCols * kPitch];
-    __shared__ uint4 s_code[kCols][5];                 // 64 bytes and 16 of padding per column
-    __shared__ uint32_t s_scale[kCols];
+    extern __shared__ uint4 s_raw[];
+    T* s_val = reinterpret_cast<T*>(s_raw);            // [kCols][kPitch]
+    uint4* s_code = s_raw + kCols * kPitch * sizeof(T) / 16;  // [kCols][5]: 64 bytes, 16 of padding
+    uint32_t* s_scale = reinterpret_cast<uint32_t*>(s_code + kCols * 5);  // [kCols]
     const int rt = (a.rows + 127) >> 7, ct = (a.cols + kCols - 1) / kCols;
     const int blocks = a.rows >> 5;
-    const int c = threadIdx.x % kCols, rq = threadIdx.x / kCols;
+    const int c = threadIdx.x % 64 * kPer, rq = threadIdx.x / 64;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t tiles = (int64_t)a.batch * rt * ct;
     for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
@@ -312,39 +312,59 @@ __global__ void __launch_bounds__(256) mx_quant_transposed_kernel(MxQuantArgs a)
         if (in) {
             const T* x = static_cast<const T*>(a.x) + b * a.batch_stride +
                          (int64_t)kb * 32 * a.row_stride + c0 + c;
-            T e[32];
+            uint32_t e[32];  // an element, or two columns' elements
+            const bool two = kPer == 2 && c + 1 < C;
 #pragma unroll
-            for (int q = 0; q < 32; ++q) e[q] = x[q * a.row_stride];
-            float v[32];
+            for (int q = 0; q < 32; ++q) {
+                const T* p = x + q * a.row_stride;
+                if constexpr (kPer == 1) {
+                    e[q] = *reinterpret_cast<const uint32_t*>(p);
+                } else if (WORDS && two) {
+                    e[q] = *reinterpret_cast<const uint32_t*>(p);
+                } else {
+                    e[q] = *reinterpret_cast<const uint16_t*>(p);
+                    if (two) e[q] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + 1) << 16;
+                }
+            }
             uint32_t m = 0;
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
-                v[q] = elem_f32(e[q]);
-                m = max(m, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+                if constexpr (kPer == 1) m = max(m, e[q] & 0x7FFFFFFFu);
+                else m = Eight<T>::max_u16x2(m, e[q] & 0x7FFF7FFFu);
             }
-            const uint32_t s = mx_scale_byte(m, a.rule);
-            uint32_t codes[4] = {};
-            if (s != 255u) {
+#pragma unroll
+            for (int h = 0; h < kPer; ++h) {
+                if (c + h >= C) break;
+                uint32_t am = m;
+                if constexpr (kPer == 2) am = Eight<T>::bits16_f32(h ? m >> 16 : m & 0xFFFFu);
+                const uint32_t s = mx_scale_byte(am, a.rule);
                 const float scale = mx_encode_scale(s);
-#pragma unroll
-                for (int q = 0; q < 32; ++q) v[q] *= scale;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) codes[q] = f32x8_to_e2m1(v + 8 * q);
-            }
-            s_code[c][rq] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-            reinterpret_cast<uint8_t*>(&s_scale[c])[rq] = (uint8_t)s;
-            if (a.values) {
-                const float d = mx_decode_scale(s);
+                uint32_t codes[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    float f[8];
-                    e2m1x8_to_f32(codes[q], f);
-                    alignas(16) T o[8];
+                    float v[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) set_elem(o[j], f[j] * d);
-                    uint4* to = reinterpret_cast<uint4*>(&s_val[c * kPitch + rq * 32 + 8 * q]);
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t w = e[8 * q + j];
+                        v[j] = scale * __uint_as_float(
+                                           kPer == 1 ? w : Eight<T>::bits16_f32(h ? w >> 16 : w & 0xFFFFu));
+                    }
+                    codes[q] = s == 255u ? 0u : f32x8_to_e2m1(v);
+                }
+                s_code[(c + h) * 5 + rq] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+                reinterpret_cast<uint8_t*>(&s_scale[c + h])[rq] = (uint8_t)s;
+                if (a.values) {
+                    const float d = mx_decode_scale(s);
 #pragma unroll
-                    for (int j = 0; j < (int)sizeof(T) / 2; ++j) to[j] = reinterpret_cast<const uint4*>(o)[j];
+                    for (int q = 0; q < 4; ++q) {
+                        float f[8];
+                        e2m1x8_to_f32(codes[q], f);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[j] *= d;
+                        Eight<T> o;
+                        o.from_f32(f);
+                        o.store(s_val + (c + h) * kPitch + rq * 32 + 8 * q);
+                    }
                 }
             }
         }
@@ -353,9 +373,12 @@ __global__ void __launch_bounds__(256) mx_quant_transposed_kernel(MxQuantArgs a)
         if (threadIdx.x < C)
             store_scales(a.sf, a.layout, b, a.cols, c0 + threadIdx.x, blocks, tr * 4, s_scale[threadIdx.x]);
         // codes: a thread per 16 bytes, four per column
-        if (threadIdx.x / 4 < C && (threadIdx.x & 3) * 32 < R)
-            *reinterpret_cast<uint4*>(a.codes + (row0 + (int64_t)(threadIdx.x >> 2) * a.rows) / 2 +
-                                      (threadIdx.x & 3) * 16) = s_code[threadIdx.x >> 2][threadIdx.x & 3];
+#pragma unroll
+        for (int h = 0; h < kPer; ++h) {
+            const int q = 64 * h + (threadIdx.x >> 2), p = threadIdx.x & 3;
+            if (q < C && p * 32 < R)
+                *reinterpret_cast<uint4*>(a.codes + (row0 + (int64_t)q * a.rows) / 2 + p * 16) = s_code[q * 5 + p];
+        }
         if (a.values) {
             constexpr int kEl = 16 / (int)sizeof(T), kLanes = 128 / kEl;  // lanes per column
             for (int q = warp * (32 / kLanes) + lane / kLanes; q < C; q += 8 * (32 / kLanes)) {
@@ -369,12 +392,13 @@ __global__ void __launch_bounds__(256) mx_quant_transposed_kernel(MxQuantArgs a)
     }
 }
 
-MxQuantKernel mx_quant_transposed_kernel_for(int dtype)
+MxQuantKernel mx_quant_transposed_kernel_for(int dtype, bool words)
 {
     switch (dtype) {
-        case MOE_BF16: return mx_quant_transposed_kernel<__nv_bfloat16>;
-        case MOE_FP16: return mx_quant_transposed_kernel<__half>;
-        default: return mx_quant_transposed_kernel<float>;
+        case MOE_BF16:
+            return words ? mx_quant_transposed_kernel<__nv_bfloat16, true> : mx_quant_transposed_kernel<__nv_bfloat16, false>;
+        case MOE_FP16: return words ? mx_quant_transposed_kernel<__half, true> : mx_quant_transposed_kernel<__half, false>;
+        default: return mx_quant_transposed_kernel<float, true>;
     }
 }
 
