@@ -422,8 +422,9 @@ MOE_API moe_status moe_get_status(moe_handle h, void* ws_d, moe_stream_t stream,
  * neither written nor read.  T, k, H: tokens, routed experts per token (1..32), elements per
  * row; x_stride, out_stride etc.: elements between consecutive token rows (>= H); sorted rows
  * are contiguous [rows_cap][H].  Sums are taken in fp32 in ascending j and rounded once.
- * Rows whose size, stride and addresses are multiples of 16 bytes move in 16-byte pieces,
- * others element by element.  Inputs and outputs must not overlap. */
+ * Addresses are multiples of the element's size; rows move in the largest pieces (16 bytes down
+ * to an element) that their size, strides and addresses are multiples of.  Inputs and outputs must
+ * not overlap. */
 
 /* Rows that hold every pair however the T tokens route among num_local experts (0 for
  * arguments out of range).
@@ -496,6 +497,7 @@ MOE_API size_t moe_mxfp4_scale_bytes(int32_t batch, int32_t rows, int32_t cols,
  *     their outputs left as they are (the padding of sorted rows);
  *   values_d (nullable): receives the values that the codes stand for, in x's dtype, contiguous
  *     in the output's shape (a quantise-dequantise pass).
+ * codes_d, values_d and tiled scales 16-byte aligned; x_d a multiple of its element's size.
  * Passage: [CK] (packed FP4 codes with block scales); the MX block form is an addition of this
  * library. */
 MOE_API moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_t rows,

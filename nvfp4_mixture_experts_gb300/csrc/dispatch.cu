@@ -91,11 +91,12 @@ struct Piece {
 // ------------------------------------------------------------------ the sort
 
 // A stable counting sort.  Every warp that takes part owns a contiguous segment of the pairs and a
-// table of counts by expert in shared memory.  Pass 1 counts the segments (32 pairs at a time: lanes
-// of equal expert found with votes, their first lane adds their number, so no atomics).  Prefix sums
-// over the block's warps, over the blocks and over the experts (group sizes rounded up to
-// row_align) turn the tables into the row of each segment's first pair of each expert.  Pass 2 walks the segments again: a pair's row is its table entry plus the number of
-// lower lanes of equal expert, and the first lane moves the entry on.
+// table of counts by expert in shared memory.  Pass 1 counts the segments (32 pairs at a time:
+// lanes of equal expert found with votes, their first lane adds their number, so no atomics).
+// Prefix sums over the block's warps, over the blocks and over the experts (group sizes rounded up
+// to row_align) turn the tables into the row of each segment's first pair of each expert.  Pass 2
+// walks the segments again: a pair's row is its table entry plus the number of lower lanes of equal
+// expert, and the first lane moves the entry on.
 //
 // Up to kSmallPairs pairs one block does it alone, in the launch that also moves the rows, every
 // block of which sorts for itself (a few hundred cycles, less than a launch); more are shared out
@@ -150,10 +151,10 @@ __device__ __forceinline__ void sort_core(const SortArgs& a, SortShared& sh, uin
     const bool works = warp < nw;
     const int64_t p0 = min((int64_t)a.P, ((int64_t)rank * nw + warp) * a.segment);
     const int64_t p1 = works ? min((int64_t)a.P, p0 + a.segment) : p0;
-    auto local_expert = [&](int id, bool in) {
+    auto local_expert = [&](int id, bool in, bool tell) {
         if (!in) return -1;
         if (id < 0 || id >= a.E) {
-            if (flag) set_status(a.status, MOE_DEV_BAD_EXPERT_ID);
+            if (tell) set_status(a.status, MOE_DEV_BAD_EXPERT_ID);
             return -1;
         }
         const int le = id - a.off;
@@ -179,11 +180,11 @@ __device__ __forceinline__ void sort_core(const SortArgs& a, SortShared& sh, uin
 #pragma unroll
     for (int i = 0; i < kSortHold; ++i) {
         if (p0 + 32 * i >= p1) break;
-        held[i] = local_expert(held[i], p0 + 32 * i + lane < p1);
+        held[i] = local_expert(held[i], p0 + 32 * i + lane < p1, flag);
         same[i] = count(held[i]);
     }
     for (int64_t p = p0 + 32 * kSortHold; p < p1; p += 32)
-        count(local_expert(p + lane < p1 ? a.ids[p + lane] : 0, p + lane < p1));
+        count(local_expert(p + lane < p1 ? a.ids[p + lane] : 0, p + lane < p1, flag));
     __syncthreads();
     // exclusive prefix over the block's warps, a thread per expert
     for (int e = tid; e < El; e += kSortThreads) {
@@ -261,9 +262,8 @@ __device__ __forceinline__ void sort_core(const SortArgs& a, SortShared& sh, uin
         place(p0 + 32 * i, held[i], same[i]);
     }
     for (int64_t p = p0 + 32 * kSortHold; p < p1; p += 32) {
-        const int id = p + lane < p1 ? a.ids[p + lane] : 0;
-        const int off = id - a.off;
-        const int le = p + lane < p1 && id >= 0 && id < a.E && off >= 0 && off < El ? off : -1;
+        const bool in = p + lane < p1;
+        const int le = local_expert(in ? a.ids[p + lane] : 0, in, false);
         place(p, le, equal_lanes(le, bits));
     }
 }

@@ -320,7 +320,7 @@ int gemv_w4a16_fused_slots(int H, int tok_rows, int list_cap);
 
 // ---- dispatch.cu: tokens sorted by expert and back, and their gradients
 constexpr int kSortThreads = 1024;
-constexpr int kSortBlocks = 8;       // blocks of the sort's cluster at most (the portable size)
+constexpr int kSortBlocks = 16;      // blocks of the sort's cluster at most
 struct SortArgs {
     const int32_t* ids;   // [P]
     int P;                // T * k
