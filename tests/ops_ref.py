@@ -41,12 +41,11 @@ def gather_sum(rows, inv, w, T, k):
     H = rows.shape[1]
     out, mag = np.zeros((T, H)), np.zeros((T, H))
     inv = inv.reshape(T, k)
-    for t in range(T):
-        for j in range(k):
-            if 0 <= inv[t, j] < rows.shape[0]:
-                v = rows[inv[t, j]] * (1.0 if w is None else float(w[t, j]))
-                out[t] += v
-                mag[t] += np.abs(v)
+    for j in range(k):
+        t = np.flatnonzero((inv[:, j] >= 0) & (inv[:, j] < rows.shape[0]))
+        v = rows[inv[t, j]] * (1.0 if w is None else w[t, j][:, None].astype(np.float64))
+        out[t] += v
+        mag[t] += np.abs(v)
     return out, mag
 
 
@@ -62,34 +61,24 @@ def quant_mxfp4(x, ceil):
     """x [R, K] fp64 (values of the input type) -> codes 0..15 [R, K], scale bytes [R, K / 32],
     values [R, K] fp64."""
     R, K = x.shape
-    b = x.reshape(R, K // 32, 32)
-    codes = np.zeros(b.shape, np.int64)
-    sf = np.zeros(b.shape[:2], np.int64)
-    vals = np.zeros(b.shape)
-    for r in range(R):
-        for i in range(K // 32):
-            blk = b[r, i]
-            if not np.all(np.isfinite(blk)):
-                sf[r, i], vals[r, i] = 255, np.nan
-                continue
-            m = np.max(np.abs(blk))
-            if m == 0:
-                e = -127
-            else:
-                e = int(np.frexp(m)[1]) - 1 - 2
-                if ceil and m > 6 * 2.0 ** e:
-                    e += 1
-                e = min(127, max(-127, e))
-            sf[r, i] = e + 127
-            q = np.abs(blk) / 2.0 ** e
-            d = np.abs(q[:, None] - E2M1_MAG[None, :])
-            c = np.empty(32, np.int64)
-            for n in range(32):
-                best = np.flatnonzero(d[n] == d[n].min())
-                c[n] = best[0] if best.size == 1 else [v for v in best if v % 2 == 0][0]
-            codes[r, i] = c + 8 * np.signbit(blk)
-            vals[r, i] = np.copysign(E2M1_MAG[c], blk) * 2.0 ** e
-    return codes.reshape(R, K), sf, vals.reshape(R, K)
+    b = np.asarray(x, np.float64).reshape(-1, 32)
+    good = np.all(np.isfinite(b), axis=1)
+    m = np.max(np.abs(np.where(good[:, None], b, 0.0)), axis=1)
+    e = np.frexp(m)[1].astype(np.int64) - 1 - 2            # m = f 2^(e + 3), f in [1/2, 1)
+    if ceil:
+        e += m > 6 * np.ldexp(1.0, e)
+    e = np.where(m == 0, -127, np.clip(e, -127, 127))
+    q = np.ldexp(np.abs(np.where(good[:, None], b, 0.0)), -e[:, None])
+    # the nearest value; of two as near (neighbouring codes) the even code
+    d = np.abs(q[..., None] - E2M1_MAG)
+    best = d == d.min(-1, keepdims=True)
+    even = best & (np.arange(8) % 2 == 0)
+    c = np.where(even.any(-1), even.argmax(-1), best.argmax(-1))
+    vals = np.ldexp(np.copysign(E2M1_MAG[c], b), e[:, None])
+    codes = np.where(good[:, None], c + 8 * np.signbit(b), 0)
+    vals[~good] = np.nan
+    sf = np.where(good, e + 127, 255)
+    return codes.reshape(R, K), sf.reshape(R, K // 32), vals.reshape(R, K)
 
 
 def pack(codes):
@@ -106,11 +95,9 @@ def tile_scales(sf, fill=0):
     R, S = sf.shape
     RB, KA = (R + 127) // 128, (S + 3) // 4
     out = np.full(RB * KA * 512, fill, np.uint8)
-    for r in range(RB * 128):
-        for kb in range(KA * 4):
-            at = ((r >> 7) * KA + (kb >> 2)) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + kb % 4
-            if r < R:
-                out[at] = sf[r, kb] if kb < S else 0
+    r, kb = np.arange(R)[:, None], np.arange(KA * 4)[None, :]
+    at = ((r >> 7) * KA + (kb >> 2)) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + kb % 4
+    out[at] = np.pad(np.asarray(sf), ((0, 0), (0, KA * 4 - S)))
     return out
 
 
