@@ -274,3 +274,39 @@ def test_rows_past_two_to_the_31_bytes():
     moe.moe_combine_backward(out, None, inv, w, dy, None)
     assert torch.all(dy[cap - 1] == 22.0) and torch.all(dy[cap - 2] == 11.0)
     assert torch.all(dy[cap - 3] == 0.0)
+
+
+@pytest.mark.parametrize("T", [40, 900])
+def test_calls_replay_in_a_graph(T):
+    """Captured dispatch (both launch forms), combine and gradient follow new ids and inputs."""
+    E, k, H = 24, 3, 96
+    rng = np.random.default_rng(T)
+    ids = torch.from_numpy(make_ids(rng, T, E, k, "spread")).cuda()
+    x, w = torch.randn(T, H, device="cuda"), torch.rand(T, k, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    counts, offsets, perm = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * k, **i32)
+    inv, rows = torch.empty(T * k, **i32), torch.empty(T * k, H, device="cuda")
+    out, dy, dw = torch.empty(T, H, device="cuda"), torch.empty(T * k, H, device="cuda"), torch.empty(T, k, device="cuda")
+
+    def step():
+        moe.moe_dispatch(x, ids, E, 0, E, 1, counts, offsets, perm, inv, rows)
+        moe.moe_combine_weighted(rows, inv, w, out)
+        moe.moe_combine_backward(out, rows, inv, w, dy, dw)
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    new = make_ids(rng, T, E, k, "spread")
+    ids.copy_(torch.from_numpy(new))
+    x.copy_(torch.randn(T, H))
+    g.replay()
+    torch.cuda.synchronize()
+    _, _, want_perm, want_inv, _, _ = ref.sort_pairs(new, E, 0, E, 1, T * k)
+    assert np.array_equal(perm.cpu(), want_perm) and np.array_equal(inv.cpu(), want_inv)
+    assert np.array_equal(f64(rows), f64(x)[want_perm // k])
+    want, mag = ref.gather_sum(f64(rows), want_inv, f64(w), T, k)
+    assert np.all(ref.rounded_ok(f64(out), want, (k + 1) * F * mag, "fp32"))
+    d = f64(out)[want_perm // k] * f64(rows)
+    got = f64(dw).reshape(-1)[want_perm]
+    assert np.all(np.abs(got - d.sum(1)) <= (H + 2) * F * np.abs(d).sum(1))

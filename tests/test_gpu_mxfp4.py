@@ -327,3 +327,72 @@ def test_product_of_quantised_rows_and_its_gradient():
     lhs = (f64(dv) @ g * f64(xv)).sum()
     rhs = (f64(dx) * f64(xv)).sum()
     assert abs(lhs - rhs) <= N * F * (np.abs(f64(dv)) @ np.abs(g) * np.abs(f64(xv))).sum()
+
+
+def test_offsets_past_two_to_the_31():
+    """Outputs and inputs of over 2^32 elements: the last rows are where they belong."""
+    cap, N, K = (1 << 20) + 128, 4128, 32
+    a = u8(cap * 16).view(cap, 16)
+    a[1 << 20:].fill_(0x22)                      # every element 1
+    sf = u8(moe.moe_mxfp4_scale_bytes(1, cap, K, moe.MOE_SF_TILED), 127)
+    w, wsf = u8(N * 16, 0x44).view(1, N, 16), u8(moe.moe_mxfp4_scale_bytes(1, N, K, moe.MOE_SF_TILED), 127)
+    out = torch.zeros(cap, N, dtype=torch.bfloat16, device="cuda")
+    i32 = lambda v: torch.tensor([v], dtype=torch.int32).cuda()  # noqa: E731
+    moe.moe_grouped_gemm_mxfp4(a, sf, i32(5), i32(1 << 20), w, wsf, out)
+    assert torch.all(out[(1 << 20):(1 << 20) + 5] == 64.0)      # 32 products 1 x 2
+    assert torch.all(out[(1 << 20) + 5:] == 0) and torch.all(out[(1 << 20) - 64:1 << 20] == 0)
+    # the quantiser reads that matrix and its transpose
+    x = out[:, :4096]
+    codes = u8(cap * 2048)
+    moe.moe_quant_mxfp4(x, codes, u8(moe.moe_mxfp4_scale_bytes(1, cap, 4096, 0)), 0)
+    got = codes.view(cap, 2048)
+    assert torch.all(got[(1 << 20):(1 << 20) + 5] == 0x66)      # 64 = 4 x 2^4
+    assert torch.all(got[(1 << 20) + 5:] == 0) and torch.all(got[:64] == 0)
+    tcodes = u8(4096 * cap // 2)
+    moe.moe_quant_mxfp4(x, tcodes, u8(moe.moe_mxfp4_scale_bytes(1, 4096, cap, 0)), 0, transpose=True)
+    got = tcodes.view(4096, cap // 2)
+    assert torch.all(got[:, 1 << 19:(1 << 19) + 2] == 0x66) and torch.all(got[:, (1 << 19) + 2] == 0x06)
+    assert torch.all(got[:, (1 << 19) + 3:] == 0) and torch.all(got[:, :64] == 0)
+
+
+def test_another_stream_orders_quantiser_and_product():
+    M, N, K = 384, 256, 512
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        x = torch.zeros(M, K, device="cuda")
+        w = torch.ones(1, N, K, device="cuda")
+        codes, wc = u8(M * K // 2).view(M, K // 2), u8(N * K // 2).view(1, N, K // 2)
+        sf = u8(moe.moe_mxfp4_scale_bytes(1, M, K, moe.MOE_SF_TILED))
+        ws = u8(moe.moe_mxfp4_scale_bytes(1, N, K, moe.MOE_SF_TILED))
+        out = torch.empty(M, N, device="cuda")
+        for i in range(1, 5):             # each call must see the one before it
+            x += 1.0
+            moe.moe_quant_mxfp4(w, wc, ws, moe.MOE_SF_TILED)
+            moe.moe_quant_mxfp4(x, codes, sf, moe.MOE_SF_TILED)
+            moe.moe_grouped_gemm_mxfp4(codes, sf, None, None, wc, ws, out)
+        total = out.sum()
+    side.synchronize()
+    assert total.item() == 4.0 * K * M * N
+
+
+def test_calls_replay_in_a_graph():
+    M, N, K = 100, 200, 256
+    x, w = torch.randn(M, K, device="cuda"), torch.randn(1, N, K, device="cuda")
+    codes, wc = u8(M * K // 2).view(M, K // 2), u8(N * K // 2).view(1, N, K // 2)
+    sf = u8(moe.moe_mxfp4_scale_bytes(1, M, K, moe.MOE_SF_TILED))
+    ws = u8(moe.moe_mxfp4_scale_bytes(1, N, K, moe.MOE_SF_TILED))
+    out = torch.empty(M, N, device="cuda")
+
+    def step():
+        moe.moe_quant_mxfp4(w, wc, ws, moe.MOE_SF_TILED)
+        moe.moe_quant_mxfp4(x, codes, sf, moe.MOE_SF_TILED)
+        moe.moe_grouped_gemm_mxfp4(codes, sf, None, None, wc, ws, out)
+
+    step()
+    first = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    x.mul_(2.0)                           # twice the rows: the same codes, scales one up
+    g.replay()
+    assert torch.equal(out, 2 * first)
