@@ -232,13 +232,19 @@ moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_
     a.rows_cap = rows_cap;
     a.dy = dy_d;
     a.dw = dw_d;
-    // Warps per token: as few as still give every SM its 16 (at 128 registers), since a token's
-    // warps wait for one another at its end; more when tokens are few, where one token's latency
-    // counts.  8192 tokens x 4096, k 8, bf16: 2 warps 169 us, 4 172, 8 180; x 2048, k 4: 55, 62,
-    // 76; 777 tokens x 1001 fp16: 10.3, 8.4, 9.4; 64 tokens x 4096: 6.7, 4.7, 3.8.
-    int warps = 2;
+    // Rows of over 4.5 KB and more than four pairs a token: the kernel that takes all pairs at once
+    // (k 8, bf16, 8192 tokens x 4096: 170 us, 182 with the one that takes the kept pairs four at a
+    // time; x 3000: 132 and 140).  Else the latter (x 2056, 3 of 8 pairs kept: 46 us, 53 with the
+    // former; x 304, k 6, 2 of 6 kept: 8.6 and 15).
+    const int64_t row = (int64_t)H * es;
+    const bool all = k > 4 && row > 4608;
+    // Warps per token: one, for long rows two, or as many more as give every SM its 16: a token's
+    // warps wait for one another at its end (7003 tokens x 1096, k 2: one warp 22 us, two 28; 8192
+    // x 4001, k 8: 275 and 258), but few tokens' latency counts (64 tokens x 4096, k 8: two warps
+    // 6.7 us, eight 3.8).
+    int warps = row <= 6144 && !all ? 1 : 2;
     while (warps < 8 && (int64_t)T * warps < 16 * num_sms()) warps *= 2;
-    return launch(combine_back_kernel_for(dtype, unit, warps), dim3(blocks_for(T, 1, 64 / warps)),
+    return launch(combine_back_kernel_for(dtype, unit, warps, all), dim3(blocks_for(T, 1, 64 / warps)),
                   dim3(32 * warps), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 

@@ -14,9 +14,9 @@ namespace moe {
 
 // A piece of a row: V elements of type T in one access of B = V sizeof(T) bytes (16, 8, 4 or 2), the
 // largest that every row of the call's tensors is aligned to.  fp32 values in, fp32 values out;
-// rounding to nearest even.  (Rows of 4001 16-bit elements, aligned to nothing more, take 146 us
-// in combine where 4004, aligned to 8 bytes, take 92; reading 16-byte blocks around every piece and
-// shifting them into place was measured at 167, and at 600 against 239 in combine's gradient:
+// rounding to nearest even.  (8192 rows of 4001 16-bit elements, aligned to nothing more, take 131
+// us in combine where 4004, aligned to 8 bytes, take 90; reading 16-byte blocks around every piece
+// and shifting them into place was measured at 167, and at 600 against 241 in combine's gradient:
 // the blocks' registers cost more loads in flight than they save instructions.)
 template <int B>
 struct Word;
@@ -413,15 +413,36 @@ DispatchKernel dispatch_rows_kernel_for(int unit_bytes)
 
 // ------------------------------------------------------------------ combine
 
-// out[t] = sum_j w[t, j] rows[inv[t k + j]] (w null: 1): a warp takes kCombineRun pieces of a token,
-// the rows and weights of the token's pairs held by its lanes, the loads of eight rows in flight;
-// fp32 sums in ascending j.
+// The pairs of a token: every lane of a warp holds one pair's row (-1 past k) and weight.
+struct Pairs {
+    int row;
+    float w;
+    __device__ __forceinline__ Pairs(const int32_t* inv, const float* weights, int64_t t, int k)
+    {
+        const int lane = threadIdx.x & 31;
+        row = -1;
+        w = 1.0f;
+        if (lane < k) {
+            row = inv[t * k + lane];
+            if (weights) w = weights[t * k + lane];
+        }
+    }
+    // the lanes of the kept pairs
+    __device__ __forceinline__ uint32_t kept(int rows_cap) const
+    {
+        return __ballot_sync(0xffffffffu, (uint32_t)row < (uint32_t)rows_cap);
+    }
+};
+
+// out[t] = sum_j w[t, j] rows[inv[t k + j]] (w null: 1): a warp takes a run of pieces of a token, the
+// rows and weights of the token's pairs held by its lanes; dropped pairs cost nothing, of the kept
+// ones four rows' loads are in flight at a time; fp32 sums in ascending j.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    constexpr int kPer = combine_run(V * (int)sizeof(T)) / 32;
+    constexpr int kPer = combine_run(V * (int)sizeof(T)) / 32, kAt = kCombineAt;
     const int lane = threadIdx.x & 31;
     const int units = a.H / V, runs = (units + 32 * kPer - 1) / (32 * kPer);
     const int64_t items = (int64_t)a.T * runs, step = (int64_t)gridDim.x * (blockDim.x >> 5);
@@ -431,43 +452,38 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
         const int64_t t = i / runs;
         const int u0 = (int)(i - t * runs) * 32 * kPer + lane;
         const bool full = u0 - lane + 32 * kPer <= units;
-        int my_row = -1;
-        float my_w = 1.0f;
-        if (lane < a.k) {
-            my_row = a.inv[t * a.k + lane];
-            if ((uint32_t)my_row >= (uint32_t)a.rows_cap) my_row = -1;
-            if (a.w) my_w = a.w[t * a.k + lane];
-        }
+        const Pairs pairs(a.inv, a.w, t, a.k);
         float acc[kPer][V] = {};
-        for (int j0 = 0; j0 < a.k; j0 += 8) {
-            Piece<T, V> p[8][kPer];
+        for (uint32_t kept = pairs.kept(a.rows_cap); kept;) {
+            Piece<T, V> p[kAt][kPer];
+            float w[kAt];
+            const int n = min(__popc(kept), kAt);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = __shfl_sync(0xffffffffu, my_row, j0 + j);  // -1 past k
-                if (row >= 0) {
-                    const T* from = y + (int64_t)row * a.H + (int64_t)u0 * V;
-                    if (full) {
+            for (int j = 0; j < kAt; ++j) {
+                if (j >= n) break;
+                const int src = __ffs(kept) - 1;
+                kept &= kept - 1;
+                const int row = __shfl_sync(0xffffffffu, pairs.row, src);
+                w[j] = __shfl_sync(0xffffffffu, pairs.w, src);
+                const T* from = y + (int64_t)row * a.H + (int64_t)u0 * V;
+                if (full) {
 #pragma unroll
-                        for (int q = 0; q < kPer; ++q) p[j][q].load(from + 32 * V * q);
-                    } else {
+                    for (int q = 0; q < kPer; ++q) p[j][q].load(from + 32 * V * q);
+                } else {
 #pragma unroll
-                        for (int q = 0; q < kPer; ++q)
-                            if (u0 + 32 * q < units) p[j][q].load(from + 32 * V * q);
-                    }
+                    for (int q = 0; q < kPer; ++q)
+                        if (u0 + 32 * q < units) p[j][q].load(from + 32 * V * q);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = __shfl_sync(0xffffffffu, my_row, j0 + j);
-                const float w = __shfl_sync(0xffffffffu, my_w, j0 + j);
-                if (row >= 0) {
+            for (int j = 0; j < kAt; ++j) {
+                if (j >= n) break;
 #pragma unroll
-                    for (int q = 0; q < kPer; ++q) {
-                        float f[V];
-                        p[j][q].unpack(f);
+                for (int q = 0; q < kPer; ++q) {
+                    float f[V];
+                    p[j][q].unpack(f);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) acc[q][e] = fmaf(w, f[e], acc[q][e]);
-                    }
+                    for (int e = 0; e < V; ++e) acc[q][e] = fmaf(w[j], f[e], acc[q][e]);
                 }
             }
         }
@@ -504,10 +520,110 @@ CombineKernel combine_rows_kernel_for(int dtype, int unit)
 
 // ------------------------------------------------------------------ combine's gradient
 
-// A block of W warps per token: dy rows = w dout, and the k dot products <dout, y row>, eight rows
-// at a time, reduced over the block.
+// A block of W warps per token: dy rows = w dout, and the dot products <dout, y row> of the kept
+// pairs, four rows at a time, reduced over the block.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(32 * W) combine_back_kernel(CombineBackArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kAt = kCombineAt, kPer = back_per(V * (int)sizeof(T));
+    __shared__ float s_dot[2][W][kMaxTopK];  // of the even and the odd tokens of the block
+    const int units = a.H / V;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T* dout = static_cast<const T*>(a.dout);
+    const T* y = static_cast<const T*>(a.y);
+    T* dy = static_cast<T*>(a.dy);
+    int odd = 0;
+    Pairs next(a.inv, a.w, blockIdx.x, a.k);  // (the grid has at most T blocks)
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, odd ^= 1) {
+        const Pairs pairs = next;
+        if (t + gridDim.x < a.T) next = Pairs(a.inv, a.w, t + gridDim.x, a.k);
+        float sum = 0.0f;  // lane j: this warp's share of pair j's dot product
+        for (uint32_t kept = pairs.kept(a.rows_cap); kept;) {
+            const int n = min(__popc(kept), kAt);
+            int row[kAt], src[kAt];
+            float w[kAt], dot[kAt];
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                src[j] = j < n ? __ffs(kept) - 1 : 0;
+                if (j < n) kept &= kept - 1;
+                row[j] = __shfl_sync(0xffffffffu, pairs.row, src[j]);
+                w[j] = __shfl_sync(0xffffffffu, pairs.w, src[j]);
+                dot[j] = 0.0f;
+            }
+            for (int u0 = threadIdx.x; u0 < units; u0 += 32 * W * kPer) {
+                const bool full = u0 - lane + 32 * W * (kPer - 1) + 31 < units;
+                Piece<T, V> pd[kPer], p[kAt][kPer];
+                const T* from = dout + t * a.dout_stride + (int64_t)u0 * V;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q)
+                    if (full || u0 + 32 * W * q < units) pd[q].load(from + 32 * W * V * q);
+                if (a.dw) {
+#pragma unroll
+                    for (int j = 0; j < kAt; ++j) {
+                        if (j >= n) break;
+                        const T* yr = y + (int64_t)row[j] * a.H + (int64_t)u0 * V;
+#pragma unroll
+                        for (int q = 0; q < kPer; ++q)
+                            if (full || u0 + 32 * W * q < units) p[j][q].load(yr + 32 * W * V * q);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) {
+                    if (!full && u0 + 32 * W * q >= units) break;
+                    float d[V];
+                    pd[q].unpack(d);
+#pragma unroll
+                    for (int j = 0; j < kAt; ++j) {
+                        if (j >= n) break;
+                        if (a.dw) {
+                            float f[V];
+                            p[j][q].unpack(f);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
+                        }
+                        if (dy) {
+                            float g[V];
+#pragma unroll
+                            for (int e = 0; e < V; ++e) g[e] = w[j] * d[e];
+                            Piece<T, V> pg;
+                            pg.pack(g);
+                            pg.store(dy + (int64_t)row[j] * a.H + (int64_t)(u0 + 32 * W * q) * V);
+                        }
+                    }
+                }
+            }
+            if (a.dw) {
+#pragma unroll
+                for (int j = 0; j < kAt; ++j) {
+                    if (j >= n) break;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+                        dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+                    if (lane == src[j]) sum = dot[j];
+                }
+            }
+        }
+        if (a.dw) {
+            if constexpr (W > 1) {
+                if (lane < a.k) s_dot[odd][warp][lane] = sum;
+                __syncthreads();  // (the other buffer is free again once every warp is here)
+                if (warp == 0) {
+                    sum = 0.0f;
+                    if (lane < a.k)
+                        for (int q = 0; q < W; ++q) sum += s_dot[odd][q][lane];
+                }
+            }
+            if (warp == 0 && lane < a.k) a.dw[t * a.k + lane] = sum;
+        }
+    }
+}
+
+// As combine_back_kernel, for long rows and more than four pairs a token: eight pairs at a time, kept or
+// not, their rows and weights loaded by every thread alike (addresses in uniform registers).
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(32 * W) combine_back_all_kernel(CombineBackArgs a)
 {
     pdl_wait();
     pdl_trigger();
@@ -598,32 +714,33 @@ __global__ void __launch_bounds__(32 * W) combine_back_kernel(CombineBackArgs a)
 }
 
 template <typename T, int V>
-static CombineBackKernel combine_back_of(int warps)
+static CombineBackKernel combine_back_of(int warps, bool all)
 {
     switch (warps) {
-        case 2: return combine_back_kernel<T, V, 2>;
-        case 4: return combine_back_kernel<T, V, 4>;
-        default: return combine_back_kernel<T, V, 8>;
+        case 1: return combine_back_kernel<T, V, 1>;
+        case 2: return all ? combine_back_all_kernel<T, V, 2> : combine_back_kernel<T, V, 2>;
+        case 4: return all ? combine_back_all_kernel<T, V, 4> : combine_back_kernel<T, V, 4>;
+        default: return all ? combine_back_all_kernel<T, V, 8> : combine_back_kernel<T, V, 8>;
     }
 }
 
 template <typename T>
-static CombineBackKernel combine_back_unit(int unit, int warps)
+static CombineBackKernel combine_back_unit(int unit, int warps, bool all)
 {
     switch (unit / (int)sizeof(T)) {
-        case 8: if constexpr (sizeof(T) == 2) return combine_back_of<T, 8>(warps);
-        case 4: return combine_back_of<T, 4>(warps);
-        case 2: return combine_back_of<T, 2>(warps);
-        default: return combine_back_of<T, 1>(warps);
+        case 8: if constexpr (sizeof(T) == 2) return combine_back_of<T, 8>(warps, all);
+        case 4: return combine_back_of<T, 4>(warps, all);
+        case 2: return combine_back_of<T, 2>(warps, all);
+        default: return combine_back_of<T, 1>(warps, all);
     }
 }
 
-CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps)
+CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps, bool all)
 {
     switch (dtype) {
-        case MOE_BF16: return combine_back_unit<__nv_bfloat16>(unit, warps);
-        case MOE_FP16: return combine_back_unit<__half>(unit, warps);
-        default: return combine_back_unit<float>(unit, warps);
+        case MOE_BF16: return combine_back_unit<__nv_bfloat16>(unit, warps, all);
+        case MOE_FP16: return combine_back_unit<__half>(unit, warps, all);
+        default: return combine_back_unit<float>(unit, warps, all);
     }
 }
 

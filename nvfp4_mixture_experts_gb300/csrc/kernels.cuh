@@ -363,7 +363,8 @@ struct CombineArgs {
     void* out;
     int64_t out_stride;   // in elements
 };
-// pieces (of `unit` bytes) of a token that a warp takes at a time: 64 registers of eight rows' pieces
+constexpr int kCombineAt = 4;         // rows whose loads are in flight together
+// pieces (of `unit` bytes) of a token that a warp takes at a time
 __host__ __device__ constexpr int combine_run(int unit)
 {
     return 32 * (unit == 16 ? 2 : unit == 8 ? 4 : 8);
@@ -384,7 +385,8 @@ struct CombineBackArgs {
     float* dw;            // nullable
 };
 using CombineBackKernel = void (*)(CombineBackArgs);
-CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps);
+// all: the form for long rows and more than four pairs a token
+CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps, bool all);
 
 // ---- mxfp4.cu: MXFP4 quantisation and scale layouts
 struct MxQuantArgs {
