@@ -299,6 +299,28 @@ __device__ __forceinline__ void group_sync(int group)
     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
+// Stores a group's staged rows j0 .. j0 + ROWS - 1 (of `live`): columns n0 .. n0 + 127 in pieces of
+// type U, the largest (16, 4 or, 16-bit types, 2 bytes) that every output row is aligned to and a
+// whole number of; th: the thread of the group.
+template <typename T, typename U, int ROWS, int PITCH>
+__device__ __forceinline__ void store_rows(const MxGemmArgs& a, const uint8_t* stage, T* out, int j0,
+                                           int live, int n0, int th)
+{
+    constexpr int kPer = (int)sizeof(U) / (int)sizeof(T);  // elements of a piece
+    constexpr int kLanes = 128 / kPer;                     // pieces of a row
+    constexpr int kAt = 128 / kLanes;                      // rows at a time
+    const int n = n0 + (th % kLanes) * kPer, jl = th / kLanes;
+    if (n >= a.N) return;
+    T* o = out + (int64_t)(j0 + jl) * a.out_stride + n;
+    const uint8_t* st = stage + jl * PITCH + (th % kLanes) * (int)sizeof(U);
+    U v[ROWS / kAt];
+#pragma unroll
+    for (int j = 0; j < ROWS / kAt; ++j) v[j] = *reinterpret_cast<const U*>(st + j * kAt * PITCH);
+#pragma unroll
+    for (int j = 0; j < ROWS / kAt; ++j)
+        if (j0 + j * kAt + jl < live) *reinterpret_cast<U*>(o + (int64_t)(j * kAt) * a.out_stride) = v[j];
+}
+
 // Stores the chunks of a group's four warps: columns n0 .. n0 + 127 (this warp holds the 32 from
 // 32 q) of the `live` first of 32 rows, out pointing at the first row.  A few rows at a time the
 // chunks are transposed into the group's staging buffer (16-bit types: 8 x 8 matrices stored
@@ -311,9 +333,6 @@ __device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t 
 {
     constexpr int kPitch = mx_epi_pitch((int)sizeof(T));  // bytes of a staged row
     constexpr int kRows = mx_epi_rows((int)sizeof(T));    // rows staged at a time
-    constexpr int kPer = 16 / (int)sizeof(T);             // elements of a piece
-    constexpr int kLanes = 128 / kPer;                    // pieces of a row
-    const int64_t stride = a.out_stride;
 #pragma unroll
     for (int j0 = 0; j0 < 32; j0 += kRows) {
         if (j0 >= live) break;
@@ -341,21 +360,12 @@ __device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t 
         }
         group_sync(group);
         const int th = 32 * q + lane;  // thread of the group
-        if (a.vec) {
-            const int n = n0 + (th % kLanes) * kPer, jl = th / kLanes;
-            if (n < a.N) {
-                T* o = out + (j0 + jl) * stride + n;
-                const uint8_t* st = stage + jl * kPitch + (th % kLanes) * 16;
-#pragma unroll
-                for (int j = 0; j < kRows; j += 128 / kLanes)
-                    if (j0 + j + jl < live)
-                        *reinterpret_cast<uint4*>(o + j * stride) =
-                            *reinterpret_cast<const uint4*>(st + j * kPitch);
-            }
-        } else if (n0 + th < a.N) {
-            T* o = out + j0 * stride + n0 + th;
-            for (int j = 0; j < kRows && j0 + j < live; ++j)
-                o[j * stride] = reinterpret_cast<const T*>(stage + j * kPitch)[th];
+        if (a.unit == 16) {
+            store_rows<T, uint4, kRows, kPitch>(a, stage, out, j0, live, n0, th);
+        } else if (a.unit == 4) {
+            store_rows<T, uint32_t, kRows, kPitch>(a, stage, out, j0, live, n0, th);
+        } else if constexpr (sizeof(T) == 2) {
+            store_rows<T, uint16_t, kRows, kPitch>(a, stage, out, j0, live, n0, th);
         }
     }
 }

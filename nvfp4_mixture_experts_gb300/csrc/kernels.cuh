@@ -402,7 +402,7 @@ struct MxQuantArgs {
 };
 constexpr int kMxQuantRun = 4 * 32;   // eights of a row that a warp takes at a time
 using MxQuantKernel = void (*)(MxQuantArgs);
-MxQuantKernel mx_quant_kernel_for(int dtype, bool vec);
+MxQuantKernel mx_quant_kernel_for(int dtype, bool vec, bool short_rows);
 MxQuantKernel mx_quant_transposed_kernel_for(int dtype, bool words);
 // columns of a tile of the transposing quantiser, and its shared memory
 constexpr int mx_transposed_cols(int elem_bytes) { return 256 / elem_bytes; }
@@ -429,7 +429,7 @@ struct MxGemmArgs {
     int G, N, K;
     void* out;
     int64_t out_stride;
-    int vec;                 // the output rows may be stored in 16-byte pieces
+    int unit;                // bytes of the pieces (16, 4 or 2) that output rows are stored in
     int stages;              // of kMxStageBytes
     uint32_t* status;
 };

@@ -267,12 +267,69 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
     }
 }
 
-MxQuantKernel mx_quant_kernel_for(int dtype, bool vec)
+// The same for short rows: a thread per eight elements of all rows, so that a warp is full whatever
+// a row's length; a block's first thread stores its scale byte.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t units = a.cols >> 3, blocks = units >> 2;
+    const uint32_t n = (uint32_t)a.batch * a.rows * units;  // (fits: checked by the caller)
+    const int RB = (a.rows + 127) >> 7, KA = ((int)blocks + 3) >> 2;
+    for (uint32_t i0 = blockIdx.x * 256u; i0 < n; i0 += gridDim.x * 256u) {
+        const uint32_t i = i0 + threadIdx.x;
+        const uint32_t row = min(i, n - 1) / units;
+        const int u = (int)(min(i, n - 1) - row * units);
+        const int b = a.batch == 1 ? 0 : (int)(row / (uint32_t)a.rows), r = (int)(row - (uint32_t)b * a.rows);
+        const bool live = i < n && !(a.perm_src && a.perm_src[r] < 0);
+        Eight<T> e = {};
+        if (live)
+            e.template load<VEC>(static_cast<const T*>(a.x) + b * a.batch_stride + r * a.row_stride + u * 8);
+        const uint32_t s = mx_scale_byte(e.amax4(), a.rule);
+        if (!live) continue;
+        float v[8];
+        e.to_f32(v);
+        const float scale = mx_encode_scale(s);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] *= scale;
+        const uint32_t codes = s == 255u ? 0u : f32x8_to_e2m1(v);
+        reinterpret_cast<uint32_t*>(a.codes)[i] = codes;
+        if ((u & 3) == 0) {
+            const int kb = u >> 2;
+            if (a.layout == MOE_SF_CANONICAL) {
+                a.sf[(size_t)row * blocks + kb] = (uint8_t)s;
+            } else {  // the last block also zeroes the scales past it in its atom
+                uint8_t* at = a.sf + mx_sf_tiled(b, RB, KA, r, kb);
+                at[0] = (uint8_t)s;
+                if (kb == (int)blocks - 1)
+                    for (int z = 1; z < 4 - (kb & 3); ++z) at[z] = 0;
+            }
+        }
+        if (a.values) {
+            const float d = mx_decode_scale(s);
+            e2m1x8_to_f32(codes, v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] *= d;
+            e.from_f32(v);
+            e.store(static_cast<T*>(a.values) + (size_t)i * 8);
+        }
+    }
+}
+
+template <typename T>
+static MxQuantKernel mx_quant_of(bool vec, bool short_rows)
+{
+    if (short_rows) return vec ? mx_quant_short_kernel<T, true> : mx_quant_short_kernel<T, false>;
+    return vec ? mx_quant_kernel<T, true> : mx_quant_kernel<T, false>;
+}
+
+MxQuantKernel mx_quant_kernel_for(int dtype, bool vec, bool short_rows)
 {
     switch (dtype) {
-        case MOE_BF16: return vec ? mx_quant_kernel<__nv_bfloat16, true> : mx_quant_kernel<__nv_bfloat16, false>;
-        case MOE_FP16: return vec ? mx_quant_kernel<__half, true> : mx_quant_kernel<__half, false>;
-        default: return vec ? mx_quant_kernel<float, true> : mx_quant_kernel<float, false>;
+        case MOE_BF16: return mx_quant_of<__nv_bfloat16>(vec, short_rows);
+        case MOE_FP16: return mx_quant_of<__half>(vec, short_rows);
+        default: return mx_quant_of<float>(vec, short_rows);
     }
 }
 
