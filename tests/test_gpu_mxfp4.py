@@ -322,11 +322,37 @@ def test_product_of_quantised_rows_and_its_gradient():
     moe.moe_grouped_gemm_mxfp4(dc, ds, None, None, tc, ts, dx)
     want, mag = f64(dv) @ f64(tv[0]).T, np.abs(f64(dv)) @ np.abs(f64(tv[0])).T
     assert np.all(ref.rounded_ok(f64(dx), want, N * F * mag, "fp32"))
-    # differences: out is linear in the quantised rows; shift one row by twice its values
-    g = f64(tv[0]).T  # the transposed quantisation's weights [N, K]
-    lhs = (f64(dv) @ g * f64(xv)).sum()
-    rhs = (f64(dx) * f64(xv)).sum()
-    assert abs(lhs - rhs) <= N * F * (np.abs(f64(dv)) @ np.abs(g) * np.abs(f64(xv))).sum()
+
+
+def test_products_gradient_is_the_difference():
+    """With weights that both quantisations hold exactly, out is linear in the rows, so for any two
+    sets of representable rows L(A2) - L(A1) = <dL/dA, A2 - A1>, L = <dout, out>."""
+    rng = np.random.default_rng(5)
+    M, N, K = 40, 96, 160
+    grid = np.array([-4.0, -2.0, -1.0, 0.0, 1.0, 2.0, 4.0])
+
+    def exact(rows, cols):   # every block has the largest magnitude 4: scale 1, codes exact
+        m = rng.choice(grid, (rows, cols))
+        m[:, ::32], m[::32, :] = 4.0, -4.0
+        return torch.from_numpy(m).float().cuda()
+
+    def quant(t, transpose=False):
+        R, C = (t.shape[1], t.shape[0]) if transpose else t.shape
+        codes, sf = u8(R * C // 2).view(R, C // 2), u8(moe.moe_mxfp4_scale_bytes(1, R, C, moe.MOE_SF_TILED))
+        moe.moe_quant_mxfp4(t, codes, sf, moe.MOE_SF_TILED, transpose=transpose)
+        return codes, sf
+
+    def product(a, w, rows, cols):
+        out = torch.empty(rows, cols, device="cuda")
+        moe.moe_grouped_gemm_mxfp4(*a, None, None, w[0][None], w[1], out)
+        return out
+
+    w = exact(N, K)
+    a1, a2, dout = exact(M, K), exact(M, K), exact(M, N)
+    loss = [float((f64(dout) * f64(product(quant(a), quant(w), M, N))).sum()) for a in (a1, a2)]
+    grad = f64(product(quant(dout), quant(w, transpose=True), M, K))
+    # every sum is of integers below 2^24: exact in fp32
+    assert loss[1] - loss[0] == (grad * (f64(a2) - f64(a1))).sum()
 
 
 def test_offsets_past_two_to_the_31():
