@@ -336,7 +336,7 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
         Tx, H = x.shape
         xs, one = x.stride()
         dt = _DTYPES[x.dtype]
-        if not (Tx == T and (one == 1 or H == 1) and dt == _DTYPES[rows.dtype] and
+        if not (Tx == T and (one == 1 or H == 1 or T == 0) and dt == _DTYPES[rows.dtype] and
                 rows.shape == (cap, H) and rows.is_contiguous()):
             _refuse("moe_dispatch")
         px, pr = x.data_ptr(), rows.data_ptr()
@@ -354,7 +354,7 @@ def moe_dispatch_backward(drows, inv, k, dx, stream=None):
     cap, Hr = drows.shape
     xs, one = dx.stride()
     dt = _DTYPES[dx.dtype]
-    if not (Hr == H and (one == 1 or H == 1) and drows.is_contiguous() and
+    if not (Hr == H and (one == 1 or H == 1 or T == 0) and drows.is_contiguous() and
             _DTYPES[drows.dtype] == dt and inv.numel() == T * k and inv.is_contiguous()):
         _refuse("moe_dispatch_backward")
     st = (_lib or load()).moe_dispatch_backward(drows.data_ptr(), dt, inv.data_ptr(), T, k, H, cap,
@@ -370,7 +370,7 @@ def moe_combine_weighted(y, inv, w, out, stream=None):
     cap, Hy = y.shape
     xs, one = out.stride()
     dt = _DTYPES[y.dtype]
-    if not (To == T and Hy == H and (one == 1 or H == 1) and y.is_contiguous() and
+    if not (To == T and Hy == H and (one == 1 or H == 1 or T == 0) and y.is_contiguous() and
             _DTYPES[out.dtype] == dt and inv.numel() == T * k and inv.is_contiguous() and
             w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32):
         _refuse("moe_combine_weighted")
@@ -387,7 +387,7 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
     To, H = dout.shape
     xs, one = dout.stride()
     dt = _DTYPES[dout.dtype]
-    ok = (To == T and (one == 1 or H == 1) and inv.numel() == T * k and inv.is_contiguous() and
+    ok = (To == T and (one == 1 or H == 1 or T == 0) and inv.numel() == T * k and inv.is_contiguous() and
           w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32)
     cap = None
     for t in (y, dy):
@@ -426,7 +426,7 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
         _refuse("moe_quant_mxfp4")
     n, dt = B * R * Cc, _DTYPES[x.dtype]
     scales = _sf_bytes(B, Cc, R >> 5, sf_layout) if transpose else _sf_bytes(B, R, Cc >> 5, sf_layout)
-    if not ((one == 1 or Cc == 1) and codes.numel() * 2 == n and codes.is_contiguous() and
+    if not ((one == 1 or Cc == 1 or n == 0) and codes.numel() * 2 == n and codes.is_contiguous() and
             sf.numel() == scales and sf.is_contiguous() and
             (perm_src is None or (perm_src.numel() == R and perm_src.element_size() == 4)) and
             (values is None or (values.numel() == n and values.is_contiguous() and
@@ -464,7 +464,7 @@ def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, w
             a_codes.element_size() == 1 and w_codes.element_size() == 1 and
             a_sf.numel() == _sf_bytes(1, cap, K2 >> 4, MOE_SF_TILED) and
             w_sf.numel() == _sf_bytes(G, N, K2 >> 4, MOE_SF_TILED) and
-            out.shape == (cap, N) and (one == 1 or N == 1) and
+            out.shape == (cap, N) and (one == 1 or N == 1 or cap == 0) and
             (counts is None) == (offsets is None) and
             (counts is None or (counts.numel() == G and offsets.numel() >= G))):
         _refuse("moe_grouped_gemm_mxfp4")

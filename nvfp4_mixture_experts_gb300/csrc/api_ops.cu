@@ -308,7 +308,9 @@ moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_
     // of them to fill the GPU (one row of 4096: 2.4 us and 1.6; 8192 x 4096: 24.8 and 29.5).
     const int64_t eights = (int64_t)batch * rows * (cols / 8);
     const int runs = ceil_div(cols / 8, kMxQuantRun);
-    const bool short_rows = eights <= (1 << 20) || 10 * (cols / 8) < 9 * runs * (int64_t)kMxQuantRun;
+    const bool short_rows =
+        eights <= (1 << 20) ||
+        (eights <= 0xffffffffll && 10 * (cols / 8) < 9 * runs * (int64_t)kMxQuantRun);
     const int64_t items = short_rows ? eights : (int64_t)batch * rows * runs;
     if (items > 0xffffffffll) return MOE_ERR_UNSUPPORTED;
     return launch(mx_quant_kernel_for(dtype, vec, short_rows),

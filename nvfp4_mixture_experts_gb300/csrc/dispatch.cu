@@ -362,28 +362,36 @@ DispatchSmallKernel dispatch_small_kernel_for(int unit_bytes)
 // ------------------------------------------------------------------ dispatch
 
 // rows[inv[t k + j]] = x[t]: a warp takes a run of pieces of one token and stores it to each of
-// the token's rows, so x is read once.
+// the token's rows, so x is read once.  Every warp loads its first run while the sort before it is
+// still at work (x was complete before the sort began; 8192 tokens x 4096 bf16, k 8: 101 -> 98 us;
+// prefetching the other runs into L2 meanwhile changed nothing: the writes are what takes the time).
 template <typename U>
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchArgs a)
 {
-    pdl_wait();
-    pdl_trigger();
-    constexpr int kRun = 8;  // pieces per lane
+    constexpr int kRun = kDispatchRun / 32;  // pieces per lane
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
     const int runs = (a.units + 32 * kRun - 1) / (32 * kRun);
+    const int64_t items = (int64_t)a.T * runs;
     const U* x = static_cast<const U*>(a.x);
     U* rows = static_cast<U*>(a.rows);
-    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-         i < (int64_t)a.T * runs; i += warps) {
+    U v[kRun];
+    auto load = [&](int64_t i) {
         const int64_t t = i / runs;
         const int u0 = (int)(i - t * runs) * 32 * kRun + lane;
-        const U* from = x + t * a.x_stride + u0;
-        const bool full = u0 - lane + 32 * kRun <= a.units;
-        U v[kRun];
 #pragma unroll
         for (int r = 0; r < kRun; ++r)
-            if (full || u0 + 32 * r < a.units) v[r] = from[32 * r];
+            if (u0 + 32 * r < a.units) v[r] = x[t * a.x_stride + u0 + 32 * r];
+    };
+    int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (i < items) load(i);
+    pdl_wait();
+    pdl_trigger();
+    for (bool loaded = true; i < items; i += warps, loaded = false) {
+        if (!loaded) load(i);
+        const int64_t t = i / runs;
+        const int u0 = (int)(i - t * runs) * 32 * kRun + lane;
+        const bool full = u0 - lane + 32 * kRun <= a.units;
         for (int j = 0; j < a.k; ++j) {
             const int row = a.inv[t * a.k + j];
             if ((uint32_t)row >= (uint32_t)a.rows_cap) continue;

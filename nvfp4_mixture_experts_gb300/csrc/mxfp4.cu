@@ -277,10 +277,11 @@ __global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
     const uint32_t units = a.cols >> 3, blocks = units >> 2;
     const uint32_t n = (uint32_t)a.batch * a.rows * units;  // (fits: checked by the caller)
     const int RB = (a.rows + 127) >> 7, KA = ((int)blocks + 3) >> 2;
-    for (uint32_t i0 = blockIdx.x * 256u; i0 < n; i0 += gridDim.x * 256u) {
-        const uint32_t i = i0 + threadIdx.x;
-        const uint32_t row = min(i, n - 1) / units;
-        const int u = (int)(min(i, n - 1) - row * units);
+    for (uint64_t i0 = blockIdx.x * 256u; i0 < n; i0 += gridDim.x * 256u) {
+        const uint64_t i = i0 + threadIdx.x;
+        const uint32_t at_most = (uint32_t)min(i, (uint64_t)n - 1);
+        const uint32_t row = at_most / units;
+        const int u = (int)(at_most - row * units);
         const int b = a.batch == 1 ? 0 : (int)(row / (uint32_t)a.rows), r = (int)(row - (uint32_t)b * a.rows);
         const bool live = i < n && !(a.perm_src && a.perm_src[r] < 0);
         Eight<T> e = {};
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] *= d;
             e.from_f32(v);
-            e.store(static_cast<T*>(a.values) + (size_t)i * 8);
+            e.store(static_cast<T*>(a.values) + i * 8);
         }
     }
 }

@@ -115,6 +115,15 @@ def test_shards_add_up():
         assert torch.all((sum(parts) - sum(one)).abs() <= (k + 1) * 2.0 ** -23 * mag)
 
 
+def test_no_tokens():
+    ex = MXExperts.from_master(4, 0, torch.randn(4, 64, 32, device="cuda"), torch.randn(4, 32, 32, device="cuda"))
+    x = torch.zeros(0, 32, device="cuda", requires_grad=True)
+    w = torch.zeros(0, 2, device="cuda", requires_grad=True)
+    out = ex(x, torch.zeros(0, 2, dtype=torch.int32, device="cuda"), w)
+    out.sum().backward()
+    assert out.shape == (0, 32) and x.grad.shape == (0, 32) and w.grad.shape == (0, 2)
+
+
 def test_quantise_pads_nothing():
     x = torch.randn(3, 64, device="cuda")
     codes, sf = quantise(x)
