@@ -101,7 +101,8 @@ struct Piece {
 // Up to kSmallPairs pairs one block does it alone, in the launch that also moves the rows, every
 // block of which sorts for itself (a few hundred cycles, less than a launch); more are shared out
 // over the blocks of one thread block cluster, which read each other's totals through distributed
-// shared memory.
+// shared memory.  A chain of latencies bounds both (loads, a dozen barriers, two cluster barriers):
+// one token's 8 pairs over 320 experts 4 us, 16384 pairs 6.5 us, 65536 pairs 10 us, 524288 pairs 55 us.
 struct SortShared {
     uint32_t tot[kMaxExperts];       // this block's pairs of each expert
     uint32_t off[kMaxExperts + 1];   // first row of each group
@@ -444,7 +445,9 @@ struct Pairs {
 
 // out[t] = sum_j w[t, j] rows[inv[t k + j]] (w null: 1): a warp takes a run of pieces of a token, the
 // rows and weights of the token's pairs held by its lanes; dropped pairs cost nothing, of the kept
-// ones four rows' loads are in flight at a time; fp32 sums in ascending j.
+// ones four rows' loads are in flight at a time; fp32 sums in ascending j.  Bound by memory: 8192
+// tokens x 4096 bf16, k 8: 91 us (604 MB, 6.6 TB/s); eight rows at a time need 115 registers, which
+// halves the warps (92 us; 2048 x 4096 fp32 with half of the pairs kept 33 us, 27.5 with four).
 template <typename T, int V>
 __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
 {
@@ -529,7 +532,10 @@ CombineKernel combine_rows_kernel_for(int dtype, int unit)
 // ------------------------------------------------------------------ combine's gradient
 
 // A block of W warps per token: dy rows = w dout, and the dot products <dout, y row> of the kept
-// pairs, four rows at a time, reduced over the block.
+// pairs, four rows at a time, reduced over the block: dout is read once for four rows, and dy leaves
+// in the pass that reads y.  Bound by memory and, for short rows, by a token's chain of loads and
+// sums: 8192 tokens x 2048 bf16, k 4: 47.5 us (302 MB, 6.4 TB/s); 7694 x 304, a quarter of six
+// pairs kept: 8.3 us.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(32 * W) combine_back_kernel(CombineBackArgs a)
 {
@@ -628,8 +634,10 @@ __global__ void __launch_bounds__(32 * W) combine_back_kernel(CombineBackArgs a)
     }
 }
 
-// As combine_back_kernel, for long rows and more than four pairs a token: eight pairs at a time, kept or
-// not, their rows and weights loaded by every thread alike (addresses in uniform registers).
+// As combine_back_kernel, for long rows and more than four pairs a token: eight pairs at a time,
+// kept or not, their rows and weights loaded by every thread alike (addresses in uniform registers),
+// so that dout is read once.  Bound by memory: 8192 tokens x 4096 bf16, k 8: 169.5 us (1.14 GB, 6.7
+// TB/s).
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(32 * W) combine_back_all_kernel(CombineBackArgs a)
 {

@@ -7,24 +7,30 @@
 // across tiles and results do not depend on the schedule.  tcgen05.mma.cta_group::2 with
 // kind::mxf4 multiplies E2M1 operands from shared memory under UE8M0 scales (one per 32 elements)
 // from TMEM.  Each CTA loads its own 128 weight rows and half of the group's rows, so a
-// 256-element k-stage brings 35 KB through each SM for 128 x 256 x 256 multiply-adds: half of
-// what a CTA by itself would need for its half of the tile.
+// 256-element k-stage brings 35 KB through each SM for 128 x 256 x 256 multiply-adds, where a CTA
+// by itself would need 51 KB.
 //
 // Warp roles (both CTAs unless said): warp 0 issues the TMA loads of its CTA's operands and
 // scales, all counted on the leader's stage barrier; warp 1 of the leader (cluster rank 0) copies
 // each stage's scales to TMEM (tcgen05.cp, in order with the MMAs) and issues the MMAs; warps
 // 2..9 read the accumulator (lane = weight row, column = group row) into registers, which frees it
-// for the MMAs, transpose it through shared memory and store 64-byte (16-bit types) or 128-byte
-// (fp32) pieces of the output rows.
+// for the MMAs, transpose it through shared memory and store whole 128-column rows.
+//
+// What bounds it: memory where weights are read once (8192 tokens of 320 experts, N 2560, K 4096:
+// 327 us for 2.26 GB, 6.9 TB/s and 4.2 PFLOP/s; 64 tokens: 198 us, 7.1 TB/s), the 35 KB per SM and
+// k-stage out of L2 where there are many rows (one group of 8192, N and K 4096: 46 us, 5.9
+// PFLOP/s, 0.62 of the tensor pipe), a chain of latencies where there are few (one row, N and K
+// 4096: 7.9 us; one token's gate_up over 320 experts, 45 MB: 14 us).
 //
 // No tile is split along its contraction, also where there are fewer tiles than pairs: a k-stage
-// of a lone tile takes some 220 cycles (its loads' latency over eight stages in flight), so 16 of
+// of a lone tile takes some 220 cycles (its loads' latency over the stages in flight), so 16 of
 // them cost less than 2 us, about what writing, counting and adding up parts would; one token's
-// gate_up (80 tiles, 45 MB of weights) is bound by memory already.
+// gate_up (80 tiles) is bound by memory already.
 //
-// TMEM (all 512 columns, so the allocation starts at column 0): two accumulators, of the even tiles at column 0 upwards, of the odd tiles
-// ending at column 448; two slots of a stage's scales in columns 448..511.  Two tiles of together
-// up to 448 columns overlap freely: the next tile's MMAs run while one is read out.
+// TMEM (all 512 columns, so the allocation starts at column 0): two accumulators, of the even
+// tiles at column 0 upwards, of the odd tiles ending at column 448; two slots of a stage's scales
+// in columns 448..511.  Two tiles of together up to 448 columns overlap freely: the next tile's
+// MMAs run while one is read out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -179,7 +179,8 @@ __device__ __forceinline__ void store_scales(uint8_t* sf, int layout, int64_t b,
 
 // Eight elements per thread, four neighbouring threads per block of 32: a warp's codes are 128
 // contiguous bytes.  A warp takes a run of kMxQuantRun eights of a row, its loads in flight
-// together.
+// together and a run ahead.  8192 x 4096 bf16: 24.9 us with values (152 MB, 6.1 TB/s: memory), 19.0
+// without (85 MB: the issue slots, 0.78 used); fp32 with values 44 us (6.5 TB/s).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
 {
@@ -267,8 +268,9 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
     }
 }
 
-// The same for short rows: a thread per eight elements of all rows, so that a warp is full whatever
-// a row's length; a block's first thread stores its scale byte.
+// The same for short rows and small matrices: a thread per eight elements of all rows, so that a warp
+// is full whatever a row's length; a block's first thread stores its scale byte.  262144 x 32 bf16
+// with values: 9.5 us (38 MB, half of it in L2); 1 x 4096: 1.5 us (the launch).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
 {
@@ -340,7 +342,8 @@ MxQuantKernel mx_quant_kernel_for(int dtype, bool vec, bool short_rows)
 // of a column (of two neighbouring columns, loaded as one word where WORDS says that they are
 // aligned), whose blocks of 32 of the transposed rows are its own: the loads run along the rows of
 // x (lanes = columns).  The transposed rows go out through shared memory, 128 elements (64 code
-// bytes) of a row at a time; a row's four scale bytes are one word.
+// bytes) of a row at a time; a row's four scale bytes are one word.  Bound by memory: 6 x 2560 x 4096
+// with values, fp32 83.5 us (537 MB, 6.4 TB/s), bf16 45.6 us (285 MB, 6.3 TB/s).
 template <typename T, bool WORDS>
 __global__ void __launch_bounds__(256) mx_quant_transposed_kernel(MxQuantArgs a)
 {
