@@ -303,14 +303,15 @@ moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_
     }
     const bool vec = rows_vec(x_d, (int64_t)cols * es, rows > 1 ? row_stride * es : 0) &&
                      (batch == 1 || batch_stride * es % 16 == 0);
-    // The kernel for long rows keeps a warp's runs in one row: it wants rows that fill whole runs
-    // (16384 x 512 bf16 with values: 10.3 us, 8.6 with the other; 262144 x 32: 69 and 9.5) and enough
-    // of them to fill the GPU (one row of 4096: 2.4 us and 1.6; 8192 x 4096: 24.8 and 29.5).
+    // The kernel for long rows keeps a warp's runs in one row: it wants rows that fill half of their
+    // runs or more (bf16 with values, this and the other: 5000 x 3584 14.4 and 17.1 us, 16384 x 512
+    // 8.6 and 8.7, 30000 x 256 9.7 and 8.2, 262144 x 32 63 and 9.7) and enough of them to fill the GPU
+    // (8192 x 4096 24.4 and 30.3, 2048 x 2048 4.7 and 4.9, 64 x 4096 2.3 and 1.6).
     const int64_t eights = (int64_t)batch * rows * (cols / 8);
     const int runs = ceil_div(cols / 8, kMxQuantRun);
     const bool short_rows =
-        eights <= (1 << 20) ||
-        (eights <= 0xffffffffll && 10 * (cols / 8) < 9 * runs * (int64_t)kMxQuantRun);
+        eights < (1 << 19) ||
+        (eights <= 0xffffffffll && 2 * (cols / 8) < runs * (int64_t)kMxQuantRun);
     const int64_t items = short_rows ? eights : (int64_t)batch * rows * runs;
     if (items > 0xffffffffll) return MOE_ERR_UNSUPPORTED;
     return launch(mx_quant_kernel_for(dtype, vec, short_rows),

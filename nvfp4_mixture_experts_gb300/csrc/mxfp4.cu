@@ -179,8 +179,9 @@ __device__ __forceinline__ void store_scales(uint8_t* sf, int layout, int64_t b,
 
 // Eight elements per thread, four neighbouring threads per block of 32: a warp's codes are 128
 // contiguous bytes.  A warp takes a run of kMxQuantRun eights of a row, its loads in flight
-// together and a run ahead.  8192 x 4096 bf16: 24.9 us with values (152 MB, 6.1 TB/s: memory), 19.0
-// without (85 MB: the issue slots, 0.78 used); fp32 with values 44 us (6.5 TB/s).
+// together.  8192 x 4096 bf16: 24.4 us with values (152 MB, 6.2 TB/s: memory), 16.1 without (85 MB, 5.3
+// TB/s: the issue slots); fp32 with values 43.6 us (6.6 TB/s).  A run loaded ahead of the work on the
+// one before took 99 registers and 17.8 us without values, the same with.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
 {
@@ -193,55 +194,33 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
     const uint32_t items = (uint32_t)a.batch * a.rows * runs;  // (fits: checked by the caller)
     const uint32_t step = gridDim.x * (blockDim.x >> 5);
     const int blocks = units >> 2, RB = (a.rows + 127) >> 7, KA = (blocks + 3) >> 2;
-    struct Item {
-        uint32_t row;   // of all matrices
-        int b, r, u0;   // matrix, row in it, this lane's first eight
-        bool live;
-    };
-    // item i of the warp, and its elements; the next item's are loaded ahead of this one's work
-    auto fetch = [&](uint32_t i, Item& it, Eight<T>(&e)[kPer]) {
-        it.live = false;
-        if (i >= items) return;
-        it.row = i / (uint32_t)runs;
-        it.u0 = (int)(i - it.row * runs) * kMxQuantRun + lane;
-        it.b = a.batch == 1 ? 0 : (int)(it.row / (uint32_t)a.rows);
-        it.r = (int)(it.row - (uint32_t)it.b * a.rows);
-        it.live = !(a.perm_src && a.perm_src[it.r] < 0);
-        if (!it.live) return;
-        const T* x = static_cast<const T*>(a.x) + it.b * a.batch_stride + it.r * a.row_stride + it.u0 * 8;
+    for (uint64_t i0 = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i0 < items; i0 += step) {
+        const uint32_t i = (uint32_t)i0;
+        const uint32_t row = i / (uint32_t)runs;                    // of all matrices
+        const int u0 = (int)(i - row * runs) * kMxQuantRun + lane;  // this lane's first eight
+        const int b = a.batch == 1 ? 0 : (int)(row / (uint32_t)a.rows);
+        const int r = (int)(row - (uint32_t)b * a.rows);
+        if (a.perm_src && a.perm_src[r] < 0) continue;
+        const T* x = static_cast<const T*>(a.x) + b * a.batch_stride + r * a.row_stride + u0 * 8;
+        Eight<T> e[kPer] = {};
 #pragma unroll
         for (int p = 0; p < kPer; ++p)
-            if (it.u0 + 32 * p < units) e[p].template load<VEC>(x + 256 * p);
-    };
-    uint32_t i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    Item next;
-    Eight<T> ahead[kPer] = {};
-    fetch(i, next, ahead);
-    for (; i < items; i += step) {
-        const Item it = next;
-        Eight<T> e[kPer];
-#pragma unroll
-        for (int p = 0; p < kPer; ++p) e[p] = ahead[p];
-        if (items - i > step) fetch(i + step, next, ahead);
-        if (!it.live) continue;
-        const int64_t at = (int64_t)it.row * units + it.u0;
+            if (u0 + 32 * p < units) e[p].template load<VEC>(x + 256 * p);
+        const int64_t at = (int64_t)row * units + u0;
         uint32_t* codes_at = reinterpret_cast<uint32_t*>(a.codes) + at;
         T* values_at = static_cast<T*>(a.values) + at * 8;
         // the scale word of this lane's first block's atom (tiled), or its scale byte
-        const int kb = it.u0 >> 2;
-        uint8_t* sf_at = a.sf + (a.layout == MOE_SF_TILED ? mx_sf_tiled(it.b, RB, KA, it.r, kb)
-                                                          : (size_t)it.row * blocks + kb);
-#pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-            const int u = it.u0 + 32 * p;
-            if (u - lane >= units) break;
-            const bool in = u < units;  // (a block's four lanes are in or out together)
+        const int kb = u0 >> 2;
+        uint8_t* sf_at = a.sf + (a.layout == MOE_SF_TILED ? mx_sf_tiled(b, RB, KA, r, kb)
+                                                          : (size_t)row * blocks + kb);
+        // piece p of the run; the bytes of blocks past the row's end are zero in the tiled layout
+        auto piece = [&](int p, bool in) {
             const uint32_t s = mx_scale_byte(e[p].amax4(), a.rule);
             // the scales of four blocks (16 lanes) in one word
             uint32_t word = in ? s << (8 * ((lane >> 2) & 3)) : 0u;
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
             word |= __shfl_xor_sync(0xffffffffu, word, 8);
-            if (!in) continue;
+            if (!in) return;
             float v[8];
             e[p].to_f32(v);
             const float scale = mx_encode_scale(s);
@@ -249,7 +228,7 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
             for (int q = 0; q < 8; ++q) v[q] *= scale;
             const uint32_t codes = s == 255u ? 0u : f32x8_to_e2m1(v);
             codes_at[32 * p] = codes;
-            // 8 blocks, two atoms, per 32 eights; the bytes past the row's blocks are zero
+            // 8 blocks, two atoms, per 32 eights
             if (a.layout == MOE_SF_TILED) {
                 if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(sf_at + 1024 * p) = word;
             } else if ((lane & 3) == 0) {
@@ -264,6 +243,15 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
                 o.from_f32(v);
                 o.store(values_at + 256 * p);
             }
+        };
+        // (a block's four lanes are in or out together)
+        if (u0 - lane + kMxQuantRun <= units) {
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) piece(p, true);
+        } else {
+#pragma unroll
+            for (int p = 0; p < kPer; ++p)
+                if (u0 - lane + 32 * p < units) piece(p, u0 + 32 * p < units);
         }
     }
 }

@@ -98,6 +98,20 @@ def test_quantiser_of_the_transpose(B, R, C, dtype):
                     layout, transpose=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("B,R,C,pad", [(1, 4100, 1056, 0), (3, 1001, 1504, 8), (1, 516, 8224, 1),
+                                       (1, 4097, 1024, 0)])
+def test_quantiser_of_large_matrices(B, R, C, pad, dtype):
+    """Rows that end inside a warp's run, and rows of no pair, in matrices of many runs."""
+    perm = np.arange(R, dtype=np.int32)
+    perm[R // 3::7] = -1
+    x = torch.zeros(B, R, C + pad, dtype=DT[dtype])[:, :, :C]
+    for b in range(B):
+        x[b] = matrix(R, C, dtype, b)
+    check_quant(x, dtype, False, moe.MOE_SF_TILED, perm=perm if B == 1 else None)
+    check_quant(x, dtype, True, moe.MOE_SF_CANONICAL)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("pad", [1, 8, 16])
