@@ -16,16 +16,20 @@
 // 2..9 read the accumulator (lane = weight row, column = group row) into registers, which frees it
 // for the MMAs, transpose it through shared memory and store whole 128-column rows.
 //
-// What bounds it: memory where weights are read once (8192 tokens of 320 experts, N 2560, K 4096:
-// 327 us for 2.26 GB, 6.9 TB/s and 4.2 PFLOP/s; 64 tokens: 198 us, 7.1 TB/s), the 35 KB per SM and
-// k-stage out of L2 where there are many rows (one group of 8192, N and K 4096: 46 us, 5.9
-// PFLOP/s, 0.62 of the tensor pipe), a chain of latencies where there are few (one row, N and K
-// 4096: 7.9 us; one token's gate_up over 320 experts, 45 MB: 14 us).
+// What bounds it.  Memory where weights are read once: 8192 tokens of 320 experts, N 2560, K 4096,
+// 328 us for 2.26 GB (6.9 TB/s, 4.2 PFLOP/s); 64 tokens, 198 us (7.1 TB/s); 257 tokens on 160
+// experts, N 4096, K 1280, fp32 out, 67.6 us (6.8 TB/s).  With few rows and few tiles the two
+// threads that issue loads and MMAs, 0.18 us a k-stage: one row, N 4096, K 4096 6.7 us, K 16384
+// 15.6 us (4 us of launch, group table, epilogue and exit); the last tiles of one token's gate_up
+// over 320 experts (80 tiles for 76 pairs) take 3 of its 13 us so.  With many rows the tensor pipe
+// and its scale copies, 0.28 us a k-stage where 16 pairs work (256 rows, N 4096, K 16384: 23 us),
+// 0.38 where all do and share L2 (one group of 8192, N and K 4096: 46 us, 5.9 PFLOP/s, 0.62 of the
+// tensor pipe).
 //
-// No tile is split along its contraction, also where there are fewer tiles than pairs: a k-stage
-// of a lone tile takes some 220 cycles (its loads' latency over the stages in flight), so 16 of
-// them cost less than 2 us, about what writing, counting and adding up parts would; one token's
-// gate_up (80 tiles) is bound by memory already.
+// No tile is split along its contraction, also where there are fewer tiles than pairs: the parts
+// would have to be written, counted and added up, through words that are zero before the call or
+// CTAs that wait for one another, for 2 us at most.  Fetching the last tiles' weights into L2 during
+// the tiles before gains nothing (13.9 us where 13.4 without).
 //
 // TMEM (all 512 columns, so the allocation starts at column 0): two accumulators, of the even
 // tiles at column 0 upwards, of the odd tiles ending at column 448; two slots of a stage's scales
@@ -234,8 +238,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // The ring of k-stages in shared memory.  Where no group has more than 64 rows a stage holds 32
 // group rows per CTA and one row block of scales instead of 128 and two, and nine of them fit
-// instead of six: with few tiles the loads in flight bound the product (one token's gate_up,
-// 16 k-stages a tile: 5 stages 350 cycles a k-stage, 8 stages 220).
+// instead of six (one token's gate_up with five stages of the large kind: 16.3 us, so 13.8).
 struct Stages {
     uint8_t* base;
     int n;                                   // stages
@@ -446,27 +449,42 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 const int nsc = ti.nt > 128 ? 2 : 1;            // row blocks of group-row scales
                 const uint32_t bytes = 2u * (16384 + 1024 + half * 128 + nsc * 1024);
                 const int wb = ti.g * ((args.N + 127) >> 7) + (wrow >> 7), tb = ti.row0 >> 7;
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait(&ctl.empty[at.stage], at.phase ^ 1u, abort)) {
-                        ok = false;
-                        break;
+                // A loop of its own for few rows, where this thread is what a lone tile waits for
+                // (one row, N 4096, K 16384: 18.2 us in the other loop, 16.7 in this one).
+                int kb = 0;
+                if (half == 16) {
+                    for (; kb < KB; ++kb) {
+                        if (!mbar_wait(&ctl.empty[at.stage], at.phase ^ 1u, abort)) break;
+                        uint8_t* p = sg.base + at.stage * sg.bytes;
+                        const uint32_t bar = full0 + at.stage * 8;
+                        if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at.stage], bytes);
+                        tma_pair_3d(p, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
+                        tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
+                        tma_pair_2d(p + sg.t, &tmT16, bar, kb * 32, trow, pol_t);
+                        tma_pair_2d(p + sg.st, &tmST, bar, kb * 256, tb, pol_t);
+                        at.next(sg.n);
                     }
-                    uint8_t* p = sg.base + at.stage * sg.bytes;
-                    const uint32_t bar = full0 + at.stage * 8;
-                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at.stage], bytes);
-                    tma_pair_3d(p, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
-                    tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
-                    if (half == 128) {
-                        tma_pair_2d(p + sg.t, &tmT, bar, kb * 32, trow, pol_t);
-                    } else {
-                        for (int i = 0; i < half; i += 16)
-                            tma_pair_2d(p + sg.t + i * 128, &tmT16, bar, kb * 32, trow + i, pol_t);
+                } else {
+                    for (; kb < KB; ++kb) {
+                        if (!mbar_wait(&ctl.empty[at.stage], at.phase ^ 1u, abort)) break;
+                        uint8_t* p = sg.base + at.stage * sg.bytes;
+                        const uint32_t bar = full0 + at.stage * 8;
+                        if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at.stage], bytes);
+                        tma_pair_3d(p, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
+                        tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
+                        if (half == 128) {
+                            tma_pair_2d(p + sg.t, &tmT, bar, kb * 32, trow, pol_t);
+                        } else {
+                            for (int i = 0; i < half; i += 16)
+                                tma_pair_2d(p + sg.t + i * 128, &tmT16, bar, kb * 32, trow + i, pol_t);
+                        }
+                        tma_pair_2d(p + sg.st, &tmST, bar, kb * 256, tb, pol_t);
+                        if (nsc == 2) tma_pair_2d(p + sg.st + 1024, &tmST, bar, kb * 256, tb + 1, pol_t);
+                        at.next(sg.n);
                     }
-                    tma_pair_2d(p + sg.st, &tmST, bar, kb * 256, tb, pol_t);
-                    if (nsc == 2) tma_pair_2d(p + sg.st + 1024, &tmST, bar, kb * 256, tb + 1, pol_t);
-                    issued = min(issued + 1, sg.n);
-                    at.next(sg.n);
                 }
+                issued = min(issued + kb, sg.n);
+                ok = kb == KB;
             }
             ok = __all_sync(0xffffffffu, ok);
         }
@@ -507,10 +525,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                     const uint32_t d_t = buf ? kAccEnd - ti.nt : 0;
                     const uint32_t idesc = idesc_mxf4(256, ti.nt), idesc2 = idesc | (2u << 4) | (2u << 29);
                     const bool two = ti.nt > 128;  // row blocks of group-row scales
+                    // a stage's barrier is looked at before the MMAs of the one before are issued
+                    // (one row, N 4096, K 16384: 16.7 us without, 15.6 with)
+                    bool ready = mbar_test(&ctl.full[at.stage], at.phase);
                     for (int kb = 0; kb < KB && ok; ++kb) {
-                        ok = mbar_wait(&ctl.full[at.stage], at.phase, abort);
+                        ok = ready || mbar_wait(&ctl.full[at.stage], at.phase, abort);
                         if (!ok) break;
                         tc_fence_after();
+                        Place next = at;
+                        next.next(sg.n);
+                        ready = mbar_test(&ctl.full[next.stage], next.phase);
                         const uint32_t o = at.stage * (sg.bytes >> 4);  // descriptor units
                         const uint64_t w = w0 + o, tk = t0 + o, cw = cw0 + o, ct = ct0 + o;
                         const uint32_t sc = kAccEnd + slot;
@@ -540,7 +564,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         }
                         tc_commit_pair(&ctl.empty[at.stage], 3);
                         slot ^= 32u;
-                        at.next(sg.n);
+                        at = next;
                     }
                     if (ok) tc_commit_pair(&ctl.acc_full[buf], 3);
                 }
