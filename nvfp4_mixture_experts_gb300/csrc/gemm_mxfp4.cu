@@ -597,11 +597,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             }
             tc_fence_after();
             const uint32_t acc = (buf ? kAccEnd - ti.nt : 0) + ((uint32_t)(q * 32) << 16);
-            const int nch = ti.nt >> 5;
+            const int nch = ti.nt >> 5, h0 = h ^ (it & 1);  // chunks; the group's first one
             uint32_t r[4][32];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (h + 2 * i < nch) load_chunk<T>(acc + 32 * (h + 2 * i), r[i]);
+                if (h0 + 2 * i < nch) load_chunk<T>(acc + 32 * (h0 + 2 * i), r[i]);
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 T* out = static_cast<T*>(args.out) + (int64_t)ti.row0 * args.out_stride;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int c = 32 * (h + 2 * i);
+                    const int c = 32 * (h0 + 2 * i);
                     if (c < ti.nt)
                         store_chunk<T>(args, r[i], stage, out + c * args.out_stride, ti.rows - c, n0, q, h,
                                        lane);
