@@ -88,8 +88,10 @@ moe_status combine_rows(const void* y_d, int32_t dtype, const int32_t* inv_d, co
     a.rows_cap = rows_cap;
     a.out = out_d;
     a.out_stride = out_stride;
-    const int64_t items = (int64_t)T * ceil_div((int)((int64_t)H * es / unit), combine_run(unit));
-    return launch(combine_rows_kernel_for(dtype, unit), dim3(blocks_for(items, 8, 16)), dim3(256), 0,
+    const int few = combine_few(k, T);
+    const int64_t items = (int64_t)ceil_div(T, combine_tokens(few)) *
+                          ceil_div((int)((int64_t)H * es / unit), combine_run(unit));
+    return launch(combine_rows_kernel_for(dtype, unit, few), dim3(blocks_for(items, 8, 16)), dim3(256), 0,
                   reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
@@ -238,14 +240,16 @@ moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_
     // former; x 304, k 6, 2 of 6 kept: 8.6 and 15).
     const int64_t row = (int64_t)H * es;
     const bool all = k > 4 && row > 4608;
-    // Warps per token: one, for long rows two, or as many more as give every SM its 16: a token's
-    // warps wait for one another at its end (7003 tokens x 1096, k 2: one warp 22 us, two 28; 8192
-    // x 4001, k 8: 275 and 258), but few tokens' latency counts (64 tokens x 4096, k 8: two warps
-    // 6.7 us, eight 3.8).
+    // Warps per token (or batch of tokens): one, for long rows two, or as many more as give every SM
+    // its 16: a token's warps wait for one another at its end (7003 tokens x 1096, k 3: one warp 20.7
+    // us, two 24.5; 8192 x 4001, k 8: 275 and 258), but few tokens' latency counts (64 tokens x 4096,
+    // k 8: two warps 6.7 us, eight 3.8).
+    const int few = combine_few(k, T), batches = ceil_div(T, combine_tokens(few));
     int warps = row <= 6144 && !all ? 1 : 2;
-    while (warps < 8 && (int64_t)T * warps < 16 * num_sms()) warps *= 2;
-    return launch(combine_back_kernel_for(dtype, unit, warps, all), dim3(blocks_for(T, 1, 64 / warps)),
-                  dim3(32 * warps), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
+    while (warps < 8 && (int64_t)batches * warps < 16 * num_sms()) warps *= 2;
+    return launch(combine_back_kernel_for(dtype, unit, warps, few, all),
+                  dim3(blocks_for(batches, 1, 64 / warps)), dim3(32 * warps), 0,
+                  reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
 size_t moe_mxfp4_scale_bytes(int32_t batch, int32_t rows, int32_t cols, int32_t sf_layout)

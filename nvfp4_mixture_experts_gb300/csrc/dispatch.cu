@@ -509,23 +509,93 @@ __global__ void __launch_bounds__(256) combine_rows_kernel(CombineArgs a)
     }
 }
 
-template <typename T>
-static CombineKernel combine_rows_of(int unit)
+// As combine_rows_kernel, for K pairs a token, one or two: a warp takes kCombineAt / K tokens at a time,
+// so that as many rows' loads are in flight: 8192 tokens x 4096 bf16, k 1: 21.9 us (134 MB, 6.1 TB/s),
+// k 2: 30.4 (201 MB, 6.6 TB/s).
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(256) combine_few_kernel(CombineArgs a)
 {
-    switch (unit / (int)sizeof(T)) {
-        case 8: if constexpr (sizeof(T) == 2) return combine_rows_kernel<T, 8>;
-        case 4: return combine_rows_kernel<T, 4>;
-        case 2: return combine_rows_kernel<T, 2>;
-        default: return combine_rows_kernel<T, 1>;
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kPer = combine_run(V * (int)sizeof(T)) / 32, kTokens = kCombineAt / K;
+    const int lane = threadIdx.x & 31;
+    const int units = a.H / V, runs = (units + 32 * kPer - 1) / (32 * kPer);
+    const int64_t items = (int64_t)((a.T + kTokens - 1) / kTokens) * runs;
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+    const T* y = static_cast<const T*>(a.y);
+    T* out = static_cast<T*>(a.out);
+    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < items; i += step) {
+        const int64_t b = i / runs, t0 = b * kTokens;
+        const int u0 = (int)(i - b * runs) * 32 * kPer + lane;
+        const int n = (int)min((int64_t)kTokens, a.T - t0);  // tokens
+        int row = -1;
+        float weight = 1.0f;
+        if (lane < n * K) {
+            row = a.inv[t0 * K + lane];
+            if (a.w) weight = a.w[t0 * K + lane];
+        }
+        Piece<T, V> p[kCombineAt][kPer];
+        bool kept[kCombineAt];
+#pragma unroll
+        for (int j = 0; j < kCombineAt; ++j) {
+            const int r = __shfl_sync(0xffffffffu, row, j);
+            kept[j] = (uint32_t)r < (uint32_t)a.rows_cap;
+            if (!kept[j]) continue;
+            const T* from = y + (int64_t)r * a.H + (int64_t)u0 * V;
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                if (u0 + 32 * q < units) p[j][q].load(from + 32 * V * q);
+        }
+#pragma unroll
+        for (int m = 0; m < kTokens; ++m) {
+            if (m >= n) break;
+            T* to = out + (t0 + m) * a.out_stride + (int64_t)u0 * V;
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+                float acc[V] = {};
+#pragma unroll
+                for (int j = m * K; j < (m + 1) * K; ++j) {
+                    const float w = __shfl_sync(0xffffffffu, weight, j);
+                    if (!kept[j]) continue;
+                    float f[V];
+                    p[j][q].unpack(f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, f[e], acc[e]);
+                }
+                if (u0 + 32 * q < units) {
+                    Piece<T, V> sum;
+                    sum.pack(acc);
+                    sum.store(to + 32 * V * q);
+                }
+            }
+        }
     }
 }
 
-CombineKernel combine_rows_kernel_for(int dtype, int unit)
+template <typename T, int V>
+static CombineKernel combine_rows_of(int few)
+{
+    return few == 1 ? combine_few_kernel<T, V, 1>
+         : few == 2 ? combine_few_kernel<T, V, 2> : combine_rows_kernel<T, V>;
+}
+
+template <typename T>
+static CombineKernel combine_rows_unit(int unit, int few)
+{
+    switch (unit / (int)sizeof(T)) {
+        case 8: if constexpr (sizeof(T) == 2) return combine_rows_of<T, 8>(few);
+        case 4: return combine_rows_of<T, 4>(few);
+        case 2: return combine_rows_of<T, 2>(few);
+        default: return combine_rows_of<T, 1>(few);
+    }
+}
+
+CombineKernel combine_rows_kernel_for(int dtype, int unit, int few)
 {
     switch (dtype) {
-        case MOE_BF16: return combine_rows_of<__nv_bfloat16>(unit);
-        case MOE_FP16: return combine_rows_of<__half>(unit);
-        default: return combine_rows_of<float>(unit);
+        case MOE_BF16: return combine_rows_unit<__nv_bfloat16>(unit, few);
+        case MOE_FP16: return combine_rows_unit<__half>(unit, few);
+        default: return combine_rows_unit<float>(unit, few);
     }
 }
 
@@ -634,6 +704,108 @@ __global__ void __launch_bounds__(32 * W) combine_back_kernel(CombineBackArgs a)
     }
 }
 
+// As combine_back_kernel, for K pairs a token, one or two: kCombineAt / K tokens at a time, so that as many
+// rows' loads are in flight: 8192 tokens x 4096 bf16, k 1: 36.8 us (201 MB, 5.5 TB/s), k 2: 52 (336 MB,
+// 6.5 TB/s).
+template <typename T, int V, int W, int K>
+__global__ void __launch_bounds__(32 * W) combine_back_few_kernel(CombineBackArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kAt = kCombineAt, kPer = back_per(V * (int)sizeof(T)), kTokens = kAt / K;
+    __shared__ float s_dot[2][W][kAt];  // of the even and the odd batches of the block
+    const int units = a.H / V;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const T* dout = static_cast<const T*>(a.dout);
+    const T* y = static_cast<const T*>(a.y);
+    T* dy = static_cast<T*>(a.dy);
+    int odd = 0;
+    for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < a.T; t0 += (int64_t)gridDim.x * kTokens, odd ^= 1) {
+        const int n = (int)min((int64_t)kTokens, a.T - t0) * K;  // pairs
+        int row = -1;
+        float weight = 0.0f;
+        if (lane < n) {
+            row = a.inv[t0 * K + lane];
+            weight = a.w[t0 * K + lane];
+        }
+        bool kept[kAt];
+        float dot[kAt];
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+            kept[j] = (uint32_t)__shfl_sync(0xffffffffu, row, j) < (uint32_t)a.rows_cap;
+            dot[j] = 0.0f;
+        }
+        for (int u = warp * 32; u < units; u += 32 * W * kPer) {  // (a warp's lanes stay together)
+            const int u0 = u + lane;
+            Piece<T, V> pd[kTokens][kPer], p[kAt][kPer];
+#pragma unroll
+            for (int m = 0; m < kTokens; ++m) {
+                if (!kept[m * K] && !kept[m * K + K - 1]) continue;
+                const T* from = dout + (t0 + m) * a.dout_stride + (int64_t)u0 * V;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q)
+                    if (u0 + 32 * W * q < units) pd[m][q].load(from + 32 * W * V * q);
+            }
+            if (a.dw) {
+#pragma unroll
+                for (int j = 0; j < kAt; ++j) {
+                    const int r = __shfl_sync(0xffffffffu, row, j);
+                    if (!kept[j]) continue;
+                    const T* yr = y + (int64_t)r * a.H + (int64_t)u0 * V;
+#pragma unroll
+                    for (int q = 0; q < kPer; ++q)
+                        if (u0 + 32 * W * q < units) p[j][q].load(yr + 32 * W * V * q);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                const int r = __shfl_sync(0xffffffffu, row, j);
+                const float w = __shfl_sync(0xffffffffu, weight, j);
+                if (!kept[j]) continue;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) {
+                    if (u0 + 32 * W * q >= units) break;
+                    float d[V];
+                    pd[j / K][q].unpack(d);
+                    if (a.dw) {
+                        float f[V];
+                        p[j][q].unpack(f);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) dot[j] = fmaf(d[e], f[e], dot[j]);
+                    }
+                    if (dy) {
+                        float g[V];
+#pragma unroll
+                        for (int e = 0; e < V; ++e) g[e] = w * d[e];
+                        Piece<T, V> pg;
+                        pg.pack(g);
+                        pg.store(dy + (int64_t)r * a.H + (int64_t)(u0 + 32 * W * q) * V);
+                    }
+                }
+            }
+        }
+        if (a.dw) {
+            float sum = 0.0f;  // lane j: this warp's share of pair j's dot product
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+                if (lane == j) sum = dot[j];
+            }
+            if constexpr (W > 1) {
+                if (lane < n) s_dot[odd][warp][lane] = sum;
+                __syncthreads();  // (the other buffer is free again once every warp is here)
+                if (warp == 0) {
+                    sum = 0.0f;
+                    if (lane < n)
+                        for (int q = 0; q < W; ++q) sum += s_dot[odd][q][lane];
+                }
+            }
+            if (warp == 0 && lane < n) a.dw[t0 * K + lane] = sum;
+        }
+    }
+}
+
 // As combine_back_kernel, for long rows and more than four pairs a token: eight pairs at a time,
 // kept or not, their rows and weights loaded by every thread alike (addresses in uniform registers),
 // so that dout is read once.  Bound by memory: 8192 tokens x 4096 bf16, k 8: 169.5 us (1.14 GB, 6.7
@@ -729,34 +901,45 @@ __global__ void __launch_bounds__(32 * W) combine_back_all_kernel(CombineBackArg
     }
 }
 
+template <typename T, int V, int W>
+static CombineBackKernel combine_back_warps(int few, bool all)
+{
+    if (few == 1) return combine_back_few_kernel<T, V, W, 1>;
+    if (few == 2) return combine_back_few_kernel<T, V, W, 2>;
+    if constexpr (W > 1) {
+        if (all) return combine_back_all_kernel<T, V, W>;
+    }
+    return combine_back_kernel<T, V, W>;
+}
+
 template <typename T, int V>
-static CombineBackKernel combine_back_of(int warps, bool all)
+static CombineBackKernel combine_back_of(int warps, int few, bool all)
 {
     switch (warps) {
-        case 1: return combine_back_kernel<T, V, 1>;
-        case 2: return all ? combine_back_all_kernel<T, V, 2> : combine_back_kernel<T, V, 2>;
-        case 4: return all ? combine_back_all_kernel<T, V, 4> : combine_back_kernel<T, V, 4>;
-        default: return all ? combine_back_all_kernel<T, V, 8> : combine_back_kernel<T, V, 8>;
+        case 1: return combine_back_warps<T, V, 1>(few, all);
+        case 2: return combine_back_warps<T, V, 2>(few, all);
+        case 4: return combine_back_warps<T, V, 4>(few, all);
+        default: return combine_back_warps<T, V, 8>(few, all);
     }
 }
 
 template <typename T>
-static CombineBackKernel combine_back_unit(int unit, int warps, bool all)
+static CombineBackKernel combine_back_unit(int unit, int warps, int few, bool all)
 {
     switch (unit / (int)sizeof(T)) {
-        case 8: if constexpr (sizeof(T) == 2) return combine_back_of<T, 8>(warps, all);
-        case 4: return combine_back_of<T, 4>(warps, all);
-        case 2: return combine_back_of<T, 2>(warps, all);
-        default: return combine_back_of<T, 1>(warps, all);
+        case 8: if constexpr (sizeof(T) == 2) return combine_back_of<T, 8>(warps, few, all);
+        case 4: return combine_back_of<T, 4>(warps, few, all);
+        case 2: return combine_back_of<T, 2>(warps, few, all);
+        default: return combine_back_of<T, 1>(warps, few, all);
     }
 }
 
-CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps, bool all)
+CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps, int few, bool all)
 {
     switch (dtype) {
-        case MOE_BF16: return combine_back_unit<__nv_bfloat16>(unit, warps, all);
-        case MOE_FP16: return combine_back_unit<__half>(unit, warps, all);
-        default: return combine_back_unit<float>(unit, warps, all);
+        case MOE_BF16: return combine_back_unit<__nv_bfloat16>(unit, warps, few, all);
+        case MOE_FP16: return combine_back_unit<__half>(unit, warps, few, all);
+        default: return combine_back_unit<float>(unit, warps, few, all);
     }
 }
 

@@ -370,7 +370,13 @@ __host__ __device__ constexpr int combine_run(int unit)
     return 32 * (unit == 16 ? 2 : unit == 8 ? 4 : 8);
 }
 using CombineKernel = void (*)(CombineArgs);
-CombineKernel combine_rows_kernel_for(int dtype, int unit);
+// Combine and its gradient for one or two pairs a token (0: their kernels for any number): a warp, or
+// a block, takes kCombineAt / few tokens together, which wants some hundreds of tokens (bf16, k 1,
+// combine and gradient, with and without: 8192 x 4096 21.9 and 32.8, 36.9 and 46.5 us; 500 x 2000 2.2
+// and 2.3, 2.3 and 3.5; 64 x 4096 2.1 and 1.6, 3.2 and 2.2).
+__host__ __device__ constexpr int combine_few(int k, int T) { return k <= 2 && T >= 256 ? k : 0; }
+__host__ __device__ constexpr int combine_tokens(int few) { return few ? kCombineAt / few : 1; }
+CombineKernel combine_rows_kernel_for(int dtype, int unit, int few);
 
 // pieces of a row that a thread of combine's gradient loads together
 __host__ __device__ constexpr int back_per(int unit) { return unit == 16 ? 1 : unit == 8 ? 2 : 4; }
@@ -386,7 +392,7 @@ struct CombineBackArgs {
 };
 using CombineBackKernel = void (*)(CombineBackArgs);
 // all: the form for long rows and more than four pairs a token
-CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps, bool all);
+CombineBackKernel combine_back_kernel_for(int dtype, int unit, int warps, int few, bool all);
 
 // ---- mxfp4.cu: MXFP4 quantisation and scale layouts
 struct MxQuantArgs {

@@ -109,6 +109,11 @@ ROWS = [  # T, H, E, k, off, El, align, ld, shift
     (70, 3, 6, 2, 0, 6, 1, 0, 0), (9, 7, 6, 2, 0, 6, 2, 2, 1), (600, 5, 6, 2, 1, 4, 1, 0, 3),
     (40, 4001, 16, 2, 0, 16, 1, 0, 0), (300, 1026, 16, 4, 0, 16, 1, 2, 0),
     (130, 2300, 16, 8, 0, 16, 1, 0, 2), (20, 777, 12, 12, 0, 12, 1, 9, 5),
+    # one or two pairs a token, several tokens together, the last ones fewer
+    (259, 4104, 16, 1, 0, 16, 1, 0, 0), (403, 1001, 20, 2, 3, 9, 1, 6, 0),
+    (1031, 520, 9, 1, 2, 4, 16, 8, 1), (258, 2300, 16, 2, 0, 16, 1, 2, 2),
+    (3001, 136, 8, 2, 4, 2, 1, 0, 0), (301, 7, 5, 1, 0, 5, 1, 1, 0),
+    (2501, 264, 6, 1, 0, 6, 128, 0, 0), (256, 2048, 4, 2, 0, 4, 1, 4, 0),
 ]
 
 
