@@ -23,8 +23,8 @@
 // 15.6 us (4 us of launch, group table, epilogue and exit); the last tiles of one token's gate_up
 // over 320 experts (80 tiles for 76 pairs) take 3 of its 13 us so.  With many rows the tensor pipe
 // (four MMAs 0.26 us a k-stage, 0.28 where 16 pairs work: 256 rows, N 4096, K 16384 23 us) and, where
-// all pairs do, L2: 36 KB per SM and k-stage in 0.38 us, 14 TB/s (one group of 8192, N and K 4096: 46
-// us, 5.9 PFLOP/s, 0.69 of the tensor pipe).
+// all pairs do, by its figures L2: 36 KB per SM and k-stage in 0.38 us, 14 TB/s (one group of 8192,
+// N and K 4096: 46 us, 5.9 PFLOP/s, 0.69 of the tensor pipe).
 //
 // No tile is split along its contraction, also where there are fewer tiles than pairs: the parts
 // would have to be written, counted and added up, through words that are zero before the call or
