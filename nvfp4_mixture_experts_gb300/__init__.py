@@ -8,6 +8,8 @@ kernels.  Importing raises if the compiled library is missing -- there is no fal
 import ctypes as C
 import os
 
+import torch
+
 from . import build as _build
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -143,11 +145,18 @@ def _stream(stream):
     if stream is None:
         global _cuda
         if _cuda is None:
-            import torch
             torch.cuda.current_stream()  # the CUDA context exists
             _cuda = torch._C
         return _cuda._cuda_getCurrentRawStream(_cuda._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _place(stream):
+    """(device, stream handle) of a launch: the current device, on which the tensors and a stream
+    given as a torch stream have to be (device -2, which no tensor has, for a stream that is not)."""
+    handle = _stream(stream)
+    dev = torch._C._cuda_getDevice()
+    return (dev if stream is None or getattr(stream, "device_index", dev) == dev else -2), handle
 
 
 # ---------------------------------------------------------------- C entry points
@@ -289,24 +298,35 @@ def moe_get_status(h, ws, stream=None):
 
 # ---------------------------------------------------------------- operators without a handle
 # Element types come from the tensors (int16 tensors are bf16 bit patterns, as above), sizes from
-# their shapes; a tensor whose type, shape or strides do not fit raises MoEError before the call.
-# (Small calls are bound by this side: each tensor's attributes are asked for once.)
+# their shapes; a tensor whose type, shape, strides or device do not fit raises MoEError before the
+# call: the C side sees addresses alone.  Ids, maps, counts and status words are int32, codes and
+# scales uint8, all contiguous; every tensor is on the current device.  (Small calls are bound by this
+# side: each tensor's attributes are asked for once.)
 
 class _Dtypes(dict):
-    """torch dtype -> moe_dtype (-1: none), filled at the first look-up."""
+    """torch dtype -> moe_dtype (-1: none)."""
 
     def __missing__(self, key):
-        import torch
-        self.update({torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_FP16,
-                     torch.float32: MOE_FP32})
-        return self.setdefault(key, -1)
+        return -1
 
 
-_DTYPES = _Dtypes()
+_DTYPES = _Dtypes({torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_FP16,
+                   torch.float32: MOE_FP32})
+_I32, _U8 = torch.int32, torch.uint8
 
 
 def _refuse(where):
     raise MoEError(MOE_ERR_INVALID, where)
+
+
+def _status_word(status):
+    """Whether a status argument (None: nothing) is an int32 word."""
+    return status is None or (status.dtype is _I32 and status.numel() >= 1)
+
+
+def _on(dev, t):
+    """Whether a tensor (None: nothing) is on the device."""
+    return t is None or t.get_device() == dev
 
 
 def _sf_bytes(batch, rows, blocks, sf_layout):
@@ -327,9 +347,12 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
     [rows_cap, H]; status: an int32 word that errors found on the device are or-ed into."""
     T, k = topk_ids.shape
     cap = perm_src.numel()
-    if not (topk_ids.is_contiguous() and topk_ids.element_size() == 4 and
-            inv.numel() == T * k and counts.numel() == num_local and
-            offsets.numel() == num_local + 1 and (x is None) == (rows is None)):
+    if not (topk_ids.dtype is _I32 and topk_ids.is_contiguous() and
+            inv.dtype is _I32 and inv.numel() == T * k and inv.is_contiguous() and
+            counts.dtype is _I32 and counts.numel() == num_local and counts.is_contiguous() and
+            offsets.dtype is _I32 and offsets.numel() == num_local + 1 and
+            offsets.is_contiguous() and perm_src.dtype is _I32 and perm_src.is_contiguous() and
+            _status_word(status) and (x is None) == (rows is None)):
         _refuse("moe_dispatch")
     H, xs, dt, px, pr = 1, 1, MOE_BF16, None, None
     if x is not None:
@@ -340,10 +363,15 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
                 rows.shape == (cap, H) and rows.is_contiguous()):
             _refuse("moe_dispatch")
         px, pr = x.data_ptr(), rows.data_ptr()
+    dev, handle = _place(stream)
+    if not (dev == topk_ids.get_device() == inv.get_device() == counts.get_device() ==
+            offsets.get_device() == perm_src.get_device() and
+            (x is None or dev == x.get_device() == rows.get_device()) and _on(dev, status)):
+        _refuse("moe_dispatch")
     st = (_lib or load()).moe_dispatch(
         px, dt, xs, topk_ids.data_ptr(), T, k, H, num_experts, local_off, num_local, row_align,
         cap, counts.data_ptr(), offsets.data_ptr(), perm_src.data_ptr(), inv.data_ptr(), pr,
-        _p(status), _stream(stream))
+        _p(status), handle)
     if st:
         _check(st, "moe_dispatch")
 
@@ -355,10 +383,14 @@ def moe_dispatch_backward(drows, inv, k, dx, stream=None):
     xs, one = dx.stride()
     dt = _DTYPES[dx.dtype]
     if not (Hr == H and (one == 1 or H == 1 or T == 0) and drows.is_contiguous() and
-            _DTYPES[drows.dtype] == dt and inv.numel() == T * k and inv.is_contiguous()):
+            _DTYPES[drows.dtype] == dt and inv.dtype is _I32 and inv.numel() == T * k and
+            inv.is_contiguous()):
+        _refuse("moe_dispatch_backward")
+    dev, handle = _place(stream)
+    if not dev == drows.get_device() == inv.get_device() == dx.get_device():
         _refuse("moe_dispatch_backward")
     st = (_lib or load()).moe_dispatch_backward(drows.data_ptr(), dt, inv.data_ptr(), T, k, H, cap,
-                                                dx.data_ptr(), xs, _stream(stream))
+                                                dx.data_ptr(), xs, handle)
     if st:
         _check(st, "moe_dispatch_backward")
 
@@ -371,11 +403,14 @@ def moe_combine_weighted(y, inv, w, out, stream=None):
     xs, one = out.stride()
     dt = _DTYPES[y.dtype]
     if not (To == T and Hy == H and (one == 1 or H == 1 or T == 0) and y.is_contiguous() and
-            _DTYPES[out.dtype] == dt and inv.numel() == T * k and inv.is_contiguous() and
-            w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32):
+            _DTYPES[out.dtype] == dt and inv.dtype is _I32 and inv.numel() == T * k and
+            inv.is_contiguous() and w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32):
+        _refuse("moe_combine_weighted")
+    dev, handle = _place(stream)
+    if not dev == y.get_device() == inv.get_device() == w.get_device() == out.get_device():
         _refuse("moe_combine_weighted")
     st = (_lib or load()).moe_combine_weighted(y.data_ptr(), dt, inv.data_ptr(), w.data_ptr(), T, k,
-                                               H, cap, out.data_ptr(), xs, _stream(stream))
+                                               H, cap, out.data_ptr(), xs, handle)
     if st:
         _check(st, "moe_combine_weighted")
 
@@ -387,8 +422,8 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
     To, H = dout.shape
     xs, one = dout.stride()
     dt = _DTYPES[dout.dtype]
-    ok = (To == T and (one == 1 or H == 1 or T == 0) and inv.numel() == T * k and inv.is_contiguous() and
-          w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32)
+    ok = (To == T and (one == 1 or H == 1 or T == 0) and inv.dtype is _I32 and inv.numel() == T * k and
+          inv.is_contiguous() and w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32)
     cap = None
     for t in (y, dy):
         if t is not None:
@@ -401,9 +436,13 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
               _DTYPES[dw.dtype] == MOE_FP32 and y is not None)
     if not ok:
         _refuse("moe_combine_backward")
+    dev, handle = _place(stream)
+    if not (dev == dout.get_device() == inv.get_device() == w.get_device() and _on(dev, y) and
+            _on(dev, dy) and _on(dev, dw)):
+        _refuse("moe_combine_backward")
     st = (_lib or load()).moe_combine_backward(dout.data_ptr(), dt, xs, _p(y), inv.data_ptr(),
                                                w.data_ptr(), T, k, H, cap or 0, _p(dy), _p(dw),
-                                               _stream(stream))
+                                               handle)
     if st:
         _check(st, "moe_combine_backward")
 
@@ -426,15 +465,21 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
         _refuse("moe_quant_mxfp4")
     n, dt = B * R * Cc, _DTYPES[x.dtype]
     scales = _sf_bytes(B, Cc, R >> 5, sf_layout) if transpose else _sf_bytes(B, R, Cc >> 5, sf_layout)
-    if not ((one == 1 or Cc == 1 or n == 0) and codes.numel() * 2 == n and codes.is_contiguous() and
-            sf.numel() == scales and sf.is_contiguous() and
-            (perm_src is None or (perm_src.numel() == R and perm_src.element_size() == 4)) and
+    if not ((one == 1 or Cc == 1 or n == 0) and codes.dtype is _U8 and codes.numel() * 2 == n and
+            codes.is_contiguous() and sf.dtype is _U8 and sf.numel() == scales and
+            sf.is_contiguous() and
+            (perm_src is None or (perm_src.dtype is _I32 and perm_src.numel() == R and
+                                  perm_src.is_contiguous())) and
             (values is None or (values.numel() == n and values.is_contiguous() and
                                 _DTYPES[values.dtype] == dt))):
         _refuse("moe_quant_mxfp4")
+    dev, handle = _place(stream)
+    if not (dev == x.get_device() == codes.get_device() == sf.get_device() and
+            _on(dev, perm_src) and _on(dev, values)):
+        _refuse("moe_quant_mxfp4")
     st = (_lib or load()).moe_quant_mxfp4(x.data_ptr(), dt, B, R, Cc, rs, bs, 1 if transpose else 0,
                                           scale_rule, _p(perm_src), codes.data_ptr(), sf.data_ptr(),
-                                          sf_layout, _p(values), _stream(stream))
+                                          sf_layout, _p(values), handle)
     if st:
         _check(st, "moe_quant_mxfp4")
 
@@ -442,9 +487,13 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
 def moe_mxfp4_tile_scales(sf, batch, rows, cols, sf_tiled, stream=None):
     if not (sf.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_CANONICAL) and
             sf_tiled.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_TILED) and
-            sf.is_contiguous() and sf_tiled.is_contiguous()):
+            sf.is_contiguous() and sf_tiled.is_contiguous() and sf.dtype is _U8 and
+            sf_tiled.dtype is _U8):
         _refuse("moe_mxfp4_tile_scales")
-    st = load().moe_mxfp4_tile_scales(_p(sf), batch, rows, cols, _p(sf_tiled), _stream(stream))
+    dev, handle = _place(stream)
+    if not dev == sf.get_device() == sf_tiled.get_device():
+        _refuse("moe_mxfp4_tile_scales")
+    st = (_lib or load()).moe_mxfp4_tile_scales(_p(sf), batch, rows, cols, _p(sf_tiled), handle)
     if st:
         _check(st, "moe_mxfp4_tile_scales")
 
@@ -461,17 +510,28 @@ def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, w
     cap, Ka = a_codes.shape
     xs, one = out.stride()
     if not (Ka == K2 and a_codes.is_contiguous() and w_codes.is_contiguous() and
-            a_codes.element_size() == 1 and w_codes.element_size() == 1 and
-            a_sf.numel() == _sf_bytes(1, cap, K2 >> 4, MOE_SF_TILED) and
-            w_sf.numel() == _sf_bytes(G, N, K2 >> 4, MOE_SF_TILED) and
+            a_codes.dtype is _U8 and w_codes.dtype is _U8 and
+            a_sf.dtype is _U8 and a_sf.numel() == _sf_bytes(1, cap, K2 >> 4, MOE_SF_TILED) and
+            a_sf.is_contiguous() and
+            w_sf.dtype is _U8 and w_sf.numel() == _sf_bytes(G, N, K2 >> 4, MOE_SF_TILED) and
+            w_sf.is_contiguous() and
             out.shape == (cap, N) and (one == 1 or N == 1 or cap == 0) and
             (counts is None) == (offsets is None) and
-            (counts is None or (counts.numel() == G and offsets.numel() >= G))):
+            (counts is None or (counts.dtype is _I32 and counts.numel() == G and
+                                counts.is_contiguous() and offsets.dtype is _I32 and
+                                offsets.numel() >= G and offsets.is_contiguous())) and
+            (ws is None or ws.is_contiguous()) and _status_word(status)):
+        _refuse("moe_grouped_gemm_mxfp4")
+    dev, handle = _place(stream)
+    if not (dev == a_codes.get_device() == a_sf.get_device() == w_codes.get_device() ==
+            w_sf.get_device() == out.get_device() and
+            (counts is None or dev == counts.get_device() == offsets.get_device()) and
+            _on(dev, ws) and _on(dev, status)):
         _refuse("moe_grouped_gemm_mxfp4")
     st = (_lib or load()).moe_grouped_gemm_mxfp4(
         a_codes.data_ptr(), a_sf.data_ptr(), cap, _p(counts), _p(offsets), G, w_codes.data_ptr(),
         w_sf.data_ptr(), N, 2 * K2, out.data_ptr(), _DTYPES[out.dtype], xs, _p(ws),
-        0 if ws is None else ws.nbytes, _p(status), _stream(stream))
+        0 if ws is None else ws.nbytes, _p(status), handle)
     if st:
         _check(st, "moe_grouped_gemm_mxfp4")
 
