@@ -553,6 +553,18 @@ MOE_API moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_
 MOE_API moe_status moe_selftest_bounded_wait(uint32_t* status_d, uint64_t limit_ns,
                                              moe_stream_t stream);
 
+/* Self-test of a wait that runs out in one of four warps that work together, as the grouped MXFP4
+ * product's epilogue does: of two groups of four warps one warp waits, with the epilogue's wait,
+ * for a phase that nothing completes, the others for one that is complete; then each group
+ * votes.  words_d[0] receives MOE_DEV_WAIT_TIMEOUT, words_d[1] a bit for every warp that went on
+ * (expected: 0xF0, the other group's; the first group's warps give up together).  limit_ns and
+ * synchronisation as moe_selftest_bounded_wait.  Returns MOE_ERR_TIMEOUT (the expected outcome),
+ * MOE_OK (any other), MOE_ERR_INVALID or MOE_ERR_CUDA.
+ * Passage: none; a self-test of this library's bounded waits (the pages have no
+ * counterpart). */
+MOE_API moe_status moe_selftest_group_wait(uint32_t* words_d, uint64_t limit_ns,
+                                           moe_stream_t stream);
+
 /* Passage: none; error text of this library (the pages have no counterpart). */
 MOE_API const char* moe_status_string(moe_status s);
 

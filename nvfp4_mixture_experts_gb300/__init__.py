@@ -74,6 +74,7 @@ SIGNATURES = {
     "moe_get_status": (C.c_int, [_V, _V, _V, C.POINTER(C.c_uint32)]),
     "moe_status_string": (C.c_char_p, [C.c_int]),
     "moe_selftest_bounded_wait": (C.c_int, [_V, C.c_uint64, _V]),
+    "moe_selftest_group_wait": (C.c_int, [_V, C.c_uint64, _V]),
     "moe_dispatch_rows_capacity": (_I, [_I] * 4),
     "moe_dispatch": (C.c_int, [_V, _I, _L, _V] + [_I] * 8 + [_V] * 7),
     "moe_dispatch_backward": (C.c_int, [_V, _I, _V] + [_I] * 4 + [_V, _L, _V]),
@@ -288,6 +289,12 @@ def moe_selftest_bounded_wait(status_word, limit_ns, stream=None):
     """Runs the bounded-wait failure self-test (status_word: a device tensor of >= 4 bytes);
     returns the status code (MOE_ERR_TIMEOUT expected)."""
     return load().moe_selftest_bounded_wait(_p(status_word), int(limit_ns), _stream(stream))
+
+
+def moe_selftest_group_wait(words, limit_ns, stream=None):
+    """Runs the self-test of a wait that runs out in one warp of a group (words: a device tensor
+    of >= 8 bytes); returns the status code (MOE_ERR_TIMEOUT expected)."""
+    return load().moe_selftest_group_wait(_p(words), int(limit_ns), _stream(stream))
 
 
 def moe_get_status(h, ws, stream=None):

@@ -402,4 +402,20 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
                         reinterpret_cast<cudaStream_t>(stream), true, tmW, tmT, tmT16, tmSW, tmST, a);
 }
 
+moe_status moe_selftest_group_wait(uint32_t* words_d, uint64_t limit_ns, moe_stream_t stream)
+{
+    const NvtxRange nvtx_range("moe_selftest_group_wait");
+    if (!words_d || !elem_aligned(words_d, 4) || limit_ns == 0 || limit_ns > kWaitLimitNs)
+        return MOE_ERR_INVALID;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint32_t words[2] = {};
+    if (cudaMemsetAsync(words_d, 0, sizeof words, s) != cudaSuccess) return MOE_ERR_CUDA;
+    group_wait_probe_kernel<<<1, 256, 0, s>>>(words_d, words_d + 1, limit_ns);
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyAsync(words, words_d, sizeof words, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return words[0] == MOE_DEV_WAIT_TIMEOUT && words[1] == 0xF0u ? MOE_ERR_TIMEOUT : MOE_OK;
+}
+
 }  // extern "C"

@@ -229,10 +229,11 @@ __device__ __forceinline__ Groups load_groups(const MxGemmArgs& a, int32_t* sm, 
     return Groups{start, cnt, first, G, (a.N + 255) / 256, most};
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns = kWaitLimitNs)
 {
     int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort, limit_ns) ? 1 : 0;
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
@@ -308,6 +309,22 @@ __device__ __forceinline__ void group_sync(int group)
     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
+// The same, and whether all four warps say ok: of four waits for one phase, some may see it complete
+// and others run out, and a warp that left alone would leave the rest at their next barrier.
+__device__ __forceinline__ bool group_all(int group, bool ok)
+{
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)ok), "r"(1 + group)
+        : "memory");
+    return all != 0;
+}
+
 // Stores a group's staged rows j0 .. j0 + ROWS - 1 (of `live`): columns n0 .. n0 + 127 in pieces of
 // type U, the largest (16, 4 or, 16-bit types, 2 bytes) that every output row is aligned to and a
 // whole number of; th: the thread of the group.
@@ -334,18 +351,19 @@ __device__ __forceinline__ void store_rows(const MxGemmArgs& a, const uint8_t* s
 // 32 q) of the `live` first of 32 rows, out pointing at the first row.  A few rows at a time the
 // chunks are transposed into the group's staging buffer (16-bit types: 8 x 8 matrices stored
 // transposed; fp32: a word per lane and row) and leave as 16-byte pieces of whole 128-column rows
-// (256 or 512 contiguous bytes), or (vec false) element by element.
+// (256 or 512 contiguous bytes), or in the smaller pieces that the output's rows are aligned to.  free:
+// the group has passed a barrier since it last read the buffer.
 template <typename T>
 __device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t (&r)[32],
                                             uint8_t* stage, T* out, int live, int n0, int q,
-                                            int group, int lane)
+                                            int group, int lane, bool free)
 {
     constexpr int kPitch = mx_epi_pitch((int)sizeof(T));  // bytes of a staged row
     constexpr int kRows = mx_epi_rows((int)sizeof(T));    // rows staged at a time
 #pragma unroll
     for (int j0 = 0; j0 < 32; j0 += kRows) {
         if (j0 >= live) break;
-        group_sync(group);  // the buffer has been read
+        if (j0 || !free) group_sync(group);  // the buffer has been read
         if constexpr (sizeof(T) == 2) {
             const uint32_t at = smem_u32(stage) + (lane & 7) * kPitch + q * 64 + (lane >> 3) * 16;
 #pragma unroll
@@ -588,7 +606,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         for (int t = pair; t < ntiles; t += npairs, ++it) {
             const Tile ti = find_tile(gs, t);
             const int buf = it & 1;
-            if (!warp_wait(&ctl.acc_full[buf], (it >> 1) & 1, abort)) {
+            // the group's warps go on or leave together (this is also the tile's first barrier: the
+            // staging buffer has been read)
+            if (!group_all(h, warp_wait(&ctl.acc_full[buf], (it >> 1) & 1, abort))) {
                 if (lane == 0) {
                     set_status(args.status, MOE_DEV_WAIT_TIMEOUT);
                     *abort = 1;
@@ -614,7 +634,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                     const int c = 32 * (h0 + 2 * i);
                     if (c < ti.nt)
                         store_chunk<T>(args, r[i], stage, out + c * args.out_stride, ti.rows - c, n0, q, h,
-                                       lane);
+                                       lane, i == 0);
                 }
             }
         }
@@ -625,6 +645,29 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(ctl.tmem, 512);
+    }
+}
+
+// Two groups of four warps that wait as the epilogue does: warp 1's phase never completes, the
+// others' has.  Bit w of *went_on: warp w passed its group's vote.
+__global__ void __launch_bounds__(256) group_wait_probe_kernel(uint32_t* status, uint32_t* went_on,
+                                                               uint64_t limit_ns)
+{
+    __shared__ uint64_t done, never;
+    __shared__ int zero;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2;
+    if (threadIdx.x == 0) {
+        mbar_init(&done, 1);
+        mbar_init(&never, 1);
+        zero = 0;
+        fence_barrier_init();
+        mbar_arrive(&done);
+    }
+    __syncthreads();
+    const bool all = group_all(group, warp_wait(warp == 1 ? &never : &done, 0, &zero, limit_ns));
+    if (lane == 0) {
+        if (all) atomicOr(went_on, 1u << warp);
+        else set_status(status, MOE_DEV_WAIT_TIMEOUT);
     }
 }
 

@@ -464,5 +464,6 @@ inline int gemm_mxfp4_smem(int stages, int G, int out_bytes)
 using MxGemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
                               MxGemmArgs);
 MxGemmKernel gemm_mxfp4_kernel_for(int out_dtype);
+__global__ void group_wait_probe_kernel(uint32_t* status, uint32_t* went_on, uint64_t limit_ns);
 
 }  // namespace moe
