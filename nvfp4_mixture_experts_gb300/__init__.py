@@ -155,6 +155,9 @@ def _stream(stream):
 def _place(stream):
     """(device, stream handle) of a launch: the current device, on which the tensors and a stream
     given as a torch stream have to be (device -2, which no tensor has, for a stream that is not)."""
+    if stream is None and _cuda is not None:
+        dev = _cuda._cuda_getDevice()
+        return dev, _cuda._cuda_getCurrentRawStream(dev)
     handle = _stream(stream)
     dev = torch._C._cuda_getDevice()
     return (dev if stream is None or getattr(stream, "device_index", dev) == dev else -2), handle
@@ -319,21 +322,11 @@ class _Dtypes(dict):
 
 _DTYPES = _Dtypes({torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_FP16,
                    torch.float32: MOE_FP32})
-_I32, _U8 = torch.int32, torch.uint8
+_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
 
 
 def _refuse(where):
     raise MoEError(MOE_ERR_INVALID, where)
-
-
-def _status_word(status):
-    """Whether a status argument (None: nothing) is an int32 word."""
-    return status is None or (status.dtype is _I32 and status.numel() >= 1)
-
-
-def _on(dev, t):
-    """Whether a tensor (None: nothing) is on the device."""
-    return t is None or t.get_device() == dev
 
 
 def _sf_bytes(batch, rows, blocks, sf_layout):
@@ -359,21 +352,24 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
             counts.dtype is _I32 and counts.numel() == num_local and counts.is_contiguous() and
             offsets.dtype is _I32 and offsets.numel() == num_local + 1 and
             offsets.is_contiguous() and perm_src.dtype is _I32 and perm_src.is_contiguous() and
-            _status_word(status) and (x is None) == (rows is None)):
+            (status is None or (status.dtype is _I32 and status.numel())) and
+            (x is None) == (rows is None)):
         _refuse("moe_dispatch")
     H, xs, dt, px, pr = 1, 1, MOE_BF16, None, None
     if x is not None:
         Tx, H = x.shape
         xs, one = x.stride()
         dt = _DTYPES[x.dtype]
+        rows_cap, Hr = rows.shape
         if not (Tx == T and (one == 1 or H == 1 or T == 0) and dt == _DTYPES[rows.dtype] and
-                rows.shape == (cap, H) and rows.is_contiguous()):
+                rows_cap == cap and Hr == H and rows.is_contiguous()):
             _refuse("moe_dispatch")
         px, pr = x.data_ptr(), rows.data_ptr()
     dev, handle = _place(stream)
     if not (dev == topk_ids.get_device() == inv.get_device() == counts.get_device() ==
             offsets.get_device() == perm_src.get_device() and
-            (x is None or dev == x.get_device() == rows.get_device()) and _on(dev, status)):
+            (x is None or dev == x.get_device() == rows.get_device()) and
+            (status is None or status.get_device() == dev)):
         _refuse("moe_dispatch")
     st = (_lib or load()).moe_dispatch(
         px, dt, xs, topk_ids.data_ptr(), T, k, H, num_experts, local_off, num_local, row_align,
@@ -411,7 +407,7 @@ def moe_combine_weighted(y, inv, w, out, stream=None):
     dt = _DTYPES[y.dtype]
     if not (To == T and Hy == H and (one == 1 or H == 1 or T == 0) and y.is_contiguous() and
             _DTYPES[out.dtype] == dt and inv.dtype is _I32 and inv.numel() == T * k and
-            inv.is_contiguous() and w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32):
+            inv.is_contiguous() and w.is_contiguous() and w.dtype is _F32):
         _refuse("moe_combine_weighted")
     dev, handle = _place(stream)
     if not dev == y.get_device() == inv.get_device() == w.get_device() == out.get_device():
@@ -430,7 +426,7 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
     xs, one = dout.stride()
     dt = _DTYPES[dout.dtype]
     ok = (To == T and (one == 1 or H == 1 or T == 0) and inv.dtype is _I32 and inv.numel() == T * k and
-          inv.is_contiguous() and w.is_contiguous() and _DTYPES[w.dtype] == MOE_FP32)
+          inv.is_contiguous() and w.is_contiguous() and w.dtype is _F32)
     cap = None
     for t in (y, dy):
         if t is not None:
@@ -440,12 +436,13 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
             cap = rows
     if dw is not None:
         ok = (ok and dw.numel() == T * k and dw.is_contiguous() and
-              _DTYPES[dw.dtype] == MOE_FP32 and y is not None)
+              dw.dtype is _F32 and y is not None)
     if not ok:
         _refuse("moe_combine_backward")
     dev, handle = _place(stream)
-    if not (dev == dout.get_device() == inv.get_device() == w.get_device() and _on(dev, y) and
-            _on(dev, dy) and _on(dev, dw)):
+    if not (dev == dout.get_device() == inv.get_device() == w.get_device() and
+            (y is None or y.get_device() == dev) and (dy is None or dy.get_device() == dev) and
+            (dw is None or dw.get_device() == dev)):
         _refuse("moe_combine_backward")
     st = (_lib or load()).moe_combine_backward(dout.data_ptr(), dt, xs, _p(y), inv.data_ptr(),
                                                w.data_ptr(), T, k, H, cap or 0, _p(dy), _p(dw),
@@ -482,7 +479,8 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
         _refuse("moe_quant_mxfp4")
     dev, handle = _place(stream)
     if not (dev == x.get_device() == codes.get_device() == sf.get_device() and
-            _on(dev, perm_src) and _on(dev, values)):
+            (perm_src is None or perm_src.get_device() == dev) and
+            (values is None or values.get_device() == dev)):
         _refuse("moe_quant_mxfp4")
     st = (_lib or load()).moe_quant_mxfp4(x.data_ptr(), dt, B, R, Cc, rs, bs, 1 if transpose else 0,
                                           scale_rule, _p(perm_src), codes.data_ptr(), sf.data_ptr(),
@@ -515,6 +513,7 @@ def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, w
     offsets int32 (both None: one group, all rows); out [rows_cap, N]."""
     G, N, K2 = w_codes.shape
     cap, Ka = a_codes.shape
+    rows, No = out.shape
     xs, one = out.stride()
     if not (Ka == K2 and a_codes.is_contiguous() and w_codes.is_contiguous() and
             a_codes.dtype is _U8 and w_codes.dtype is _U8 and
@@ -522,18 +521,20 @@ def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, w
             a_sf.is_contiguous() and
             w_sf.dtype is _U8 and w_sf.numel() == _sf_bytes(G, N, K2 >> 4, MOE_SF_TILED) and
             w_sf.is_contiguous() and
-            out.shape == (cap, N) and (one == 1 or N == 1 or cap == 0) and
+            rows == cap and No == N and (one == 1 or N == 1 or cap == 0) and
             (counts is None) == (offsets is None) and
             (counts is None or (counts.dtype is _I32 and counts.numel() == G and
                                 counts.is_contiguous() and offsets.dtype is _I32 and
                                 offsets.numel() >= G and offsets.is_contiguous())) and
-            (ws is None or ws.is_contiguous()) and _status_word(status)):
+            (ws is None or ws.is_contiguous()) and
+            (status is None or (status.dtype is _I32 and status.numel()))):
         _refuse("moe_grouped_gemm_mxfp4")
     dev, handle = _place(stream)
     if not (dev == a_codes.get_device() == a_sf.get_device() == w_codes.get_device() ==
             w_sf.get_device() == out.get_device() and
             (counts is None or dev == counts.get_device() == offsets.get_device()) and
-            _on(dev, ws) and _on(dev, status)):
+            (ws is None or ws.get_device() == dev) and
+            (status is None or status.get_device() == dev)):
         _refuse("moe_grouped_gemm_mxfp4")
     st = (_lib or load()).moe_grouped_gemm_mxfp4(
         a_codes.data_ptr(), a_sf.data_ptr(), cap, _p(counts), _p(offsets), G, w_codes.data_ptr(),
