@@ -45,6 +45,7 @@ namespace moe {
 namespace {
 
 constexpr int kAccEnd = 448;                 // TMEM columns of accumulators; scales above
+constexpr uint64_t kCopyLandNs = 1000000;    // after a wait that ran out, for copies in flight
 
 struct Ctl {
     uint64_t full[kMxMaxStages], empty[kMxMaxStages], acc_full[2], acc_empty[2], drain;
@@ -641,6 +642,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // Where a wait of this CTA ran out, copies that it issued after the leader had given up may be on
+    // their way, counted on barriers of the leader's that nobody waits for: they land before it leaves
+    // (a copy takes microseconds).
+    if (*abort)
+        for (const uint64_t t0 = globaltimer(); globaltimer() - t0 < kCopyLandNs;) __nanosleep(1000);
     cluster_sync();  // the leader's MMAs have read this CTA's memory; both CTAs leave together
     if (warp == 1) {
         tc_fence_after();
