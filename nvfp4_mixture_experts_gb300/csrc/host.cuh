@@ -40,6 +40,13 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
 
 inline EncodeTiledFn encode_fn()
 {
+    // A host thread that has made no runtime call that needs a context has none, and encoding, a
+    // driver call, does not make it current; setting the thread's device does.
+    thread_local const bool context = [] {
+        int dev = 0;
+        return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+    }();
+    if (!context) return nullptr;
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
