@@ -418,7 +418,8 @@ MOE_API moe_status moe_forward_buffers(moe_handle h, void* ws_d, int32_t T, int3
 MOE_API moe_status moe_get_status(moe_handle h, void* ws_d, moe_stream_t stream, uint32_t* bits);
 
 /* ---- Tokens sorted by expert, and back, with their gradients.  No handle: sizes are
- * arguments, and the rows carry any of the moe_dtype types.  A row that belongs to no pair is
+ * arguments, and the rows carry any of the moe_dtype types.  Calls of several host threads, each
+ * on a stream and buffers of its own, need no lock.  A row that belongs to no pair is
  * neither written nor read.  T, k, H: tokens, routed experts per token (1..32), elements per
  * row; x_stride, out_stride etc.: elements between consecutive token rows (>= H); sorted rows
  * are contiguous [rows_cap][H].  Sums are taken in fp32 in ascending j and rounded once.

@@ -54,11 +54,13 @@ moe_status check_rows(int dtype, int T, int k, int H, int rows_cap)
 }
 
 // Raises a kernel's limit of dynamic shared memory where the default (48 KB with the static part,
-// up to 17 KB here) does not do.
-bool allow_smem(const void* kern, size_t bytes)
+// up to 17 KB here) does not do.  The limit belongs to the kernel, not to a launch, so it is always
+// raised to the `most` that any call takes: another thread's call between this and the launch may set
+// it too, but not lower.
+bool allow_smem(const void* kern, size_t bytes, size_t most)
 {
     return bytes <= 31 * 1024 ||
-           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ==
                cudaSuccess;
 }
 
@@ -164,15 +166,16 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
     }
     const bool small = P <= kSmallPairs;
     const size_t smem = sort_smem(num_local, small ? ceil_div((int)P, 32) : 32);
+    const size_t most = sort_smem(kMaxExperts, 32);
     if (small) {
         a.segment = 32;
         const DispatchSmallKernel kern = dispatch_small_kernel_for(unit);
-        if (!allow_smem(reinterpret_cast<const void*>(kern), smem)) return MOE_ERR_CUDA;
+        if (!allow_smem(reinterpret_cast<const void*>(kern), smem, most)) return MOE_ERR_CUDA;
         const int blocks = std::max(1, std::min(x_d ? T : ceil_div(rows_cap, 8192), num_sms()));
         return launch(kern, dim3(blocks), dim3(kSortThreads), smem, s, true, a, d);
     }
     a.rows_follow = x_d && rows_cap > 0 && num_local > 0;
-    if (!allow_smem(reinterpret_cast<const void*>(sort_pairs_kernel), smem) ||
+    if (!allow_smem(reinterpret_cast<const void*>(sort_pairs_kernel), smem, most) ||
         cudaFuncSetAttribute(sort_pairs_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
             cudaSuccess)
         return MOE_ERR_CUDA;
@@ -302,8 +305,9 @@ moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_
         // 16-bit types: two neighbouring columns are one aligned word in every row
         const bool words = addr(x_d) % 4 == 0 && row_stride % 2 == 0 && (batch == 1 || batch_stride % 2 == 0);
         const MxQuantKernel kern = mx_quant_transposed_kernel_for(dtype, words);
-        if (!allow_smem(reinterpret_cast<const void*>(kern), mx_transposed_smem(es))) return MOE_ERR_CUDA;
-        return launch(kern, dim3(blocks_for(tiles, 1, 16)), dim3(256), mx_transposed_smem(es), s, true, a);
+        const size_t smem = mx_transposed_smem(es);
+        if (!allow_smem(reinterpret_cast<const void*>(kern), smem, smem)) return MOE_ERR_CUDA;
+        return launch(kern, dim3(blocks_for(tiles, 1, 16)), dim3(256), smem, s, true, a);
     }
     const bool vec = rows_vec(x_d, (int64_t)cols * es, rows > 1 ? row_stride * es : 0) &&
                      (batch == 1 || batch_stride * es % 16 == 0);
@@ -391,9 +395,7 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
     a.stages = kMxStages;
     while (gemm_mxfp4_smem(a.stages, num_groups, es) > kSmemLimit) --a.stages;  // many groups: 5
     const int smem = gemm_mxfp4_smem(a.stages, num_groups, es);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
+    if (!allow_smem(reinterpret_cast<const void*>(kern), smem, kSmemLimit)) return MOE_ERR_CUDA;
     // at most this many tiles, however the rows fall into groups
     const int64_t tiles = std::min<int64_t>(num_groups + rows_cap / kMxTileRows, ceil_div(rows_cap, 128)) *
                           ceil_div(N, 256);
