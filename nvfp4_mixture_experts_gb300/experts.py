@@ -9,7 +9,8 @@ calls them:
             -> moe_quant_mxfp4 -> product with W13^T -> moe_dispatch_backward
 
 The quantisation of activations and gradients is passed straight through; the weights (adapters
-and routers train around them) have no gradient.  The elementwise gate is torch's, on all rows of
+and routers train around them) have no gradient, and the gradients have none (second derivatives
+raise).  The elementwise gate is torch's, on all rows of
 the sorted buffers: rows of no pair hold stale values that nothing downstream reads.
 """
 import torch
@@ -74,6 +75,18 @@ class MXExperts:
         return _Experts.apply(x, topk_w, topk_ids, self)
 
 
+class _FirstOrder(torch.autograd.Function):
+    """Gradients that are part of a graph (create_graph) and have no gradient of their own."""
+
+    @staticmethod
+    def forward(ctx, *grads):
+        return tuple(g.clone() for g in grads)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("MXExperts has no second derivatives")
+
+
 class _Experts(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, topk_w, topk_ids, ex):
@@ -103,6 +116,16 @@ class _Experts(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout):
+        with torch.no_grad():
+            grads = _Experts.gradients(ctx, dout)
+        # Under create_graph the gradients depend on x, topk_w and dout, but the kernels leave no
+        # graph: a second derivative must not be taken for zero.
+        if torch.is_grad_enabled():
+            grads = _FirstOrder.apply(*(g.requires_grad_() for g in grads))
+        return (*grads, None, None)
+
+    @staticmethod
+    def gradients(ctx, dout):
         ex, k = ctx.ex, ctx.k
         if ex.w13_t is None:
             raise RuntimeError("MXExperts without transposed weights has no backward")
@@ -117,4 +140,4 @@ class _Experts(torch.autograd.Function):
         drows = ctx.product(dgu, ex.w13_t, ex.hidden, y.dtype)
         dx = torch.empty_like(dout)
         moe_dispatch_backward(drows, inv, k, dx)
-        return dx, dw, None, None
+        return dx, dw
