@@ -44,7 +44,11 @@ def train(tokens=2048, hidden=1024, inter=512, experts=32, top_k=4, steps=20, lr
         losses.append(loss.detach())
         if say and step % 5 == 0:
             say("step %3d  loss %.4f" % (step, losses[-1].item()))
-    return torch.stack(losses).tolist()
+    losses = torch.stack(losses).tolist()
+    status, bits = ex.get_status()
+    if status:
+        raise RuntimeError("errors found on the device: bits %#x" % bits)
+    return losses
 
 
 if __name__ == "__main__":

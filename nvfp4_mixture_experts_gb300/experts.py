@@ -15,10 +15,11 @@ the sorted buffers: rows of no pair hold stale values that nothing downstream re
 """
 import torch
 
-from . import (MOE_MX_CEIL, MOE_SF_CANONICAL, MOE_SF_TILED, moe_combine_backward,
-               moe_combine_weighted, moe_dispatch, moe_dispatch_backward,
-               moe_dispatch_rows_capacity, moe_grouped_gemm_mxfp4, moe_mxfp4_scale_bytes,
-               moe_mxfp4_tile_scales, moe_quant_mxfp4)
+from . import (MOE_DEV_WAIT_TIMEOUT, MOE_ERR_DEVICE_STATUS, MOE_ERR_TIMEOUT, MOE_MX_CEIL, MOE_OK,
+               MOE_SF_CANONICAL, MOE_SF_TILED, moe_combine_backward, moe_combine_weighted,
+               moe_dispatch, moe_dispatch_backward, moe_dispatch_rows_capacity,
+               moe_grouped_gemm_mxfp4, moe_mxfp4_scale_bytes, moe_mxfp4_tile_scales,
+               moe_quant_mxfp4)
 
 ROW_ALIGN = 128  # groups start on whole row blocks of scales, as the product reads them
 
@@ -47,6 +48,7 @@ class MXExperts:
         self.num_local, two_inter, half_hidden = w13.shape
         self.hidden, self.inter = 2 * half_hidden, two_inter // 2
         self.w13, self.w2, self.w13_t, self.w2_t = (w13, w13_sf), (w2, w2_sf), w13_t, w2_t
+        self.status = torch.zeros(1, dtype=torch.int32, device=w13.device)
 
     @classmethod
     def from_master(cls, num_experts, local_off, w13, w2, backward=True):
@@ -71,8 +73,21 @@ class MXExperts:
 
     def __call__(self, x, topk_ids, topk_w):
         """The shard's partial sum [T, H] in x's type for tokens x [T, H] routed to topk_ids
-        (int32 [T, k]) with weights topk_w (float32 [T, k]); differentiable in x and topk_w."""
+        (int32 [T, k]) with weights topk_w (float32 [T, k]); differentiable in x and topk_w.
+        Asynchronous: errors found on the device are read with get_status."""
         return _Experts.apply(x, topk_w, topk_ids, self)
+
+
+    def get_status(self):
+        """(status, bits), as moe_get_status: waits for the current stream, reads the MOE_DEV_* bits
+        that the forwards and backwards since the last reading found on the device (an expert id out
+        of range, whose pair was dropped; a wait that ran out, whose results are incomplete) and
+        clears them.  MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_DEVICE_STATUS."""
+        bits = self.status.item()
+        self.status.zero_()
+        if bits & MOE_DEV_WAIT_TIMEOUT:
+            return MOE_ERR_TIMEOUT, bits
+        return (MOE_ERR_DEVICE_STATUS if bits else MOE_OK), bits
 
 
 class _FirstOrder(torch.autograd.Function):
@@ -97,11 +112,12 @@ class _Experts(torch.autograd.Function):
         perm, inv = torch.empty(cap, **i32), torch.empty(T * k, **i32)
         rows = torch.empty(cap, ex.hidden, dtype=dt, device=dev)
         moe_dispatch(x, topk_ids, ex.num_experts, ex.local_off, ex.num_local, ROW_ALIGN, counts,
-                     offsets, perm, inv, rows)
+                     offsets, perm, inv, rows, ex.status)
 
         def product(a, w, cols, dtype):
             out = torch.empty(cap, cols, dtype=dtype, device=dev)
-            moe_grouped_gemm_mxfp4(*quantise(a, perm_src=perm), counts, offsets, *w, out)
+            moe_grouped_gemm_mxfp4(*quantise(a, perm_src=perm), counts, offsets, *w, out,
+                                   status=ex.status)
             return out
 
         gu = product(rows, ex.w13, 2 * ex.inter, torch.float32)

@@ -39,3 +39,24 @@ def test_first_derivatives_do_not_change_under_create_graph(lib):
     ex(x, ids, w).sum().backward()
     assert x.grad.shape == x.shape and not x.grad.requires_grad
     assert w.grad.shape == w.shape and not w.grad.requires_grad
+
+
+def test_every_call_that_can_find_errors_on_the_device_is_lent_the_status_word(lib):
+    ex, (x, ids, w) = layer(), inputs()
+    del lib.calls[:]
+    ex(x, ids, w).sum().backward()
+    lent = {"moe_dispatch": [], "moe_grouped_gemm_mxfp4": []}
+    for name, args in lib.calls:
+        if name in lent:
+            lent[name].append(args[-2])          # the argument before the stream
+    assert lent == {"moe_dispatch": [ex.status.data_ptr()],
+                    "moe_grouped_gemm_mxfp4": [ex.status.data_ptr()] * 4}
+
+
+@pytest.mark.parametrize("bits,status", [(0, moe.MOE_OK), (moe.MOE_DEV_BAD_EXPERT_ID, moe.MOE_ERR_DEVICE_STATUS),
+                                         (moe.MOE_DEV_WAIT_TIMEOUT | moe.MOE_DEV_BAD_INDEX, moe.MOE_ERR_TIMEOUT)])
+def test_status_is_read_and_cleared(lib, bits, status):
+    ex = layer(backward=False)
+    ex.status.fill_(bits)
+    assert ex.get_status() == (status, bits)
+    assert ex.get_status() == (moe.MOE_OK, 0)
