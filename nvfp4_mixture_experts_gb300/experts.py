@@ -16,7 +16,7 @@ the sorted buffers: rows of no pair hold stale values that nothing downstream re
 import torch
 
 from . import (MOE_DEV_WAIT_TIMEOUT, MOE_ERR_DEVICE_STATUS, MOE_ERR_TIMEOUT, MOE_MX_CEIL, MOE_OK,
-               MOE_SF_CANONICAL, MOE_SF_TILED, moe_combine_backward, moe_combine_weighted,
+               MOE_SF_TILED, moe_combine_backward, moe_combine_weighted,
                moe_dispatch, moe_dispatch_backward, moe_dispatch_rows_capacity,
                moe_grouped_gemm_mxfp4, moe_mxfp4_scale_bytes, moe_mxfp4_tile_scales,
                moe_quant_mxfp4)
@@ -64,7 +64,6 @@ class MXExperts:
         tiled = []
         for codes, sf in ((w13, w13_sf), (w2, w2_sf)):
             n, rows, cols = codes.shape[0], codes.shape[1], codes.shape[2] * 2
-            assert sf.numel() == moe_mxfp4_scale_bytes(n, rows, cols, MOE_SF_CANONICAL)
             t = torch.empty(moe_mxfp4_scale_bytes(n, rows, cols, MOE_SF_TILED), dtype=torch.uint8,
                             device=codes.device)
             moe_mxfp4_tile_scales(sf, n, rows, cols, t)

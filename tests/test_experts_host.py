@@ -60,3 +60,16 @@ def test_status_is_read_and_cleared(lib, bits, status):
     ex.status.fill_(bits)
     assert ex.get_status() == (status, bits)
     assert ex.get_status() == (moe.MOE_OK, 0)
+
+
+def test_checkpoint_scales_of_another_size_are_refused(lib):
+    def parts():
+        return [torch.zeros(E, 2 * I, H // 2, dtype=torch.uint8), torch.zeros(E, 2 * I, H // 32, dtype=torch.uint8),
+                torch.zeros(E, H, I // 2, dtype=torch.uint8), torch.zeros(E, H, I // 32, dtype=torch.uint8)]
+
+    MXExperts.from_checkpoint(E, 0, *parts())
+    for i in (1, 3):
+        bad = parts()
+        bad[i] = bad[i][:, 1:].contiguous()
+        with pytest.raises(moe.MoEError):
+            MXExperts.from_checkpoint(E, 0, *bad)
