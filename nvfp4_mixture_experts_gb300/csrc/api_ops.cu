@@ -20,6 +20,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // Whether an address is a multiple of an element's size (null: yes).
 bool elem_aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
+// The same of arrays of 32-bit words: indices, counts, weights, status.
+template <typename... P>
+bool words_aligned(const P*... p)
+{
+    return (elem_aligned(p, 4) && ...);
+}
+
 // The largest power of two up to 16 that divides addresses, row sizes and strides (or-ed together).
 int largest_unit(uint64_t ored) { return (int)((ored | 16) & (~(ored | 16) + 1)); }
 
@@ -76,7 +83,7 @@ moe_status combine_rows(const void* y_d, int32_t dtype, const int32_t* inv_d, co
     if (T == 0) return MOE_OK;
     const int es = elem_bytes(dtype);
     if (!inv_d || !out_d || (rows_cap && !y_d) || (T > 1 && out_stride < H) ||
-        !elem_aligned(y_d, es) || !elem_aligned(out_d, es))
+        !elem_aligned(y_d, es) || !elem_aligned(out_d, es) || !words_aligned(inv_d, w_d))
         return MOE_ERR_INVALID;
     const int unit = largest_unit(addr(y_d) | addr(out_d) | (uint64_t)H * es |
                                   (T > 1 ? (uint64_t)out_stride * es : 0));
@@ -127,7 +134,8 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
         return MOE_ERR_INVALID;
     if (x_d && T > 1 && x_stride < H) return MOE_ERR_INVALID;
     if (!offsets_d || (num_local && !counts_d) || (T && (!topk_ids_d || !inv_d)) ||
-        (rows_cap && !perm_src_d))
+        (rows_cap && !perm_src_d) ||
+        !words_aligned(topk_ids_d, counts_d, offsets_d, perm_src_d, inv_d, status_d))
         return MOE_ERR_INVALID;
     if (x_d && (!elem_aligned(x_d, elem_bytes(dtype)) || !elem_aligned(rows_d, elem_bytes(dtype))))
         return MOE_ERR_INVALID;
@@ -221,7 +229,8 @@ moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_
         (T > 1 && dout_stride < H))
         return MOE_ERR_INVALID;
     const int es = elem_bytes(dtype);
-    if (!elem_aligned(dout_d, es) || !elem_aligned(y_d, es) || !elem_aligned(dy_d, es))
+    if (!elem_aligned(dout_d, es) || !elem_aligned(y_d, es) || !elem_aligned(dy_d, es) ||
+        !words_aligned(inv_d, w_d, dw_d))
         return MOE_ERR_INVALID;
     const int unit = largest_unit(addr(dout_d) | (dw_d ? addr(y_d) : 0) | addr(dy_d) | (uint64_t)H * es |
                                   (T > 1 ? (uint64_t)dout_stride * es : 0));
@@ -283,7 +292,8 @@ moe_status moe_quant_mxfp4(const void* x_d, int32_t dtype, int32_t batch, int32_
         (batch > 1 && batch_stride < 0))
         return MOE_ERR_INVALID;
     if (!aligned16(codes_d) || (values_d && !aligned16(values_d)) ||
-        (sf_layout == MOE_SF_TILED && !aligned16(sf_d)) || !elem_aligned(x_d, elem_bytes(dtype)))
+        (sf_layout == MOE_SF_TILED && !aligned16(sf_d)) || !elem_aligned(x_d, elem_bytes(dtype)) ||
+        !words_aligned(perm_src_d))
         return MOE_ERR_INVALID;
     MxQuantArgs a = {};
     a.x = x_d;
@@ -366,7 +376,8 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
         return MOE_ERR_INVALID;
     if (!aligned16(a_codes_d) || !aligned16(a_sf_d) || !aligned16(w_codes_d) || !aligned16(w_sf_d) ||
         (reinterpret_cast<uintptr_t>(out_d) % elem_bytes(out_dtype)) != 0 ||
-        (reinterpret_cast<uintptr_t>(ws_d) & 255) != 0 || (ws_bytes && !ws_d))
+        (reinterpret_cast<uintptr_t>(ws_d) & 255) != 0 || (ws_bytes && !ws_d) ||
+        !words_aligned(counts_d, offsets_d, status_d))
         return MOE_ERR_INVALID;
     const int KA = (K / 32 + 3) / 4, es = elem_bytes(out_dtype);
     CUtensorMap tmW, tmT, tmT16, tmSW, tmST;
