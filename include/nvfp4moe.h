@@ -440,7 +440,7 @@ MOE_API int32_t moe_dispatch_rows_capacity(int32_t T, int32_t k, int32_t num_loc
  *     last offset the total; perm_src_d [rows_cap] and inv_d [T*k] as above.  A pair whose row
  *     would pass rows_cap is dropped (inv -1) and sets MOE_DEV_ROWS_OVERFLOW; counts and
  *     offsets keep counting it;
- *   x_d and rows_d both NULL: the maps alone.
+ *   x_d and rows_d both NULL: the maps alone (and so, where T or rows_cap is 0, with either NULL).
  * num_experts and num_local up to 1024; row_align a power of two up to 128; status_d nullable.
  * Passage: [EP] (tokens reach the local experts of the shard, grouped by expert); rows in
  * bf16/fp16/fp32 for training are an addition of this library. */

@@ -427,6 +427,7 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
     dt = _DTYPES[dout.dtype]
     ok = (To == T and (one == 1 or H == 1 or T == 0) and inv.dtype is _I32 and inv.numel() == T * k and
           inv.is_contiguous() and w.is_contiguous() and w.dtype is _F32)
+    ok = ok and not (dy is None and dw is None)
     cap = None
     for t in (y, dy):
         if t is not None:

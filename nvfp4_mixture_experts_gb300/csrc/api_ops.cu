@@ -126,18 +126,19 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
                         uint32_t* status_d, moe_stream_t stream)
 {
     const NvtxRange nvtx_range("moe_dispatch");
-    if (!x_d != !rows_d) return MOE_ERR_INVALID;
-    const moe_status st = check_rows(x_d ? dtype : MOE_BF16, T, k, x_d ? H : 1, rows_cap);
+    const bool move = x_d && rows_d;  // (a tensor of no tokens or of no rows may have no address)
+    if (!move && ((rows_d && T > 0) || (x_d && rows_cap > 0))) return MOE_ERR_INVALID;
+    const moe_status st = check_rows(move ? dtype : MOE_BF16, T, k, move ? H : 1, rows_cap);
     if (st != MOE_OK) return st;
     if (num_experts < 1 || local_off < 0 || num_local < 0 || !align_ok(row_align) ||
         (int64_t)local_off + num_local > num_experts || k > num_experts)
         return MOE_ERR_INVALID;
-    if (x_d && T > 1 && x_stride < H) return MOE_ERR_INVALID;
+    if (move && T > 1 && x_stride < H) return MOE_ERR_INVALID;
     if (!offsets_d || (num_local && !counts_d) || (T && (!topk_ids_d || !inv_d)) ||
         (rows_cap && !perm_src_d) ||
         !words_aligned(topk_ids_d, counts_d, offsets_d, perm_src_d, inv_d, status_d))
         return MOE_ERR_INVALID;
-    if (x_d && (!elem_aligned(x_d, elem_bytes(dtype)) || !elem_aligned(rows_d, elem_bytes(dtype))))
+    if (move && (!elem_aligned(x_d, elem_bytes(dtype)) || !elem_aligned(rows_d, elem_bytes(dtype))))
         return MOE_ERR_INVALID;
     const int64_t P = (int64_t)T * k;
     if (num_experts > kMaxExperts || P + (int64_t)num_local * (row_align - 1) > 0x7fffffff)
@@ -159,7 +160,7 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
     a.status = status_d;
     DispatchArgs d = {};
     int unit = 16;
-    if (x_d) {
+    if (move) {
         const int es = elem_bytes(dtype);
         unit = largest_unit(addr(x_d) | addr(rows_d) | (uint64_t)H * es | (T > 1 ? (uint64_t)x_stride * es : 0));
         d.x = x_d;
@@ -179,10 +180,10 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
         a.segment = 32;
         const DispatchSmallKernel kern = dispatch_small_kernel_for(unit);
         if (!allow_smem(reinterpret_cast<const void*>(kern), smem, most)) return MOE_ERR_CUDA;
-        const int blocks = std::max(1, std::min(x_d ? T : ceil_div(rows_cap, 8192), num_sms()));
+        const int blocks = std::max(1, std::min(move ? T : ceil_div(rows_cap, 8192), num_sms()));
         return launch(kern, dim3(blocks), dim3(kSortThreads), smem, s, true, a, d);
     }
-    a.rows_follow = x_d && rows_cap > 0 && num_local > 0;
+    a.rows_follow = move && rows_cap > 0 && num_local > 0;
     if (!allow_smem(reinterpret_cast<const void*>(sort_pairs_kernel), smem, most) ||
         cudaFuncSetAttribute(sort_pairs_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
             cudaSuccess)
@@ -225,6 +226,7 @@ moe_status moe_combine_backward(const void* dout_d, int32_t dtype, int64_t dout_
     const moe_status st = check_rows(dtype, T, k, H, rows_cap);
     if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
+    if (!dy_d && !dw_d && rows_cap == 0) return MOE_OK;  // (dy has no rows, so it may have no address)
     if (!dout_d || !inv_d || !w_d || (!dy_d && !dw_d) || (dw_d && rows_cap && !y_d) ||
         (T > 1 && dout_stride < H))
         return MOE_ERR_INVALID;

@@ -15,11 +15,11 @@ the sorted buffers: rows of no pair hold stale values that nothing downstream re
 """
 import torch
 
-from . import (MOE_DEV_WAIT_TIMEOUT, MOE_ERR_DEVICE_STATUS, MOE_ERR_TIMEOUT, MOE_MX_CEIL, MOE_OK,
-               MOE_SF_TILED, moe_combine_backward, moe_combine_weighted,
-               moe_dispatch, moe_dispatch_backward, moe_dispatch_rows_capacity,
-               moe_grouped_gemm_mxfp4, moe_mxfp4_scale_bytes, moe_mxfp4_tile_scales,
-               moe_quant_mxfp4)
+from . import (MOE_DEV_WAIT_TIMEOUT, MOE_ERR_DEVICE_STATUS, MOE_ERR_TIMEOUT, MOE_ERR_UNSUPPORTED,
+               MOE_MX_CEIL, MOE_OK, MOE_SF_TILED, MoEError, moe_combine_backward,
+               moe_combine_weighted, moe_dispatch, moe_dispatch_backward,
+               moe_dispatch_rows_capacity, moe_grouped_gemm_mxfp4, moe_mxfp4_scale_bytes,
+               moe_mxfp4_tile_scales, moe_quant_mxfp4)
 
 ROW_ALIGN = 128  # groups start on whole row blocks of scales, as the product reads them
 
@@ -106,6 +106,8 @@ class _Experts(torch.autograd.Function):
     def forward(ctx, x, topk_w, topk_ids, ex):
         (T, k), dev, dt = topk_ids.shape, x.device, x.dtype
         cap = moe_dispatch_rows_capacity(T, k, ex.num_local, ROW_ALIGN)
+        if T and not cap:  # rows of no capacity would hold no pair
+            raise MoEError(MOE_ERR_UNSUPPORTED, "MXExperts: %d tokens, top-%d" % (T, k))
         i32 = dict(dtype=torch.int32, device=dev)
         counts, offsets = torch.empty(ex.num_local, **i32), torch.empty(ex.num_local + 1, **i32)
         perm, inv = torch.empty(cap, **i32), torch.empty(T * k, **i32)
