@@ -388,9 +388,9 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
     if (!make_tmap_3d(&tmW, w_codes_d, U32, K / 8, N, num_groups, K / 2, 32, 128, SW) ||
         !make_tmap(&tmT, a_codes_d, U32, K / 8, rows_cap, K / 2, 32, 128, SW) ||
         !make_tmap(&tmT16, a_codes_d, U32, K / 8, rows_cap, K / 2, 32, 16, SW) ||
-        !make_tmap(&tmSW, w_sf_d, U32, KA * 128, (uint64_t)num_groups * ceil_div(N, 128), KA * 512,
+        !make_tmap(&tmSW, w_sf_d, U32, KA * 128, (uint64_t)num_groups * ceil_div(N, 128), (uint64_t)KA * 512,
                    256, 1, NOSW) ||
-        !make_tmap(&tmST, a_sf_d, U32, KA * 128, ceil_div(rows_cap, 128), KA * 512, 256, 1, NOSW))
+        !make_tmap(&tmST, a_sf_d, U32, KA * 128, ceil_div(rows_cap, 128), (uint64_t)KA * 512, 256, 1, NOSW))
         return MOE_ERR_CUDA;
     MxGemmArgs a = {};
     a.rows_cap = rows_cap;

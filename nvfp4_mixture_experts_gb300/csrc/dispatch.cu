@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(256) combine_few_kernel(CombineArgs a)
     constexpr int kPer = combine_run(V * (int)sizeof(T)) / 32, kTokens = kCombineAt / K;
     const int lane = threadIdx.x & 31;
     const int units = a.H / V, runs = (units + 32 * kPer - 1) / (32 * kPer);
-    const int64_t items = (int64_t)((a.T + kTokens - 1) / kTokens) * runs;
+    const int64_t items = (int64_t)div_up(a.T, kTokens) * runs;
     const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
     const T* y = static_cast<const T*>(a.y);
     T* out = static_cast<T*>(a.out);

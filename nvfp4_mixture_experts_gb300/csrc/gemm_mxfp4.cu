@@ -198,7 +198,7 @@ __device__ __forceinline__ Groups load_groups(const MxGemmArgs& a, int32_t* sm, 
         }
         c[i] = max(c[i], 0);
         most = max(most, c[i]);
-        sum += (c[i] + kMxTileRows - 1) / kMxTileRows;
+        sum += div_up(c[i], kMxTileRows);
     }
     int v = sum;
 #pragma unroll
@@ -223,11 +223,11 @@ __device__ __forceinline__ Groups load_groups(const MxGemmArgs& a, int32_t* sm, 
             start[g0 + i] = pre;
             cnt[g0 + i] = c[i];
             first[g0 + i] = o[i];
-            pre += (c[i] + kMxTileRows - 1) / kMxTileRows;
+            pre += div_up(c[i], kMxTileRows);
         }
     if (tid == kMxThreads - 1) start[G] = pre;  // (no groups of its own, or the last ones)
     __syncthreads();
-    return Groups{start, cnt, first, G, (a.N + 255) / 256, most};
+    return Groups{start, cnt, first, G, div_up(a.N, 256), most};
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int KB = (args.K + 255) / 256;
+    const int KB = div_up(args.K, 256);
 
     if (warp == 0 && elect_one()) {
         for (int s = 0; s < kMxMaxStages; ++s) {
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 const int trow = ti.row0 + (int)rank * half, wrow = ti.n0 + (int)rank * 128;
                 const int nsc = ti.nt > 128 ? 2 : 1;            // row blocks of group-row scales
                 const uint32_t bytes = 2u * (16384 + 1024 + half * 128 + nsc * 1024);
-                const int wb = ti.g * ((args.N + 127) >> 7) + (wrow >> 7), tb = ti.row0 >> 7;
+                const int wb = ti.g * div_up(args.N, 128) + (wrow >> 7), tb = ti.row0 >> 7;
                 // A loop of its own for few rows, where this thread is what a lone tile waits for
                 // (one row, N 4096, K 16384: 18.2 us in the other loop, 16.7 in this one).
                 int kb = 0;

@@ -94,7 +94,7 @@ inline bool make_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType d
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+inline int ceil_div(int a, int b) { return moe::div_up(a, b); }
 
 inline moe_status check_launch()
 {

@@ -5,6 +5,9 @@
 
 namespace moe {
 
+// a / b rounded up, for a >= 0 up to the largest int
+__host__ __device__ constexpr int div_up(int a, int b) { return a / b + (a % b != 0); }
+
 constexpr int kPairsPerBlock = 1024;   // grouping: pairs per block of the counting sort
 
 // Debug builds (MOE_DEBUG defined) check every padded-row index and pair index that a

@@ -164,7 +164,7 @@ __device__ __forceinline__ void store_scales(uint8_t* sf, int layout, int64_t b,
                                              int blocks, int kb, uint32_t word)
 {
     if (layout == MOE_SF_TILED) {
-        *reinterpret_cast<uint32_t*>(sf + mx_sf_tiled(b, (R + 127) >> 7, (blocks + 3) >> 2, r, kb)) = word;
+        *reinterpret_cast<uint32_t*>(sf + mx_sf_tiled(b, div_up(R, 128), (blocks + 3) >> 2, r, kb)) = word;
     } else {
         uint8_t* o = sf + (b * R + r) * blocks + kb;
 #pragma unroll
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
     const int runs = (units + kMxQuantRun - 1) / kMxQuantRun;
     const uint32_t items = (uint32_t)a.batch * a.rows * runs;  // (fits: checked by the caller)
     const uint32_t step = gridDim.x * (blockDim.x >> 5);
-    const int blocks = units >> 2, RB = (a.rows + 127) >> 7, KA = (blocks + 3) >> 2;
+    const int blocks = units >> 2, RB = div_up(a.rows, 128), KA = (blocks + 3) >> 2;
     for (uint64_t i0 = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i0 < items; i0 += step) {
         const uint32_t i = (uint32_t)i0;
         const uint32_t row = i / (uint32_t)runs;                    // of all matrices
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
     pdl_trigger();
     const uint32_t units = a.cols >> 3, blocks = units >> 2;
     const uint32_t n = (uint32_t)a.batch * a.rows * units;  // (fits: checked by the caller)
-    const int RB = (a.rows + 127) >> 7, KA = ((int)blocks + 3) >> 2;
+    const int RB = div_up(a.rows, 128), KA = ((int)blocks + 3) >> 2;
     for (uint64_t i0 = blockIdx.x * 256u; i0 < n; i0 += gridDim.x * 256u) {
         const uint64_t i = i0 + threadIdx.x;
         const uint32_t at_most = (uint32_t)min(i, (uint64_t)n - 1);
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(256) mx_quant_transposed_kernel(MxQuantArgs a)
     T* s_val = reinterpret_cast<T*>(s_raw);            // [kCols][kPitch]
     uint4* s_code = s_raw + kCols * kPitch * sizeof(T) / 16;  // [kCols][5]: 64 bytes, 16 of padding
     uint32_t* s_scale = reinterpret_cast<uint32_t*>(s_code + kCols * 5);  // [kCols]
-    const int rt = (a.rows + 127) >> 7, ct = (a.cols + kCols - 1) / kCols;
+    const int rt = div_up(a.rows, 128), ct = div_up(a.cols, kCols);
     const int blocks = a.rows >> 5;
     const int c = threadIdx.x % 64 * kPer, rq = threadIdx.x / 64;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -457,7 +457,7 @@ MxQuantKernel mx_quant_transposed_kernel_for(int dtype, bool words)
 __global__ void __launch_bounds__(256) mx_tile_scales_kernel(const uint8_t* sf, int batch, int rows,
                                                              int blocks, uint8_t* tiled)
 {
-    const int RB = (rows + 127) >> 7, KA = (blocks + 3) >> 2;
+    const int RB = div_up(rows, 128), KA = (blocks + 3) >> 2;
     const int64_t n = (int64_t)batch * RB * KA * 128;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
          i += (int64_t)gridDim.x * blockDim.x) {
