@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "host.cuh"
 
@@ -69,6 +70,36 @@ bool allow_smem(const void* kern, size_t bytes, size_t most)
     return bytes <= 31 * 1024 ||
            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ==
                cudaSuccess;
+}
+
+// Blocks of the large sort's cluster: 16, more than the portable 8 (65536 pairs over 320 experts: 10.1
+// us, 14.4 with 8; 16384: 6.5 and 7.6), where the device takes one such cluster with the most shared
+// memory that a call wants (a part of a GPU may have no processing cluster of 16 SMs).  Asked once for a
+// device; the debug flavour always takes 8, so that its tests run that form.  0: an error.
+int sort_cluster_blocks(size_t most)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::atomic<int>* slot = dev < 64 ? &known[dev] : nullptr;
+    int blocks = slot ? slot->load(std::memory_order_relaxed) : 0;
+    if (blocks) return blocks;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortBlocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortBlocks);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = most;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const bool asked = cudaOccupancyMaxActiveClusters(&clusters, sort_pairs_kernel, &cfg) == cudaSuccess;
+    if (!asked) cudaGetLastError();  // (a size the device has no such cluster for may be an error)
+    blocks = asked && clusters > 0 && !kDebugChecks ? kSortBlocks : kSortBlocks / 2;
+    if (slot) slot->store(blocks, std::memory_order_relaxed);
+    return blocks;
 }
 
 bool align_ok(int a) { return a >= 1 && a <= 128 && (a & (a - 1)) == 0; }
@@ -184,14 +215,14 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
         return launch(kern, dim3(blocks), dim3(kSortThreads), smem, s, true, a, d);
     }
     a.rows_follow = move && rows_cap > 0 && num_local > 0;
-    if (!allow_smem(reinterpret_cast<const void*>(sort_pairs_kernel), smem, most) ||
+    if (!allow_smem(reinterpret_cast<const void*>(sort_pairs_kernel), most, most) ||
         cudaFuncSetAttribute(sort_pairs_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
             cudaSuccess)
         return MOE_ERR_CUDA;
-    // A cluster of 16 blocks, more than the portable 8 (65536 pairs over 320 experts: 10.1 us, 14.4
-    // with 8; 16384: 6.5 and 7.6): each of the GPU's processing clusters has 16 SMs and more.
-    a.segment = ceil_div((int)((P + 31) / 32), kSortBlocks * 32) * 32;
-    const moe_status sorted = launch_cluster(sort_pairs_kernel, kSortBlocks, dim3(kSortBlocks),
+    const int blocks = sort_cluster_blocks(most);
+    if (!blocks) return MOE_ERR_CUDA;
+    a.segment = ceil_div((int)((P + 31) / 32), blocks * 32) * 32;
+    const moe_status sorted = launch_cluster(sort_pairs_kernel, blocks, dim3(blocks),
                                              dim3(kSortThreads), smem, s, true, a);
     if (sorted != MOE_OK || !a.rows_follow) return sorted;
     const int64_t runs = (int64_t)T * ceil_div(d.units, kDispatchRun);
