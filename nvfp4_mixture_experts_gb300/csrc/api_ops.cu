@@ -68,8 +68,7 @@ moe_status check_rows(int dtype, int T, int k, int H, int rows_cap)
 bool allow_smem(const void* kern, size_t bytes, size_t most)
 {
     return bytes <= 31 * 1024 ||
-           cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ==
-               cudaSuccess;
+           taken(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
 }
 
 // Blocks of the large sort's cluster: 16, more than the portable 8 (65536 pairs over 320 experts: 10.1
@@ -80,7 +79,7 @@ int sort_cluster_blocks(size_t most)
 {
     static std::atomic<int> known[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (!taken(cudaGetDevice(&dev))) return 0;
     std::atomic<int>* slot = dev < 64 ? &known[dev] : nullptr;
     int blocks = slot ? slot->load(std::memory_order_relaxed) : 0;
     if (blocks) return blocks;
@@ -95,8 +94,8 @@ int sort_cluster_blocks(size_t most)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int clusters = 0;
-    const bool asked = cudaOccupancyMaxActiveClusters(&clusters, sort_pairs_kernel, &cfg) == cudaSuccess;
-    if (!asked) cudaGetLastError();  // (a size the device has no such cluster for may be an error)
+    // (a size that the device has no cluster of may be an error)
+    const bool asked = taken(cudaOccupancyMaxActiveClusters(&clusters, sort_pairs_kernel, &cfg));
     blocks = asked && clusters > 0 && !kDebugChecks ? kSortBlocks : kSortBlocks / 2;
     if (slot) slot->store(blocks, std::memory_order_relaxed);
     return blocks;
@@ -216,8 +215,7 @@ moe_status moe_dispatch(const void* x_d, int32_t dtype, int64_t x_stride,
     }
     a.rows_follow = move && rows_cap > 0 && num_local > 0;
     if (!allow_smem(reinterpret_cast<const void*>(sort_pairs_kernel), most, most) ||
-        cudaFuncSetAttribute(sort_pairs_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-            cudaSuccess)
+        !taken(cudaFuncSetAttribute(sort_pairs_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)))
         return MOE_ERR_CUDA;
     const int blocks = sort_cluster_blocks(most);
     if (!blocks) return MOE_ERR_CUDA;

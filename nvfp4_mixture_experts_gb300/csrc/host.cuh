@@ -96,6 +96,14 @@ inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 inline int ceil_div(int a, int b) { return moe::div_up(a, b); }
 
+// Whether a runtime call succeeded; the error of one that did not is reported by its caller, and taken
+// from the thread's last error, where the check of a later launch would find it.
+inline bool taken(cudaError_t e)
+{
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess;
+}
+
 inline moe_status check_launch()
 {
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -117,9 +125,7 @@ moe_status launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cu
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
+    return taken(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...)) ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // A launch whose blocks wait on one another (the fused W4A16 GEMV's down items wait for gate_up
@@ -141,9 +147,7 @@ moe_status launch_coop(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
+    return taken(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...)) ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // As launch, for a kernel whose blocks run as clusters of `blocks`.
@@ -165,9 +169,7 @@ moe_status launch_cluster(void (*kern)(KArgs...), int blocks, dim3 grid, dim3 bl
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) == cudaSuccess
-               ? MOE_OK
-               : MOE_ERR_CUDA;
+    return taken(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...)) ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // As launch, for a kernel whose blocks run as CTA pairs.
