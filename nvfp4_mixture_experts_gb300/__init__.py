@@ -330,6 +330,7 @@ class _Dtypes(dict):
 _DTYPES = _Dtypes({torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_FP16,
                    torch.float32: MOE_FP32})
 _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
+_MOST = 0x7fffffff  # sizes are 32-bit numbers on the C side; an or of sizes passes it if one does
 
 
 def _refuse(where):
@@ -344,6 +345,8 @@ def _sf_bytes(batch, rows, blocks, sf_layout):
 
 
 def moe_dispatch_rows_capacity(T, k, num_local, row_align):
+    if not 0 <= T <= _MOST:
+        return 0
     return load().moe_dispatch_rows_capacity(T, k, num_local, row_align)
 
 
@@ -354,7 +357,7 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
     [rows_cap, H]; status: an int32 word that errors found on the device are or-ed into."""
     T, k = topk_ids.shape
     cap = perm_src.numel()
-    if not (topk_ids.dtype is _I32 and topk_ids.is_contiguous() and
+    if not ((T | k | cap) <= _MOST and topk_ids.dtype is _I32 and topk_ids.is_contiguous() and
             inv.dtype is _I32 and inv.numel() == T * k and inv.is_contiguous() and
             counts.dtype is _I32 and counts.numel() == num_local and counts.is_contiguous() and
             offsets.dtype is _I32 and offsets.numel() == num_local + 1 and
@@ -368,7 +371,7 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
         xs, one = x.stride()
         dt = _DTYPES[x.dtype]
         rows_cap, Hr = rows.shape
-        if not (Tx == T and (one == 1 or H == 1 or T == 0) and dt == _DTYPES[rows.dtype] and
+        if not (Tx == T and H <= _MOST and (one == 1 or H == 1 or T == 0) and dt == _DTYPES[rows.dtype] and
                 rows_cap == cap and Hr == H and rows.is_contiguous()):
             _refuse("moe_dispatch")
         px, pr = x.data_ptr(), rows.data_ptr()
@@ -392,7 +395,7 @@ def moe_dispatch_backward(drows, inv, k, dx, stream=None):
     cap, Hr = drows.shape
     xs, one = dx.stride()
     dt = _DTYPES[dx.dtype]
-    if not (Hr == H and (one == 1 or H == 1 or T == 0) and drows.is_contiguous() and
+    if not (Hr == H and (T | H | cap) <= _MOST and (one == 1 or H == 1 or T == 0) and drows.is_contiguous() and
             _DTYPES[drows.dtype] == dt and inv.dtype is _I32 and inv.numel() == T * k and
             inv.is_contiguous()):
         _refuse("moe_dispatch_backward")
@@ -412,7 +415,8 @@ def moe_combine_weighted(y, inv, w, out, stream=None):
     cap, Hy = y.shape
     xs, one = out.stride()
     dt = _DTYPES[y.dtype]
-    if not (To == T and Hy == H and (one == 1 or H == 1 or T == 0) and y.is_contiguous() and
+    if not (To == T and Hy == H and (T | H | cap) <= _MOST and (one == 1 or H == 1 or T == 0) and
+            y.is_contiguous() and
             _DTYPES[out.dtype] == dt and inv.dtype is _I32 and inv.numel() == T * k and
             inv.is_contiguous() and w.is_contiguous() and w.dtype is _F32):
         _refuse("moe_combine_weighted")
@@ -434,12 +438,12 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
     dt = _DTYPES[dout.dtype]
     ok = (To == T and (one == 1 or H == 1 or T == 0) and inv.dtype is _I32 and inv.numel() == T * k and
           inv.is_contiguous() and w.is_contiguous() and w.dtype is _F32)
-    ok = ok and not (dy is None and dw is None)
+    ok = ok and not (dy is None and dw is None) and (T | H) <= _MOST
     cap = None
     for t in (y, dy):
         if t is not None:
             rows, Ht = t.shape
-            ok = (ok and Ht == H and t.is_contiguous() and _DTYPES[t.dtype] == dt and
+            ok = (ok and Ht == H and rows <= _MOST and t.is_contiguous() and _DTYPES[t.dtype] == dt and
                   (cap is None or cap == rows))
             cap = rows
     if dw is not None:
@@ -460,6 +464,8 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
 
 
 def moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout):
+    if not 0 <= (batch | rows | cols) <= _MOST:
+        return 0
     return load().moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout)
 
 
@@ -477,7 +483,7 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
         _refuse("moe_quant_mxfp4")
     n, dt = B * R * Cc, _DTYPES[x.dtype]
     scales = _sf_bytes(B, Cc, R >> 5, sf_layout) if transpose else _sf_bytes(B, R, Cc >> 5, sf_layout)
-    if not ((one == 1 or Cc == 1 or n == 0) and codes.dtype is _U8 and codes.numel() * 2 == n and
+    if not ((B | R | Cc) <= _MOST and (one == 1 or Cc == 1 or n == 0) and codes.dtype is _U8 and codes.numel() * 2 == n and
             codes.is_contiguous() and sf.dtype is _U8 and sf.numel() == scales and
             sf.is_contiguous() and
             (perm_src is None or (perm_src.dtype is _I32 and perm_src.numel() == R and
@@ -498,7 +504,8 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
 
 
 def moe_mxfp4_tile_scales(sf, batch, rows, cols, sf_tiled, stream=None):
-    if not (sf.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_CANONICAL) and
+    if not ((batch | rows | cols) <= _MOST and
+            sf.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_CANONICAL) and
             sf_tiled.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_TILED) and
             sf.is_contiguous() and sf_tiled.is_contiguous() and sf.dtype is _U8 and
             sf_tiled.dtype is _U8):
@@ -523,7 +530,7 @@ def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, w
     cap, Ka = a_codes.shape
     rows, No = out.shape
     xs, one = out.stride()
-    if not (Ka == K2 and a_codes.is_contiguous() and w_codes.is_contiguous() and
+    if not (Ka == K2 and (cap | G | N | 2 * K2) <= _MOST and a_codes.is_contiguous() and w_codes.is_contiguous() and
             a_codes.dtype is _U8 and w_codes.dtype is _U8 and
             a_sf.dtype is _U8 and a_sf.numel() == _sf_bytes(1, cap, K2 >> 4, MOE_SF_TILED) and
             a_sf.is_contiguous() and
