@@ -531,8 +531,9 @@ MOE_API size_t moe_mxfp4_workspace_size(int32_t rows_cap, int32_t num_groups, in
  * effect.  The gradient with respect to A is the same product of the output's gradient with
  * the transposed matrices (moe_quant_mxfp4, transpose 1).
  * K a multiple of 32; num_groups 1..1024; codes 16-byte aligned, scales 16-byte aligned.
- * ws_d, ws_bytes: at least moe_mxfp4_workspace_size bytes, 256-byte aligned; NULL where that is
- * 0.  It must not be used by another call that may run at the same time.
+ * ws_d, ws_bytes: a workspace of at least moe_mxfp4_workspace_size bytes, 256-byte aligned, or
+ * NULL where that is 0.  It is 0 for every size today and nothing is read or written there; a
+ * version that needs one will want it for one call at a time.
  * Passage: [CK] and [EP] (the grouped FP4 products of the local experts); the MX block form is
  * an addition of this library. */
 MOE_API moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_d,

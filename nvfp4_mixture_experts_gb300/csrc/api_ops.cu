@@ -435,7 +435,7 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_t* a_sf_
     a.status = status_d;
     const MxGemmKernel kern = gemm_mxfp4_kernel_for(out_dtype);
     a.stages = kMxStages;
-    while (gemm_mxfp4_smem(a.stages, num_groups, es) > kSmemLimit) --a.stages;  // many groups: 5
+    while (gemm_mxfp4_smem(a.stages, num_groups, es) > kSmemLimit) --a.stages;  // over 618 groups: 5
     const int smem = gemm_mxfp4_smem(a.stages, num_groups, es);
     if (!allow_smem(reinterpret_cast<const void*>(kern), smem, kSmemLimit)) return MOE_ERR_CUDA;
     // at most this many tiles, however the rows fall into groups

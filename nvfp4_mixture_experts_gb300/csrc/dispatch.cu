@@ -99,10 +99,12 @@ struct Piece {
 // expert, and the first lane moves the entry on.
 //
 // Up to kSmallPairs pairs one block does it alone, in the launch that also moves the rows, every
-// block of which sorts for itself (a few hundred cycles, less than a launch); more are shared out
-// over the blocks of one thread block cluster, which read each other's totals through distributed
-// shared memory.  A chain of latencies bounds both (loads, a dozen barriers, two cluster barriers):
-// one token's 8 pairs over 320 experts 4 us, 16384 pairs 6.5 us, 65536 pairs 10 us, 524288 pairs 55 us.
+// block of which sorts for itself (one token's dispatch 5.4 us so, 8.0 when the rows were moved by a
+// second launch); more are shared out over the blocks of one thread block cluster, which read each
+// other's totals through distributed shared memory.  A chain of latencies bounds both (loads, a dozen
+// barriers, two cluster barriers): the maps of one token's 8 pairs over 320 experts take 3.9 us, over 8
+// experts 2.5 (a launch that does nothing much 1.2), of 16384 pairs 6.5 us, 65536 pairs 10 us, 524288
+// pairs 55 us.
 struct SortShared {
     uint32_t tot[kMaxExperts];       // this block's pairs of each expert
     uint32_t off[kMaxExperts + 1];   // first row of each group
@@ -366,6 +368,8 @@ DispatchSmallKernel dispatch_small_kernel_for(int unit_bytes)
 // the token's rows, so x is read once.  Every warp loads its first run while the sort before it is
 // still at work (x was complete before the sort began; 8192 tokens x 4096 bf16, k 8: 101 -> 98 us;
 // prefetching the other runs into L2 meanwhile changed nothing: the writes are what takes the time).
+// Rows of 4001 such elements, aligned to nothing more, move two bytes a lane: 123 us, eight times the
+// loads and stores of the 98.
 template <typename U>
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(DispatchArgs a)
 {

@@ -17,11 +17,11 @@
 // for the MMAs, transpose it through shared memory and store whole 128-column rows.
 //
 // What bounds it.  Memory where weights are read once: 8192 tokens of 320 experts, N 2560, K 4096,
-// 328 us for 2.26 GB (6.9 TB/s, 4.2 PFLOP/s); 64 tokens, 198 us (7.1 TB/s); 257 tokens on 160
+// 326 us for 2.26 GB (6.9 TB/s, 4.2 PFLOP/s); 64 tokens, 198 us (7.1 TB/s); 257 tokens on 160
 // experts, N 4096, K 1280, fp32 out, 67.6 us (6.8 TB/s).  With few rows and few tiles the two
 // threads that issue loads and MMAs, 0.18 us a k-stage: one row, N 4096, K 4096 6.7 us, K 16384
 // 15.6 us (4 us of launch, group table, epilogue and exit); the last tiles of one token's gate_up
-// over 320 experts (80 tiles for 76 pairs) take 3 of its 13 us so.  With many rows the tensor pipe
+// over 320 experts (80 tiles for 76 pairs) take 3 of its 12 us so.  With many rows the tensor pipe
 // (four MMAs 0.26 us a k-stage, 0.28 where 16 pairs work: 256 rows, N 4096, K 16384 23 us) and, where
 // all pairs do, by its figures L2: 36 KB per SM and k-stage in 0.38 us, 14 TB/s (one group of 8192,
 // N and K 4096: 46 us, 5.9 PFLOP/s, 0.69 of the tensor pipe).

@@ -449,7 +449,7 @@ constexpr int kMxThreads = (2 + kMxEpiWarps) * 32;
 // 2 KB (small: 1 KB)
 constexpr int kMxStageBytes = 16384 + 16384 + 1024 + 2048;
 constexpr int kMxSmallStageBytes = 16384 + 4096 + 1024 + 1024;
-constexpr int kMxStages = 6;                 // as many as fit beside the tables of 490 groups
+constexpr int kMxStages = 6;                 // as many as fit beside the tables of 618 groups (fp32 out: 639)
 constexpr int kMxMaxStages = kMxStages * kMxStageBytes / kMxSmallStageBytes;
 constexpr int kMxCtlBytes = 256;
 // Staging of the output: two groups of four epilogue warps, each with rows of 128 elements (padded

