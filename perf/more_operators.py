@@ -288,7 +288,7 @@ def run(s):
 
 
 def _out8(codes, sf):
-    return dict(codes=codes.view(F8), scales=sf.view(E8))
+    return dict(codes=codes.view(F8), scales=sf.view(-1).view(E8))
 
 
 def _run_own(s):
