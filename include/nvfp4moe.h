@@ -53,6 +53,9 @@
  *     per 128 rows x 4 scales, inside an atom row m (0..127) scale kk (0..3) at byte
  *     (m % 32) * 16 + (m / 32) * 4 + kk.  The scales of K blocks past K are 0; those of rows
  *     past R are not used.
+ *   MXFP8 matrices [B][R][K]: as MXFP4 matrices, with a byte per element (E4M3: 4 exponent and 3
+ *     fraction bits, largest 448): codes uint8 [B][R][K], the same scales in the same layouts
+ *     (moe_mxfp4_scale_bytes gives their size, moe_mxfp4_tile_scales converts them).
  *   Sorted rows (moe_dispatch): the kept (token, expert) pairs grouped by local expert, in
  *     ascending pair index p = t*k + j inside a group, each group starting on a multiple of
  *     row_align (1: no padding; 128: what moe_grouped_gemm_mxfp4 reads).  There is no shared
@@ -106,13 +109,26 @@ typedef enum {
     MOE_FP32 = 2
 } moe_dtype;
 
-/* Where the scale bytes of an MXFP4 matrix lie (see "MXFP4 matrices" above). */
+/* How moe_route_scores scores an expert: softmax over all logits, or each logit's sigmoid. */
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0,
+    MOE_SCORE_SIGMOID = 1
+} moe_score;
+
+/* The score of a group of experts (moe_route_scores): its largest key, or the sum of its two largest. */
+typedef enum {
+    MOE_GROUP_MAX = 0,
+    MOE_GROUP_TOP2 = 1
+} moe_group_score;
+
+/* Where the scale bytes of an MX matrix lie (see "MXFP4 matrices" above). */
 typedef enum {
     MOE_SF_CANONICAL = 0,
     MOE_SF_TILED = 1
 } moe_sf_layout;
 
-/* The block scale 2^e of moe_quant_mxfp4, for m the largest magnitude of the block. */
+/* The block scale 2^e of MXFP4 (MXFP8: 8 and 448 in the place of 2 and 6), for m the largest
+ * magnitude of the block. */
 typedef enum {
     MOE_MX_FLOOR = 0,       /* e = floor(log2 m) - 2: m may pass 6 * 2^e and saturate */
     MOE_MX_CEIL = 1         /* the least e with m <= 6 * 2^e: nothing saturates */
@@ -124,7 +140,7 @@ typedef enum {
 #define MOE_DEV_ROWS_OVERFLOW  0x4u   /* padded rows exceeded capacity: pairs dropped */
 #define MOE_DEV_BAD_INDEX      0x8u   /* library built with MOE_DEBUG only: a padded-row or
                                          pair index read from a buffer was out of range; the
-                                         access was skipped.  moe_grouped_gemm_mxfp4 (every
+                                         access was skipped.  moe_grouped_gemm_mxfp4 and _mxfp8 (every
                                          build): a group's rows do not start on a multiple of
                                          128 or do not lie within rows_cap; the group was
                                          skipped */
@@ -543,6 +559,122 @@ MOE_API moe_status moe_grouped_gemm_mxfp4(const uint8_t* a_codes_d, const uint8_
                                           int32_t N, int32_t K, void* out_d, int32_t out_dtype,
                                           int64_t out_stride, void* ws_d, size_t ws_bytes,
                                           uint32_t* status_d, moe_stream_t stream);
+
+/* ---- Around the experts, with activations held in 8 bits (see "MXFP8 matrices" above): routing
+ * from logits, norm, quantisation, the gate, and the product of MXFP8 rows with MXFP4 weights, with the
+ * gradients that have kernels of their own.  No handle; strides in elements between consecutive rows;
+ * addresses, overlap and threads as for the sorted rows, but where an overlap is allowed below. */
+
+/* Routing from given logits [T][num_experts] (a dtype and row stride).  Expert e of a token has the
+ * score s_e = softmax(logits)_e or sigmoid(logit_e) (moe_score) and the key s_e + bias_e (bias_d
+ * nullable; it steers the choice alone).  num_groups > 1: the experts fall into num_groups groups of
+ * num_experts / num_groups neighbours; the topk_groups groups of the largest scores (moe_group_score;
+ * TOP2 of a group with one expert left: its key) are kept.  topk_ids_d [T][k]: the experts of the k
+ * largest keys in the kept groups, the largest first, equal keys in ascending order (of groups too).
+ * topk_w_d [T][k] fp32: scale * s, or with renormalise 1 scale * s / (the sum of the token's k scores),
+ * 0 where that sum is 0.  Keys are told apart as 64-bit arithmetic does (logits themselves without a
+ * bias).
+ *   A logit of -infinity (a masked expert) has score 0 and is chosen after all others of the kept
+ *   groups; so is an expert whose bias is -infinity or NaN.  A NaN logit counts as -infinity in the
+ *   choice, and all weights of its token are NaN; so they are where a softmax has
+ *   infinite logits (which share its sum in the choice).
+ * num_experts up to 1024, k up to 32 and to the experts of the kept groups, num_groups up to 32.
+ * Passage: [OV] (top-8 routing); sigmoid scores, bias and groups are an addition of this library. */
+MOE_API moe_status moe_route_scores(const void* logits_d, int32_t dtype, int64_t stride,
+                                    const float* bias_d, int32_t T, int32_t num_experts, int32_t k,
+                                    int32_t score, int32_t num_groups, int32_t topk_groups,
+                                    int32_t group_score, int32_t renormalise, float scale,
+                                    int32_t* topk_ids_d, float* topk_w_d, moe_stream_t stream);
+
+/* The gradient of moe_route_scores with respect to the logits: dlogits_d [T][num_experts] in the
+ * logits' type, for the weights' gradient dtopk_w_d [T][k] and the same score, renormalise and scale.
+ * The choice has no gradient (nor has the bias).  Positions with the same expert add up; an id outside
+ * [0, num_experts) counts as a position with weight 0.  A token whose weights are NaN has NaN gradients.
+ * Passage: none; training is an addition of this library (the pages serve only). */
+MOE_API moe_status moe_route_scores_backward(const void* logits_d, int32_t dtype, int64_t stride,
+                                             const int32_t* topk_ids_d, const float* dtopk_w_d,
+                                             int32_t T, int32_t num_experts, int32_t k,
+                                             int32_t score, int32_t renormalise, float scale,
+                                             void* dlogits_d, int64_t dstride, moe_stream_t stream);
+
+/* Root-mean-square norm of rows [T][H] with the residual's addition: h = x + residual in the rows' type
+ * (residual_d NULL: h = x), rstd = 1 / sqrt(mean(h^2) + eps), y = h * rstd * weight (weight_d [H] in the
+ * rows' type, NULL: ones), all sums in fp32.  Each output may be NULL: h_d (needs a residual), y_d,
+ * rstd_d [T] fp32, and codes_d with sf_d: y, before its rounding to the rows' type, as an MXFP8 matrix
+ * [1][T][H] (H a multiple of 32; codes and tiled scales 16-byte aligned).
+ * h_d may be x_d or residual_d, and y_d may be x_d, with the same stride.  H up to 16384.
+ * Passage: none; the norm before a layer is an addition of this library. */
+MOE_API moe_status moe_rmsnorm(const void* x_d, int32_t dtype, int64_t x_stride,
+                               const void* residual_d, int64_t residual_stride,
+                               const void* weight_d, float eps, int32_t T, int32_t H, void* h_d,
+                               int64_t h_stride, void* y_d, int64_t y_stride, float* rstd_d,
+                               uint8_t* codes_d, uint8_t* sf_d, int32_t sf_layout,
+                               int32_t scale_rule, moe_stream_t stream);
+
+/* Bytes of workspace that moe_rmsnorm_backward needs for the weight's gradient (32 MiB at most; 0 for
+ * arguments out of range, and for one row).
+ * Passage: none; workspace sizing of this library (the pages have no counterpart). */
+MOE_API size_t moe_rmsnorm_workspace_size(int32_t T, int32_t H);
+
+/* The gradient of moe_rmsnorm, from y's gradient dy and (dh_d nullable) the gradient that h has from
+ * elsewhere: dx = rstd * (dy * weight - h * rstd * mean(dy * weight * h * rstd)) + dh, which is the
+ * gradient of x and of the residual alike, and dweight_d [H] fp32 = sum over the rows of dy * h * rstd
+ * (nullable; summed in an order that depends on T and H alone).  ws_d: at least
+ * moe_rmsnorm_workspace_size bytes, 256-byte aligned, used by one call at a time (none is needed where
+ * dweight_d is NULL).  dx_d may be dy_d, dh_d or h_d, with the same stride.
+ * Passage: none; training is an addition of this library (the pages serve only). */
+MOE_API moe_status moe_rmsnorm_backward(const void* dy_d, int32_t dtype, int64_t dy_stride,
+                                        const void* dh_d, int64_t dh_stride, const void* h_d,
+                                        int64_t h_stride, const void* weight_d,
+                                        const float* rstd_d, int32_t T, int32_t H, void* dx_d,
+                                        int64_t dx_stride, float* dweight_d, void* ws_d,
+                                        size_t ws_bytes, moe_stream_t stream);
+
+/* MXFP8 quantiser: as moe_quant_mxfp4 without a transpose, with E4M3 elements that saturate at 448.
+ * Passage: [CK] (codes with FP8 block scales); the MX block form is an addition of this library. */
+MOE_API moe_status moe_quant_mxfp8(const void* x_d, int32_t dtype, int32_t batch, int32_t rows,
+                                   int32_t cols, int64_t row_stride, int64_t batch_stride,
+                                   int32_t scale_rule, const int32_t* perm_src_d,
+                                   uint8_t* codes_d, uint8_t* sf_d, int32_t sf_layout,
+                                   void* values_d, moe_stream_t stream);
+
+/* The gate: of rows [rows][2 * inter] (gate columns first, then up) silu(gate) * up, computed in fp32,
+ * as an MXFP8 matrix [1][rows][inter]; and (ckpt_d with ckpt_sf_d, nullable) gate and up themselves as
+ * an MXFP8 matrix [1][rows][2 * inter] with canonical scales, the checkpoint that the gradient reads.
+ * Rows r with perm_src_d[r] < 0 (nullable) are neither read nor written.  inter a multiple of 32;
+ * codes and tiled scales 16-byte aligned.
+ * Passage: [CK] (silu(gate) * up of the fused projection); the MX block form and the checkpoint are an
+ * addition of this library. */
+MOE_API moe_status moe_swiglu_mxfp8(const void* gate_up_d, int32_t dtype, int64_t stride,
+                                    int32_t rows, int32_t inter, const int32_t* perm_src_d,
+                                    int32_t scale_rule, uint8_t* codes_d, uint8_t* sf_d,
+                                    int32_t sf_layout, uint8_t* ckpt_d, uint8_t* ckpt_sf_d,
+                                    moe_stream_t stream);
+
+/* The gate's gradient from the gradient ds [rows][inter] of silu(gate) * up and the checkpoint that
+ * moe_swiglu_mxfp8 wrote: with s = sigmoid(gate), dgate = ds * up * s * (1 + gate * (1 - s)) and
+ * dup = ds * gate * s, as an MXFP8 matrix [1][rows][2 * inter] (codes_d with sf_d) and/or in ds's type
+ * (dgate_up_d, contiguous, 16-byte aligned); either may be NULL.  perm_src_d, inter and alignment as
+ * there.
+ * Passage: none; training is an addition of this library (the pages serve only). */
+MOE_API moe_status moe_swiglu_mxfp8_backward(const void* ds_d, int32_t dtype, int64_t stride,
+                                             const uint8_t* ckpt_d, const uint8_t* ckpt_sf_d,
+                                             int32_t rows, int32_t inter,
+                                             const int32_t* perm_src_d, int32_t scale_rule,
+                                             uint8_t* codes_d, uint8_t* sf_d, int32_t sf_layout,
+                                             void* dgate_up_d, moe_stream_t stream);
+
+/* Grouped product of MXFP8 rows with MXFP4 weights: moe_grouped_gemm_mxfp4 with a_codes_d
+ * [rows_cap][K] (a byte per element); K a multiple of 128, w_codes_d 32-byte aligned, no workspace.
+ * Passage: [CK] and [EP] (the grouped products of the local experts with FP4 weights); the MX block
+ * form is an addition of this library. */
+MOE_API moe_status moe_grouped_gemm_mxfp8(const uint8_t* a_codes_d, const uint8_t* a_sf_d,
+                                          int32_t rows_cap, const int32_t* counts_d,
+                                          const int32_t* offsets_d, int32_t num_groups,
+                                          const uint8_t* w_codes_d, const uint8_t* w_sf_d,
+                                          int32_t N, int32_t K, void* out_d, int32_t out_dtype,
+                                          int64_t out_stride, uint32_t* status_d,
+                                          moe_stream_t stream);
 
 /* Self-test of the failure path of the pipelines' bounded waits: one thread waits, with the
  * same bounded wait the kernels use, on an mbarrier phase that nothing completes, so the

@@ -27,6 +27,8 @@ MOE_DEV_BAD_INDEX = 8
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
 MOE_SF_CANONICAL, MOE_SF_TILED = 0, 1
 MOE_MX_FLOOR, MOE_MX_CEIL = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 
 class moe_config(C.Structure):
@@ -54,6 +56,7 @@ class _Int:
 _V = C.c_void_p
 _I = _Int
 _L = C.c_int64
+_F = C.c_float
 _SZ = C.c_size_t
 
 # name -> (restype, argtypes); the list mirrors include/nvfp4moe.h
@@ -93,6 +96,17 @@ SIGNATURES = {
     "moe_mxfp4_workspace_size": (_SZ, [_I] * 4),
     "moe_grouped_gemm_mxfp4": (C.c_int, [_V, _V, _I, _V, _V, _I, _V, _V, _I, _I, _V, _I, _L, _V,
                                          _SZ, _V, _V]),
+    "moe_route_scores": (C.c_int, [_V, _I, _L, _V] + [_I] * 8 + [_F, _V, _V, _V]),
+    "moe_route_scores_backward": (C.c_int, [_V, _I, _L, _V, _V] + [_I] * 5 + [_F, _V, _L, _V]),
+    "moe_rmsnorm": (C.c_int, [_V, _I, _L, _V, _L, _V, _F, _I, _I, _V, _L, _V, _L, _V, _V, _V, _I, _I,
+                              _V]),
+    "moe_rmsnorm_workspace_size": (_SZ, [_I] * 2),
+    "moe_rmsnorm_backward": (C.c_int, [_V, _I, _L, _V, _L, _V, _L, _V, _V, _I, _I, _V, _L, _V, _V, _SZ,
+                                       _V]),
+    "moe_quant_mxfp8": (C.c_int, [_V] + [_I] * 4 + [_L, _L, _I, _V, _V, _V, _I, _V, _V]),
+    "moe_swiglu_mxfp8": (C.c_int, [_V, _I, _L, _I, _I, _V, _I, _V, _V, _I, _V, _V, _V]),
+    "moe_swiglu_mxfp8_backward": (C.c_int, [_V, _I, _L, _V, _V, _I, _I, _V, _I, _V, _V, _I, _V, _V]),
+    "moe_grouped_gemm_mxfp8": (C.c_int, [_V, _V, _I, _V, _V, _I, _V, _V, _I, _I, _V, _I, _L, _V, _V]),
 }
 
 _lib = None
@@ -469,10 +483,9 @@ def moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout):
     return load().moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout)
 
 
-def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_FLOOR,
-                    perm_src=None, values=None, stream=None):
-    """x [rows, cols] or [batch, rows, cols] (columns contiguous); codes uint8, sf uint8 and values
-    (x's type) hold the MXFP4 matrix, or with transpose that of each matrix's transpose."""
+def _quant(where, per, x, codes, sf, sf_layout, transpose, perm_src, values, stream):
+    """The arguments that moe_quant_mxfp4 (per: two codes a byte) and moe_quant_mxfp8 (one) begin with,
+    checked: x's, and the stream's handle."""
     shape, stride = x.shape, x.stride()
     if len(shape) == 3:
         (B, R, Cc), (bs, rs, one) = shape, stride
@@ -480,27 +493,46 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
         (R, Cc), (rs, one) = shape, stride
         B, bs = 1, 0
     else:
-        _refuse("moe_quant_mxfp4")
+        _refuse(where)
     n, dt = B * R * Cc, _DTYPES[x.dtype]
     scales = _sf_bytes(B, Cc, R >> 5, sf_layout) if transpose else _sf_bytes(B, R, Cc >> 5, sf_layout)
-    if not ((B | R | Cc) <= _MOST and (one == 1 or Cc == 1 or n == 0) and codes.dtype is _U8 and codes.numel() * 2 == n and
-            codes.is_contiguous() and sf.dtype is _U8 and sf.numel() == scales and
-            sf.is_contiguous() and
+    if not ((B | R | Cc) <= _MOST and (one == 1 or Cc == 1 or n == 0) and codes.dtype is _U8 and
+            codes.numel() * per == n and codes.is_contiguous() and sf.dtype is _U8 and
+            sf.numel() == scales and sf.is_contiguous() and
             (perm_src is None or (perm_src.dtype is _I32 and perm_src.numel() == R and
                                   perm_src.is_contiguous())) and
             (values is None or (values.numel() == n and values.is_contiguous() and
                                 _DTYPES[values.dtype] == dt))):
-        _refuse("moe_quant_mxfp4")
+        _refuse(where)
     dev, handle = _place(stream)
     if not (dev == x.get_device() == codes.get_device() == sf.get_device() and
             (perm_src is None or perm_src.get_device() == dev) and
             (values is None or values.get_device() == dev)):
-        _refuse("moe_quant_mxfp4")
-    st = (_lib or load()).moe_quant_mxfp4(x.data_ptr(), dt, B, R, Cc, rs, bs, 1 if transpose else 0,
-                                          scale_rule, _p(perm_src), codes.data_ptr(), sf.data_ptr(),
-                                          sf_layout, _p(values), handle)
+        _refuse(where)
+    return (x.data_ptr(), dt, B, R, Cc, rs, bs), handle
+
+
+def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_FLOOR,
+                    perm_src=None, values=None, stream=None):
+    """x [rows, cols] or [batch, rows, cols] (columns contiguous); codes uint8, sf uint8 and values
+    (x's type) hold the MXFP4 matrix, or with transpose that of each matrix's transpose."""
+    args, handle = _quant("moe_quant_mxfp4", 2, x, codes, sf, sf_layout, transpose, perm_src, values,
+                          stream)
+    st = (_lib or load()).moe_quant_mxfp4(*args, 1 if transpose else 0, scale_rule, _p(perm_src),
+                                          codes.data_ptr(), sf.data_ptr(), sf_layout, _p(values), handle)
     if st:
         _check(st, "moe_quant_mxfp4")
+
+
+def moe_quant_mxfp8(x, codes, sf, sf_layout, scale_rule=MOE_MX_CEIL, perm_src=None, values=None,
+                    stream=None):
+    """x [rows, cols] or [batch, rows, cols] (columns contiguous) -> codes uint8 of x's shape and sf
+    uint8, its MXFP8 matrix, and values (x's type; None)."""
+    args, handle = _quant("moe_quant_mxfp8", 1, x, codes, sf, sf_layout, False, perm_src, values, stream)
+    st = (_lib or load()).moe_quant_mxfp8(*args, scale_rule, _p(perm_src), codes.data_ptr(),
+                                          sf.data_ptr(), sf_layout, _p(values), handle)
+    if st:
+        _check(st, "moe_quant_mxfp8")
 
 
 def moe_mxfp4_tile_scales(sf, batch, rows, cols, sf_tiled, stream=None):
@@ -522,16 +554,15 @@ def moe_mxfp4_workspace_size(rows_cap, num_groups, N, K):
     return load().moe_mxfp4_workspace_size(rows_cap, num_groups, N, K)
 
 
-def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, ws=None,
-                           status=None, stream=None):
-    """a_codes [rows_cap, K/2], w_codes [num_groups, N, K/2] (uint8) with tiled scales; counts and
-    offsets int32 (both None: one group, all rows); out [rows_cap, N]."""
+def _product(where, per, a_codes, a_sf, counts, offsets, w_codes, w_sf, out, ws, status, stream):
+    """The arguments that moe_grouped_gemm_mxfp4 (per: two codes of a byte in the rows) and
+    moe_grouped_gemm_mxfp8 (one) begin with, checked, and the stream's handle."""
     G, N, K2 = w_codes.shape
     cap, Ka = a_codes.shape
     rows, No = out.shape
     xs, one = out.stride()
-    if not (Ka == K2 and (cap | G | N | 2 * K2) <= _MOST and a_codes.is_contiguous() and w_codes.is_contiguous() and
-            a_codes.dtype is _U8 and w_codes.dtype is _U8 and
+    if not (Ka * per == 2 * K2 and (cap | G | N | 2 * K2) <= _MOST and a_codes.is_contiguous() and
+            w_codes.is_contiguous() and a_codes.dtype is _U8 and w_codes.dtype is _U8 and
             a_sf.dtype is _U8 and a_sf.numel() == _sf_bytes(1, cap, K2 >> 4, MOE_SF_TILED) and
             a_sf.is_contiguous() and
             w_sf.dtype is _U8 and w_sf.numel() == _sf_bytes(G, N, K2 >> 4, MOE_SF_TILED) and
@@ -543,20 +574,198 @@ def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, w
                                 offsets.numel() >= G and offsets.is_contiguous())) and
             (ws is None or ws.is_contiguous()) and
             (status is None or (status.dtype is _I32 and status.numel()))):
-        _refuse("moe_grouped_gemm_mxfp4")
+        _refuse(where)
     dev, handle = _place(stream)
     if not (dev == a_codes.get_device() == a_sf.get_device() == w_codes.get_device() ==
             w_sf.get_device() == out.get_device() and
             (counts is None or dev == counts.get_device() == offsets.get_device()) and
             (ws is None or ws.get_device() == dev) and
             (status is None or status.get_device() == dev)):
-        _refuse("moe_grouped_gemm_mxfp4")
-    st = (_lib or load()).moe_grouped_gemm_mxfp4(
-        a_codes.data_ptr(), a_sf.data_ptr(), cap, _p(counts), _p(offsets), G, w_codes.data_ptr(),
-        w_sf.data_ptr(), N, 2 * K2, out.data_ptr(), _DTYPES[out.dtype], xs, _p(ws),
-        0 if ws is None else ws.nbytes, _p(status), handle)
+        _refuse(where)
+    return (a_codes.data_ptr(), a_sf.data_ptr(), cap, _p(counts), _p(offsets), G, w_codes.data_ptr(),
+            w_sf.data_ptr(), N, 2 * K2, out.data_ptr(), _DTYPES[out.dtype], xs), handle
+
+
+def moe_grouped_gemm_mxfp4(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, ws=None,
+                           status=None, stream=None):
+    """a_codes [rows_cap, K/2], w_codes [num_groups, N, K/2] (uint8) with tiled scales; counts and
+    offsets int32 (both None: one group, all rows); out [rows_cap, N]."""
+    args, handle = _product("moe_grouped_gemm_mxfp4", 2, a_codes, a_sf, counts, offsets, w_codes, w_sf,
+                            out, ws, status, stream)
+    st = (_lib or load()).moe_grouped_gemm_mxfp4(*args, _p(ws), 0 if ws is None else ws.nbytes,
+                                                 _p(status), handle)
     if st:
         _check(st, "moe_grouped_gemm_mxfp4")
+
+
+def moe_grouped_gemm_mxfp8(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, status=None, stream=None):
+    """a_codes [rows_cap, K], w_codes [num_groups, N, K/2] (uint8) with tiled scales; counts and
+    offsets int32 (both None: one group, all rows); out [rows_cap, N]."""
+    args, handle = _product("moe_grouped_gemm_mxfp8", 1, a_codes, a_sf, counts, offsets, w_codes, w_sf,
+                            out, None, status, stream)
+    st = (_lib or load()).moe_grouped_gemm_mxfp8(*args, _p(status), handle)
+    if st:
+        _check(st, "moe_grouped_gemm_mxfp8")
+
+
+def _rows(t, T, H, dt):
+    """Whether t is [T, H] rows of a moe_dtype with contiguous columns, or None."""
+    return t is None or (tuple(t.shape) == (T, H) and _DTYPES[t.dtype] == dt and
+                         (t.stride(1) == 1 or H == 1 or T == 0))
+
+
+def _stride(t):
+    return 0 if t is None else t.stride(0)
+
+
+def _flat(t, n, dtype):
+    """Whether t is n contiguous elements of a torch dtype, or None."""
+    return t is None or (t.dtype is dtype and t.numel() == n and t.is_contiguous())
+
+
+def _all_on(dev, *tensors):
+    return all(t is None or t.get_device() == dev for t in tensors)
+
+
+def moe_route_scores(logits, topk_ids, topk_w, bias=None, score=MOE_SCORE_SOFTMAX, num_groups=1,
+                     topk_groups=1, group_score=MOE_GROUP_MAX, renormalise=True, scale=1.0, stream=None):
+    """logits [T, num_experts], bias float32 [num_experts] (None) -> topk_ids int32 [T, k], topk_w
+    float32 [T, k]."""
+    T, E = logits.shape
+    Tk, k = topk_ids.shape
+    stride, one = logits.stride()
+    if not (Tk == T and (T | E | k) <= _MOST and (one == 1 or E == 1 or T == 0) and
+            _flat(topk_ids, T * k, _I32) and _flat(topk_w, T * k, _F32) and _flat(bias, E, _F32)):
+        _refuse("moe_route_scores")
+    dev, handle = _place(stream)
+    if not (dev == logits.get_device() == topk_ids.get_device() == topk_w.get_device() and
+            (bias is None or bias.get_device() == dev)):
+        _refuse("moe_route_scores")
+    st = (_lib or load()).moe_route_scores(
+        logits.data_ptr(), _DTYPES[logits.dtype], stride, _p(bias), T, E, k, score, num_groups, topk_groups,
+        group_score, 1 if renormalise else 0, scale, topk_ids.data_ptr(), topk_w.data_ptr(), handle)
+    if st:
+        _check(st, "moe_route_scores")
+
+
+def moe_route_scores_backward(logits, topk_ids, dtopk_w, dlogits, score=MOE_SCORE_SOFTMAX,
+                              renormalise=True, scale=1.0, stream=None):
+    """logits [T, num_experts], topk_ids int32 [T, k], dtopk_w float32 [T, k] -> dlogits (logits' type)
+    [T, num_experts]."""
+    T, E = logits.shape
+    Tk, k = topk_ids.shape
+    stride, one = logits.stride()
+    dt = _DTYPES[logits.dtype]
+    if not (Tk == T and (T | E | k) <= _MOST and (one == 1 or E == 1 or T == 0) and
+            _flat(topk_ids, T * k, _I32) and _flat(dtopk_w, T * k, _F32) and _rows(dlogits, T, E, dt)):
+        _refuse("moe_route_scores_backward")
+    dev, handle = _place(stream)
+    if not (dev == logits.get_device() == topk_ids.get_device() == dtopk_w.get_device() ==
+            dlogits.get_device()):
+        _refuse("moe_route_scores_backward")
+    st = (_lib or load()).moe_route_scores_backward(
+        logits.data_ptr(), dt, stride, topk_ids.data_ptr(), dtopk_w.data_ptr(), T, E, k, score,
+        1 if renormalise else 0, scale, dlogits.data_ptr(), dlogits.stride(0), handle)
+    if st:
+        _check(st, "moe_route_scores_backward")
+
+
+def moe_rmsnorm(x, weight, eps, residual=None, h=None, y=None, rstd=None, codes=None, sf=None,
+                sf_layout=MOE_SF_TILED, scale_rule=MOE_MX_CEIL, stream=None):
+    """x [T, H], weight [H] (None: ones), residual [T, H] (None) -> any of h, y [T, H] (x's type), rstd
+    float32 [T], and codes [T, H] with sf (uint8), y's MXFP8 matrix."""
+    T, H = x.shape
+    stride, one = x.stride()
+    dt = _DTYPES[x.dtype]
+    if not ((T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and _flat(weight, H, x.dtype) and
+            (residual is None or _rows(residual, T, H, dt)) and (h is None or _rows(h, T, H, dt)) and
+            (y is None or _rows(y, T, H, dt)) and _flat(rstd, T, _F32) and (codes is None) == (sf is None) and
+            (codes is None or (_flat(codes, T * H, _U8) and
+                               _flat(sf, _sf_bytes(1, T, H >> 5, sf_layout), _U8)))):
+        _refuse("moe_rmsnorm")
+    dev, handle = _place(stream)
+    if not (x.get_device() == dev and _all_on(dev, weight, residual, h, y, rstd, codes, sf)):
+        _refuse("moe_rmsnorm")
+    st = (_lib or load()).moe_rmsnorm(
+        x.data_ptr(), dt, stride, _p(residual), _stride(residual), _p(weight), eps, T, H, _p(h), _stride(h),
+        _p(y), _stride(y), _p(rstd), _p(codes), _p(sf), sf_layout, scale_rule, handle)
+    if st:
+        _check(st, "moe_rmsnorm")
+
+
+def moe_rmsnorm_workspace_size(T, H):
+    return load().moe_rmsnorm_workspace_size(T, H)
+
+
+def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, ws=None, dh=None, stream=None):
+    """dy, h [T, H], weight [H] (None: ones), rstd float32 [T], dh [T, H] (None) -> dx [T, H] and
+    dweight float32 [H] (None); ws: moe_rmsnorm_workspace_size bytes where dweight is given."""
+    T, H = dy.shape
+    stride, one = dy.stride()
+    dt = _DTYPES[dy.dtype]
+    if not ((T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and h is not None and dx is not None and
+            _rows(h, T, H, dt) and _rows(dx, T, H, dt) and (dh is None or _rows(dh, T, H, dt)) and
+            _flat(weight, H, dy.dtype) and rstd is not None and _flat(rstd, T, _F32) and
+            _flat(dweight, H, _F32) and (ws is None or ws.is_contiguous())):
+        _refuse("moe_rmsnorm_backward")
+    dev, handle = _place(stream)
+    if not (dev == dy.get_device() == h.get_device() == dx.get_device() == rstd.get_device() and
+            _all_on(dev, dh, weight, dweight, ws)):
+        _refuse("moe_rmsnorm_backward")
+    st = (_lib or load()).moe_rmsnorm_backward(
+        dy.data_ptr(), dt, stride, _p(dh), _stride(dh), h.data_ptr(), h.stride(0), _p(weight),
+        rstd.data_ptr(), T, H, dx.data_ptr(), dx.stride(0), _p(dweight), _p(ws),
+        0 if ws is None else ws.nbytes, handle)
+    if st:
+        _check(st, "moe_rmsnorm_backward")
+
+
+def moe_swiglu_mxfp8(gate_up, codes, sf, sf_layout, ckpt=None, ckpt_sf=None, perm_src=None,
+                     scale_rule=MOE_MX_CEIL, stream=None):
+    """gate_up [rows, 2 * inter] -> codes [rows, inter] with sf (uint8), silu(gate) * up as an MXFP8
+    matrix, and ckpt [rows, 2 * inter] with canonical scales ckpt_sf (None), that of gate_up."""
+    R, I2 = gate_up.shape
+    stride, one = gate_up.stride()
+    I = I2 >> 1
+    if not ((R | I2) <= _MOST and not I2 & 1 and (one == 1 or R == 0) and _flat(codes, R * I, _U8) and
+            _flat(sf, _sf_bytes(1, R, I >> 5, sf_layout), _U8) and (ckpt is None) == (ckpt_sf is None) and
+            _flat(ckpt, R * I2, _U8) and _flat(ckpt_sf, R * (I2 >> 5), _U8) and _flat(perm_src, R, _I32)):
+        _refuse("moe_swiglu_mxfp8")
+    dev, handle = _place(stream)
+    if not (dev == gate_up.get_device() == codes.get_device() == sf.get_device() and
+            _all_on(dev, ckpt, ckpt_sf, perm_src)):
+        _refuse("moe_swiglu_mxfp8")
+    st = (_lib or load()).moe_swiglu_mxfp8(
+        gate_up.data_ptr(), _DTYPES[gate_up.dtype], stride, R, I, _p(perm_src), scale_rule, codes.data_ptr(),
+        sf.data_ptr(), sf_layout, _p(ckpt), _p(ckpt_sf), handle)
+    if st:
+        _check(st, "moe_swiglu_mxfp8")
+
+
+def moe_swiglu_mxfp8_backward(ds, ckpt, ckpt_sf, codes=None, sf=None, sf_layout=MOE_SF_TILED,
+                              perm_src=None, dgate_up=None, scale_rule=MOE_MX_CEIL, stream=None):
+    """ds [rows, inter] and the checkpoint of moe_swiglu_mxfp8 -> codes [rows, 2 * inter] with sf
+    (uint8), gate_up's gradient as an MXFP8 matrix, and/or dgate_up [rows, 2 * inter] in ds's type."""
+    R, I = ds.shape
+    stride, one = ds.stride()
+    dt = _DTYPES[ds.dtype]
+    if not ((R | 2 * I) <= _MOST and (one == 1 or I == 1 or R == 0) and ckpt is not None and
+            ckpt_sf is not None and _flat(ckpt, 2 * R * I, _U8) and _flat(ckpt_sf, R * (2 * I >> 5), _U8) and
+            (codes is None) == (sf is None) and
+            (codes is None or (_flat(codes, 2 * R * I, _U8) and
+                               _flat(sf, _sf_bytes(1, R, 2 * I >> 5, sf_layout), _U8))) and
+            (dgate_up is None or (_DTYPES[dgate_up.dtype] == dt and dgate_up.numel() == 2 * R * I and
+                                  dgate_up.is_contiguous())) and _flat(perm_src, R, _I32)):
+        _refuse("moe_swiglu_mxfp8_backward")
+    dev, handle = _place(stream)
+    if not (dev == ds.get_device() == ckpt.get_device() == ckpt_sf.get_device() and
+            _all_on(dev, codes, sf, perm_src, dgate_up)):
+        _refuse("moe_swiglu_mxfp8_backward")
+    st = (_lib or load()).moe_swiglu_mxfp8_backward(
+        ds.data_ptr(), dt, stride, ckpt.data_ptr(), ckpt_sf.data_ptr(), R, I, _p(perm_src), scale_rule,
+        _p(codes), _p(sf), sf_layout, _p(dgate_up), handle)
+    if st:
+        _check(st, "moe_swiglu_mxfp8_backward")
 
 
 from .layer import MoELayer, make_config  # noqa: E402,F401

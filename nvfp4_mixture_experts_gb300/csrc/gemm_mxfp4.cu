@@ -135,6 +135,27 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_taddr, uint64_t ades
         : "memory");
 }
 
+// Instruction descriptor of kind::mxf8f6f4: E2M1 (the weights) x E4M3 (the group rows), UE8M0 scales,
+// fp32 accumulation, both operands K-major; the scale ids (which of the four bytes of a scale column a
+// K = 32 step uses) are added per step.
+__device__ __forceinline__ uint32_t idesc_mxf8(int M, int N)
+{
+    return (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
+}
+
+__device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d_taddr, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t sfa_taddr,
+                                                 uint32_t sfb_taddr, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_taddr),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_taddr), "r"(sfb_taddr), "r"(accumulate)
+        : "memory");
+}
+
 // What a tile covers.  Tiles run over the groups' token tiles (256 group rows), and inside one
 // over the 256-row weight tiles, so that tiles in flight at a time share their group rows in L2.
 struct Tile {
@@ -400,7 +421,7 @@ __device__ __forceinline__ void store_chunk(const MxGemmArgs& a, const uint32_t 
 
 }  // namespace
 
-template <typename T>
+template <typename T, bool A8>
 __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
                       const __grid_constant__ CUtensorMap tmT16,
@@ -415,7 +436,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int KB = div_up(args.K, 256);
+    // A8: the group rows are MXFP8 and a k-stage holds 128 elements instead of 256, in as many bytes of
+    // shared memory (the weights are spread to a byte each on their way in)
+    constexpr int kSf = A8 ? 512 : 1024;         // bytes of a row block's scales per k-stage
+    constexpr int kWb = A8 ? 8192 : 16384;       // bytes that a copy of weights counts (of the packed codes)
+    constexpr int kXw = A8 ? 128 : 32;           // of a k-stage in the weights' map: elements, or words
+    const int KB = div_up(args.K, A8 ? 128 : 256);
 
     if (warp == 0 && elect_one()) {
         for (int s = 0; s < kMxMaxStages; ++s) {
@@ -466,7 +492,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 const int half = ti.nt >> 1;                    // group rows of this CTA
                 const int trow = ti.row0 + (int)rank * half, wrow = ti.n0 + (int)rank * 128;
                 const int nsc = ti.nt > 128 ? 2 : 1;            // row blocks of group-row scales
-                const uint32_t bytes = 2u * (16384 + 1024 + half * 128 + nsc * 1024);
+                const uint32_t bytes = 2u * (kWb + kSf + half * 128 + nsc * kSf);
                 const int wb = ti.g * div_up(args.N, 128) + (wrow >> 7), tb = ti.row0 >> 7;
                 // A loop of its own for few rows, where this thread is what a lone tile waits for
                 // (one row, N 4096, K 16384: 18.2 us in the other loop, 16.7 in this one).
@@ -477,10 +503,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         uint8_t* p = sg.base + at.stage * sg.bytes;
                         const uint32_t bar = full0 + at.stage * 8;
                         if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at.stage], bytes);
-                        tma_pair_3d(p, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
-                        tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
+                        tma_pair_3d(p, &tmW, bar, kb * kXw, wrow, ti.g, pol_w);
+                        tma_pair_2d(p + sg.sw, &tmSW, bar, kb * (kSf / 4), wb, pol_w);
                         tma_pair_2d(p + sg.t, &tmT16, bar, kb * 32, trow, pol_t);
-                        tma_pair_2d(p + sg.st, &tmST, bar, kb * 256, tb, pol_t);
+                        tma_pair_2d(p + sg.st, &tmST, bar, kb * (kSf / 4), tb, pol_t);
                         at.next(sg.n);
                     }
                 } else {
@@ -489,16 +515,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         uint8_t* p = sg.base + at.stage * sg.bytes;
                         const uint32_t bar = full0 + at.stage * 8;
                         if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at.stage], bytes);
-                        tma_pair_3d(p, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
-                        tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
+                        tma_pair_3d(p, &tmW, bar, kb * kXw, wrow, ti.g, pol_w);
+                        tma_pair_2d(p + sg.sw, &tmSW, bar, kb * (kSf / 4), wb, pol_w);
                         if (half == 128) {
                             tma_pair_2d(p + sg.t, &tmT, bar, kb * 32, trow, pol_t);
                         } else {
                             for (int i = 0; i < half; i += 16)
                                 tma_pair_2d(p + sg.t + i * 128, &tmT16, bar, kb * 32, trow + i, pol_t);
                         }
-                        tma_pair_2d(p + sg.st, &tmST, bar, kb * 256, tb, pol_t);
-                        if (nsc == 2) tma_pair_2d(p + sg.st + 1024, &tmST, bar, kb * 256, tb + 1, pol_t);
+                        tma_pair_2d(p + sg.st, &tmST, bar, kb * (kSf / 4), tb, pol_t);
+                        if (nsc == 2) tma_pair_2d(p + sg.st + kSf, &tmST, bar, kb * (kSf / 4), tb + 1, pol_t);
                         at.next(sg.n);
                     }
                 }
@@ -542,7 +568,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         ok = mbar_wait_cluster(&ctl.acc_empty[buf ^ 1], ((it - 1) >> 1) & 1, abort);
                     tc_fence_after();
                     const uint32_t d_t = buf ? kAccEnd - ti.nt : 0;
-                    const uint32_t idesc = idesc_mxf4(256, ti.nt), idesc2 = idesc | (2u << 4) | (2u << 29);
+                    const uint32_t idesc = A8 ? idesc_mxf8(256, ti.nt) : idesc_mxf4(256, ti.nt);
+                    const uint32_t idesc2 = idesc | (2u << 4) | (2u << 29);
                     const bool two = ti.nt > 128;  // row blocks of group-row scales
                     // a stage's barrier is looked at before the MMAs of the one before are issued
                     // (one row, N 4096, K 16384: 16.7 us without, 15.6 with)
@@ -558,7 +585,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         const uint64_t w = w0 + o, tk = t0 + o, cw = cw0 + o, ct = ct0 + o;
                         const uint32_t sc = kAccEnd + slot;
                         const int left = args.K - kb * 256;
-                        if (left >= 256) {
+                        if constexpr (A8) {
+                            tc_cp_sf_pair(sc, cw);
+                            tc_cp_sf_pair(sc + 8, ct);
+                            if (two) tc_cp_sf_pair(sc + 12, ct + 32);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                tc_mma_mxf8_pair(d_t, w + 2 * j, tk + 2 * j, idesc | (j << 4) | (j << 29), sc,
+                                                 sc + 8, (kb | j) != 0);
+                        } else if (left >= 256) {
                             tc_cp_sf_pair(sc, cw);
                             tc_cp_sf_pair(sc + 8, ct);
                             if (two) tc_cp_sf_pair(sc + 12, ct + 64);
@@ -677,13 +712,19 @@ __global__ void __launch_bounds__(256) group_wait_probe_kernel(uint32_t* status,
     }
 }
 
-MxGemmKernel gemm_mxfp4_kernel_for(int out_dtype)
+template <bool A8>
+static MxGemmKernel gemm_mx_of(int out_dtype)
 {
     switch (out_dtype) {
-        case MOE_BF16: return gemm_mxfp4_kernel<__nv_bfloat16>;
-        case MOE_FP16: return gemm_mxfp4_kernel<__half>;
-        default: return gemm_mxfp4_kernel<float>;
+        case MOE_BF16: return gemm_mxfp4_kernel<__nv_bfloat16, A8>;
+        case MOE_FP16: return gemm_mxfp4_kernel<__half, A8>;
+        default: return gemm_mxfp4_kernel<float, A8>;
     }
+}
+
+MxGemmKernel gemm_mxfp4_kernel_for(bool eight_bits, int out_dtype)
+{
+    return eight_bits ? gemm_mx_of<true>(out_dtype) : gemm_mx_of<false>(out_dtype);
 }
 
 }  // namespace moe

@@ -411,7 +411,8 @@ struct MxQuantArgs {
 };
 constexpr int kMxQuantRun = 4 * 32;   // eights of a row that a warp takes at a time
 using MxQuantKernel = void (*)(MxQuantArgs);
-MxQuantKernel mx_quant_kernel_for(int dtype, bool vec, bool short_rows);
+// eight_bits: MXFP8 instead of MXFP4
+MxQuantKernel mx_quant_kernel_for(bool eight_bits, int dtype, bool vec, bool short_rows);
 MxQuantKernel mx_quant_transposed_kernel_for(int dtype, bool words);
 // columns of a tile of the transposing quantiser, and its shared memory
 constexpr int mx_transposed_cols(int elem_bytes) { return 256 / elem_bytes; }
@@ -466,7 +467,123 @@ inline int gemm_mxfp4_smem(int stages, int G, int out_bytes)
 }
 using MxGemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
                               MxGemmArgs);
-MxGemmKernel gemm_mxfp4_kernel_for(int out_dtype);
+// eight_bits: of MXFP8 group rows
+MxGemmKernel gemm_mxfp4_kernel_for(bool eight_bits, int out_dtype);
 __global__ void group_wait_probe_kernel(uint32_t* status, uint32_t* went_on, uint64_t limit_ns);
+
+// ---- route_scores.cu: routing from logits, and the gradient of the logits
+constexpr int kRouteWarps = 4;       // tokens of a block
+constexpr int kRouteGroups = 32;     // groups at most: a lane each
+struct RouteArgs {
+    const void* logits;
+    int64_t stride;       // in elements
+    const float* bias;    // nullable
+    int T, E, k;
+    int score;            // moe_score
+    int groups, topk_groups, group_score;
+    int renorm;
+    float scale;
+    int32_t* ids;
+    float* w;
+};
+using RouteKernel = void (*)(RouteArgs);
+RouteKernel route_scores_kernel_for(int dtype, int E);
+inline size_t route_smem(int E, int groups) { return groups > 1 ? (size_t)kRouteWarps * E * 8 : 0; }
+
+struct RouteBackArgs {
+    const void* logits;
+    int64_t stride;       // in elements
+    const int32_t* ids;
+    const float* dw;
+    int T, E, k;
+    int score, renorm;
+    float scale;
+    void* dlogits;
+    int64_t dstride;
+};
+using RouteBackKernel = void (*)(RouteBackArgs);
+RouteBackKernel route_back_kernel_for(int dtype);
+
+// ---- norm.cu: root-mean-square norm and its gradient
+constexpr int kNormMost = 16384;     // elements of a row: two eights in each of 1024 threads
+struct NormArgs {
+    const void* x;
+    int64_t x_stride;     // (strides in elements)
+    const void* res;      // nullable
+    int64_t res_stride;
+    const void* w;        // nullable: ones
+    float eps;
+    int T, H;
+    void* h;              // nullable
+    int64_t h_stride;
+    void* y;              // nullable
+    int64_t y_stride;
+    float* rstd;          // nullable
+    uint8_t* codes;       // nullable, with sf
+    uint8_t* sf;
+    int layout, rule;
+};
+using NormKernel = void (*)(NormArgs);
+// per: eights of a thread (1 or 2); one: a warp per row; vec: 16-byte pieces
+NormKernel norm_kernel_for(int dtype, int per, bool one, bool vec);
+
+struct NormBackArgs {
+    const void* dy;
+    int64_t dy_stride;
+    const void* h;
+    int64_t h_stride;
+    const void* w;        // nullable: ones
+    const float* rstd;
+    const void* dh;       // nullable
+    int64_t dh_stride;
+    int T, H;
+    void* dx;
+    int64_t dx_stride;
+    float* dw;            // nullable
+    float* ws;            // [parts][H]
+    int parts;
+};
+using NormBackKernel = void (*)(NormBackArgs);
+NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec);
+__global__ void norm_parts_kernel(const float* ws, int parts, int H, float* dw);
+// Parts of the weight's gradient: two blocks per SM of 152, each with a row (or, short rows, eight) at a
+// time.
+constexpr int kNormBlocks = 304;
+__host__ __device__ constexpr bool norm_one(int H, int per) { return H <= 256 * per; }
+inline int norm_parts(int T, int H, int per)
+{
+    const int most = norm_one(H, per) ? 8 * kNormBlocks : kNormBlocks;
+    return T < most ? T : most;
+}
+
+// ---- swiglu.cu: silu(gate) * up with 8-bit checkpoints, and its gradient
+struct SwigluArgs {
+    const void* gu;
+    int64_t gu_stride;    // in elements
+    int rows, inter, rule;
+    const int32_t* perm_src;  // nullable: rows with a negative entry are skipped
+    uint8_t* codes;
+    uint8_t* sf;
+    int layout;
+    uint8_t* ckpt;        // nullable, with ckpt_sf
+    uint8_t* ckpt_sf;
+};
+using SwigluKernel = void (*)(SwigluArgs);
+SwigluKernel swiglu_kernel_for(int dtype, bool vec);
+
+struct SwigluBackArgs {
+    const void* ds;
+    int64_t ds_stride;    // in elements
+    const uint8_t* ckpt;
+    const uint8_t* ckpt_sf;
+    int rows, inter, rule;
+    const int32_t* perm_src;
+    uint8_t* codes;       // nullable, with sf
+    uint8_t* sf;
+    int layout;
+    void* dgu;            // nullable
+};
+using SwigluBackKernel = void (*)(SwigluBackArgs);
+SwigluBackKernel swiglu_back_kernel_for(int dtype, bool vec);
 
 }  // namespace moe

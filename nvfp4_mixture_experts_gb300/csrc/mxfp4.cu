@@ -1,162 +1,9 @@
-// MXFP4: quantisation (of a matrix or of its transpose) and the tiled scale layout.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include <type_traits>
-
-#include "kernels.cuh"
+// MXFP4 and MXFP8: quantisation (MXFP4 also of a matrix's transpose) and the tiled scale layout.
+#include "mx.cuh"
 
 namespace moe {
 
 namespace {
-
-// Eight elements of a row as raw words.
-template <typename T>
-struct Eight {
-    static constexpr int kWords = 2 * (int)sizeof(T);
-    uint32_t w[kWords];
-
-    template <bool VEC>
-    __device__ __forceinline__ void load(const T* x)
-    {
-        if constexpr (VEC) {
-#pragma unroll
-            for (int q = 0; q < kWords / 4; ++q) {
-                const uint4 v = reinterpret_cast<const uint4*>(x)[q];
-                w[4 * q] = v.x;
-                w[4 * q + 1] = v.y;
-                w[4 * q + 2] = v.z;
-                w[4 * q + 3] = v.w;
-            }
-        } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = reinterpret_cast<const uint32_t*>(x)[q];
-        } else {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(x);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) w[q] = h[2 * q] | (uint32_t)h[2 * q + 1] << 16;
-        }
-    }
-    // bits (as fp32) of the largest magnitude over the eights of four neighbouring lanes; 16-bit
-    // types compare two magnitudes at a time (their bits are ordered as they are)
-    __device__ __forceinline__ uint32_t amax4() const
-    {
-        uint32_t m = 0;
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) m = max(m, w[q] & 0x7FFFFFFFu);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) m = max_u16x2(m, w[q] & 0x7FFF7FFFu);
-            m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            return bits16_f32(max(m & 0xFFFFu, m >> 16));
-        }
-    }
-    // the bits, as fp32, of a 16-bit element's value
-    static __device__ __forceinline__ uint32_t bits16_f32(uint32_t h)
-    {
-        if constexpr (std::is_same<T, __half>::value)
-            return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
-        else return h << 16;
-    }
-    __device__ __forceinline__ void to_f32(float (&v)[8]) const
-    {
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(w[q]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (std::is_same<T, __half>::value) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[q]));
-                    v[2 * q] = f.x;
-                    v[2 * q + 1] = f.y;
-                } else {
-                    v[2 * q] = __uint_as_float(w[q] << 16);
-                    v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void from_f32(const float (&v)[8])
-    {
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(v[q]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if constexpr (std::is_same<T, __half>::value) {
-                    const __half2 h = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
-                    w[q] = *reinterpret_cast<const uint32_t*>(&h);
-                } else {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
-                    w[q] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void store(T* x) const  // 16-byte aligned
-    {
-#pragma unroll
-        for (int q = 0; q < kWords / 4; ++q)
-            reinterpret_cast<uint4*>(x)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-    }
-    static __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
-    {
-        uint32_t r;
-        asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-};
-
-// The scale byte of a block from the bits of its largest magnitude (the magnitudes' bits are
-// ordered as the magnitudes are, infinities and NaNs above every number): exponent field - 2, one
-// more under the ceil rule when the significand passes 1.5 (m = 1.5 * 2^(e+2) is 6 * 2^e), at
-// least 0 (2^-127).  255 for an infinity or a NaN.
-__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits, int rule)
-{
-    if (amax_bits >= 0x7F800000u) return 255u;
-    int b = (int)(amax_bits >> 23) - 2;
-    if (rule == MOE_MX_CEIL && (amax_bits & 0x7FFFFFu) > 0x400000u) ++b;
-    return (uint32_t)max(b, 0);
-}
-
-// 2^(127 - s): what elements of a block with scale byte s (0..253) are multiplied by (255: any
-// number; its codes are not used).
-__device__ __forceinline__ float mx_encode_scale(uint32_t s)
-{
-    return __uint_as_float((254u - s) << 23);
-}
-
-// 2^(s - 127); s = 255: NaN.
-__device__ __forceinline__ float mx_decode_scale(uint32_t s)
-{
-    return s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s == 0 ? 0x400000u : s << 23);
-}
-
-// The values of eight E2M1 codes (a 32-bit word, the first in the lowest nibble).
-__device__ __forceinline__ void e2m1x8_to_f32(uint32_t codes, float (&v)[8])
-{
-    uint32_t h[4];
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(codes));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 p = *reinterpret_cast<const __half2*>(&h[i]);
-        v[2 * i] = __low2float(p);
-        v[2 * i + 1] = __high2float(p);
-    }
-}
 
 // Stores the scale bytes of blocks kb .. kb + 3 of row r (kb a multiple of 4; the bytes of blocks
 // past the row's end are zero, as the tiled layout wants them).
@@ -182,7 +29,7 @@ __device__ __forceinline__ void store_scales(uint8_t* sf, int layout, int64_t b,
 // together.  8192 x 4096 bf16: 24.4 us with values (152 MB, 6.2 TB/s: memory), 16.1 without (85 MB, 5.3
 // TB/s: the issue slots); fp32 with values 43.6 us (6.6 TB/s).  A run loaded ahead of the work on the
 // one before took 99 registers and 17.8 us without values, the same with.
-template <typename T, bool VEC>
+template <typename F, typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
 {
     pdl_wait();
@@ -207,7 +54,7 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
         for (int p = 0; p < kPer; ++p)
             if (u0 + 32 * p < units) e[p].template load<VEC>(x + 256 * p);
         const int64_t at = (int64_t)row * units + u0;
-        uint32_t* codes_at = reinterpret_cast<uint32_t*>(a.codes) + at;
+        typename F::Codes* codes_at = reinterpret_cast<typename F::Codes*>(a.codes) + at;
         T* values_at = static_cast<T*>(a.values) + at * 8;
         // the scale word of this lane's first block's atom (tiled), or its scale byte
         const int kb = u0 >> 2;
@@ -215,7 +62,7 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
                                                           : (size_t)row * blocks + kb);
         // piece p of the run; the bytes of blocks past the row's end are zero in the tiled layout
         auto piece = [&](int p, bool in) {
-            const uint32_t s = mx_scale_byte(e[p].amax4(), a.rule);
+            const uint32_t s = mx_scale_byte<F>(e[p].amax4(), a.rule);
             // the scales of four blocks (16 lanes) in one word
             uint32_t word = in ? s << (8 * ((lane >> 2) & 3)) : 0u;
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
@@ -226,7 +73,7 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
             const float scale = mx_encode_scale(s);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] *= scale;
-            const uint32_t codes = s == 255u ? 0u : f32x8_to_e2m1(v);
+            const typename F::Codes codes = s == 255u ? F::zero() : F::encode(v);
             codes_at[32 * p] = codes;
             // 8 blocks, two atoms, per 32 eights
             if (a.layout == MOE_SF_TILED) {
@@ -236,7 +83,7 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
             }
             if (a.values) {
                 const float d = mx_decode_scale(s);
-                e2m1x8_to_f32(codes, v);
+                F::decode(codes, v);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] *= d;
                 Eight<T> o;
@@ -259,7 +106,7 @@ __global__ void __launch_bounds__(256) mx_quant_kernel(MxQuantArgs a)
 // The same for short rows and small matrices: a thread per eight elements of all rows, so that a warp
 // is full whatever a row's length; a block's first thread stores its scale byte.  262144 x 32 bf16
 // with values: 9.5 us (38 MB, half of it in L2); 1 x 4096: 1.5 us (the launch).
-template <typename T, bool VEC>
+template <typename F, typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
 {
     pdl_wait();
@@ -277,15 +124,15 @@ __global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
         Eight<T> e = {};
         if (live)
             e.template load<VEC>(static_cast<const T*>(a.x) + b * a.batch_stride + r * a.row_stride + u * 8);
-        const uint32_t s = mx_scale_byte(e.amax4(), a.rule);
+        const uint32_t s = mx_scale_byte<F>(e.amax4(), a.rule);
         if (!live) continue;
         float v[8];
         e.to_f32(v);
         const float scale = mx_encode_scale(s);
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] *= scale;
-        const uint32_t codes = s == 255u ? 0u : f32x8_to_e2m1(v);
-        reinterpret_cast<uint32_t*>(a.codes)[i] = codes;
+        const typename F::Codes codes = s == 255u ? F::zero() : F::encode(v);
+        reinterpret_cast<typename F::Codes*>(a.codes)[i] = codes;
         if ((u & 3) == 0) {
             const int kb = u >> 2;
             if (a.layout == MOE_SF_CANONICAL) {
@@ -299,7 +146,7 @@ __global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
         }
         if (a.values) {
             const float d = mx_decode_scale(s);
-            e2m1x8_to_f32(codes, v);
+            F::decode(codes, v);
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] *= d;
             e.from_f32(v);
@@ -308,20 +155,26 @@ __global__ void __launch_bounds__(256) mx_quant_short_kernel(MxQuantArgs a)
     }
 }
 
-template <typename T>
+template <typename F, typename T>
 static MxQuantKernel mx_quant_of(bool vec, bool short_rows)
 {
-    if (short_rows) return vec ? mx_quant_short_kernel<T, true> : mx_quant_short_kernel<T, false>;
-    return vec ? mx_quant_kernel<T, true> : mx_quant_kernel<T, false>;
+    if (short_rows) return vec ? mx_quant_short_kernel<F, T, true> : mx_quant_short_kernel<F, T, false>;
+    return vec ? mx_quant_kernel<F, T, true> : mx_quant_kernel<F, T, false>;
 }
 
-MxQuantKernel mx_quant_kernel_for(int dtype, bool vec, bool short_rows)
+template <typename F>
+static MxQuantKernel mx_quant_of(int dtype, bool vec, bool short_rows)
 {
     switch (dtype) {
-        case MOE_BF16: return mx_quant_of<__nv_bfloat16>(vec, short_rows);
-        case MOE_FP16: return mx_quant_of<__half>(vec, short_rows);
-        default: return mx_quant_of<float>(vec, short_rows);
+        case MOE_BF16: return mx_quant_of<F, __nv_bfloat16>(vec, short_rows);
+        case MOE_FP16: return mx_quant_of<F, __half>(vec, short_rows);
+        default: return mx_quant_of<F, float>(vec, short_rows);
     }
+}
+
+MxQuantKernel mx_quant_kernel_for(bool eight_bits, int dtype, bool vec, bool short_rows)
+{
+    return eight_bits ? mx_quant_of<E4M3>(dtype, vec, short_rows) : mx_quant_of<E2M1>(dtype, vec, short_rows);
 }
 
 // ------------------------------------------------------------------ a matrix's transpose
@@ -386,7 +239,7 @@ __global__ void __launch_bounds__(256) mx_quant_transposed_kernel(MxQuantArgs a)
                 if (c + h >= C) break;
                 uint32_t am = m;
                 if constexpr (kPer == 2) am = Eight<T>::bits16_f32(h ? m >> 16 : m & 0xFFFFu);
-                const uint32_t s = mx_scale_byte(am, a.rule);
+                const uint32_t s = mx_scale_byte<E2M1>(am, a.rule);
                 const float scale = mx_encode_scale(s);
                 uint32_t codes[4];
 #pragma unroll
