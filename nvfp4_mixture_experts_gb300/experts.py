@@ -8,18 +8,29 @@ calls them:
   backward  moe_combine_backward -> moe_quant_mxfp4 -> product with W2^T -> the gate's gradient
             -> moe_quant_mxfp4 -> product with W13^T -> moe_dispatch_backward
 
+With act_bits 8 the activations and gradients are MXFP8 instead, and the gate's own operators hold
+what the backward pass needs of gate and up in 8 bits:
+
+  forward   moe_dispatch -> moe_quant_mxfp8 -> moe_grouped_gemm_mxfp8 (gate_up) -> moe_swiglu_mxfp8
+            -> moe_grouped_gemm_mxfp8 (down) -> moe_combine_weighted
+  backward  moe_combine_backward -> moe_quant_mxfp8 -> product with W2^T
+            -> moe_swiglu_mxfp8_backward -> product with W13^T -> moe_dispatch_backward
+
+MXShared is the same gate and products on every token: the shared expert.
+
 The quantisation of activations and gradients is passed straight through; the weights (adapters
 and routers train around them) have no gradient, and the gradients have none (second derivatives
-raise).  The elementwise gate is torch's, on all rows of
+raise).  With act_bits 4 the elementwise gate is torch's, on all rows of
 the sorted buffers: rows of no pair hold stale values that nothing downstream reads.
 """
 import torch
 
-from . import (MOE_DEV_WAIT_TIMEOUT, MOE_ERR_DEVICE_STATUS, MOE_ERR_TIMEOUT, MOE_ERR_UNSUPPORTED,
-               MOE_MX_CEIL, MOE_OK, MOE_SF_TILED, MoEError, moe_combine_backward,
+from . import (MOE_DEV_WAIT_TIMEOUT, MOE_ERR_DEVICE_STATUS, MOE_ERR_INVALID, MOE_ERR_TIMEOUT,
+               MOE_ERR_UNSUPPORTED, MOE_MX_CEIL, MOE_OK, MOE_SF_TILED, MoEError, moe_combine_backward,
                moe_combine_weighted, moe_dispatch, moe_dispatch_backward,
-               moe_dispatch_rows_capacity, moe_grouped_gemm_mxfp4, moe_mxfp4_scale_bytes,
-               moe_mxfp4_tile_scales, moe_quant_mxfp4)
+               moe_dispatch_rows_capacity, moe_grouped_gemm_mxfp4, moe_grouped_gemm_mxfp8,
+               moe_mxfp4_scale_bytes, moe_mxfp4_tile_scales, moe_quant_mxfp4, moe_quant_mxfp8,
+               moe_swiglu_mxfp8, moe_swiglu_mxfp8_backward)
 
 ROW_ALIGN = 128  # groups start on whole row blocks of scales, as the product reads them
 
@@ -36,30 +47,85 @@ def quantise(x, transpose=False, perm_src=None, scale_rule=MOE_MX_CEIL):
     return codes, sf
 
 
+def _empty8(rows, cols, device):
+    """Room for an MXFP8 matrix [rows, cols] with tiled scales."""
+    codes = torch.empty(rows, cols, dtype=torch.uint8, device=device)
+    return codes, torch.empty(moe_mxfp4_scale_bytes(1, rows, cols, MOE_SF_TILED), dtype=torch.uint8,
+                              device=device)
+
+
+def quantise8(x, perm_src=None):
+    """(codes, tiled scales) of the rows x [rows, cols] as an MXFP8 matrix."""
+    codes, sf = _empty8(*x.shape, x.device)
+    moe_quant_mxfp8(x, codes, sf, MOE_SF_TILED, perm_src=perm_src)
+    return codes, sf
+
+
+class _Gated8:
+    """silu(gate) * up between two products of MXFP8 rows with MXFP4 weights, and its gradient.  counts,
+    offsets, perm: the rows' groups (None: one group, of all rows)."""
+
+    def __init__(self, ex, counts=None, offsets=None, perm=None):
+        self.ex, self.groups, self.perm = ex, (counts, offsets), perm
+
+    def product(self, a, w, cols, dtype):
+        out = torch.empty(a[0].shape[0], cols, dtype=dtype, device=a[0].device)
+        moe_grouped_gemm_mxfp8(*a, *self.groups, *w, out, status=self.ex.status)
+        return out
+
+    def forward(self, a, dtype, keep):
+        """a: the rows' codes and tiled scales; (rows of the down product, checkpoint or None)."""
+        ex, rows, dev = self.ex, a[0].shape[0], a[0].device
+        gu = self.product(a, ex.w13, 2 * ex.inter, dtype)
+        s, ckpt = _empty8(rows, ex.inter, dev), (None, None)
+        if keep:
+            ckpt = (torch.empty(rows, 2 * ex.inter, dtype=torch.uint8, device=dev),
+                    torch.empty(rows, ex.inter // 16, dtype=torch.uint8, device=dev))
+        moe_swiglu_mxfp8(gu, *s, MOE_SF_TILED, ckpt=ckpt[0], ckpt_sf=ckpt[1], perm_src=self.perm)
+        return self.product(s, ex.w2, ex.hidden, dtype), ckpt
+
+    def backward(self, dy, ckpt):
+        """The gradient of the rows for the gradient dy of the down product's."""
+        ex = self.ex
+        if ex.w13_t is None:
+            raise RuntimeError("%s without transposed weights has no backward" % type(ex).__name__)
+        ds = self.product(quantise8(dy, self.perm), ex.w2_t, ex.inter, dy.dtype)
+        dgu = _empty8(dy.shape[0], 2 * ex.inter, dy.device)
+        moe_swiglu_mxfp8_backward(ds, *ckpt, *dgu, MOE_SF_TILED, perm_src=self.perm)
+        return self.product(dgu, ex.w13_t, ex.hidden, dy.dtype)
+
+
 class MXExperts:
     """Experts local_off .. local_off + num_local - 1 of num_experts: w13 [num_local, 2I, H] (gate
-    rows, then up rows) and w2 [num_local, H, I], H and I multiples of 32."""
+    rows, then up rows) and w2 [num_local, H, I], H and I multiples of 32 (with act_bits 8, of 128)."""
 
-    def __init__(self, num_experts, local_off, w13, w13_sf, w2, w2_sf, w13_t=None, w2_t=None):
+    def __init__(self, num_experts, local_off, w13, w13_sf, w2, w2_sf, w13_t=None, w2_t=None,
+                 act_bits=4):
         """w13, w2: MXFP4 codes [num_local, rows, cols / 2] with tiled scales w13_sf, w2_sf.  w13_t,
         w2_t: (codes, scales) of each expert's transposed matrices; without them there is no
-        backward."""
+        backward.  act_bits: of the activations and gradients that the products read (4 or 8)."""
         self.num_experts, self.local_off = num_experts, local_off
         self.num_local, two_inter, half_hidden = w13.shape
         self.hidden, self.inter = 2 * half_hidden, two_inter // 2
+        self.act_bits = act_bits
+        if act_bits not in (4, 8):
+            raise MoEError(MOE_ERR_INVALID, "MXExperts: act_bits %r" % (act_bits,))
+        if act_bits == 8 and (self.hidden % 128 or self.inter % 128):
+            raise MoEError(MOE_ERR_UNSUPPORTED, "MXExperts: hidden %d, inter %d with 8-bit activations"
+                           % (self.hidden, self.inter))
         self.w13, self.w2, self.w13_t, self.w2_t = (w13, w13_sf), (w2, w2_sf), w13_t, w2_t
         self.status = torch.zeros(1, dtype=torch.int32, device=w13.device)
 
     @classmethod
-    def from_master(cls, num_experts, local_off, w13, w2, backward=True):
+    def from_master(cls, num_experts, local_off, w13, w2, backward=True, act_bits=4):
         """Quantises bf16/fp16/fp32 master weights; for the backward pass their transposes too
         (blocks of 32 run along the contraction, so a transpose has its own codes)."""
         return cls(num_experts, local_off, *quantise(w13), *quantise(w2),
                    quantise(w13, transpose=True) if backward else None,
-                   quantise(w2, transpose=True) if backward else None)
+                   quantise(w2, transpose=True) if backward else None, act_bits=act_bits)
 
     @classmethod
-    def from_checkpoint(cls, num_experts, local_off, w13, w13_sf, w2, w2_sf):
+    def from_checkpoint(cls, num_experts, local_off, w13, w13_sf, w2, w2_sf, act_bits=4):
         """Codes and canonical scales [num_local, rows, cols / 32] of a checkpoint (forward only)."""
         tiled = []
         for codes, sf in ((w13, w13_sf), (w2, w2_sf)):
@@ -68,7 +134,7 @@ class MXExperts:
                             device=codes.device)
             moe_mxfp4_tile_scales(sf, n, rows, cols, t)
             tiled += [codes, t]
-        return cls(num_experts, local_off, *tiled)
+        return cls(num_experts, local_off, *tiled, act_bits=act_bits)
 
     def __call__(self, x, topk_ids, topk_w):
         """The shard's partial sum [T, H] in x's type for tokens x [T, H] routed to topk_ids
@@ -87,6 +153,29 @@ class MXExperts:
         if bits & MOE_DEV_WAIT_TIMEOUT:
             return MOE_ERR_TIMEOUT, bits
         return (MOE_ERR_DEVICE_STATUS if bits else MOE_OK), bits
+
+
+class MXShared(MXExperts):
+    """The shared expert: MXFP4 weights w13 [1, 2I, H] and w2 [1, H, I] applied to every token with 8-bit
+    activations.  Made as MXExperts are, from_master(w13, w2) or from_checkpoint(w13, w13_sf, w2, w2_sf)."""
+
+    def __init__(self, num_experts, local_off, *args, **kw):
+        super().__init__(num_experts, local_off, *args, **dict(kw, act_bits=8))
+        if self.num_local != 1:
+            raise MoEError(MOE_ERR_INVALID, "MXShared: %d experts" % self.num_local)
+
+    @classmethod
+    def from_master(cls, w13, w2, backward=True):
+        return super().from_master(1, 0, w13, w2, backward=backward, act_bits=8)
+
+    @classmethod
+    def from_checkpoint(cls, w13, w13_sf, w2, w2_sf):
+        return super().from_checkpoint(1, 0, w13, w13_sf, w2, w2_sf, act_bits=8)
+
+    def __call__(self, x, eight=None):
+        """[T, H] in x's type for tokens x [T, H]; differentiable in x.  eight: x as an MXFP8 matrix with
+        tiled scales, where the caller has it already (moe_rmsnorm's)."""
+        return _Shared.apply(x, *(eight or (None, None)), self)
 
 
 class _FirstOrder(torch.autograd.Function):
@@ -115,6 +204,16 @@ class _Experts(torch.autograd.Function):
         moe_dispatch(x, topk_ids, ex.num_experts, ex.local_off, ex.num_local, ROW_ALIGN, counts,
                      offsets, perm, inv, rows, ex.status)
 
+        w = topk_w.detach().float().contiguous()
+        out = torch.empty(T, ex.hidden, dtype=dt, device=dev)
+        if ex.act_bits == 8:
+            gated = _Gated8(ex, counts, offsets, perm)
+            y, ckpt = gated.forward(quantise8(rows, perm), dt, any(ctx.needs_input_grad))
+            moe_combine_weighted(y, inv, w, out)
+            ctx.ex, ctx.gated, ctx.k = ex, gated, k
+            ctx.save_for_backward(y, w, inv, *ckpt)
+            return out
+
         def product(a, w, cols, dtype):
             out = torch.empty(cap, cols, dtype=dtype, device=dev)
             moe_grouped_gemm_mxfp4(*quantise(a, perm_src=perm), counts, offsets, *w, out,
@@ -124,8 +223,6 @@ class _Experts(torch.autograd.Function):
         gu = product(rows, ex.w13, 2 * ex.inter, torch.float32)
         gate, up = gu[:, :ex.inter], gu[:, ex.inter:]
         y = product(torch.nn.functional.silu(gate) * up, ex.w2, ex.hidden, dt)
-        w = topk_w.detach().float().contiguous()
-        out = torch.empty(T, ex.hidden, dtype=dt, device=dev)
         moe_combine_weighted(y, inv, w, out)
         ctx.ex, ctx.product, ctx.k = ex, product, k
         ctx.save_for_backward(gu, y, w, inv)
@@ -146,6 +243,14 @@ class _Experts(torch.autograd.Function):
         ex, k = ctx.ex, ctx.k
         if ex.w13_t is None:
             raise RuntimeError("MXExperts without transposed weights has no backward")
+        if ex.act_bits == 8:
+            y, w, inv, *ckpt = ctx.saved_tensors
+            dout = dout.to(y.dtype).contiguous()
+            dy, dw = torch.empty_like(y), torch.empty_like(w)
+            moe_combine_backward(dout, y, inv, w, dy, dw)
+            dx = torch.empty_like(dout)
+            moe_dispatch_backward(ctx.gated.backward(dy, ckpt), inv, k, dx)
+            return dx, dw
         gu, y, w, inv = ctx.saved_tensors
         dout = dout.to(y.dtype).contiguous()
         dy, dw = torch.empty_like(y), torch.empty_like(w)
@@ -158,3 +263,22 @@ class _Experts(torch.autograd.Function):
         dx = torch.empty_like(dout)
         moe_dispatch_backward(drows, inv, k, dx)
         return dx, dw
+
+
+class _Shared(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, codes, sf, ex):
+        gated = _Gated8(ex)
+        eight = quantise8(x) if codes is None else (codes, sf)
+        y, ckpt = gated.forward(eight, x.dtype, ctx.needs_input_grad[0])
+        ctx.gated, ctx.dtype = gated, x.dtype
+        ctx.save_for_backward(*ckpt)
+        return y
+
+    @staticmethod
+    def backward(ctx, dout):
+        with torch.no_grad():
+            dx = ctx.gated.backward(dout.to(ctx.dtype).contiguous(), ctx.saved_tensors)
+        if torch.is_grad_enabled():
+            dx, = _FirstOrder.apply(dx.requires_grad_())
+        return dx, None, None, None
