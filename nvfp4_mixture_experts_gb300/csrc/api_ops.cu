@@ -569,6 +569,7 @@ moe_status moe_route_scores(const void* logits_d, int32_t dtype, int64_t stride,
     a.groups = topk_groups == num_groups ? 1 : num_groups;  // (of all groups: no choice among them)
     a.topk_groups = a.groups == 1 ? 1 : topk_groups;
     a.group_score = group_score;
+    a.group = FastDiv(num_experts / num_groups);
     a.renorm = renormalise;
     a.scale = scale;
     a.ids = topk_ids_d;
@@ -608,7 +609,7 @@ moe_status moe_route_scores_backward(const void* logits_d, int32_t dtype, int64_
     a.scale = scale;
     a.dlogits = dlogits_d;
     a.dstride = dstride;
-    return launch(route_back_kernel_for(dtype), dim3(ceil_div(T, kRouteWarps)), dim3(32 * kRouteWarps), 0,
+    return launch(route_back_kernel_for(dtype, score == MOE_SCORE_SOFTMAX && !renormalise, num_experts), dim3(ceil_div(T, kRouteWarps)), dim3(32 * kRouteWarps), 0,
                   reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
@@ -712,9 +713,9 @@ moe_status moe_rmsnorm_backward(const void* dy_d, int32_t dtype, int64_t dy_stri
     const int per = norm_per(T, H);
     const bool one = norm_one(H, per);
     a.parts = norm_parts(T, H, per);
-    const moe_status done = launch(norm_back_kernel_for(dtype, per, one, vec),
-                                   dim3(one ? ceil_div(a.parts, 8) : a.parts),
-                                   dim3(one ? 256 : norm_threads(H, per)), 0, s, true, a);
+    const int threads = one ? 256 : norm_threads(H, per);
+    const moe_status done = launch(norm_back_kernel_for(dtype, per, one, vec, threads),
+                                   dim3(one ? ceil_div(a.parts, 8) : a.parts), dim3(threads), 0, s, true, a);
     if (done != MOE_OK || !dweight_d || a.parts == 1) return done;
     return launch(norm_parts_kernel, dim3(ceil_div(H, 32)), dim3(256), 0, s, true, a.ws, a.parts, H, dweight_d);
 }
@@ -736,6 +737,8 @@ moe_status moe_swiglu_mxfp8(const void* gate_up_d, int32_t dtype, int64_t stride
     a.gu_stride = stride;
     a.rows = rows;
     a.inter = inter;
+    a.eights = (uint32_t)((int64_t)rows * (inter / 8));
+    a.units = FastDiv(inter / 8);
     a.rule = scale_rule;
     a.perm_src = perm_src_d;
     a.codes = codes_d;
@@ -745,7 +748,7 @@ moe_status moe_swiglu_mxfp8(const void* gate_up_d, int32_t dtype, int64_t stride
     a.ckpt_sf = ckpt_sf_d;
     const int es = elem_bytes(dtype);
     const bool vec = rows_vec(gate_up_d, (int64_t)inter * es, rows > 1 ? stride * es : 0);
-    return launch(swiglu_kernel_for(dtype, vec), dim3(blocks_for((int64_t)rows * (inter / 8), 256, 16)),
+    return launch(swiglu_kernel_for(dtype, vec), dim3(blocks_for((int64_t)rows * (inter / 8), 256, 8)),
                   dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
@@ -770,6 +773,8 @@ moe_status moe_swiglu_mxfp8_backward(const void* ds_d, int32_t dtype, int64_t st
     a.ckpt_sf = ckpt_sf_d;
     a.rows = rows;
     a.inter = inter;
+    a.eights = (uint32_t)((int64_t)rows * (inter / 8));
+    a.units = FastDiv(inter / 8);
     a.rule = scale_rule;
     a.perm_src = perm_src_d;
     a.codes = codes_d;
@@ -778,7 +783,7 @@ moe_status moe_swiglu_mxfp8_backward(const void* ds_d, int32_t dtype, int64_t st
     a.dgu = dgate_up_d;
     const int es = elem_bytes(dtype);
     const bool vec = rows_vec(ds_d, (int64_t)inter * es, rows > 1 ? stride * es : 0);
-    return launch(swiglu_back_kernel_for(dtype, vec), dim3(blocks_for((int64_t)rows * (inter / 8), 256, 16)),
+    return launch(swiglu_back_kernel_for(dtype, vec), dim3(blocks_for((int64_t)rows * (inter / 8), 256, 8)),
                   dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 

@@ -471,6 +471,26 @@ using MxGemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap
 MxGemmKernel gemm_mxfp4_kernel_for(bool eight_bits, int out_dtype);
 __global__ void group_wait_probe_kernel(uint32_t* status, uint32_t* went_on, uint64_t limit_ns);
 
+// Division of 32-bit numbers by one that a launch fixes, by a product (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994, figure 4.1).
+struct FastDiv {
+    uint32_t d, m, s1, s2;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t by) : d(by)
+    {
+        uint32_t l = 0;
+        while (l < 32 && (1ull << l) < by) ++l;   // 2^l >= by
+        m = (uint32_t)((1ull << 32) * ((1ull << l) - by) / by + 1);
+        s1 = l < 1 ? l : 1;
+        s2 = l < 1 ? 0 : l - 1;
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const
+    {
+        const uint32_t t = __umulhi(m, n);
+        return (t + ((n - t) >> s1)) >> s2;
+    }
+};
+
 // ---- route_scores.cu: routing from logits, and the gradient of the logits
 constexpr int kRouteWarps = 4;       // tokens of a block
 constexpr int kRouteGroups = 32;     // groups at most: a lane each
@@ -481,6 +501,7 @@ struct RouteArgs {
     int T, E, k;
     int score;            // moe_score
     int groups, topk_groups, group_score;
+    FastDiv group;        // by the experts of a group
     int renorm;
     float scale;
     int32_t* ids;
@@ -502,7 +523,8 @@ struct RouteBackArgs {
     int64_t dstride;
 };
 using RouteBackKernel = void (*)(RouteBackArgs);
-RouteBackKernel route_back_kernel_for(int dtype);
+// dense: every logit has a gradient (softmax scores that are not renormalised)
+RouteBackKernel route_back_kernel_for(int dtype, bool dense, int E);
 
 // ---- norm.cu: root-mean-square norm and its gradient
 constexpr int kNormMost = 16384;     // elements of a row: two eights in each of 1024 threads
@@ -544,7 +566,7 @@ struct NormBackArgs {
     int parts;
 };
 using NormBackKernel = void (*)(NormBackArgs);
-NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec);
+NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec, int threads);
 __global__ void norm_parts_kernel(const float* ws, int parts, int H, float* dw);
 // Parts of the weight's gradient: two blocks per SM of 152, each with a row (or, short rows, eight) at a
 // time.
@@ -561,6 +583,8 @@ struct SwigluArgs {
     const void* gu;
     int64_t gu_stride;    // in elements
     int rows, inter, rule;
+    uint32_t eights;      // of all rows
+    FastDiv units;        // by the eights of a row
     const int32_t* perm_src;  // nullable: rows with a negative entry are skipped
     uint8_t* codes;
     uint8_t* sf;
@@ -577,6 +601,8 @@ struct SwigluBackArgs {
     const uint8_t* ckpt;
     const uint8_t* ckpt_sf;
     int rows, inter, rule;
+    uint32_t eights;      // of all rows
+    FastDiv units;        // by the eights of a row
     const int32_t* perm_src;
     uint8_t* codes;       // nullable, with sf
     uint8_t* sf;

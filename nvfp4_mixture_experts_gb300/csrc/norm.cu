@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_kernel(NormArgs a)
 // With d = dy w and x^ = h rstd: dx = rstd (d - x^ mean(d x^)) + dh, dw = sum over the rows of dy x^.  A
 // block (ONE: a warp) takes every (number of parts)-th row and holds its part of dw in registers; the
 // parts are added up in order by the second kernel, so results do not change from call to call.
-template <typename T, int PER, bool ONE, bool VEC>
-__global__ void __launch_bounds__(ONE ? 256 : 1024) norm_back_kernel(NormBackArgs a)
+template <typename T, int PER, bool ONE, bool VEC, int NT>
+__global__ void __launch_bounds__(NT) norm_back_kernel(NormBackArgs a)
 {
     __shared__ float s_part[2][32];
     pdl_wait();
@@ -158,9 +158,12 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_back_kernel(NormBackArg
             for (int i = 0; i < 8; ++i) w[p][i] = 1.0f;
     }
     int buf = 0;
-    for (int64_t row = part; row < a.T; row += a.parts) {
-        const float rstd = a.rstd[row];
-        Eight<T> dy[PER] = {}, h[PER] = {}, dh[PER] = {};
+    Eight<T> dy[PER] = {}, h[PER] = {}, dh[PER] = {};
+    float rstd = 0.0f;
+    // The next row's loads are in flight during this one's sum: a block has few rows at a time.
+    auto load = [&](int64_t row, Eight<T>(&dy)[PER], Eight<T>(&h)[PER], Eight<T>(&dh)[PER], float& rstd) {
+        if (row >= a.T) return;
+        rstd = a.rstd[row];
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             const int u = tid + p * nt;
@@ -170,6 +173,12 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_back_kernel(NormBackArg
                 if (a.dh) load_eight<VEC>(dh[p], static_cast<const T*>(a.dh) + row * a.dh_stride, u, a.H);
             }
         }
+    };
+    load(part, dy, h, dh, rstd);
+    for (int64_t row = part; row < a.T; row += a.parts) {
+        Eight<T> dy2[PER] = {}, h2[PER] = {}, dh2[PER] = {};
+        float rstd2 = 0.0f;
+        load(row + a.parts, dy2, h2, dh2, rstd2);
         float dot = 0.0f;
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
@@ -199,6 +208,13 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_back_kernel(NormBackArg
             o.from_f32(d);
             store_eight<VEC>(o, static_cast<T*>(a.dx) + row * a.dx_stride, u, a.H);
         }
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            dy[p] = dy2[p];
+            h[p] = h2[p];
+            dh[p] = dh2[p];
+        }
+        rstd = rstd2;
     }
     if (!a.dw || part >= a.parts) return;
     float* out = a.parts == 1 ? a.dw : a.ws + (int64_t)part * a.H;
@@ -250,21 +266,20 @@ NormKernel norm_kernel_for(int dtype, int per, bool one, bool vec)
     }
 }
 
-template <typename T>
-static NormBackKernel norm_back_of(int per, bool one, bool vec)
+template <typename T, bool VEC>
+static NormBackKernel norm_back_of(int per, bool one, int threads)
 {
-    if (one) return per == 1 ? (vec ? norm_back_kernel<T, 1, true, true> : norm_back_kernel<T, 1, true, false>)
-                             : (vec ? norm_back_kernel<T, 2, true, true> : norm_back_kernel<T, 2, true, false>);
-    return per == 1 ? (vec ? norm_back_kernel<T, 1, false, true> : norm_back_kernel<T, 1, false, false>)
-                    : (vec ? norm_back_kernel<T, 2, false, true> : norm_back_kernel<T, 2, false, false>);
+    if (one) return per == 1 ? norm_back_kernel<T, 1, true, VEC, 256> : norm_back_kernel<T, 2, true, VEC, 256>;
+    return threads <= 512 ? norm_back_kernel<T, 2, false, VEC, 512> : norm_back_kernel<T, 2, false, VEC, 1024>;
 }
 
-NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec)
+NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec, int threads)
 {
     switch (dtype) {
-        case MOE_BF16: return norm_back_of<__nv_bfloat16>(per, one, vec);
-        case MOE_FP16: return norm_back_of<__half>(per, one, vec);
-        default: return norm_back_of<float>(per, one, vec);
+        case MOE_BF16:
+            return vec ? norm_back_of<__nv_bfloat16, true>(per, one, threads) : norm_back_of<__nv_bfloat16, false>(per, one, threads);
+        case MOE_FP16: return vec ? norm_back_of<__half, true>(per, one, threads) : norm_back_of<__half, false>(per, one, threads);
+        default: return vec ? norm_back_of<float, true>(per, one, threads) : norm_back_of<float, false>(per, one, threads);
     }
 }
 

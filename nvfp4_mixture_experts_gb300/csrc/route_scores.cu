@@ -84,6 +84,73 @@ __device__ __forceinline__ K take_max(K (&key)[PL], int& expert)
     return best;
 }
 
+// The `rounds` largest keys in order (equal ones by expert), that of lane j in `kept` and its expert in
+// `mine`.  Keys as large as the rounds-th largest of the lanes' maxima are the only ones that can be among
+// them: mostly few, which move to a lane each and are ranked by counting (8192 tokens of 320 experts, 8 of
+// 160 in the best groups: 11 of 5 rounds of all keys, 2 of this).  More than 32, as of equal logits: in
+// rounds.
+template <int PL>
+__device__ __forceinline__ void choose_32(const uint32_t (&key)[PL], int rounds, uint32_t* s_key, int* s_expert,
+                                          uint32_t& kept, int& mine)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t x = key[0];
+#pragma unroll
+    for (int i = 1; i < PL; ++i) x = max(x, key[i]);
+    uint32_t bound = 1;
+    for (int j = 0; j < rounds; ++j) {
+        bound = warp_max(x);
+        if (lane == __ffs(__ballot_sync(kAll, x == bound)) - 1) x = 0;
+    }
+    bound = max(bound, 1u);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        const bool in = key[i] >= bound;
+        const uint32_t mask = __ballot_sync(kAll, in);
+        const int at = n + __popc(mask & ((1u << lane) - 1));
+        if (in && at < 32) {
+            s_key[at] = key[i];
+            s_expert[at] = 32 * i + lane;
+        }
+        n += __popc(mask);
+    }
+    kept = 0;
+    mine = 0;
+    if (n <= 32) {
+        __syncwarp();
+        const uint32_t k = lane < n ? s_key[lane] : 0u;
+        const int e = s_expert[lane];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const uint32_t o = __shfl_sync(kAll, k, j);
+            rank += o > k || (o == k && j < lane);   // (they lie in the order of the experts)
+        }
+        __syncwarp();
+        if (lane < n) {
+            s_key[rank] = k;
+            s_expert[rank] = e;
+        }
+        __syncwarp();
+        if (lane < min(n, rounds)) {
+            kept = s_key[lane];
+            mine = s_expert[lane];
+        }
+        return;
+    }
+    uint32_t left[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) left[i] = key[i];
+    for (int j = 0; j < min(rounds, 32); ++j) {
+        int e;
+        const uint32_t k = take_max<PL>(left, e);
+        if (lane == j) {
+            kept = k;
+            mine = e;
+        }
+    }
+}
+
 // Bit g: group g is among the topk_groups best; ties go to the lower group.  score: lane g's group.  `edge`
 // receives the scores of the last group taken and the first left out.
 template <typename F>
@@ -117,12 +184,8 @@ __device__ __forceinline__ F group_score(const F* keys, int groups, int n, bool 
     if (g < groups)
         for (int i = lane % per; i < n; i += per) {
             const F v = keys[g * n + i];
-            if (v > a) {
-                b = a;
-                a = v;
-            } else if (v > b) {
-                b = v;
-            }
+            b = fmax(b, fmin(a, v));
+            a = fmax(a, v);
         }
     for (int o = 1; o < per; o <<= 1) {
         const F c = __shfl_xor_sync(kAll, a, o), d = __shfl_xor_sync(kAll, b, o);
@@ -133,50 +196,69 @@ __device__ __forceinline__ F group_score(const F* keys, int groups, int n, bool 
     return __shfl_sync(kAll, s, (lane * per) & 31);
 }
 
-// The choice with keys in 64 bits: expert j of lane j.  (Out of line: few tokens need it.)
-template <int PL>
-__device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[PL], double* s_keys)
-{
-    const int lane = threadIdx.x & 31;
-    double m = -INFINITY, sum = 0.0;
-    if (a.score == MOE_SCORE_SOFTMAX) {
-        float mf = -INFINITY;
+// A token's scores in 64 bits.  (What follows is out of line and reads the logits again: few tokens need it.)
+template <typename T>
+struct Scores64 {
+    const RouteArgs& a;
+    const T* x;
+    double m, sum;
+    __device__ __forceinline__ float logit(int e) const
+    {
+        const float l = to_f32(x[e]);
+        return l != l ? -INFINITY : l;
+    }
+    __device__ Scores64(const RouteArgs& a, const T* x) : a(a), x(x), m(0.0), sum(1.0)
+    {
+        if (a.score != MOE_SCORE_SOFTMAX) return;
+        const int lane = threadIdx.x & 31;
+        float top = -INFINITY;
+        for (int e = lane; e < a.E; e += 32) top = fmaxf(top, logit(e));
 #pragma unroll
-        for (int i = 0; i < PL; ++i) mf = fmaxf(mf, l[i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(kAll, mf, o));
-        m = mf;
-        for (int i = 0; i < PL; ++i)
-            if (l[i] > -INFINITY) sum += l[i] == m ? 1.0 : exp((double)l[i] - m);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        m = top;
+        sum = 0.0;
+        for (int e = lane; e < a.E; e += 32) {
+            const float l = logit(e);
+            if (l > -INFINITY) sum += l == m ? 1.0 : exp((double)l - m);
+        }
         sum = warp_sum(sum);
     }
+    // the key of a sum: score and bias
+    __device__ double key(int e) const
+    {
+        const float l = logit(e);
+        if (l == -INFINITY) return -INFINITY;
+        double v = a.score == MOE_SCORE_SOFTMAX ? (l == m ? 1.0 : exp((double)l - m)) / sum
+                                                : 1.0 / (1.0 + exp(-(double)l));
+        if (a.bias) v += (double)a.bias[e];
+        return v >= -DBL_MAX ? v : -INFINITY;  // a bias of -infinity or NaN
+    }
+};
+
+// The choice with all keys in 64 bits: expert j of lane j.
+template <int PL, typename T>
+__device__ __noinline__ int choose_64(const RouteArgs& a, const T* x, double* s_keys)
+{
+    const int lane = threadIdx.x & 31;
+    const Scores64<T> sc(a, x);
     uint64_t key[PL];
-    const int n = a.E / a.groups;
-#pragma unroll
     for (int i = 0; i < PL; ++i) {
         const int e = 32 * i + lane;
         key[i] = 0;
         if (e >= a.E) continue;
-        double v = -INFINITY, own = l[i];
-        if (l[i] > -INFINITY) {
-            v = a.score == MOE_SCORE_SOFTMAX ? (l[i] == m ? 1.0 : exp((double)l[i] - m)) / sum : 1.0 / (1.0 + exp(-(double)l[i]));
-            if (a.bias) v += (double)a.bias[e];
-            if (!(v >= -DBL_MAX)) v = -INFINITY;  // a bias of -infinity or NaN
-            if (a.bias) own = v;
-        }
+        const double v = sc.key(e);
         if (a.groups > 1) s_keys[e] = v;
-        key[i] = ordered(own);
+        key[i] = ordered(a.bias ? v : (double)sc.logit(e));
     }
     if (a.groups > 1) {
         __syncwarp();
         double edge[2];
-        const uint32_t in = best_groups(group_score(s_keys, a.groups, n, a.group_score == MOE_GROUP_TOP2),
+        const uint32_t in = best_groups(group_score(s_keys, a.groups, a.E / a.groups, a.group_score == MOE_GROUP_TOP2),
                                         a.groups, a.topk_groups, edge);
         __syncwarp();
-#pragma unroll
         for (int i = 0; i < PL; ++i) {
             const int e = 32 * i + lane;
-            if (e < a.E && !(in >> (e / n) & 1)) key[i] = 0;
+            if (e < a.E && !(in >> a.group.div(e) & 1)) key[i] = 0;
         }
     }
     int mine = 0;
@@ -188,6 +270,43 @@ __device__ __noinline__ int choose_64(const RouteArgs& a, const float (&l)[PL], 
     return mine;
 }
 
+// The order of n candidates, one a lane, by their keys in 64 bits: expert j of lane j.
+template <typename T>
+__device__ __noinline__ int order_64(const RouteArgs& a, const T* x, int mine, int n)
+{
+    const int lane = threadIdx.x & 31;
+    const Scores64<T> sc(a, x);
+    const double k = lane < n ? sc.key(mine) : -INFINITY;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+        const double o = __shfl_sync(kAll, k, j);
+        const int e = __shfl_sync(kAll, mine, j);
+        rank += o > k || (o == k && e < mine);
+    }
+    int out = 0;
+    for (int j = 0; j < n; ++j) {
+        const int r = __shfl_sync(kAll, rank, j), e = __shfl_sync(kAll, mine, j);
+        if (r == lane) out = e;
+    }
+    return out;
+}
+
+__device__ __forceinline__ float ex2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
 }  // namespace
 
 // A warp per token, expert 32 i + lane in the registers of a lane.
@@ -195,6 +314,8 @@ template <int PL, typename T>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArgs a)
 {
     extern __shared__ double s_all[];  // [kRouteWarps][E] keys, where there are groups
+    __shared__ uint32_t s_key[kRouteWarps][32];
+    __shared__ int s_expert[kRouteWarps][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -204,15 +325,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
     const T* x = static_cast<const T*>(a.logits) + t * a.stride;
     float l[PL];
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) l[i] = 32 * i + lane < a.E ? to_f32(x[32 * i + lane]) : -INFINITY;
     bool nan = false;  // of this token's weights: a logit is NaN, which ranks last, or has no softmax
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-        const int e = 32 * i + lane;
-        l[i] = e < a.E ? to_f32(x[e]) : -INFINITY;
         nan = nan || l[i] != l[i] || (softmax && l[i] == INFINITY);
         if (l[i] != l[i]) l[i] = -INFINITY;
     }
-    const bool summed = a.bias || (a.groups > 1 && a.group_score == MOE_GROUP_TOP2);  // keys of sums
+    const bool top2 = a.groups > 1 && a.group_score == MOE_GROUP_TOP2;
+    const bool summed = a.bias || top2;  // keys of sums
     float m = 0.0f, inv = 1.0f;
     if (softmax && (summed || !a.renorm)) {
         m = -INFINITY;
@@ -223,22 +345,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
         if (m == -INFINITY) m = 0.0f;
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) sum += expf(l[i] == m ? 0.0f : l[i] - m);
+        for (int i = 0; i < PL; ++i) sum += ex2_approx(kLog2e * (l[i] == m ? 0.0f : l[i] - m));
         sum = warp_sum(sum);
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    auto score = [&](float v) { return softmax ? expf(v == m ? 0.0f : v - m) * inv : 1.0f / (1.0f + expf(-v)); };
     uint32_t key[PL];
-    const int n = a.E / a.groups;
-    // How far apart two 32-bit keys are that may be in the other order: twice the rounding of a key, itself
-    // within 2^-22 of a sigmoid (of the largest softmax score 2^-19: the sum's terms) and 2^-24 of the sum.
+    // How far apart two 32-bit keys are that may be in the other order, twice a key's own error: of a
+    // sigmoid 2^-22 (its instructions are within 2^-22 and 2^-23 of their results, its exponent within
+    // |l| 2^-24), of a softmax score 2^-18 of the largest (a lane's sum of up to 32 terms), and 2^-24 of
+    // the sum with the bias.
     const float slack = softmax ? inv * 0x1p-17f : 0x1p-20f;
     auto near = [&](float hi, float lo) {
         return hi - lo <= slack + 0x1p-22f * fminf(fmaxf(fabsf(hi), fabsf(lo)), FLT_MAX);
     };
-    bool again = false;
     float* keys32 = reinterpret_cast<float*>(s_keys);
-    const bool sums = a.groups > 1 && a.group_score == MOE_GROUP_TOP2;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
         const int e = 32 * i + lane;
@@ -246,62 +366,68 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
         if (e >= a.E) continue;
         float v = l[i], s = v;  // the expert's key, and what its group's score is made of
         if (summed && v > -INFINITY) {
-            s = score(v);
+            s = softmax ? ex2_approx(kLog2e * (v == m ? 0.0f : v - m)) * inv
+                        : rcp_approx(1.0f + ex2_approx(-kLog2e * v));
             if (a.bias) {
                 s += a.bias[e];
                 if (!(s >= -FLT_MAX)) s = -INFINITY;  // a bias of -infinity or NaN
                 v = s;
             }
         }
-        if (a.groups > 1) keys32[e] = sums ? s : v;
+        if (a.groups > 1) keys32[e] = top2 ? s : v;
         key[i] = ordered(v);
     }
+    bool again = false;
     if (a.groups > 1) {
         __syncwarp();
         float edge[2];
-        const uint32_t in = best_groups(group_score(keys32, a.groups, n, sums), a.groups, a.topk_groups, edge);
+        const uint32_t in = best_groups(group_score(keys32, a.groups, a.E / a.groups, top2), a.groups,
+                                        a.topk_groups, edge);
         __syncwarp();
         // (a group's score is two keys)
-        if (summed && a.topk_groups < a.groups) again = near(0.25f * edge[0], 0.25f * edge[1]);
+        again = summed && near(0.25f * edge[0], 0.25f * edge[1]);
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const int e = 32 * i + lane;
-            if (e < a.E && !(in >> (e / n) & 1)) key[i] = 0;
-        }
+        for (int i = 0; i < PL; ++i)
+            if (!(in >> (a.group.div(32 * i + lane) & 31) & 1)) key[i] = 0;
     }
     int mine = 0;
     if (!again) {
-        // lane j: the key and expert taken j-th; one more than k where the order of sums may need 64 bits
+        // one more than k where the order of sums may need 64 bits
         const int rounds = a.bias && a.k < a.E ? a.k + 1 : a.k;
-        uint32_t kept = 0, k = 0;
-        int e = 0;
-        for (int j = 0; j < rounds; ++j) {
-            k = take_max<PL>(key, e);
-            if (lane == j) {
-                mine = e;
-                kept = k;
-            }
-        }
+        uint32_t kept;
+        choose_32<PL>(key, rounds, s_key[warp], s_expert[warp], kept, mine);
         if (a.bias) {
-            uint32_t next = __shfl_down_sync(kAll, kept, 1);
-            int after = __shfl_down_sync(kAll, mine, 1);
-            if (lane == 31) {  // (of 32 taken, the 33rd)
-                next = rounds == 33 ? k : 0u;
-                after = e;
-            }
+            const uint32_t next = __shfl_down_sync(kAll, kept, 1);
+            const int after = __shfl_down_sync(kAll, mine, 1);
             // (the sums of equal terms are equal)
-            bool apart = lane >= rounds - 1 || !next || !near(unordered(kept), unordered(next));
+            bool apart = lane >= rounds - 1 || lane == 31 || !next || !near(unordered(kept), unordered(next));
             apart = apart || (to_f32(x[mine]) == to_f32(x[after]) && a.bias[mine] == a.bias[after]);
-            again = !__all_sync(kAll, apart);
+            if (!__all_sync(kAll, apart) || rounds > 32) {
+                // every expert that may be among the k: those with keys near the k-th, or before it
+                int n = 0;
+                float last = 0.0f;
+                for (bool more = true; more;) {
+                    int e;
+                    const uint32_t k = take_max<PL>(key, e);
+                    more = k && (n < a.k || near(last, unordered(k)));
+                    if (!more) break;
+                    if (n == 32) again = true;
+                    if (again) break;
+                    if (lane == n) mine = e;
+                    if (n < a.k) last = unordered(k);
+                    ++n;
+                }
+                if (!again) mine = order_64(a, x, mine, n);
+            }
         }
     }
-    if (again) mine = choose_64<PL>(a, l, s_keys);
+    if (again) mine = choose_64<PL>(a, x, s_keys);
     // lane j < k: the chosen expert's logit and weight
     const bool chosen = lane < a.k;
     float v = chosen ? to_f32(x[mine]) : -INFINITY, w;
     if (v != v) v = -INFINITY;
     if (!a.renorm) {
-        w = v > -INFINITY ? score(v) : 0.0f;
+        w = v == -INFINITY ? 0.0f : softmax ? expf(v - m) * inv : 1.0f / (1.0f + expf(-v));
     } else {
         // of softmax scores the same factor falls out; sigmoids of very negative logits are taken relative
         // to the largest: 1 / (1 + e^-l) = e^l / (1 + e^l)
@@ -323,11 +449,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
     }
 }
 
-// A warp per token.  Scores of their own and renormalised ones: the chosen experts' logits alone have
-// gradients, q (g - r) f with g_j = scale dw_j, q the weight / scale, r = sum_i g_i q_i, f the score's own
-// derivative over it (softmax 1, sigmoid 1 - s); not renormalised sigmoids g s (1 - s).  Softmax scores that
-// are not renormalised: p_e (sum of the g_j of expert e - sum_j g_j p_j), for every expert e.
-template <typename T>
+// A warp per token.  Renormalised scores and sigmoids: the chosen experts' logits alone have gradients,
+// q (g - r) f with g_j = scale dw_j, q the weight / scale, r = sum_i g_i q_i, f the score's own derivative
+// over it (softmax 1, sigmoid 1 - s); not renormalised g s (1 - s).  Softmax scores that are not
+// renormalised: p_e (sum of the g_j of expert e - sum_j g_j p_j), for every expert e (PL > 0: expert 32 i +
+// lane in the registers of a lane).
+template <int PL, typename T>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackArgs a)
 {
     pdl_wait();
@@ -343,26 +470,29 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
     const bool chosen = id >= 0;
     const float v = chosen ? to_f32(x[id]) : -INFINITY;
     float g = chosen ? a.dw[t * a.k + lane] * a.scale : 0.0f;
-    float d = 0.0f;
-    if (softmax && !a.renorm) {
-        float m = -INFINITY, sum = 0.0f;
-        for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(x[e]));
+    float p = 0.0f, r = 0.0f;
+    if constexpr (PL > 0) {
+        float l[PL], m = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            l[i] = 32 * i + lane < a.E ? to_f32(x[32 * i + lane]) : -INFINITY;
+            m = fmaxf(m, l[i]);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
         if (m == -INFINITY) m = 0.0f;
-        for (int e = lane; e < a.E; e += 32) sum += expf(to_f32(x[e]) - m);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            l[i] = expf(l[i] - m);
+            sum += l[i];
+        }
         sum = warp_sum(sum);
         const float inv = sum > 0.0f ? 1.0f / sum : sum;
-        const float p = chosen ? expf(v - m) * inv : 0.0f;
-        const float r = warp_sum(chosen ? g * p : 0.0f);
-        for (int e = lane; e < a.E; e += 32) from_f32(-expf(to_f32(x[e]) - m) * inv * r, dx[e]);
-        float all = 0.0f;  // of the positions that chose the same expert
-        for (int j = 0; j < a.k; ++j) {
-            const int other = __shfl_sync(kAll, id, j);
-            const float gj = __shfl_sync(kAll, g, j);
-            if (other == id) all += gj;
-        }
-        d = p * (all - r);
+        p = chosen ? expf(v - m) * inv : 0.0f;
+        r = warp_sum(chosen ? g * p : 0.0f);
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            if (32 * i + lane < a.E) from_f32(-l[i] * inv * r, dx[32 * i + lane]);
     } else {
         for (int e = lane; e < a.E; e += 32) from_f32(0.0f, dx[e]);
         if (a.renorm) {
@@ -380,45 +510,58 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
             if (!chosen) q = 0.0f;
             const float sum = warp_sum(q);
             q = sum > 0.0f ? q / sum : sum;
-            const float r = warp_sum(chosen ? g * q : 0.0f);
-            g = chosen ? q * (g - r) * f : 0.0f;
+            const float mean = warp_sum(chosen ? g * q : 0.0f);
+            g = chosen ? q * (g - mean) * f : 0.0f;
         } else {
             const float s = 1.0f / (1.0f + expf(-v));
             g = chosen ? g * s / (1.0f + expf(v)) : 0.0f;
         }
-        for (int j = 0; j < a.k; ++j) {
-            const int other = __shfl_sync(kAll, id, j);
-            const float gj = __shfl_sync(kAll, g, j);
-            if (other == id) d += gj;
-        }
     }
+    float all = 0.0f;  // of the positions that chose the same expert
+    for (int j = 0; j < a.k; ++j) {
+        const int other = __shfl_sync(kAll, id, j);
+        const float gj = __shfl_sync(kAll, g, j);
+        if (other == id) all += gj;
+    }
+    if constexpr (PL > 0) all = p * (all - r);
     __syncwarp();  // the row is written; its chosen experts' are written again
-    if (chosen) from_f32(d, dx[id]);
+    if (chosen) from_f32(all, dx[id]);
 }
 
-template <typename T>
-static RouteKernel route_of(int E)
+// Registers of a lane for a token's experts (a step in the middle of each octave: 8 tokens' worth of 320
+// experts in 10 registers instead of 16).
+template <template <int, typename> class K, typename T, typename F>
+static F with_pl(int E)
 {
-    return E <= 64 ? route_scores_kernel<2, T> : E <= 128 ? route_scores_kernel<4, T>
-         : E <= 256 ? route_scores_kernel<8, T> : E <= 384 ? route_scores_kernel<12, T>
-         : E <= 512 ? route_scores_kernel<16, T> : route_scores_kernel<32, T>;
+    return E <= 64 ? K<2, T>::get() : E <= 128 ? K<4, T>::get() : E <= 192 ? K<6, T>::get()
+         : E <= 256 ? K<8, T>::get() : E <= 320 ? K<10, T>::get() : E <= 384 ? K<12, T>::get()
+         : E <= 512 ? K<16, T>::get() : K<32, T>::get();
 }
+template <int PL, typename T>
+struct Forward {
+    static RouteKernel get() { return route_scores_kernel<PL, T>; }
+};
+template <int PL, typename T>
+struct Dense {
+    static RouteBackKernel get() { return route_back_kernel<PL, T>; }
+};
 
 RouteKernel route_scores_kernel_for(int dtype, int E)
 {
     switch (dtype) {
-        case MOE_BF16: return route_of<__nv_bfloat16>(E);
-        case MOE_FP16: return route_of<__half>(E);
-        default: return route_of<float>(E);
+        case MOE_BF16: return with_pl<Forward, __nv_bfloat16, RouteKernel>(E);
+        case MOE_FP16: return with_pl<Forward, __half, RouteKernel>(E);
+        default: return with_pl<Forward, float, RouteKernel>(E);
     }
 }
 
-RouteBackKernel route_back_kernel_for(int dtype)
+RouteBackKernel route_back_kernel_for(int dtype, bool dense, int E)
 {
     switch (dtype) {
-        case MOE_BF16: return route_back_kernel<__nv_bfloat16>;
-        case MOE_FP16: return route_back_kernel<__half>;
-        default: return route_back_kernel<float>;
+        case MOE_BF16:
+            return dense ? with_pl<Dense, __nv_bfloat16, RouteBackKernel>(E) : route_back_kernel<0, __nv_bfloat16>;
+        case MOE_FP16: return dense ? with_pl<Dense, __half, RouteBackKernel>(E) : route_back_kernel<0, __half>;
+        default: return dense ? with_pl<Dense, float, RouteBackKernel>(E) : route_back_kernel<0, float>;
     }
 }
 

@@ -27,14 +27,15 @@ __device__ __forceinline__ float sigmoid(float g)
     return rcp_approx(1.0f + ex2_approx(-1.4426950408889634f * g));
 }
 
-// bits of the largest magnitude of the eights of four neighbouring lanes
+// bits of the largest magnitude of the eights of four neighbouring lanes (a NaN's are the largest)
 __device__ __forceinline__ uint32_t amax4(const float (&v)[8])
 {
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
+    uint32_t b = __float_as_uint(m);
+    b = max(b, __shfl_xor_sync(0xffffffffu, b, 1));
+    return max(b, __shfl_xor_sync(0xffffffffu, b, 2));
 }
 
 // Eight u of a row of `blocks` blocks as MXFP8 (all lanes of the warp; `live` ones store).  A block's first
@@ -73,19 +74,37 @@ __device__ __forceinline__ void load_mx8(const uint8_t* codes, const uint8_t* sf
 
 }  // namespace
 
-// A thread per eight columns of all rows.
+// The kernels' work is 32 eights in a row's order, one a lane, which may be of several short rows.  A warp
+// asks for 32 of its items at a time whether any of their rows is live, each lane for one, so that padding
+// costs it one load (groups of few rows: a decode batch's rows are padding but for one in eighty).
+template <typename F>
+__device__ __forceinline__ void for_live_eights(const int32_t* perm_src, uint32_t n, const FastDiv& units, F work)
+{
+    const int lane = threadIdx.x & 31;
+    const uint64_t items = ((uint64_t)n + 31) / 32, step = gridDim.x * (blockDim.x >> 5);
+    for (uint64_t i0 = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i0 < items; i0 += 32 * step) {
+        const uint64_t mine = i0 + lane * step;
+        bool any = mine < items;
+        if (any && perm_src) {
+            const uint32_t last = units.div((uint32_t)min(32 * mine + 31, (uint64_t)n - 1));
+            any = false;
+            for (uint32_t r = units.div((uint32_t)(32 * mine)); r <= last; ++r) any = any || perm_src[r] >= 0;
+        }
+        for (uint32_t left = __ballot_sync(0xffffffffu, any); left; left &= left - 1) {
+            const uint64_t at = 32 * (i0 + (__ffs(left) - 1) * step) + lane;
+            const uint32_t i = (uint32_t)min(at, (uint64_t)n - 1), row = units.div(i);
+            work((int64_t)row, (int)(i - row * units.d), at < n && !(perm_src && perm_src[row] < 0));
+        }
+    }
+}
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    const uint32_t units = a.inter >> 3, n = (uint32_t)a.rows * units;  // (fits: checked by the caller)
-    const int blocks = a.inter >> 5;
-    for (uint64_t i0 = blockIdx.x * 256u; i0 < n; i0 += gridDim.x * 256u) {
-        const uint32_t i = (uint32_t)min(i0 + threadIdx.x, (uint64_t)n - 1);
-        const int64_t row = i / units;
-        const int u = (int)(i - (uint32_t)row * units);
-        const bool live = i0 + threadIdx.x < n && !(a.perm_src && a.perm_src[row] < 0);
+    const int blocks = a.inter >> 5, units = a.inter >> 3;
+    for_live_eights(a.perm_src, a.eights, a.units, [&](int64_t row, int u, bool live) {
         Eight<T> e = {}, f = {};
         if (live) {
             const T* x = static_cast<const T*>(a.gu) + row * a.gu_stride + 8 * u;
@@ -101,9 +120,9 @@ __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a)
         store_mx8(s, a.rule, a.codes, a.sf, a.layout, row, u, blocks, live);
         if (a.ckpt) {
             store_mx8(g, a.rule, a.ckpt, a.ckpt_sf, MOE_SF_CANONICAL, row, u, 2 * blocks, live);
-            store_mx8(v, a.rule, a.ckpt, a.ckpt_sf, MOE_SF_CANONICAL, row, u + (int)units, 2 * blocks, live);
+            store_mx8(v, a.rule, a.ckpt, a.ckpt_sf, MOE_SF_CANONICAL, row, u + units, 2 * blocks, live);
         }
-    }
+    });
 }
 
 // With s = sigmoid(g): dg = ds u s (1 + g (1 - s)), du = ds g s.
@@ -112,19 +131,14 @@ __global__ void __launch_bounds__(256) swiglu_back_kernel(SwigluBackArgs a)
 {
     pdl_wait();
     pdl_trigger();
-    const uint32_t units = a.inter >> 3, n = (uint32_t)a.rows * units;  // (fits: checked by the caller)
-    const int blocks = a.inter >> 5;
-    for (uint64_t i0 = blockIdx.x * 256u; i0 < n; i0 += gridDim.x * 256u) {
-        const uint32_t i = (uint32_t)min(i0 + threadIdx.x, (uint64_t)n - 1);
-        const int64_t row = i / units;
-        const int u = (int)(i - (uint32_t)row * units);
-        const bool live = i0 + threadIdx.x < n && !(a.perm_src && a.perm_src[row] < 0);
+    const int blocks = a.inter >> 5, units = a.inter >> 3;
+    for_live_eights(a.perm_src, a.eights, a.units, [&](int64_t row, int u, bool live) {
         float g[8] = {}, v[8] = {}, d[8] = {};
         if (live) {
             Eight<T> e;
             e.template load<VEC>(static_cast<const T*>(a.ds) + row * a.ds_stride + 8 * u);
             load_mx8(a.ckpt, a.ckpt_sf, row, u, 2 * blocks, g);
-            load_mx8(a.ckpt, a.ckpt_sf, row, u + (int)units, 2 * blocks, v);
+            load_mx8(a.ckpt, a.ckpt_sf, row, u + units, 2 * blocks, v);
             e.to_f32(d);
         }
         float dg[8], du[8];
@@ -144,9 +158,9 @@ __global__ void __launch_bounds__(256) swiglu_back_kernel(SwigluBackArgs a)
         }
         if (a.codes) {
             store_mx8(dg, a.rule, a.codes, a.sf, a.layout, row, u, 2 * blocks, live);
-            store_mx8(du, a.rule, a.codes, a.sf, a.layout, row, u + (int)units, 2 * blocks, live);
+            store_mx8(du, a.rule, a.codes, a.sf, a.layout, row, u + units, 2 * blocks, live);
         }
-    }
+    });
 }
 
 SwigluKernel swiglu_kernel_for(int dtype, bool vec)
