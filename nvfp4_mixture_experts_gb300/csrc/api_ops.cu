@@ -219,22 +219,24 @@ moe_status grouped_gemm(bool eight_bits, const uint8_t* a_codes_d, const uint8_t
         !words_aligned(counts_d, offsets_d, status_d))
         return MOE_ERR_INVALID;
     const int KA = (K / 32 + 3) / 4, es = elem_bytes(out_dtype);
-    CUtensorMap tmW, tmT, tmT16, tmSW, tmST;
+    CUtensorMap tmW, tmT, tmT16, tmT32, tmT64, tmSW, tmST;
     constexpr auto U32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
     constexpr auto SW = CU_TENSOR_MAP_SWIZZLE_128B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
     // 16U4_ALIGN16B: 16 packed codes become 16 bytes of shared memory (8 of them padding), as
     // kind::mxf8f6f4 reads E2M1 operands
     constexpr auto U4 = CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B;
     const uint64_t row = eight_bits ? K : K / 2;   // bytes of a group row
-    const uint32_t sf_box = eight_bits ? 128 : 256;
     if (!(eight_bits ? make_tmap_3d(&tmW, w_codes_d, U4, K, N, num_groups, K / 2, 128, 128, SW)
                      : make_tmap_3d(&tmW, w_codes_d, U32, K / 8, N, num_groups, K / 2, 32, 128, SW)) ||
         !make_tmap(&tmT, a_codes_d, U32, row / 4, rows_cap, row, 32, 128, SW) ||
         !make_tmap(&tmT16, a_codes_d, U32, row / 4, rows_cap, row, 32, 16, SW) ||
+        (eight_bits && (!make_tmap(&tmT32, a_codes_d, U32, row / 4, rows_cap, row, 32, 32, SW) ||
+                        !make_tmap(&tmT64, a_codes_d, U32, row / 4, rows_cap, row, 32, 64, SW))) ||
         !make_tmap(&tmSW, w_sf_d, U32, KA * 128, (uint64_t)num_groups * ceil_div(N, 128), (uint64_t)KA * 512,
-                   sf_box, 1, NOSW) ||
-        !make_tmap(&tmST, a_sf_d, U32, KA * 128, ceil_div(rows_cap, 128), (uint64_t)KA * 512, sf_box, 1, NOSW))
+                   256, 1, NOSW) ||
+        !make_tmap(&tmST, a_sf_d, U32, KA * 128, ceil_div(rows_cap, 128), (uint64_t)KA * 512, 256, 1, NOSW))
         return MOE_ERR_CUDA;
+    if (!eight_bits) tmT32 = tmT64 = tmT16;  // (not used)
     MxGemmArgs a = {};
     a.rows_cap = rows_cap;
     a.counts = counts_d;
@@ -257,7 +259,8 @@ moe_status grouped_gemm(bool eight_bits, const uint8_t* a_codes_d, const uint8_t
                           ceil_div(N, 256);
     const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, num_sms() / 2));
     return launch_pairs(kern, dim3(2 * pairs), dim3(kMxThreads), smem,
-                        reinterpret_cast<cudaStream_t>(stream), true, tmW, tmT, tmT16, tmSW, tmST, a);
+                        reinterpret_cast<cudaStream_t>(stream), true, tmW, tmT, tmT16, tmT32, tmT64, tmSW, tmST,
+                        a);
 }
 
 // What the calls with an MX result share: its layout and rule, and the addresses of an MXFP8 matrix
@@ -300,8 +303,6 @@ int norm_per(int T, int H)
     (void)T;
     return H <= 256 ? 1 : 2;
 }
-
-int norm_threads(int H, int per) { return ceil_div(ceil_div(H, 8), 32 * per) * 32; }
 
 }  // namespace
 
@@ -665,7 +666,7 @@ moe_status moe_rmsnorm(const void* x_d, int32_t dtype, int64_t x_stride, const v
 size_t moe_rmsnorm_workspace_size(int32_t T, int32_t H)
 {
     if (check_norm(MOE_BF16, T, H) != MOE_OK) return 0;
-    const int parts = norm_parts(T, H, norm_per(T, H));
+    const int parts = norm_parts(T, H, norm_per(T, H), 2);  // (no fewer than of fp32)
     return parts > 1 ? (size_t)parts * H * 4 : 0;
 }
 
@@ -712,10 +713,16 @@ moe_status moe_rmsnorm_backward(const void* dy_d, int32_t dtype, int64_t dy_stri
                      rows_vec(dx_d, row, dx_stride * some);
     const int per = norm_per(T, H);
     const bool one = norm_one(H, per);
-    a.parts = norm_parts(T, H, per);
+    a.parts = norm_parts(T, H, per, es);
     const int threads = one ? 256 : norm_threads(H, per);
-    const moe_status done = launch(norm_back_kernel_for(dtype, per, one, vec, threads),
-                                   dim3(one ? ceil_div(a.parts, 8) : a.parts), dim3(threads), 0, s, true, a);
+    const NormBackKernel kern = norm_back_kernel_for(dtype, per, one, vec, threads);
+    size_t smem = 0;
+    if (vec && !one) {
+        a.depth = norm_depth(threads, es);
+        smem = (size_t)a.depth * norm_row_bytes(threads, es);
+        if (!allow_smem(reinterpret_cast<const void*>(kern), smem, kNormRingMost)) return MOE_ERR_CUDA;
+    }
+    const moe_status done = launch(kern, dim3(one ? ceil_div(a.parts, 8) : a.parts), dim3(threads), smem, s, true, a);
     if (done != MOE_OK || !dweight_d || a.parts == 1) return done;
     return launch(norm_parts_kernel, dim3(ceil_div(H, 32)), dim3(256), 0, s, true, a.ws, a.parts, H, dweight_d);
 }
@@ -737,8 +744,8 @@ moe_status moe_swiglu_mxfp8(const void* gate_up_d, int32_t dtype, int64_t stride
     a.gu_stride = stride;
     a.rows = rows;
     a.inter = inter;
-    a.eights = (uint32_t)((int64_t)rows * (inter / 8));
-    a.units = FastDiv(inter / 8);
+    a.n = (uint32_t)((int64_t)rows * (inter / 16));
+    a.units = FastDiv(inter / 16);
     a.rule = scale_rule;
     a.perm_src = perm_src_d;
     a.codes = codes_d;
@@ -748,7 +755,7 @@ moe_status moe_swiglu_mxfp8(const void* gate_up_d, int32_t dtype, int64_t stride
     a.ckpt_sf = ckpt_sf_d;
     const int es = elem_bytes(dtype);
     const bool vec = rows_vec(gate_up_d, (int64_t)inter * es, rows > 1 ? stride * es : 0);
-    return launch(swiglu_kernel_for(dtype, vec), dim3(blocks_for((int64_t)rows * (inter / 8), 256, 8)),
+    return launch(swiglu_kernel_for(dtype, vec), dim3(blocks_for((int64_t)rows * (inter / 16), 256, 8)),
                   dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 
@@ -773,8 +780,8 @@ moe_status moe_swiglu_mxfp8_backward(const void* ds_d, int32_t dtype, int64_t st
     a.ckpt_sf = ckpt_sf_d;
     a.rows = rows;
     a.inter = inter;
-    a.eights = (uint32_t)((int64_t)rows * (inter / 8));
-    a.units = FastDiv(inter / 8);
+    a.n = (uint32_t)((int64_t)rows * (inter / 16));
+    a.units = FastDiv(inter / 16);
     a.rule = scale_rule;
     a.perm_src = perm_src_d;
     a.codes = codes_d;
@@ -783,7 +790,7 @@ moe_status moe_swiglu_mxfp8_backward(const void* ds_d, int32_t dtype, int64_t st
     a.dgu = dgate_up_d;
     const int es = elem_bytes(dtype);
     const bool vec = rows_vec(ds_d, (int64_t)inter * es, rows > 1 ? stride * es : 0);
-    return launch(swiglu_back_kernel_for(dtype, vec), dim3(blocks_for((int64_t)rows * (inter / 8), 256, 8)),
+    return launch(swiglu_back_kernel_for(dtype, vec), dim3(blocks_for((int64_t)rows * (inter / 16), 256, 8)),
                   dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
 }
 

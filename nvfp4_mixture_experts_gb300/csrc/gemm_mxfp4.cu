@@ -261,18 +261,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // The ring of k-stages in shared memory.  Where no group has more than 64 rows a stage holds 32
 // group rows per CTA and one row block of scales instead of 128 and two, and nine of them fit
-// instead of six (one token's gate_up with five stages of the large kind: 16.3 us, so 13.8).
+// instead of six (one token's gate_up with five stages of the large kind: 16.3 us, so 13.8).  Operands of
+// 8-bit rows take twice the room, as two halves of 128 elements: three stages, or five small ones.
+template <bool A8>
 struct Stages {
     uint8_t* base;
     int n;                                   // stages
-    uint32_t bytes, t, sw, st;               // of a stage; offsets of its parts (weights at 0)
+    uint32_t bytes, t, half, sw, st;         // of a stage; offsets of its parts (weights at 0; half: between
+                                             // the group rows' halves)
     __device__ __forceinline__ Stages(uint8_t* p, int big, bool small) : base(p)
     {
-        n = small ? big * kMxStageBytes / kMxSmallStageBytes : big;
-        bytes = small ? kMxSmallStageBytes : kMxStageBytes;
-        t = 16384;
-        sw = t + (small ? 4096 : 16384);
+        half = small ? 4096 : 16384;
+        t = A8 ? 32768 : 16384;
+        sw = t + (A8 ? 2 : 1) * half;
         st = sw + 1024;
+        bytes = A8 ? (small ? 43008 : 68608) : (small ? kMxSmallStageBytes : kMxStageBytes);
+        n = big * kMxStageBytes / bytes;
     }
 };
 
@@ -425,6 +429,8 @@ template <typename T, bool A8>
 __global__ void __launch_bounds__(kMxThreads, 1)
     gemm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
                       const __grid_constant__ CUtensorMap tmT16,
+                      const __grid_constant__ CUtensorMap tmT32,
+                      const __grid_constant__ CUtensorMap tmT64,
                       const __grid_constant__ CUtensorMap tmSW,
                       const __grid_constant__ CUtensorMap tmST, MxGemmArgs args)
 {
@@ -436,12 +442,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    // A8: the group rows are MXFP8 and a k-stage holds 128 elements instead of 256, in as many bytes of
-    // shared memory (the weights are spread to a byte each on their way in)
-    constexpr int kSf = A8 ? 512 : 1024;         // bytes of a row block's scales per k-stage
-    constexpr int kWb = A8 ? 8192 : 16384;       // bytes that a copy of weights counts (of the packed codes)
-    constexpr int kXw = A8 ? 128 : 32;           // of a k-stage in the weights' map: elements, or words
-    const int KB = div_up(args.K, A8 ? 128 : 256);
+    // A8: the group rows are MXFP8, and the weights are spread to a byte each on their way in; a k-stage's
+    // halves of 128 elements are copies of their own (a copy of weights counts its packed bytes).  Stages of
+    // 128 elements: 80 groups of 256 rows x 2560 x 4096 138 us, 320 of 2 rows 287 us.
+    constexpr int kHalves = A8 ? 2 : 1;
+    const int KB = div_up(args.K, 256);
 
     if (warp == 0 && elect_one()) {
         for (int s = 0; s < kMxMaxStages; ++s) {
@@ -458,6 +463,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         prefetch_tmap(&tmW);
         prefetch_tmap(&tmT);
         prefetch_tmap(&tmT16);
+        if (A8) {
+            prefetch_tmap(&tmT32);
+            prefetch_tmap(&tmT64);
+        }
         prefetch_tmap(&tmSW);
         prefetch_tmap(&tmST);
     }
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     cluster_wait();    // ... and the peer's
     tc_fence_after();
     const int ntiles = gs.start[gs.G] * gs.NB;
-    const Stages sg(ring, args.stages, gs.most <= 64);
+    const Stages<A8> sg(ring, args.stages, gs.most <= 64);
     volatile int* abort = &ctl.abort_flag;
 
     if (warp == 0) {
@@ -492,7 +501,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 const int half = ti.nt >> 1;                    // group rows of this CTA
                 const int trow = ti.row0 + (int)rank * half, wrow = ti.n0 + (int)rank * 128;
                 const int nsc = ti.nt > 128 ? 2 : 1;            // row blocks of group-row scales
-                const uint32_t bytes = 2u * (kWb + kSf + half * 128 + nsc * kSf);
+                const uint32_t bytes = 2u * (16384 + 1024 + kHalves * half * 128 + nsc * 1024);
                 const int wb = ti.g * div_up(args.N, 128) + (wrow >> 7), tb = ti.row0 >> 7;
                 // A loop of its own for few rows, where this thread is what a lone tile waits for
                 // (one row, N 4096, K 16384: 18.2 us in the other loop, 16.7 in this one).
@@ -503,10 +512,18 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         uint8_t* p = sg.base + at.stage * sg.bytes;
                         const uint32_t bar = full0 + at.stage * 8;
                         if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at.stage], bytes);
-                        tma_pair_3d(p, &tmW, bar, kb * kXw, wrow, ti.g, pol_w);
-                        tma_pair_2d(p + sg.sw, &tmSW, bar, kb * (kSf / 4), wb, pol_w);
-                        tma_pair_2d(p + sg.t, &tmT16, bar, kb * 32, trow, pol_t);
-                        tma_pair_2d(p + sg.st, &tmST, bar, kb * (kSf / 4), tb, pol_t);
+                        if constexpr (A8) {
+                            tma_pair_3d(p, &tmW, bar, kb * 256, wrow, ti.g, pol_w);
+                            tma_pair_3d(p + 16384, &tmW, bar, kb * 256 + 128, wrow, ti.g, pol_w);
+                            tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
+                            tma_pair_2d(p + sg.t, &tmT16, bar, kb * 64, trow, pol_t);
+                            tma_pair_2d(p + sg.t + sg.half, &tmT16, bar, kb * 64 + 32, trow, pol_t);
+                        } else {
+                            tma_pair_3d(p, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
+                            tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
+                            tma_pair_2d(p + sg.t, &tmT16, bar, kb * 32, trow, pol_t);
+                        }
+                        tma_pair_2d(p + sg.st, &tmST, bar, kb * 256, tb, pol_t);
                         at.next(sg.n);
                     }
                 } else {
@@ -515,16 +532,34 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         uint8_t* p = sg.base + at.stage * sg.bytes;
                         const uint32_t bar = full0 + at.stage * 8;
                         if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at.stage], bytes);
-                        tma_pair_3d(p, &tmW, bar, kb * kXw, wrow, ti.g, pol_w);
-                        tma_pair_2d(p + sg.sw, &tmSW, bar, kb * (kSf / 4), wb, pol_w);
-                        if (half == 128) {
-                            tma_pair_2d(p + sg.t, &tmT, bar, kb * 32, trow, pol_t);
+                        if constexpr (A8) {
+                            tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint8_t* q = p + sg.t + h * sg.half;
+                                const int x = kb * 64 + h * 32;
+                                tma_pair_3d(p + h * 16384, &tmW, bar, kb * 256 + h * 128, wrow, ti.g, pol_w);
+                                // boxes of 128, 64, 32 and 16 rows (of 16 alone: 8192 tokens' gate_up 603 us,
+                                // so 578)
+                                if (half & 128) tma_pair_2d(q, &tmT, bar, x, trow, pol_t);
+                                if (half & 64) tma_pair_2d(q, &tmT64, bar, x, trow, pol_t);
+                                if (half & 32)
+                                    tma_pair_2d(q + (half & 64) * 128, &tmT32, bar, x, trow + (half & 64), pol_t);
+                                if (half & 16)
+                                    tma_pair_2d(q + (half & 96) * 128, &tmT16, bar, x, trow + (half & 96), pol_t);
+                            }
                         } else {
-                            for (int i = 0; i < half; i += 16)
-                                tma_pair_2d(p + sg.t + i * 128, &tmT16, bar, kb * 32, trow + i, pol_t);
+                            tma_pair_3d(p, &tmW, bar, kb * 32, wrow, ti.g, pol_w);
+                            tma_pair_2d(p + sg.sw, &tmSW, bar, kb * 256, wb, pol_w);
+                            if (half == 128) {
+                                tma_pair_2d(p + sg.t, &tmT, bar, kb * 32, trow, pol_t);
+                            } else {
+                                for (int i = 0; i < half; i += 16)
+                                    tma_pair_2d(p + sg.t + i * 128, &tmT16, bar, kb * 32, trow + i, pol_t);
+                            }
                         }
-                        tma_pair_2d(p + sg.st, &tmST, bar, kb * (kSf / 4), tb, pol_t);
-                        if (nsc == 2) tma_pair_2d(p + sg.st + kSf, &tmST, bar, kb * (kSf / 4), tb + 1, pol_t);
+                        tma_pair_2d(p + sg.st, &tmST, bar, kb * 256, tb, pol_t);
+                        if (nsc == 2) tma_pair_2d(p + sg.st + 1024, &tmST, bar, kb * 256, tb + 1, pol_t);
                         at.next(sg.n);
                     }
                 }
@@ -586,13 +621,19 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         const uint32_t sc = kAccEnd + slot;
                         const int left = args.K - kb * 256;
                         if constexpr (A8) {
-                            tc_cp_sf_pair(sc, cw);
-                            tc_cp_sf_pair(sc + 8, ct);
-                            if (two) tc_cp_sf_pair(sc + 12, ct + 32);
+                            // K = 32 steps; the last k-stage may hold one half alone
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                tc_mma_mxf8_pair(d_t, w + 2 * j, tk + 2 * j, idesc | (j << 4) | (j << 29), sc,
-                                                 sc + 8, (kb | j) != 0);
+                            for (int h = 0; h < 2; ++h) {
+                                if (h && left <= 128) break;
+                                tc_cp_sf_pair(sc + 4 * h, cw + 32 * h);
+                                tc_cp_sf_pair(sc + 8 + 8 * h, ct + 32 * h);
+                                if (two) tc_cp_sf_pair(sc + 12 + 8 * h, ct + 64 + 32 * h);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    tc_mma_mxf8_pair(d_t, w + 1024 * h + 2 * j, tk + (sg.half >> 4) * h + 2 * j,
+                                                     idesc | (j << 4) | (j << 29), sc + 4 * h, sc + 8 + 8 * h,
+                                                     (kb | h | j) != 0);
+                            }
                         } else if (left >= 256) {
                             tc_cp_sf_pair(sc, cw);
                             tc_cp_sf_pair(sc + 8, ct);

@@ -465,8 +465,8 @@ inline int gemm_mxfp4_smem(int stages, int G, int out_bytes)
 {
     return 1024 + stages * kMxStageBytes + mx_epi_bytes(out_bytes) + kMxCtlBytes + 4 * (3 * G + 1);
 }
-using MxGemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
-                              MxGemmArgs);
+using MxGemmKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap,
+                              CUtensorMap, MxGemmArgs);
 // eight_bits: of MXFP8 group rows
 MxGemmKernel gemm_mxfp4_kernel_for(bool eight_bits, int out_dtype);
 __global__ void group_wait_probe_kernel(uint32_t* status, uint32_t* went_on, uint64_t limit_ns);
@@ -564,18 +564,34 @@ struct NormBackArgs {
     float* dw;            // nullable
     float* ws;            // [parts][H]
     int parts;
+    int depth;            // rows in flight of the kernel with a ring (1 to 3)
 };
 using NormBackKernel = void (*)(NormBackArgs);
 NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec, int threads);
 __global__ void norm_parts_kernel(const float* ws, int parts, int H, float* dw);
-// Parts of the weight's gradient: two blocks per SM of 152, each with a row (or, short rows, eight) at a
-// time.
-constexpr int kNormBlocks = 304;
 __host__ __device__ constexpr bool norm_one(int H, int per) { return H <= 256 * per; }
-inline int norm_parts(int T, int H, int per)
+inline int norm_threads(int H, int per) { return div_up(div_up(H, 8), 32 * per) * 32; }
+// Blocks of an SM that the gradient's registers and rings are made for: 24 warps of 16-bit types, 16 of fp32,
+// or one block.  (8192 x 4096 bf16 with two blocks and a row in flight in registers: 56 us.)
+inline int norm_per_sm(int threads, int elem_bytes)
 {
-    const int most = norm_one(H, per) ? 8 * kNormBlocks : kNormBlocks;
+    const int n = (elem_bytes == 2 ? 768 : 512) / threads;
+    return n < 1 ? 1 : n;
+}
+// Parts of the weight's gradient: the blocks (short rows: two blocks' warps) that 152 SMs hold.
+inline int norm_parts(int T, int H, int per, int elem_bytes)
+{
+    const int most = norm_one(H, per) ? 152 * 16 : 152 * norm_per_sm(norm_threads(H, per), elem_bytes);
     return T < most ? T : most;
+}
+// The ring: up to three rows of three tensors in a block's share of an SM's shared memory.
+inline int norm_row_bytes(int threads, int elem_bytes) { return 3 * 2 * threads * 8 * elem_bytes; }
+constexpr int kNormRingMost = 2 * 3 * 2 * 1024 * 8 * 2;   // of any launch: two rows of 1024 threads, 16-bit types
+inline int norm_depth(int threads, int elem_bytes)
+{
+    const int share = 233472 / norm_per_sm(threads, elem_bytes) - 1024 - 256;  // (what the system and the sums take)
+    const int d = share / norm_row_bytes(threads, elem_bytes);
+    return d < 1 ? 1 : d > 3 ? 3 : d;
 }
 
 // ---- swiglu.cu: silu(gate) * up with 8-bit checkpoints, and its gradient
@@ -583,8 +599,8 @@ struct SwigluArgs {
     const void* gu;
     int64_t gu_stride;    // in elements
     int rows, inter, rule;
-    uint32_t eights;      // of all rows
-    FastDiv units;        // by the eights of a row
+    uint32_t n;           // sixteens of all rows
+    FastDiv units;        // by the sixteens of a row
     const int32_t* perm_src;  // nullable: rows with a negative entry are skipped
     uint8_t* codes;
     uint8_t* sf;
@@ -601,8 +617,8 @@ struct SwigluBackArgs {
     const uint8_t* ckpt;
     const uint8_t* ckpt_sf;
     int rows, inter, rule;
-    uint32_t eights;      // of all rows
-    FastDiv units;        // by the eights of a row
+    uint32_t n;           // sixteens of all rows
+    FastDiv units;        // by the sixteens of a row
     const int32_t* perm_src;
     uint8_t* codes;       // nullable, with sf
     uint8_t* sf;

@@ -11,6 +11,39 @@
 
 namespace moe {
 
+// Two fp32 numbers, multiplied and added in one instruction.
+struct F2 {
+    uint64_t v;
+    F2() = default;
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+    __device__ __forceinline__ float2 get() const
+    {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+        return r;
+    }
+    __device__ __forceinline__ F2 operator*(F2 o) const
+    {
+        F2 r;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(v), "l"(o.v));
+        return r;
+    }
+    __device__ __forceinline__ F2 operator+(F2 o) const
+    {
+        F2 r;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(v), "l"(o.v));
+        return r;
+    }
+};
+// a b + c
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // Eight elements of a row as raw words.
 template <typename T>
 struct Eight {
@@ -142,6 +175,28 @@ struct Eight {
         return r;
     }
 };
+
+template <typename T>
+__device__ __forceinline__ void to_pairs(const Eight<T>& e, F2 (&v)[4])
+{
+    float f[8];
+    e.to_f32(f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = F2(f[2 * i], f[2 * i + 1]);
+}
+
+template <typename T>
+__device__ __forceinline__ void from_pairs(const F2 (&v)[4], Eight<T>& e)
+{
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = v[i].get();
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+    }
+    e.from_f32(f);
+}
 
 // 2^(127 - s): what elements of a block with scale byte s (0..253) are multiplied by (255: any
 // number; its codes are not used).

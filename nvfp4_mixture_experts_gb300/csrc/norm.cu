@@ -64,25 +64,26 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_kernel(NormArgs a)
                 if (a.res)
                     load_eight<VEC>(r[p], static_cast<const T*>(a.res) + row * a.res_stride, tid + p * nt, a.H);
             }
-        float v[PER][8], sum = 0.0f;
+        F2 v[PER][4], sums(0.0f);
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            e[p].to_f32(v[p]);
+            to_pairs(e[p], v[p]);
             if (a.res) {
-                float q[8];
-                r[p].to_f32(q);
+                F2 q[4];
+                to_pairs(r[p], q);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[p][i] += q[i];
+                for (int i = 0; i < 4; ++i) v[p][i] = v[p][i] + q[i];
                 // the stream holds h in its own type, and its norm is that of what it holds
-                e[p].from_f32(v[p]);
-                e[p].to_f32(v[p]);
+                from_pairs(v[p], e[p]);
+                to_pairs(e[p], v[p]);
                 if (a.h && tid + p * nt < units)
                     store_eight<VEC>(e[p], static_cast<T*>(a.h) + row * a.h_stride, tid + p * nt, a.H);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(v[p][i], v[p][i], sum);
+            for (int i = 0; i < 4; ++i) sums = fma2(v[p][i], v[p][i], sums);
         }
-        sum = row_sum<ONE>(sum, s_part, buf);
+        const float2 both = sums.get();
+        const float sum = row_sum<ONE>(both.x + both.y, s_part, buf);
         buf ^= 1;
         const float rstd = rsqrtf(sum / (float)a.H + a.eps);
         if (a.rstd && tid == 0) a.rstd[row] = rstd;
@@ -92,24 +93,31 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_kernel(NormArgs a)
             const bool in = u < units;
             if (u - lane >= units) break;  // (a warp's lanes stay together)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[p][i] *= rstd;
+            for (int i = 0; i < 4; ++i) v[p][i] = v[p][i] * F2(rstd);
             if (a.w) {
                 Eight<T> w = {};
                 if (in) load_eight<VEC>(w, static_cast<const T*>(a.w), u, a.H);
-                float q[8];
-                w.to_f32(q);
+                F2 q[4];
+                to_pairs(w, q);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[p][i] *= q[i];
+                for (int i = 0; i < 4; ++i) v[p][i] = v[p][i] * q[i];
             }
             if (a.y && in) {
                 Eight<T> o;
-                o.from_f32(v[p]);
+                from_pairs(v[p], o);
                 store_eight<VEC>(o, static_cast<T*>(a.y) + row * a.y_stride, u, a.H);
             }
             if (a.codes) {  // H % 32 == 0: a block's four lanes are in or out together
-                uint32_t m = 0;
+                float f[8], top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[p][i]) & 0x7FFFFFFFu);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 q = v[p][i].get();
+                    f[2 * i] = q.x;
+                    f[2 * i + 1] = q.y;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(f[i])));
+                uint32_t m = __float_as_uint(top);
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 const uint32_t s = mx_scale_byte<E4M3>(m, a.rule);
@@ -118,10 +126,14 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_kernel(NormArgs a)
                 word |= __shfl_xor_sync(0xffffffffu, word, 4);
                 word |= __shfl_xor_sync(0xffffffffu, word, 8);
                 if (!in) continue;
-                const float scale = mx_encode_scale(s);
+                const F2 scale(mx_encode_scale(s));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[p][i] *= scale;
-                reinterpret_cast<uint2*>(a.codes)[row * units + u] = s == 255u ? E4M3::zero() : E4M3::encode(v[p]);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 q = (v[p][i] * scale).get();
+                    f[2 * i] = q.x;
+                    f[2 * i + 1] = q.y;
+                }
+                reinterpret_cast<uint2*>(a.codes)[row * units + u] = s == 255u ? E4M3::zero() : E4M3::encode(f);
                 const int kb = u >> 2;
                 if (a.layout == MOE_SF_TILED) {
                     if ((lane & 15) == 0)
@@ -227,6 +239,130 @@ __global__ void __launch_bounds__(NT) norm_back_kernel(NormBackArgs a)
     }
 }
 
+// The same for rows in 16-byte pieces that a block takes: a.depth rows' loads are in flight, copied into
+// shared memory where each thread reads what it copied itself (so no barrier is needed for them, and no
+// registers hold them): a block has one row in its registers and its sum waits for all of them.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, NT == 256 ? 6 / (int)sizeof(T) + (sizeof(T) == 4) : 1) norm_back_ring_kernel(NormBackArgs a)
+{
+    constexpr int PER = 2, kPieces = (int)sizeof(T) / 2;  // eights of a thread, 16-byte pieces of an eight
+    extern __shared__ uint4 s_ring[];                     // [depth][3][PER][kPieces][threads]
+    __shared__ float s_part[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, nt = blockDim.x, units = a.H >> 3, part = blockIdx.x;
+    const int tensor = PER * kPieces * nt, stage = 3 * tensor;   // pieces
+    auto copy = [&](int slot, int64_t row) {
+        if (row < a.T) {
+            const T* from[3] = {static_cast<const T*>(a.dy) + row * a.dy_stride,
+                                static_cast<const T*>(a.h) + row * a.h_stride,
+                                a.dh ? static_cast<const T*>(a.dh) + row * a.dh_stride : nullptr};
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                if (!from[x]) continue;
+#pragma unroll
+                for (int p = 0; p < PER; ++p)
+                    if (tid + p * nt < units)
+#pragma unroll
+                        for (int q = 0; q < kPieces; ++q)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(
+                                             s_ring + slot * stage + x * tensor + (p * kPieces + q) * nt + tid)),
+                                         "l"(reinterpret_cast<const uint4*>(from[x] + 8 * (tid + p * nt)) + q)
+                                         : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");   // (of no copies past the last row)
+    };
+    auto read = [&](int slot, int x, int p) {
+        Eight<T> e;
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            const uint4 v = s_ring[slot * stage + x * tensor + (p * kPieces + q) * nt + tid];
+            e.w[4 * q] = v.x;
+            e.w[4 * q + 1] = v.y;
+            e.w[4 * q + 2] = v.z;
+            e.w[4 * q + 3] = v.w;
+        }
+        return e;
+    };
+    for (int d = 0; d < a.depth; ++d) copy(d, part + (int64_t)d * a.parts);
+    F2 acc[PER][4], w[PER][4];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        Eight<T> e = {};
+        if (a.w && tid + p * nt < units) e.template load<true>(static_cast<const T*>(a.w) + 8 * (tid + p * nt));
+        to_pairs(e, w[p]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[p][i] = F2(0.0f);
+            if (!a.w) w[p][i] = F2(1.0f);
+        }
+    }
+    int buf = 0, slot = 0;
+    float rstd_next = part < a.T ? a.rstd[part] : 0.0f;
+    for (int64_t row = part; row < a.T; row += a.parts) {
+        const float rstd = rstd_next;
+        if (row + a.parts < a.T) rstd_next = a.rstd[row + a.parts];
+        // (the thread's own copies of the oldest row have landed)
+        if (a.depth == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else if (a.depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 2;" ::: "memory");
+        F2 d[PER][4], x[PER][4], dot(0.0f);
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            if (tid + p * nt >= units) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[p][i] = x[p][i] = F2(0.0f);
+                continue;
+            }
+            to_pairs(read(slot, 0, p), d[p]);
+            to_pairs(read(slot, 1, p), x[p]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[p][i] = x[p][i] * F2(rstd);
+                acc[p][i] = fma2(d[p][i], x[p][i], acc[p][i]);
+                d[p][i] = d[p][i] * w[p][i];
+                dot = fma2(d[p][i], x[p][i], dot);
+            }
+        }
+        const float2 both = dot.get();
+        const float mean = row_sum<false>(both.x + both.y, s_part, buf) / (float)a.H;
+        buf ^= 1;
+        const F2 less(-mean), r(rstd);
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            if (tid + p * nt >= units) break;
+            F2 q[4];
+            if (a.dh) to_pairs(read(slot, 2, p), q);
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!a.dh) q[i] = F2(0.0f);
+                const float2 v = fma2(r, fma2(x[p][i], less, d[p][i]), q[i]).get();
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            }
+            Eight<T> o;
+            o.from_f32(f);
+            o.store(static_cast<T*>(a.dx) + row * a.dx_stride + 8 * (tid + p * nt));
+        }
+        copy(slot, row + (int64_t)a.depth * a.parts);   // (over what this thread has read)
+        slot = slot + 1 == a.depth ? 0 : slot + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!a.dw) return;
+    float* out = a.parts == 1 ? a.dw : a.ws + (int64_t)part * a.H;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        if (tid + p * nt < units)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = acc[p][i].get();
+                out[8 * (tid + p * nt) + 2 * i] = v.x;
+                out[8 * (tid + p * nt) + 2 * i + 1] = v.y;
+            }
+}
+
 // dw[c] = the sum of the parts' column c: 32 columns a block, each by eight threads of the block that
 // take every eighth part.
 __global__ void __launch_bounds__(256) norm_parts_kernel(const float* ws, int parts, int H, float* dw)
@@ -266,20 +402,23 @@ NormKernel norm_kernel_for(int dtype, int per, bool one, bool vec)
     }
 }
 
-template <typename T, bool VEC>
-static NormBackKernel norm_back_of(int per, bool one, int threads)
+template <typename T>
+static NormBackKernel norm_back_of(int per, bool one, bool vec, int threads)
 {
-    if (one) return per == 1 ? norm_back_kernel<T, 1, true, VEC, 256> : norm_back_kernel<T, 2, true, VEC, 256>;
-    return threads <= 512 ? norm_back_kernel<T, 2, false, VEC, 512> : norm_back_kernel<T, 2, false, VEC, 1024>;
+    if (one && per == 1) return vec ? norm_back_kernel<T, 1, true, true, 256> : norm_back_kernel<T, 1, true, false, 256>;
+    if (one) return vec ? norm_back_kernel<T, 2, true, true, 256> : norm_back_kernel<T, 2, true, false, 256>;
+    if (vec)
+        return threads <= 256 ? norm_back_ring_kernel<T, 256>
+             : threads <= 512 ? norm_back_ring_kernel<T, 512> : norm_back_ring_kernel<T, 1024>;
+    return threads <= 512 ? norm_back_kernel<T, 2, false, false, 512> : norm_back_kernel<T, 2, false, false, 1024>;
 }
 
 NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec, int threads)
 {
     switch (dtype) {
-        case MOE_BF16:
-            return vec ? norm_back_of<__nv_bfloat16, true>(per, one, threads) : norm_back_of<__nv_bfloat16, false>(per, one, threads);
-        case MOE_FP16: return vec ? norm_back_of<__half, true>(per, one, threads) : norm_back_of<__half, false>(per, one, threads);
-        default: return vec ? norm_back_of<float, true>(per, one, threads) : norm_back_of<float, false>(per, one, threads);
+        case MOE_BF16: return norm_back_of<__nv_bfloat16>(per, one, vec, threads);
+        case MOE_FP16: return norm_back_of<__half>(per, one, vec, threads);
+        default: return norm_back_of<float>(per, one, vec, threads);
     }
 }
 

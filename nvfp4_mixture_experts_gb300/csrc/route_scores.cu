@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
 {
     extern __shared__ double s_all[];  // [kRouteWarps][E] keys, where there are groups
     __shared__ uint32_t s_key[kRouteWarps][32];
-    __shared__ int s_expert[kRouteWarps][32];
+    __shared__ int s_expert[kRouteWarps][32], s_group[kRouteWarps][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
     bool nan = false;  // of this token's weights: a logit is NaN, which ranks last, or has no softmax
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-        nan = nan || l[i] != l[i] || (softmax && l[i] == INFINITY);
-        if (l[i] != l[i]) l[i] = -INFINITY;
+        nan = nan || l[i] != l[i];
+        l[i] = fmaxf(l[i], -INFINITY);
     }
     const bool top2 = a.groups > 1 && a.group_score == MOE_GROUP_TOP2;
     const bool summed = a.bias || top2;  // keys of sums
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
         for (int i = 0; i < PL; ++i) m = fmaxf(m, l[i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        nan = nan || m == INFINITY;
         if (m == -INFINITY) m = 0.0f;
         float sum = 0.0f;
 #pragma unroll
@@ -365,37 +366,50 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
         key[i] = 0;
         if (e >= a.E) continue;
         float v = l[i], s = v;  // the expert's key, and what its group's score is made of
-        if (summed && v > -INFINITY) {
+        if (summed) {
             s = softmax ? ex2_approx(kLog2e * (v == m ? 0.0f : v - m)) * inv
                         : rcp_approx(1.0f + ex2_approx(-kLog2e * v));
-            if (a.bias) {
-                s += a.bias[e];
-                if (!(s >= -FLT_MAX)) s = -INFINITY;  // a bias of -infinity or NaN
-                v = s;
-            }
+            if (a.bias) s += a.bias[e];
+            if (v == -INFINITY || !(s >= -FLT_MAX)) s = -INFINITY;  // masked; a bias of -infinity or NaN
+            if (a.bias) v = s;
         }
         if (a.groups > 1) keys32[e] = top2 ? s : v;
-        key[i] = ordered(v);
+        else key[i] = ordered(v);
     }
     bool again = false;
+    int n = 1, *group = s_group[warp];
     if (a.groups > 1) {
+        n = (int)a.group.d;
         __syncwarp();
         float edge[2];
-        const uint32_t in = best_groups(group_score(keys32, a.groups, a.E / a.groups, top2), a.groups,
-                                        a.topk_groups, edge);
+        const uint32_t in = best_groups(group_score(keys32, a.groups, n, top2), a.groups, a.topk_groups, edge);
+        if (in >> lane & 1) group[__popc(in & ((1u << lane) - 1))] = lane * n;
         __syncwarp();
         // (a group's score is two keys)
         again = summed && near(0.25f * edge[0], 0.25f * edge[1]);
+        // the kept groups' experts one after another: position 32 i + lane
+        const int count = a.topk_groups * n;
 #pragma unroll
-        for (int i = 0; i < PL; ++i)
-            if (!(in >> (a.group.div(32 * i + lane) & 31) & 1)) key[i] = 0;
+        for (int i = 0; i < PL; ++i) {
+            const int p = 32 * i + lane;
+            if (p < count) {
+                const int q = (int)a.group.div(p), e = group[q] + p - q * n;
+                key[i] = ordered(a.bias || !top2 ? keys32[e] : fmaxf(to_f32(x[e]), -INFINITY));
+            }
+        }
     }
+    auto expert = [&](int p) {
+        if (a.groups == 1) return p;
+        const int q = (int)a.group.div(p);
+        return group[q] + p - q * n;
+    };
     int mine = 0;
     if (!again) {
         // one more than k where the order of sums may need 64 bits
         const int rounds = a.bias && a.k < a.E ? a.k + 1 : a.k;
         uint32_t kept;
         choose_32<PL>(key, rounds, s_key[warp], s_expert[warp], kept, mine);
+        mine = expert(mine);
         if (a.bias) {
             const uint32_t next = __shfl_down_sync(kAll, kept, 1);
             const int after = __shfl_down_sync(kAll, mine, 1);
@@ -404,20 +418,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
             apart = apart || (to_f32(x[mine]) == to_f32(x[after]) && a.bias[mine] == a.bias[after]);
             if (!__all_sync(kAll, apart) || rounds > 32) {
                 // every expert that may be among the k: those with keys near the k-th, or before it
-                int n = 0;
+                int c = 0;
                 float last = 0.0f;
                 for (bool more = true; more;) {
-                    int e;
-                    const uint32_t k = take_max<PL>(key, e);
-                    more = k && (n < a.k || near(last, unordered(k)));
+                    int p;
+                    const uint32_t k = take_max<PL>(key, p);
+                    more = k && (c < a.k || near(last, unordered(k)));
                     if (!more) break;
-                    if (n == 32) again = true;
+                    if (c == 32) again = true;
                     if (again) break;
-                    if (lane == n) mine = e;
-                    if (n < a.k) last = unordered(k);
-                    ++n;
+                    if (lane == c) mine = expert(p);
+                    if (c < a.k) last = unordered(k);
+                    ++c;
                 }
-                if (!again) mine = order_64(a, x, mine, n);
+                if (!again) mine = order_64(a, x, mine, c);
             }
         }
     }
