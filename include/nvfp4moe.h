@@ -619,7 +619,7 @@ MOE_API size_t moe_rmsnorm_workspace_size(int32_t T, int32_t H);
 /* The gradient of moe_rmsnorm, from y's gradient dy and (dh_d nullable) the gradient that h has from
  * elsewhere: dx = rstd * (dy * weight - h * rstd * mean(dy * weight * h * rstd)) + dh, which is the
  * gradient of x and of the residual alike, and dweight_d [H] fp32 = sum over the rows of dy * h * rstd
- * (nullable; summed in an order that depends on the sizes and the type alone).  ws_d: at least
+ * (nullable; summed in an order that depends on the sizes and alignment alone).  ws_d: at least
  * moe_rmsnorm_workspace_size bytes, 256-byte aligned, used by one call at a time (none is needed where
  * dweight_d is NULL).  dx_d may be dy_d, dh_d or h_d, with the same stride.
  * Passage: none; training is an addition of this library (the pages serve only). */

@@ -608,23 +608,15 @@ def moe_grouped_gemm_mxfp8(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, s
         _check(st, "moe_grouped_gemm_mxfp8")
 
 
-def _rows(t, T, H, dt):
-    """Whether t is [T, H] rows of a moe_dtype with contiguous columns, or None."""
-    return t is None or (tuple(t.shape) == (T, H) and _DTYPES[t.dtype] == dt and
-                         (t.stride(1) == 1 or H == 1 or T == 0))
-
-
-def _stride(t):
-    return 0 if t is None else t.stride(0)
+def _rows(t, shape, dt):
+    """Whether t is rows of a shape and moe_dtype with contiguous columns."""
+    return (t.shape == shape and _DTYPES[t.dtype] == dt and
+            (t.stride(1) == 1 or shape[1] == 1 or shape[0] == 0))
 
 
 def _flat(t, n, dtype):
-    """Whether t is n contiguous elements of a torch dtype, or None."""
-    return t is None or (t.dtype is dtype and t.numel() == n and t.is_contiguous())
-
-
-def _all_on(dev, *tensors):
-    return all(t is None or t.get_device() == dev for t in tensors)
+    """Whether t is n contiguous elements of a torch dtype."""
+    return t.dtype is dtype and t.numel() == n and t.is_contiguous()
 
 
 def moe_route_scores(logits, topk_ids, topk_w, bias=None, score=MOE_SCORE_SOFTMAX, num_groups=1,
@@ -635,7 +627,8 @@ def moe_route_scores(logits, topk_ids, topk_w, bias=None, score=MOE_SCORE_SOFTMA
     Tk, k = topk_ids.shape
     stride, one = logits.stride()
     if not (Tk == T and (T | E | k) <= _MOST and (one == 1 or E == 1 or T == 0) and
-            _flat(topk_ids, T * k, _I32) and _flat(topk_w, T * k, _F32) and _flat(bias, E, _F32)):
+            topk_ids.dtype is _I32 and topk_ids.is_contiguous() and _flat(topk_w, T * k, _F32) and
+            (bias is None or _flat(bias, E, _F32))):
         _refuse("moe_route_scores")
     dev, handle = _place(stream)
     if not (dev == logits.get_device() == topk_ids.get_device() == topk_w.get_device() and
@@ -652,12 +645,14 @@ def moe_route_scores_backward(logits, topk_ids, dtopk_w, dlogits, score=MOE_SCOR
                               renormalise=True, scale=1.0, stream=None):
     """logits [T, num_experts], topk_ids int32 [T, k], dtopk_w float32 [T, k] -> dlogits (logits' type)
     [T, num_experts]."""
-    T, E = logits.shape
+    shape = logits.shape
+    T, E = shape
     Tk, k = topk_ids.shape
     stride, one = logits.stride()
     dt = _DTYPES[logits.dtype]
     if not (Tk == T and (T | E | k) <= _MOST and (one == 1 or E == 1 or T == 0) and
-            _flat(topk_ids, T * k, _I32) and _flat(dtopk_w, T * k, _F32) and _rows(dlogits, T, E, dt)):
+            topk_ids.dtype is _I32 and topk_ids.is_contiguous() and _flat(dtopk_w, T * k, _F32) and
+            _rows(dlogits, shape, dt)):
         _refuse("moe_route_scores_backward")
     dev, handle = _place(stream)
     if not (dev == logits.get_device() == topk_ids.get_device() == dtopk_w.get_device() ==
@@ -674,47 +669,68 @@ def moe_rmsnorm(x, weight, eps, residual=None, h=None, y=None, rstd=None, codes=
                 sf_layout=MOE_SF_TILED, scale_rule=MOE_MX_CEIL, stream=None):
     """x [T, H], weight [H] (None: ones), residual [T, H] (None) -> any of h, y [T, H] (x's type), rstd
     float32 [T], and codes [T, H] with sf (uint8), y's MXFP8 matrix."""
-    T, H = x.shape
-    stride, one = x.stride()
-    dt = _DTYPES[x.dtype]
-    if not ((T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and _flat(weight, H, x.dtype) and
-            (residual is None or _rows(residual, T, H, dt)) and (h is None or _rows(h, T, H, dt)) and
-            (y is None or _rows(y, T, H, dt)) and _flat(rstd, T, _F32) and (codes is None) == (sf is None) and
-            (codes is None or (_flat(codes, T * H, _U8) and
-                               _flat(sf, _sf_bytes(1, T, H >> 5, sf_layout), _U8)))):
-        _refuse("moe_rmsnorm")
+    shape, xt = x.shape, x.dtype
+    T, H = shape
+    xs, one = x.stride()
+    dt = _DTYPES[xt]
     dev, handle = _place(stream)
-    if not (x.get_device() == dev and _all_on(dev, weight, residual, h, y, rstd, codes, sf)):
+    ok = (T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and x.get_device() == dev
+    pr = ph = py = pw = ps = pc = pf = None
+    rs = hs = ys = 0
+    if weight is not None:
+        ok = ok and _flat(weight, H, xt) and weight.get_device() == dev
+        pw = weight.data_ptr()
+    if residual is not None:
+        ok = ok and _rows(residual, shape, dt) and residual.get_device() == dev
+        pr, rs = residual.data_ptr(), residual.stride(0)
+    if h is not None:
+        ok = ok and _rows(h, shape, dt) and h.get_device() == dev
+        ph, hs = h.data_ptr(), h.stride(0)
+    if y is not None:
+        ok = ok and _rows(y, shape, dt) and y.get_device() == dev
+        py, ys = y.data_ptr(), y.stride(0)
+    if rstd is not None:
+        ok = ok and _flat(rstd, T, _F32) and rstd.get_device() == dev
+        ps = rstd.data_ptr()
+    if codes is not None or sf is not None:
+        ok = (ok and codes is not None and sf is not None and _flat(codes, T * H, _U8) and
+              _flat(sf, _sf_bytes(1, T, H >> 5, sf_layout), _U8) and
+              dev == codes.get_device() == sf.get_device())
+        pc, pf = _p(codes), _p(sf)
+    if not ok:
         _refuse("moe_rmsnorm")
-    st = (_lib or load()).moe_rmsnorm(
-        x.data_ptr(), dt, stride, _p(residual), _stride(residual), _p(weight), eps, T, H, _p(h), _stride(h),
-        _p(y), _stride(y), _p(rstd), _p(codes), _p(sf), sf_layout, scale_rule, handle)
+    st = (_lib or load()).moe_rmsnorm(x.data_ptr(), dt, xs, pr, rs, pw, eps, T, H, ph, hs, py, ys, ps, pc, pf,
+                                      sf_layout, scale_rule, handle)
     if st:
         _check(st, "moe_rmsnorm")
 
 
 def moe_rmsnorm_workspace_size(T, H):
+    if not 0 <= (T | H) <= _MOST:
+        return 0
     return load().moe_rmsnorm_workspace_size(T, H)
 
 
 def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, ws=None, dh=None, stream=None):
     """dy, h [T, H], weight [H] (None: ones), rstd float32 [T], dh [T, H] (None) -> dx [T, H] and
     dweight float32 [H] (None); ws: moe_rmsnorm_workspace_size bytes where dweight is given."""
-    T, H = dy.shape
+    shape = dy.shape
+    T, H = shape
     stride, one = dy.stride()
     dt = _DTYPES[dy.dtype]
-    if not ((T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and h is not None and dx is not None and
-            _rows(h, T, H, dt) and _rows(dx, T, H, dt) and (dh is None or _rows(dh, T, H, dt)) and
-            _flat(weight, H, dy.dtype) and rstd is not None and _flat(rstd, T, _F32) and
-            _flat(dweight, H, _F32) and (ws is None or ws.is_contiguous())):
+    if not ((T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and _rows(h, shape, dt) and
+            _rows(dx, shape, dt) and (dh is None or _rows(dh, shape, dt)) and
+            (weight is None or _flat(weight, H, dy.dtype)) and _flat(rstd, T, _F32) and
+            (dweight is None or _flat(dweight, H, _F32)) and (ws is None or ws.is_contiguous())):
         _refuse("moe_rmsnorm_backward")
     dev, handle = _place(stream)
     if not (dev == dy.get_device() == h.get_device() == dx.get_device() == rstd.get_device() and
-            _all_on(dev, dh, weight, dweight, ws)):
+            (dh is None or dh.get_device() == dev) and (weight is None or weight.get_device() == dev) and
+            (dweight is None or dweight.get_device() == dev) and (ws is None or ws.get_device() == dev)):
         _refuse("moe_rmsnorm_backward")
     st = (_lib or load()).moe_rmsnorm_backward(
-        dy.data_ptr(), dt, stride, _p(dh), _stride(dh), h.data_ptr(), h.stride(0), _p(weight),
-        rstd.data_ptr(), T, H, dx.data_ptr(), dx.stride(0), _p(dweight), _p(ws),
+        dy.data_ptr(), dt, stride, _p(dh), 0 if dh is None else dh.stride(0), h.data_ptr(), h.stride(0),
+        _p(weight), rstd.data_ptr(), T, H, dx.data_ptr(), dx.stride(0), _p(dweight), _p(ws),
         0 if ws is None else ws.nbytes, handle)
     if st:
         _check(st, "moe_rmsnorm_backward")
@@ -729,11 +745,13 @@ def moe_swiglu_mxfp8(gate_up, codes, sf, sf_layout, ckpt=None, ckpt_sf=None, per
     I = I2 >> 1
     if not ((R | I2) <= _MOST and not I2 & 1 and (one == 1 or R == 0) and _flat(codes, R * I, _U8) and
             _flat(sf, _sf_bytes(1, R, I >> 5, sf_layout), _U8) and (ckpt is None) == (ckpt_sf is None) and
-            _flat(ckpt, R * I2, _U8) and _flat(ckpt_sf, R * (I2 >> 5), _U8) and _flat(perm_src, R, _I32)):
+            (ckpt is None or (_flat(ckpt, R * I2, _U8) and _flat(ckpt_sf, R * (I2 >> 5), _U8))) and
+            (perm_src is None or _flat(perm_src, R, _I32))):
         _refuse("moe_swiglu_mxfp8")
     dev, handle = _place(stream)
     if not (dev == gate_up.get_device() == codes.get_device() == sf.get_device() and
-            _all_on(dev, ckpt, ckpt_sf, perm_src)):
+            (ckpt is None or dev == ckpt.get_device() == ckpt_sf.get_device()) and
+            (perm_src is None or perm_src.get_device() == dev)):
         _refuse("moe_swiglu_mxfp8")
     st = (_lib or load()).moe_swiglu_mxfp8(
         gate_up.data_ptr(), _DTYPES[gate_up.dtype], stride, R, I, _p(perm_src), scale_rule, codes.data_ptr(),
@@ -749,17 +767,19 @@ def moe_swiglu_mxfp8_backward(ds, ckpt, ckpt_sf, codes=None, sf=None, sf_layout=
     R, I = ds.shape
     stride, one = ds.stride()
     dt = _DTYPES[ds.dtype]
-    if not ((R | 2 * I) <= _MOST and (one == 1 or I == 1 or R == 0) and ckpt is not None and
-            ckpt_sf is not None and _flat(ckpt, 2 * R * I, _U8) and _flat(ckpt_sf, R * (2 * I >> 5), _U8) and
-            (codes is None) == (sf is None) and
+    if not ((R | 2 * I) <= _MOST and (one == 1 or I == 1 or R == 0) and _flat(ckpt, 2 * R * I, _U8) and
+            _flat(ckpt_sf, R * (2 * I >> 5), _U8) and (codes is None) == (sf is None) and
             (codes is None or (_flat(codes, 2 * R * I, _U8) and
                                _flat(sf, _sf_bytes(1, R, 2 * I >> 5, sf_layout), _U8))) and
             (dgate_up is None or (_DTYPES[dgate_up.dtype] == dt and dgate_up.numel() == 2 * R * I and
-                                  dgate_up.is_contiguous())) and _flat(perm_src, R, _I32)):
+                                  dgate_up.is_contiguous())) and
+            (perm_src is None or _flat(perm_src, R, _I32))):
         _refuse("moe_swiglu_mxfp8_backward")
     dev, handle = _place(stream)
     if not (dev == ds.get_device() == ckpt.get_device() == ckpt_sf.get_device() and
-            _all_on(dev, codes, sf, perm_src, dgate_up)):
+            (codes is None or dev == codes.get_device() == sf.get_device()) and
+            (dgate_up is None or dgate_up.get_device() == dev) and
+            (perm_src is None or perm_src.get_device() == dev)):
         _refuse("moe_swiglu_mxfp8_backward")
     st = (_lib or load()).moe_swiglu_mxfp8_backward(
         ds.data_ptr(), dt, stride, ckpt.data_ptr(), ckpt_sf.data_ptr(), R, I, _p(perm_src), scale_rule,

@@ -666,7 +666,7 @@ moe_status moe_rmsnorm(const void* x_d, int32_t dtype, int64_t x_stride, const v
 size_t moe_rmsnorm_workspace_size(int32_t T, int32_t H)
 {
     if (check_norm(MOE_BF16, T, H) != MOE_OK) return 0;
-    const int parts = norm_parts(T, H, norm_per(T, H), 2);  // (no fewer than of fp32)
+    const int parts = norm_parts(T, H, norm_per(T, H));
     return parts > 1 ? (size_t)parts * H * 4 : 0;
 }
 
@@ -713,7 +713,7 @@ moe_status moe_rmsnorm_backward(const void* dy_d, int32_t dtype, int64_t dy_stri
                      rows_vec(dx_d, row, dx_stride * some);
     const int per = norm_per(T, H);
     const bool one = norm_one(H, per);
-    a.parts = norm_parts(T, H, per, es);
+    a.parts = norm_parts(T, H, per);
     const int threads = one ? 256 : norm_threads(H, per);
     const NormBackKernel kern = norm_back_kernel_for(dtype, per, one, vec, threads);
     size_t smem = 0;
@@ -724,7 +724,7 @@ moe_status moe_rmsnorm_backward(const void* dy_d, int32_t dtype, int64_t dy_stri
     }
     const moe_status done = launch(kern, dim3(one ? ceil_div(a.parts, 8) : a.parts), dim3(threads), smem, s, true, a);
     if (done != MOE_OK || !dweight_d || a.parts == 1) return done;
-    return launch(norm_parts_kernel, dim3(ceil_div(H, 32)), dim3(256), 0, s, true, a.ws, a.parts, H, dweight_d);
+    return launch(norm_parts_kernel, dim3(ceil_div(H, 32)), dim3(1024), 0, s, true, a.ws, a.parts, H, dweight_d);
 }
 
 moe_status moe_swiglu_mxfp8(const void* gate_up_d, int32_t dtype, int64_t stride, int32_t rows, int32_t inter,

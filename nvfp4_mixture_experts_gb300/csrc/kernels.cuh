@@ -571,17 +571,13 @@ NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec, int 
 __global__ void norm_parts_kernel(const float* ws, int parts, int H, float* dw);
 __host__ __device__ constexpr bool norm_one(int H, int per) { return H <= 256 * per; }
 inline int norm_threads(int H, int per) { return div_up(div_up(H, 8), 32 * per) * 32; }
-// Blocks of an SM that the gradient's registers and rings are made for: 24 warps of 16-bit types, 16 of fp32,
-// or one block.  (8192 x 4096 bf16 with two blocks and a row in flight in registers: 56 us.)
-inline int norm_per_sm(int threads, int elem_bytes)
-{
-    const int n = (elem_bytes == 2 ? 768 : 512) / threads;
-    return n < 1 ? 1 : n;
-}
+// Blocks of an SM that the gradient's registers and rings are made for: up to 19 warps, or one block.  (8192 x 4096
+// bf16, main kernel alone: two blocks with three rows in flight 44 us, with one 63, three blocks 48.)
+inline int norm_per_sm(int threads) { return threads > 304 ? 1 : 608 / threads; }
 // Parts of the weight's gradient: the blocks (short rows: two blocks' warps) that 152 SMs hold.
-inline int norm_parts(int T, int H, int per, int elem_bytes)
+inline int norm_parts(int T, int H, int per)
 {
-    const int most = norm_one(H, per) ? 152 * 16 : 152 * norm_per_sm(norm_threads(H, per), elem_bytes);
+    const int most = norm_one(H, per) ? 152 * 16 : 152 * norm_per_sm(norm_threads(H, per));
     return T < most ? T : most;
 }
 // The ring: up to three rows of three tensors in a block's share of an SM's shared memory.
@@ -589,7 +585,7 @@ inline int norm_row_bytes(int threads, int elem_bytes) { return 3 * 2 * threads 
 constexpr int kNormRingMost = 2 * 3 * 2 * 1024 * 8 * 2;   // of any launch: two rows of 1024 threads, 16-bit types
 inline int norm_depth(int threads, int elem_bytes)
 {
-    const int share = 233472 / norm_per_sm(threads, elem_bytes) - 1024 - 256;  // (what the system and the sums take)
+    const int share = 233472 / norm_per_sm(threads) - 1024 - 256;  // (what the system and the sums take)
     const int d = share / norm_row_bytes(threads, elem_bytes);
     return d < 1 ? 1 : d > 3 ? 3 : d;
 }

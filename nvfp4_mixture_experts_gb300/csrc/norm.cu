@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(NT) norm_back_kernel(NormBackArgs a)
 // shared memory where each thread reads what it copied itself (so no barrier is needed for them, and no
 // registers hold them): a block has one row in its registers and its sum waits for all of them.
 template <typename T, int NT>
-__global__ void __launch_bounds__(NT, NT == 256 ? 6 / (int)sizeof(T) + (sizeof(T) == 4) : 1) norm_back_ring_kernel(NormBackArgs a)
+__global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_back_ring_kernel(NormBackArgs a)
 {
     constexpr int PER = 2, kPieces = (int)sizeof(T) / 2;  // eights of a thread, 16-byte pieces of an eight
     extern __shared__ uint4 s_ring[];                     // [depth][3][PER][kPieces][threads]
@@ -298,11 +298,14 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 / (int)sizeof(T) + (sizeof(T
             if (!a.w) w[p][i] = F2(1.0f);
         }
     }
-    int buf = 0, slot = 0;
-    float rstd_next = part < a.T ? a.rstd[part] : 0.0f;
-    for (int64_t row = part; row < a.T; row += a.parts) {
-        const float rstd = rstd_next;
-        if (row + a.parts < a.T) rstd_next = a.rstd[row + a.parts];
+    int buf = 0, slot = 0, at = 0;
+    float rstds = 0.0f;   // of 32 of the block's rows, one a lane
+    for (int64_t row = part; row < a.T; row += a.parts, at = (at + 1) & 31) {
+        if (at == 0) {
+            const int64_t mine = row + (int64_t)(tid & 31) * a.parts;
+            rstds = mine < a.T ? a.rstd[mine] : 0.0f;
+        }
+        const float rstd = __shfl_sync(0xffffffffu, rstds, at);
         // (the thread's own copies of the oldest row have landed)
         if (a.depth == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
         else if (a.depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -356,32 +359,33 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 / (int)sizeof(T) + (sizeof(T
     for (int p = 0; p < PER; ++p)
         if (tid + p * nt < units)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 v = acc[p][i].get();
-                out[8 * (tid + p * nt) + 2 * i] = v.x;
-                out[8 * (tid + p * nt) + 2 * i + 1] = v.y;
-            }
+            for (int i = 0; i < 4; ++i)   // (dw itself need not be aligned to more than an element)
+                if (a.parts == 1) {
+                    const float2 v = acc[p][i].get();
+                    out[8 * (tid + p * nt) + 2 * i] = v.x;
+                    out[8 * (tid + p * nt) + 2 * i + 1] = v.y;
+                } else {
+                    reinterpret_cast<uint64_t*>(out)[4 * (tid + p * nt) + i] = acc[p][i].v;
+                }
 }
 
-// dw[c] = the sum of the parts' column c: 32 columns a block, each by eight threads of the block that
-// take every eighth part.
-__global__ void __launch_bounds__(256) norm_parts_kernel(const float* ws, int parts, int H, float* dw)
+// dw[c] = the sum of the parts' column c: 32 columns a block, each by 32 threads that take every 32nd part.
+__global__ void __launch_bounds__(1024) norm_parts_kernel(const float* ws, int parts, int H, float* dw)
 {
-    __shared__ float s[8][32];
+    __shared__ float s[32][33];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (c < H)
 #pragma unroll 8
-        for (int p = warp; p < parts; p += 8) v += ws[(int64_t)p * H + c];
+        for (int p = warp; p < parts; p += 32) v += ws[(int64_t)p * H + c];
     s[warp][lane] = v;
     __syncthreads();
-    if (warp == 0 && c < H) {
+    v = s[lane][warp];   // column `warp` of the block's
 #pragma unroll
-        for (int q = 1; q < 8; ++q) v += s[q][lane];
-        dw[c] = v;
-    }
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && blockIdx.x * 32 + warp < H) dw[blockIdx.x * 32 + warp] = v;
 }
 
 template <typename T>

@@ -217,11 +217,14 @@ struct Scores64 {
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
         m = top;
         sum = 0.0;
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = logit(e);
-            if (l > -INFINITY) sum += l == m ? 1.0 : exp((double)l - m);
-        }
-        sum = warp_sum(sum);
+        double part[4] = {};   // (four exponentials at a time: 64-bit instructions take long)
+        for (int e0 = lane; e0 < a.E; e0 += 128)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float l = e0 + 32 * q < a.E ? logit(e0 + 32 * q) : -INFINITY;
+                part[q] += l == -INFINITY ? 0.0 : l == m ? 1.0 : exp((double)l - m);
+            }
+        sum = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
     }
     // the key of a sum: score and bias
     __device__ double key(int e) const
@@ -270,6 +273,63 @@ __device__ __noinline__ int choose_64(const RouteArgs& a, const T* x, double* s_
     return mine;
 }
 
+// The kept groups where scores lie nearer to the border than 32-bit keys can tell: lane g's group has the
+// score `score`, its keys are keys[g n ..]; edge: the border's scores; near: whether two keys may be in the
+// other order.  Groups well above the border are in; those near it have their few largest keys, four at
+// most, taken in 64 bits, a lane each.  False: more keys than that are near one another.
+template <typename T, typename Near>
+__device__ __noinline__ bool border_groups(const RouteArgs& a, const T* x, const float* keys, float score,
+                                           const float (&edge)[2], Near near, int* s_expert, uint32_t& in)
+{
+    const int lane = threadIdx.x & 31, n = (int)a.group.d;
+    const bool two = a.group_score == MOE_GROUP_TOP2;
+    const bool mine = lane < a.groups;
+    // (a group's score is two keys; the border's two scores are near each other)
+    auto by = [&](float hi, float lo) { return near(0.125f * hi, 0.125f * lo); };
+    const bool border = mine && (by(fmaxf(score, edge[0]), fminf(score, edge[0])) ||
+                                 by(fmaxf(score, edge[1]), fminf(score, edge[1])));
+    const uint32_t borders = __ballot_sync(kAll, border);
+    const uint32_t above = __ballot_sync(kAll, mine && !border && score > edge[0]);
+    const int rank = __popc(borders & ((1u << lane) - 1));
+    if (__popc(borders) > 8) return false;
+    int count = 0;
+    if (border) {
+        const float* k = keys + lane * n;
+        float p = -INFINITY, q = -INFINITY;
+        for (int i = 0; i < n; ++i) {
+            q = fmaxf(q, fminf(p, k[i]));
+            p = fmaxf(p, k[i]);
+        }
+        const float least = two && q > -INFINITY ? q : p;
+        for (int i = 0; i < n; ++i)
+            if (k[i] > -INFINITY && (k[i] >= least || near(least, k[i]))) {
+                if (count < 4) s_expert[4 * rank + count] = lane * n + i;
+                ++count;
+            }
+    }
+    __syncwarp();
+    if (__any_sync(kAll, count > 4)) return false;
+    // lane 4 r + i: candidate i of the r-th group at the border
+    const int owner = __fns(borders, 0, (lane >> 2) + 1);   // (-1: none)
+    const int have = __shfl_sync(kAll, count, owner & 31);
+    const Scores64<T> sc(a, x);
+    const double v = owner >= 0 && (lane & 3) < have ? sc.key(s_expert[lane]) : -INFINITY;
+    double p = -INFINITY, q = -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+        const double c = __shfl_sync(kAll, v, (4 * rank + i) & 31);
+        q = fmax(q, fmin(p, c));
+        p = fmax(p, c);
+    }
+    const double exact = two && q > -INFINITY ? p + q : p;
+    int before = __popc(above);
+    for (int g = 0; g < a.groups; ++g) {
+        const double o = __shfl_sync(kAll, exact, g);
+        if (borders >> g & 1) before += o > exact || (o == exact && g < lane);
+    }
+    in = above | __ballot_sync(kAll, border && before < a.topk_groups);
+    return true;
+}
+
 // The order of n candidates, one a lane, by their keys in 64 bits: expert j of lane j.
 template <typename T>
 __device__ __noinline__ int order_64(const RouteArgs& a, const T* x, int mine, int n)
@@ -294,14 +354,14 @@ __device__ __noinline__ int order_64(const RouteArgs& a, const T* x, int mine, i
 __device__ __forceinline__ float ex2_approx(float x)
 {
     float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
 __device__ __forceinline__ float rcp_approx(float x)
 {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -382,11 +442,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
         n = (int)a.group.d;
         __syncwarp();
         float edge[2];
-        const uint32_t in = best_groups(group_score(keys32, a.groups, n, top2), a.groups, a.topk_groups, edge);
+        const float score = group_score(keys32, a.groups, n, top2);
+        uint32_t in = best_groups(score, a.groups, a.topk_groups, edge);
+        if (summed && near(0.25f * edge[0], 0.25f * edge[1]))
+            again = !border_groups(a, x, keys32, score, edge, near, s_expert[warp], in);
         if (in >> lane & 1) group[__popc(in & ((1u << lane) - 1))] = lane * n;
         __syncwarp();
-        // (a group's score is two keys)
-        again = summed && near(0.25f * edge[0], 0.25f * edge[1]);
         // the kept groups' experts one after another: position 32 i + lane
         const int count = a.topk_groups * n;
 #pragma unroll

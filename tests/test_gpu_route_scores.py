@@ -113,6 +113,38 @@ def test_sums_nearer_than_32_bits():
         check(dev(near.astype(np.float32)), dev(bias), k, kind, 8, 3, True, False)
 
 
+@pytest.mark.parametrize("biased", [False, True])
+def test_groups_nearer_than_32_bits(biased):
+    """Groups whose two largest scores (or whose largest score and bias) have sums that are equal up to
+    2^-24 or so."""
+    rng = np.random.default_rng(1)
+    T, G, n = 300, 8, 20
+    for kind, mid in (("softmax", 0.5), ("sigmoid", 0.5), ("sigmoid", 0.55)):
+        l = rng.uniform(-9, -6, size=(T, G, n))
+        d = rng.uniform(0.01, 0.3, size=(T, G))
+        for i, v in enumerate((mid + d, mid - d)):
+            at = np.log(v / (1 - v)) if kind == "sigmoid" else np.log(v)
+            np.put_along_axis(l, np.full((T, G, 1), 3 + 5 * i), at[..., None], 2)
+        l = l.reshape(T, G * n).astype(np.float32)
+        bias = None
+        if biased:   # of one expert a group, by which the largest keys of token 0 are equal
+            s = np.stack([ref.scores(r, kind) for r in l.astype(np.float64)]).reshape(T, G, n)
+            bias = np.zeros((G, n))
+            bias[:, 3] = 2 - s[0, :, 3]
+            l[1:, 3::n] = l[0, 3::n] + rng.integers(-2, 3, size=(T - 1, G)) * 2.0 ** -24
+            if kind == "softmax":   # the same sum of exponentials for every token, or nearly
+                l[1:] = np.where(np.isin(np.arange(G * n) % n, (3,)), l[1:], l[0])
+            bias = dev(bias.reshape(-1))
+        for topg in (1, 3, 7):
+            if kind == "sigmoid" and mid == 0.5 and not biased:
+                # the two logits are each other's negatives, their scores' sums 1 and their order that of
+                # 64-bit roundings: any groups, but the largest in the ones chosen
+                ids, _ = run(dev(l), bias, 2, kind, G, topg, True, False)
+                assert torch.all((ids % n == 3) | (ids % n == 8))
+                continue
+            check(dev(l), bias, 2, kind, G, topg, not biased, False)
+
+
 def test_far_logits():
     """Scores that are 0 or 1 in 32 bits: renormalised weights are still their quotients."""
     l = torch.tensor([[-120.0, -121.0, -125.0, -300.0], [-30.0, -31.0, 40.0, 41.0], [90.0, 95.0, -95.0, 20.0],
