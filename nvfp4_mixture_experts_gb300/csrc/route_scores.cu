@@ -84,57 +84,70 @@ __device__ __forceinline__ K take_max(K (&key)[PL], int& expert)
     return best;
 }
 
-// The `rounds` largest keys in order (equal ones by expert), that of lane j in `kept` and its expert in
-// `mine`.  Keys as large as the rounds-th largest of the lanes' maxima are the only ones that can be among
-// them: mostly few, which move to a lane each and are ranked by counting (8192 tokens of 320 experts, 8 of
-// 160 in the best groups: 11 of 5 rounds of all keys, 2 of this).  More than 32, as of equal logits: in
-// rounds.
+// The lanes' numbers sorted, the largest in lane 0 (a bitonic network).
+__device__ __forceinline__ uint32_t warp_sort(uint32_t x)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j; j >>= 1) {
+            const uint32_t y = __shfl_xor_sync(kAll, x, j);
+            const bool larger = ((lane & j) == 0) == ((lane & k) == 0);
+            x = larger ? max(x, y) : min(x, y);
+        }
+    return x;
+}
+
+// The `rounds` largest keys (at 32 i + lane in key[i]; 0: none) in order, equal ones by position: that of lane
+// j in `kept` and its position in `mine`.  Keys as large as the rounds-th largest of the lanes' maxima are the
+// only ones that can be among them: mostly few, which are put together with their positions and ranked by
+// counting, a lane each (8192 tokens of 320 experts, top-8: 567 instructions a token with the bound found and
+// the keys put together in votes, 10.6 us).  More than 32, as of equal logits: in rounds over all keys.
 template <int PL>
-__device__ __forceinline__ void choose_32(const uint32_t (&key)[PL], int rounds, uint32_t* s_key, int* s_expert,
-                                          uint32_t& kept, int& mine)
+__device__ __forceinline__ void choose_32(const uint32_t (&key)[PL], int rounds, uint64_t* s_key, uint32_t& kept,
+                                          int& mine)
 {
     const int lane = threadIdx.x & 31;
     uint32_t x = key[0];
 #pragma unroll
     for (int i = 1; i < PL; ++i) x = max(x, key[i]);
-    uint32_t bound = 1;
-    for (int j = 0; j < rounds; ++j) {
-        bound = warp_max(x);
-        if (lane == __ffs(__ballot_sync(kAll, x == bound)) - 1) x = 0;
-    }
-    bound = max(bound, 1u);
-    int n = 0;
+    const uint32_t bound = rounds > 32 ? 1u : max(__shfl_sync(kAll, warp_sort(x), rounds - 1), 1u);
+    int own = 0;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-        const bool in = key[i] >= bound;
-        const uint32_t mask = __ballot_sync(kAll, in);
-        const int at = n + __popc(mask & ((1u << lane) - 1));
-        if (in && at < 32) {
-            s_key[at] = key[i];
-            s_expert[at] = 32 * i + lane;
-        }
-        n += __popc(mask);
+    for (int i = 0; i < PL; ++i) own += key[i] >= bound;
+    int n = own;   // of this lane and those before it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, n, o);
+        if (lane >= o) n += y;
     }
+    int at = n - own;
+    n = __shfl_sync(kAll, n, 31);
     kept = 0;
     mine = 0;
     if (n <= 32) {
+        // key and, of equal keys the larger for the lower position, its complement; an even number of them
+        s_key[lane] = 0;
         __syncwarp();
-        const uint32_t k = lane < n ? s_key[lane] : 0u;
-        const int e = s_expert[lane];
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            if (key[i] >= bound) s_key[at++] = (uint64_t)key[i] << 32 | ~(uint32_t)(32 * i + lane);
+        __syncwarp();
+        const uint64_t k = s_key[lane];
         int rank = 0;
-        for (int j = 0; j < n; ++j) {
-            const uint32_t o = __shfl_sync(kAll, k, j);
-            rank += o > k || (o == k && j < lane);   // (they lie in the order of the experts)
+        for (int j = 0; j < n; j += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s_key + j);
+            rank += o.x > k;
+            rank += o.y > k;
         }
         __syncwarp();
-        if (lane < n) {
-            s_key[rank] = k;
-            s_expert[rank] = e;
-        }
+        if (lane < n) s_key[rank] = k;
         __syncwarp();
         if (lane < min(n, rounds)) {
-            kept = s_key[lane];
-            mine = s_expert[lane];
+            const uint64_t r = s_key[lane];
+            kept = (uint32_t)(r >> 32);
+            mine = (int)~(uint32_t)r;
         }
         return;
     }
@@ -150,6 +163,11 @@ __device__ __forceinline__ void choose_32(const uint32_t (&key)[PL], int rounds,
         }
     }
 }
+
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
 
 // Bit g: group g is among the topk_groups best; ties go to the lower group.  score: lane g's group.  `edge`
 // receives the scores of the last group taken and the first left out.
@@ -172,9 +190,9 @@ __device__ __forceinline__ uint32_t best_groups(F score, int groups, int take, F
 
 // Lane g < groups: the score of group g, keys [E] in shared memory: its largest, or the sum of its two
 // largest (the largest alone where the second is -infinity).  32 / (groups rounded up to a power of two)
-// lanes look at a group together.
+// lanes look at a group together.  least: the smaller of the two keys, or the largest where the score is of one.
 template <typename F>
-__device__ __forceinline__ F group_score(const F* keys, int groups, int n, bool two)
+__device__ __forceinline__ F group_score(const F* keys, int groups, int n, bool two, F* least = nullptr)
 {
     const int lane = threadIdx.x & 31;
     int per = 32;
@@ -182,17 +200,20 @@ __device__ __forceinline__ F group_score(const F* keys, int groups, int n, bool 
     const int g = lane / per;
     F a = -(F)INFINITY, b = -(F)INFINITY;
     if (g < groups)
+#pragma unroll 4
         for (int i = lane % per; i < n; i += per) {
             const F v = keys[g * n + i];
-            b = fmax(b, fmin(a, v));
-            a = fmax(a, v);
+            b = larger(b, smaller(a, v));
+            a = larger(a, v);
         }
     for (int o = 1; o < per; o <<= 1) {
         const F c = __shfl_xor_sync(kAll, a, o), d = __shfl_xor_sync(kAll, b, o);
-        b = fmax(fmin(a, c), fmax(b, d));
-        a = fmax(a, c);
+        b = larger(smaller(a, c), larger(b, d));
+        a = larger(a, c);
     }
-    const F s = two && b > -(F)INFINITY ? a + b : a;
+    const bool sum = two && b > -(F)INFINITY;
+    const F s = sum ? a + b : a;
+    if (least) *least = __shfl_sync(kAll, sum ? b : a, (lane * per) & 31);
     return __shfl_sync(kAll, s, (lane * per) & 31);
 }
 
@@ -274,12 +295,14 @@ __device__ __noinline__ int choose_64(const RouteArgs& a, const T* x, double* s_
 }
 
 // The kept groups where scores lie nearer to the border than 32-bit keys can tell: lane g's group has the
-// score `score`, its keys are keys[g n ..]; edge: the border's scores; near: whether two keys may be in the
-// other order.  Groups well above the border are in; those near it have their few largest keys, four at
-// most, taken in 64 bits, a lane each.  False: more keys than that are near one another.
+// score `score`, made of keys of at least `least`, and its keys are keys[g n ..]; edge: the border's scores;
+// near: whether two keys may be in the other order.  Groups well above the border are in; those near it have
+// their few largest keys, four at most, taken in 64 bits, a lane each.  False: more keys than that are near
+// one another.
 template <typename T, typename Near>
 __device__ __noinline__ bool border_groups(const RouteArgs& a, const T* x, const float* keys, float score,
-                                           const float (&edge)[2], Near near, int* s_expert, uint32_t& in)
+                                           float least, const float (&edge)[2], Near near, int* s_expert,
+                                           uint32_t& in)
 {
     const int lane = threadIdx.x & 31, n = (int)a.group.d;
     const bool two = a.group_score == MOE_GROUP_TOP2;
@@ -290,41 +313,43 @@ __device__ __noinline__ bool border_groups(const RouteArgs& a, const T* x, const
                                  by(fmaxf(score, edge[1]), fminf(score, edge[1])));
     const uint32_t borders = __ballot_sync(kAll, border);
     const uint32_t above = __ballot_sync(kAll, mine && !border && score > edge[0]);
-    const int rank = __popc(borders & ((1u << lane) - 1));
     if (__popc(borders) > 8) return false;
-    int count = 0;
-    if (border) {
-        const float* k = keys + lane * n;
-        float p = -INFINITY, q = -INFINITY;
-        for (int i = 0; i < n; ++i) {
-            q = fmaxf(q, fminf(p, k[i]));
-            p = fmaxf(p, k[i]);
+    // candidate i of the r-th group at the border in s_expert[4 r + i], where there is one
+    int e = -1, r = 0;   // lane 4 r + i: that candidate
+    s_expert[lane] = -1;
+    __syncwarp();
+    for (uint32_t left = borders; left; left &= left - 1, ++r) {
+        const int g = __ffs(left) - 1;
+        const float low = __shfl_sync(kAll, least, g);
+        int count = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const float k = i0 + lane < n ? keys[g * n + i0 + lane] : -INFINITY;
+            const bool is = k > -INFINITY && (k >= low || near(low, k));
+            const uint32_t mask = __ballot_sync(kAll, is);
+            const int at = count + __popc(mask & ((1u << lane) - 1));
+            if (is && at < 4) s_expert[4 * r + at] = g * n + i0 + lane;
+            count += __popc(mask);
         }
-        const float least = two && q > -INFINITY ? q : p;
-        for (int i = 0; i < n; ++i)
-            if (k[i] > -INFINITY && (k[i] >= least || near(least, k[i]))) {
-                if (count < 4) s_expert[4 * rank + count] = lane * n + i;
-                ++count;
-            }
+        if (count > 4) return false;
     }
     __syncwarp();
-    if (__any_sync(kAll, count > 4)) return false;
-    // lane 4 r + i: candidate i of the r-th group at the border
-    const int owner = __fns(borders, 0, (lane >> 2) + 1);   // (-1: none)
-    const int have = __shfl_sync(kAll, count, owner & 31);
+    e = s_expert[lane];
     const Scores64<T> sc(a, x);
-    const double v = owner >= 0 && (lane & 3) < have ? sc.key(s_expert[lane]) : -INFINITY;
+    const double v = e >= 0 ? sc.key(e) : -INFINITY;
+    const int rank = __popc(borders & ((1u << lane) - 1));
     double p = -INFINITY, q = -INFINITY;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const double c = __shfl_sync(kAll, v, (4 * rank + i) & 31);
-        q = fmax(q, fmin(p, c));
-        p = fmax(p, c);
+        q = larger(q, smaller(p, c));
+        p = larger(p, c);
     }
     const double exact = two && q > -INFINITY ? p + q : p;
     int before = __popc(above);
-    for (int g = 0; g < a.groups; ++g) {
+    for (uint32_t left = borders; left; left &= left - 1) {
+        const int g = __ffs(left) - 1;
         const double o = __shfl_sync(kAll, exact, g);
-        if (borders >> g & 1) before += o > exact || (o == exact && g < lane);
+        before += o > exact || (o == exact && g < lane);
     }
     in = above | __ballot_sync(kAll, border && before < a.topk_groups);
     return true;
@@ -371,11 +396,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // A warp per token, expert 32 i + lane in the registers of a lane.
 template <int PL, typename T>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArgs a)
+__global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scores_kernel(RouteArgs a)
 {
     extern __shared__ double s_all[];  // [kRouteWarps][E] keys, where there are groups
-    __shared__ uint32_t s_key[kRouteWarps][32];
-    __shared__ int s_expert[kRouteWarps][32], s_group[kRouteWarps][32];
+    __shared__ alignas(16) uint64_t s_key[kRouteWarps][32];
+    __shared__ int s_group[kRouteWarps][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -387,6 +412,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
     const bool softmax = a.score == MOE_SCORE_SOFTMAX;
 #pragma unroll
     for (int i = 0; i < PL; ++i) l[i] = 32 * i + lane < a.E ? to_f32(x[32 * i + lane]) : -INFINITY;
+    float bias[PL];    // (loaded here: no load passes the stores to shared memory below)
+#pragma unroll
+    for (int i = 0; i < PL; ++i) bias[i] = a.bias && 32 * i + lane < a.E ? a.bias[32 * i + lane] : 0.0f;
     bool nan = false;  // of this token's weights: a logit is NaN, which ranks last, or has no softmax
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
@@ -429,7 +457,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
         if (summed) {
             s = softmax ? ex2_approx(kLog2e * (v == m ? 0.0f : v - m)) * inv
                         : rcp_approx(1.0f + ex2_approx(-kLog2e * v));
-            if (a.bias) s += a.bias[e];
+            s += bias[i];
             if (v == -INFINITY || !(s >= -FLT_MAX)) s = -INFINITY;  // masked; a bias of -infinity or NaN
             if (a.bias) v = s;
         }
@@ -442,10 +470,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
         n = (int)a.group.d;
         __syncwarp();
         float edge[2];
-        const float score = group_score(keys32, a.groups, n, top2);
+        float least;
+        const float score = group_score(keys32, a.groups, n, top2, &least);
         uint32_t in = best_groups(score, a.groups, a.topk_groups, edge);
         if (summed && near(0.25f * edge[0], 0.25f * edge[1]))
-            again = !border_groups(a, x, keys32, score, edge, near, s_expert[warp], in);
+            again = !border_groups(a, x, keys32, score, least, edge, near, reinterpret_cast<int*>(s_key[warp]), in);
         if (in >> lane & 1) group[__popc(in & ((1u << lane) - 1))] = lane * n;
         __syncwarp();
         // the kept groups' experts one after another: position 32 i + lane
@@ -469,15 +498,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(RouteArg
         // one more than k where the order of sums may need 64 bits
         const int rounds = a.bias && a.k < a.E ? a.k + 1 : a.k;
         uint32_t kept;
-        choose_32<PL>(key, rounds, s_key[warp], s_expert[warp], kept, mine);
+        choose_32<PL>(key, rounds, s_key[warp], kept, mine);
         mine = expert(mine);
         if (a.bias) {
             const uint32_t next = __shfl_down_sync(kAll, kept, 1);
             const int after = __shfl_down_sync(kAll, mine, 1);
-            // (the sums of equal terms are equal)
             bool apart = lane >= rounds - 1 || lane == 31 || !next || !near(unordered(kept), unordered(next));
-            apart = apart || (to_f32(x[mine]) == to_f32(x[after]) && a.bias[mine] == a.bias[after]);
-            if (!__all_sync(kAll, apart) || rounds > 32) {
+            bool all = __all_sync(kAll, apart);
+            if (!all) {   // (the sums of equal terms are equal)
+                apart = apart || (to_f32(x[mine]) == to_f32(x[after]) && a.bias[mine] == a.bias[after]);
+                all = __all_sync(kAll, apart);
+            }
+            if (!all || rounds > 32) {
                 // every expert that may be among the k: those with keys near the k-th, or before it
                 int c = 0;
                 float last = 0.0f;
