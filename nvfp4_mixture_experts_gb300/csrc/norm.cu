@@ -52,9 +52,9 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_kernel(NormArgs a)
     const int tid = ONE ? threadIdx.x & 31 : threadIdx.x, nt = ONE ? 32 : blockDim.x;
     const int lane = threadIdx.x & 31;
     const int units = div_up(a.H, 8), blocks = a.H >> 5, KA = (blocks + 3) >> 2;
-    const int step = ONE ? gridDim.x * 8 : gridDim.x;
+    const int64_t step = ONE ? (int64_t)gridDim.x * 8 : gridDim.x;
     int buf = 0;
-    for (int64_t row = ONE ? blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x; row < a.T; row += step) {
+    for (int64_t row = ONE ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x; row < a.T; row += step) {
         const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
         Eight<T> e[PER] = {}, r[PER] = {};
 #pragma unroll

@@ -133,7 +133,7 @@ __device__ __forceinline__ void for_live(const int32_t* perm_src, uint32_t n, co
 }  // namespace
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a)
+__global__ void __launch_bounds__(256, 4) swiglu_kernel(SwigluArgs a)
 {
     pdl_wait();
     pdl_trigger();
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a)
 
 // With s = sigmoid(g): dg = ds u s (1 + g (1 - s)), du = ds g s.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) swiglu_back_kernel(SwigluBackArgs a)
+__global__ void __launch_bounds__(256, 4) swiglu_back_kernel(SwigluBackArgs a)
 {
     pdl_wait();
     pdl_trigger();

@@ -175,6 +175,8 @@ class MXShared(MXExperts):
     def __call__(self, x, eight=None):
         """[T, H] in x's type for tokens x [T, H]; differentiable in x.  eight: x as an MXFP8 matrix with
         tiled scales, where the caller has it already (moe_rmsnorm's)."""
+        if eight is not None and tuple(eight[0].shape) != tuple(x.shape):
+            raise MoEError(MOE_ERR_INVALID, "MXShared: codes %s of rows %s" % (tuple(eight[0].shape), tuple(x.shape)))
         return _Shared.apply(x, *(eight or (None, None)), self)
 
 

@@ -55,6 +55,8 @@ def test_sizes_and_bits_that_do_not_fit(lib):
             MXExperts.from_master(E, 0, torch.randn(E, 2 * i, h), torch.randn(E, h, i), act_bits=bits)
     with pytest.raises(moe.MoEError):
         MXShared.from_master(torch.randn(2, 2 * I, H), torch.randn(2, H, I))
+    with pytest.raises(moe.MoEError):   # the codes of other rows
+        shared()(torch.randn(T, H), (torch.zeros(T - 1, H, dtype=torch.uint8), torch.zeros(2048, dtype=torch.uint8)))
 
 
 def test_no_backward_without_transposed_weights(lib):
