@@ -611,8 +611,8 @@ MOE_API moe_status moe_rmsnorm(const void* x_d, int32_t dtype, int64_t x_stride,
                                uint8_t* codes_d, uint8_t* sf_d, int32_t sf_layout,
                                int32_t scale_rule, moe_stream_t stream);
 
-/* Bytes of workspace that moe_rmsnorm_backward needs for the weight's gradient (32 MiB at most; 0 for
- * arguments out of range, and for one row).
+/* Bytes of workspace that moe_rmsnorm_backward needs for the weight's gradient (32 MiB at most; 0
+ * where it needs none, and for arguments out of range).
  * Passage: none; workspace sizing of this library (the pages have no counterpart). */
 MOE_API size_t moe_rmsnorm_workspace_size(int32_t T, int32_t H);
 

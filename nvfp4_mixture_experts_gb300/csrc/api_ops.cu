@@ -297,13 +297,6 @@ moe_status check_swiglu(int dtype, int rows, int inter, int sf_layout, int scale
                                                                                          : MOE_OK;
 }
 
-// Eights of a row that a thread of the norm's kernels holds.
-int norm_per(int T, int H)
-{
-    (void)T;
-    return H <= 256 ? 1 : 2;
-}
-
 }  // namespace
 
 extern "C" {
@@ -653,20 +646,30 @@ moe_status moe_rmsnorm(const void* x_d, int32_t dtype, int64_t x_stride, const v
     a.sf = sf_d;
     a.layout = sf_layout;
     a.rule = scale_rule;
-    const int64_t row = (int64_t)H * es, some = T > 1 ? es : 0;
-    const bool vec = H % 8 == 0 && rows_vec(x_d, row, x_stride * some) && rows_vec(residual_d, row, residual_stride * some) &&
-                     rows_vec(weight_d, row, 0) && rows_vec(h_d, row, h_d ? h_stride * some : 0) &&
-                     rows_vec(y_d, row, y_d ? y_stride * some : 0);
-    const int per = norm_per(T, H);
-    const bool one = norm_one(H, per);
-    return launch(norm_kernel_for(dtype, per, one, vec), dim3(one ? ceil_div(T, 8) : T),
-                  dim3(one ? 256 : norm_threads(H, per)), 0, reinterpret_cast<cudaStream_t>(stream), true, a);
+    const uint64_t some = T > 1 ? es : 0;   // (of one row strides are of no effect)
+    int piece = largest_unit(addr(x_d) | addr(residual_d) | addr(weight_d) | addr(h_d) | addr(y_d) |
+                                   (uint64_t)H * es | x_stride * some | (residual_d ? residual_stride * some : 0) |
+                                   (h_d ? h_stride * some : 0) | (y_d ? y_stride * some : 0));
+    if (H <= kNormShort && H % 8) piece = std::min(piece, 8);  // (a warp's eights are whole)
+    const int threads = norm_threads(H);
+    // (fp32 rows of an odd number of 16-byte pieces have no whole eights: in the ring, whatever it takes)
+    if (piece == 16 && H > kNormShort) {
+        a.depth = norm_depth(threads, es, residual_d ? 2 : 1);
+        if (!a.depth && H % 8) a.depth = 1;
+    }
+    const NormKernel kern = norm_kernel_for(dtype, H, piece, codes_d != nullptr, threads, a.depth > 0);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!a.depth)
+        return launch(kern, dim3(H <= kNormShort ? ceil_div(T, 8) : T), dim3(threads), 0, s, true, a);
+    const size_t smem = (size_t)a.depth * norm_row_bytes(threads, es, 2);  // (room for both, whatever is given)
+    if (!allow_smem(reinterpret_cast<const void*>(kern), smem, kNormRingMost)) return MOE_ERR_CUDA;
+    return launch(kern, dim3(std::min(T, num_sms() * norm_per_sm(threads, false))), dim3(threads), smem, s, true, a);
 }
 
 size_t moe_rmsnorm_workspace_size(int32_t T, int32_t H)
 {
     if (check_norm(MOE_BF16, T, H) != MOE_OK) return 0;
-    const int parts = norm_parts(T, H, norm_per(T, H));
+    const int parts = norm_parts(T, H);
     return parts > 1 ? (size_t)parts * H * 4 : 0;
 }
 
@@ -707,24 +710,23 @@ moe_status moe_rmsnorm_backward(const void* dy_d, int32_t dtype, int64_t dy_stri
     a.dx_stride = dx_stride;
     a.dw = dweight_d;
     a.ws = static_cast<float*>(ws_d);
-    const int64_t row = (int64_t)H * es, some = T > 1 ? es : 0;
-    const bool vec = H % 8 == 0 && rows_vec(dy_d, row, dy_stride * some) && rows_vec(h_d, row, h_stride * some) &&
-                     rows_vec(dh_d, row, dh_d ? dh_stride * some : 0) && rows_vec(weight_d, row, 0) &&
-                     rows_vec(dx_d, row, dx_stride * some);
-    const int per = norm_per(T, H);
-    const bool one = norm_one(H, per);
-    a.parts = norm_parts(T, H, per);
-    const int threads = one ? 256 : norm_threads(H, per);
-    const NormBackKernel kern = norm_back_kernel_for(dtype, per, one, vec, threads);
+    const uint64_t some = T > 1 ? es : 0;
+    int piece = largest_unit(addr(dy_d) | addr(dh_d) | addr(h_d) | addr(weight_d) | addr(dx_d) |
+                                   (uint64_t)H * es | dy_stride * some | h_stride * some | dx_stride * some |
+                                   (dh_d ? dh_stride * some : 0));
+    if (H <= kNormShort && H % 8) piece = std::min(piece, 8);  // (a warp's eights are whole)
+    const int threads = norm_threads(H);
+    const NormBackKernel kern = norm_back_kernel_for(dtype, H, piece, threads);
+    a.parts = norm_parts(T, H);
     size_t smem = 0;
-    if (vec && !one) {
-        a.depth = norm_depth(threads, es);
-        smem = (size_t)a.depth * norm_row_bytes(threads, es);
+    if (piece == 16 && H > kNormShort) {
+        a.depth = norm_back_depth(threads, es);
+        smem = (size_t)a.depth * norm_row_bytes(threads, es, 3);
         if (!allow_smem(reinterpret_cast<const void*>(kern), smem, kNormRingMost)) return MOE_ERR_CUDA;
     }
-    const moe_status done = launch(kern, dim3(one ? ceil_div(a.parts, 8) : a.parts), dim3(threads), smem, s, true, a);
+    const moe_status done = launch(kern, dim3(a.parts), dim3(threads), smem, s, true, a);
     if (done != MOE_OK || !dweight_d || a.parts == 1) return done;
-    return launch(norm_parts_kernel, dim3(ceil_div(H, 32)), dim3(1024), 0, s, true, a.ws, a.parts, H, dweight_d);
+    return launch(norm_parts_kernel, dim3(ceil_div(H, 8)), dim3(256), 0, s, true, a.ws, a.parts, H, dweight_d);
 }
 
 moe_status moe_swiglu_mxfp8(const void* gate_up_d, int32_t dtype, int64_t stride, int32_t rows, int32_t inter,

@@ -527,7 +527,7 @@ using RouteBackKernel = void (*)(RouteBackArgs);
 RouteBackKernel route_back_kernel_for(int dtype, bool dense, int E);
 
 // ---- norm.cu: root-mean-square norm and its gradient
-constexpr int kNormMost = 16384;     // elements of a row: two eights in each of 1024 threads
+constexpr int kNormMost = 16384;     // elements of a row: 16 in each of 1024 threads
 struct NormArgs {
     const void* x;
     int64_t x_stride;     // (strides in elements)
@@ -544,10 +544,12 @@ struct NormArgs {
     uint8_t* codes;       // nullable, with sf
     uint8_t* sf;
     int layout, rule;
+    int depth;            // rows in flight of the kernel with a ring (1 to 3)
 };
 using NormKernel = void (*)(NormArgs);
-// per: eights of a thread (1 or 2); one: a warp per row; vec: 16-byte pieces
-NormKernel norm_kernel_for(int dtype, int per, bool one, bool vec);
+// piece: bytes that the rows' sizes, strides and addresses are multiples of; codes: there is an MXFP8 result;
+// ring: the kernel with a ring (long rows in 16-byte pieces)
+NormKernel norm_kernel_for(int dtype, int H, int piece, bool codes, int threads, bool ring);
 
 struct NormBackArgs {
     const void* dy;
@@ -567,26 +569,44 @@ struct NormBackArgs {
     int depth;            // rows in flight of the kernel with a ring (1 to 3)
 };
 using NormBackKernel = void (*)(NormBackArgs);
-NormBackKernel norm_back_kernel_for(int dtype, int per, bool one, bool vec, int threads);
+NormBackKernel norm_back_kernel_for(int dtype, int H, int piece, int threads);
 __global__ void norm_parts_kernel(const float* ws, int parts, int H, float* dw);
-__host__ __device__ constexpr bool norm_one(int H, int per) { return H <= 256 * per; }
-inline int norm_threads(int H, int per) { return div_up(div_up(H, 8), 32 * per) * 32; }
-// Blocks of an SM that the gradient's registers and rings are made for: up to 19 warps, or one block.  (8192 x 4096
-// bf16, main kernel alone: two blocks with three rows in flight 44 us, with one 63, three blocks 48.)
-inline int norm_per_sm(int threads) { return threads > 304 ? 1 : 608 / threads; }
-// Parts of the weight's gradient: the blocks (short rows: two blocks' warps) that 152 SMs hold.
-inline int norm_parts(int T, int H, int per)
+// Rows up to this have a warp each, eight a block; longer ones a block, 16 elements a thread.
+constexpr int kNormShort = 512;
+inline int norm_threads(int H) { return H <= kNormShort ? 256 : div_up(div_up(H, 16), 32) * 32; }
+// Blocks of an SM that the kernels with a ring have registers for: 24 warps (32 of larger blocks), the
+// gradient's 19, or one block.  (The gradient of 8192 x 4096 bf16, main kernel alone: two blocks with three rows
+// in flight 44 us, with one 63, three blocks 48.)
+inline int norm_per_sm(int threads, bool back)
 {
-    const int most = norm_one(H, per) ? 152 * 16 : 152 * norm_per_sm(norm_threads(H, per));
-    return T < most ? T : most;
+    const int most = back ? 608 : threads <= 256 ? 768 : 1024;
+    return threads > most / 2 ? 1 : most / threads;
 }
-// The ring: up to three rows of three tensors in a block's share of an SM's shared memory.
-inline int norm_row_bytes(int threads, int elem_bytes) { return 3 * 2 * threads * 8 * elem_bytes; }
-constexpr int kNormRingMost = 2 * 3 * 2 * 1024 * 8 * 2;   // of any launch: two rows of 1024 threads, 16-bit types
-inline int norm_depth(int threads, int elem_bytes)
+// Parts of the weight's gradient: the blocks that 152 SMs hold.
+inline int norm_parts(int T, int H)
 {
-    const int share = 233472 / norm_per_sm(threads) - 1024 - 256;  // (what the system and the sums take)
-    const int d = share / norm_row_bytes(threads, elem_bytes);
+    const int rows = H <= kNormShort ? div_up(T, 8) : T;
+    const int most = 152 * (H <= kNormShort ? 2 : norm_per_sm(norm_threads(H), true));
+    return rows < most ? rows : most;
+}
+// Rows of the ring.  The gradient's: up to three of three tensors, in a block's share of an SM's shared memory.
+constexpr int kNormRingMost = 3 * 1024 * 16 * 4;   // bytes of any launch: one row of 1024 threads, fp32
+inline int norm_row_bytes(int threads, int elem_bytes, int tensors) { return tensors * threads * 16 * elem_bytes; }
+inline int norm_back_depth(int threads, int elem_bytes)
+{
+    const int share = 233472 / norm_per_sm(threads, true) - 1024 - 256;  // (what the system and the sums take)
+    const int d = (share < kNormRingMost ? share : kNormRingMost) / norm_row_bytes(threads, elem_bytes, 3);
+    return d < 1 ? 1 : d > 3 ? 3 : d;
+}
+// The norm's own: as many as keep 48 KB of an SM's loads in flight (8192 x 4096 bf16: with the residual and all
+// results one row 50.5 us, two 57.6, y alone one row 28.8, two 24.7, three 26.5).  0, where one row of each
+// block is over 64 KB: the kernel that loads a row into registers, one block a row (the first with fp32: 86.3 us,
+// with the ring 98.4; of bf16 53.1 and 34.8).
+inline int norm_depth(int threads, int elem_bytes, int tensors)
+{
+    const int row = norm_row_bytes(threads, elem_bytes, tensors) * norm_per_sm(threads, false);
+    if (row > 64 * 1024) return 0;
+    const int d = 48 * 1024 / row;
     return d < 1 ? 1 : d > 3 ? 3 : d;
 }
 

@@ -143,10 +143,10 @@ def test_gradient(T, H, dtype, pad, off):
             slack = r64[:, None] * (4 * 2.0 ** -24 * np.abs(d64 * wf) + 36 * 2.0 ** -24 * x * mean)
             slack = slack + 2.0 ** -23 * (np.abs(e64) + r64[:, None] * (np.abs(d64 * wf) + x * mean))
             assert np.all(ops_ref.rounded_ok(f64(dx), want, slack, dtype))
-            # the rows of a part, then the parts by 32 threads: at least 152 parts with their share of the
-            # rows, or as many as the workspace holds
+            # the rows of a part (at least 152 parts with their share of the rows, or as many as the
+            # workspace holds), short rows' eight warps, then the parts by 32 threads
             most = max(1, moe.moe_rmsnorm_workspace_size(T, H) // (4 * H))
-            n = -(-T // 152) + -(-most // 32) + 5 + 2
+            n = -(-T // 152) + 8 + -(-most // 32) + 5 + 2
             assert np.all(np.abs(f64(dw) - want_w) <= n * 2.0 ** -24 * (np.abs(d64) * x).sum(0) + 1e-37)
             again = torch.empty_like(dw)
             moe.moe_rmsnorm_backward(dy, h, weight, rstd, dx, again, ws, dh=extra)

@@ -35,8 +35,8 @@ ROUTE_BACK = dict(l=P, dtype=0, stride=64, ids=P, dw=P, T=4, E=64, k=4, score=0,
                   dstride=64, stream=None)
 NORM = dict(x=P, dtype=0, xs=64, r=P, rs=64, w=P, eps=1e-6, T=4, H=64, h=P, hs=64, y=P, ys=64, rstd=P, codes=P,
             sf=P, layout=1, rule=1, stream=None)
-NORM_BACK = dict(dy=P, dtype=0, dys=64, dh=P, dhs=64, h=P, hs=64, w=P, rstd=P, T=4, H=64, dx=P, dxs=64, dw=P,
-                 ws=P, ws_bytes=4 * 64 * 4, stream=None)
+NORM_BACK = dict(dy=P, dtype=0, dys=1024, dh=P, dhs=1024, h=P, hs=1024, w=P, rstd=P, T=4, H=1024, dx=P, dxs=1024,
+                 dw=P, ws=P, ws_bytes=4 * 1024 * 4, stream=None)
 QUANT = dict(x=P, dtype=0, batch=1, rows=4, cols=64, rs=64, bs=0, rule=0, perm=None, codes=P, sf=P, layout=1,
              values=None, stream=None)
 GATE = dict(gu=P, dtype=0, stride=128, rows=4, inter=64, perm=None, rule=1, codes=P, sf=P, layout=1, ck=P,
@@ -63,7 +63,7 @@ INVALID = [
         dict(codes=ODD), dict(sf=ODD), dict(h=None, y=None, rstd=None, codes=None, sf=None)]),
     ("moe_rmsnorm_backward", NORM_BACK, [
         dict(dtype=3), dict(T=-1), dict(H=0), dict(dy=None), dict(h=None), dict(rstd=None), dict(dx=None),
-        dict(dys=63), dict(hs=63), dict(dxs=63), dict(dhs=63), dict(dy=BYTE), dict(dh=BYTE), dict(h=BYTE),
+        dict(dys=1023), dict(hs=1023), dict(dxs=1023), dict(dhs=1023), dict(dy=BYTE), dict(dh=BYTE), dict(h=BYTE),
         dict(w=BYTE), dict(dx=BYTE), dict(dw=HALF), dict(rstd=HALF), dict(ws=None), dict(ws=ODD)]),
     ("moe_quant_mxfp8", QUANT, [
         dict(dtype=3), dict(batch=-1), dict(rows=-1), dict(cols=0), dict(rule=2), dict(layout=2), dict(x=None),
@@ -124,14 +124,14 @@ def test_nothing_to_do(lib, name, defaults, kw):
 
 def test_a_workspace_that_is_too_small(lib):
     assert call(lib, "moe_rmsnorm_backward", NORM_BACK, ws_bytes=0, ws=None) == moe.MOE_ERR_WORKSPACE
-    assert call(lib, "moe_rmsnorm_backward", NORM_BACK, ws_bytes=4 * 64 * 4 - 1) == moe.MOE_ERR_WORKSPACE
+    assert call(lib, "moe_rmsnorm_backward", NORM_BACK, ws_bytes=4 * 1024 * 4 - 1) == moe.MOE_ERR_WORKSPACE
 
 
 def test_workspace_sizes():
     size = moe.moe_rmsnorm_workspace_size
     assert size(1, 64) == 0 and size(0, 64) == 0 and size(-1, 64) == 0 and size(4, 0) == 0 and size(4, 16385) == 0
-    assert size(4, 64) == 4 * 64 * 4
-    for T in (2, 1000, 10 ** 6, BIG):
+    assert size(4, 1024) == 4 * 1024 * 4 and size(8, 64) == 0 and size(9, 64) == 2 * 64 * 4
+    for T in (9, 1000, 10 ** 6, BIG):
         for H in (1, 512, 513, 4096, 16384):
             assert 0 < size(T, H) <= 32 << 20
 
