@@ -608,10 +608,12 @@ def moe_grouped_gemm_mxfp8(a_codes, a_sf, counts, offsets, w_codes, w_sf, out, s
         _check(st, "moe_grouped_gemm_mxfp8")
 
 
-def _rows(t, shape, dt):
-    """Whether t is rows of a shape and moe_dtype with contiguous columns."""
-    return (t.shape == shape and _DTYPES[t.dtype] == dt and
-            (t.stride(1) == 1 or shape[1] == 1 or shape[0] == 0))
+def _row_stride(t, shape, dt, dev):
+    """The row stride of a tensor of rows of this shape, moe_dtype and device with contiguous columns, or -1."""
+    if t.shape != shape or _DTYPES[t.dtype] != dt or t.get_device() != dev:
+        return -1
+    stride, one = t.stride()
+    return stride if one == 1 or shape[1] == 1 or shape[0] == 0 else -1
 
 
 def _flat(t, n, dtype):
@@ -651,16 +653,15 @@ def moe_route_scores_backward(logits, topk_ids, dtopk_w, dlogits, score=MOE_SCOR
     stride, one = logits.stride()
     dt = _DTYPES[logits.dtype]
     if not (Tk == T and (T | E | k) <= _MOST and (one == 1 or E == 1 or T == 0) and
-            topk_ids.dtype is _I32 and topk_ids.is_contiguous() and _flat(dtopk_w, T * k, _F32) and
-            _rows(dlogits, shape, dt)):
+            topk_ids.dtype is _I32 and topk_ids.is_contiguous() and _flat(dtopk_w, T * k, _F32)):
         _refuse("moe_route_scores_backward")
     dev, handle = _place(stream)
-    if not (dev == logits.get_device() == topk_ids.get_device() == dtopk_w.get_device() ==
-            dlogits.get_device()):
+    ds = _row_stride(dlogits, shape, dt, dev)
+    if not (ds >= 0 and dev == logits.get_device() == topk_ids.get_device() == dtopk_w.get_device()):
         _refuse("moe_route_scores_backward")
     st = (_lib or load()).moe_route_scores_backward(
         logits.data_ptr(), dt, stride, topk_ids.data_ptr(), dtopk_w.data_ptr(), T, E, k, score,
-        1 if renormalise else 0, scale, dlogits.data_ptr(), dlogits.stride(0), handle)
+        1 if renormalise else 0, scale, dlogits.data_ptr(), ds, handle)
     if st:
         _check(st, "moe_route_scores_backward")
 
@@ -681,14 +682,12 @@ def moe_rmsnorm(x, weight, eps, residual=None, h=None, y=None, rstd=None, codes=
         ok = ok and _flat(weight, H, xt) and weight.get_device() == dev
         pw = weight.data_ptr()
     if residual is not None:
-        ok = ok and _rows(residual, shape, dt) and residual.get_device() == dev
-        pr, rs = residual.data_ptr(), residual.stride(0)
+        pr, rs = residual.data_ptr(), _row_stride(residual, shape, dt, dev)
     if h is not None:
-        ok = ok and _rows(h, shape, dt) and h.get_device() == dev
-        ph, hs = h.data_ptr(), h.stride(0)
+        ph, hs = h.data_ptr(), _row_stride(h, shape, dt, dev)
     if y is not None:
-        ok = ok and _rows(y, shape, dt) and y.get_device() == dev
-        py, ys = y.data_ptr(), y.stride(0)
+        py, ys = y.data_ptr(), _row_stride(y, shape, dt, dev)
+    ok = ok and rs >= 0 and hs >= 0 and ys >= 0
     if rstd is not None:
         ok = ok and _flat(rstd, T, _F32) and rstd.get_device() == dev
         ps = rstd.data_ptr()
@@ -718,19 +717,18 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, ws=None, dh=None
     T, H = shape
     stride, one = dy.stride()
     dt = _DTYPES[dy.dtype]
-    if not ((T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and _rows(h, shape, dt) and
-            _rows(dx, shape, dt) and (dh is None or _rows(dh, shape, dt)) and
-            (weight is None or _flat(weight, H, dy.dtype)) and _flat(rstd, T, _F32) and
-            (dweight is None or _flat(dweight, H, _F32)) and (ws is None or ws.is_contiguous())):
-        _refuse("moe_rmsnorm_backward")
     dev, handle = _place(stream)
-    if not (dev == dy.get_device() == h.get_device() == dx.get_device() == rstd.get_device() and
-            (dh is None or dh.get_device() == dev) and (weight is None or weight.get_device() == dev) and
-            (dweight is None or dweight.get_device() == dev) and (ws is None or ws.get_device() == dev)):
+    es = 0 if dh is None else _row_stride(dh, shape, dt, dev)
+    hs, xs = _row_stride(h, shape, dt, dev), _row_stride(dx, shape, dt, dev)
+    if not ((T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and es >= 0 and hs >= 0 and xs >= 0 and
+            dev == dy.get_device() == rstd.get_device() and _flat(rstd, T, _F32) and
+            (weight is None or (_flat(weight, H, dy.dtype) and weight.get_device() == dev)) and
+            (dweight is None or (_flat(dweight, H, _F32) and dweight.get_device() == dev)) and
+            (ws is None or (ws.is_contiguous() and ws.get_device() == dev))):
         _refuse("moe_rmsnorm_backward")
     st = (_lib or load()).moe_rmsnorm_backward(
-        dy.data_ptr(), dt, stride, _p(dh), 0 if dh is None else dh.stride(0), h.data_ptr(), h.stride(0),
-        _p(weight), rstd.data_ptr(), T, H, dx.data_ptr(), dx.stride(0), _p(dweight), _p(ws),
+        dy.data_ptr(), dt, stride, _p(dh), es, h.data_ptr(), hs,
+        _p(weight), rstd.data_ptr(), T, H, dx.data_ptr(), xs, _p(dweight), _p(ws),
         0 if ws is None else ws.nbytes, handle)
     if st:
         _check(st, "moe_rmsnorm_backward")

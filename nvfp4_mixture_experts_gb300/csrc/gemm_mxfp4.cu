@@ -1,5 +1,5 @@
 // The grouped MXFP4 product on CTA pairs: out[r][n] = sum_i A[r][i] W_g[n][i] over the rows r of
-// each group g.
+// each group g; and (A8) that of MXFP8 rows with MXFP4 weights.
 //
 // One tile is 256 weight rows (the MMA's M side: 128 in each CTA of the pair) by up to 256 rows of
 // one group (its N side, in steps of 32: a group costs round_up(rows, 32) columns, where rows on
@@ -30,6 +30,17 @@
 // would have to be written, counted and added up, through words that are zero before the call or
 // CTAs that wait for one another, for 2 us at most.  Fetching the last tiles' weights into L2 during
 // the tiles before gains nothing (13.9 us where 13.4 without).
+//
+// A8.  kind::mxf8f6f4 reads 16 weights of 4 bits as 8 bytes and 8 of padding, which the tensor map spreads
+// them to on their way into shared memory (its bytes are counted packed), so a k-stage of 256 elements takes
+// 64 KB of a CTA's shared memory instead of 32 and its eight MMAs 0.47 us of the tensor pipe instead of 0.26;
+// the MMAs round the running sum towards zero, by a unit of fp32's last place each at most.  Few rows are
+// bound by memory as above (64 tokens' gate_up 217 - 225 us, 6.5 TB/s; one row, K 16384, 18.4 us).  Many rows
+// are not: 320 groups of 205 rows x 2560 x 4096 take 489 - 495 us, where the loads alone take 405 (three stages
+// hold 52 KB of weights in flight an SM, and L2 gives 12.7 TB/s), the MMAs and the rows' loads without the
+// weights 388, and with weights that L2 holds 422; asking L2 for weights some stages ahead gains nothing.  In
+// a loop of seconds the power limit lowers the clock, 558 - 580 us for 8192 tokens.  One group of 8192, N and K
+// 4096: 80 us, 3.4 PFLOP/s.
 //
 // TMEM (all 512 columns, so the allocation starts at column 0): two accumulators, of the even
 // tiles at column 0 upwards, of the odd tiles ending at column 448; two slots of a stage's scales

@@ -1,5 +1,12 @@
 // silu(gate) * up as an MXFP8 matrix, with a checkpoint of gate and up in 8 bits, and the gradient that
 // reads the checkpoint.
+//
+// A lane has 16 columns, half of a block of 32, so that a block's scale takes one exchange and what a lane
+// finds out about its row is paid for by 16 results; products and sums are of two numbers an instruction.
+// 65536 rows of I 1280 bf16: forward 99 us with the checkpoint (6.0 TB/s, memory) and 72 without; the
+// gradient 102 us (5.0 TB/s), bound by its instructions (0.67 of the issue slots; 250 for 8 columns of 32
+// lanes; with 8 columns a lane 430, 162 us).  Held to 64 registers: four blocks an SM (74 registers, three:
+// 117 us).
 #include "mx.cuh"
 
 namespace moe {
