@@ -625,8 +625,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
             if (!chosen) q = 0.0f;
             const float sum = warp_sum(q);
             q = sum > 0.0f ? q / sum : sum;
-            const float mean = warp_sum(chosen ? g * q : 0.0f);
-            g = chosen ? q * (g - mean) * f : 0.0f;
+            // g - r as the sum of q_i (g - g_i): where one weight is nearly all, g - r cancels
+            float d = 0.0f;
+            for (int i = 0; i < a.k; ++i)
+                d = fmaf(__shfl_sync(kAll, q, i), g - __shfl_sync(kAll, g, i), d);
+            g = chosen ? q * d * f : 0.0f;
         } else {
             const float s = 1.0f / (1.0f + expf(-v));
             g = chosen ? g * s / (1.0f + expf(v)) : 0.0f;

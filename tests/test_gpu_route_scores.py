@@ -248,6 +248,21 @@ def test_gradient_against_differences():
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_gradient_where_one_weight_is_nearly_all(kind):
+    """Renormalised weights of 1 - 1e-7 and 1e-7: the differences of their gradients, not what is left of
+    them."""
+    l = torch.tensor([[16.0, -0.1, 0.3, 1.0], [-2.0, -18.0, -19.0, -17.5]], device="cuda")
+    ids = torch.tensor([[0, 1, 2], [0, 1, 3]], dtype=torch.int32, device="cuda")
+    dw = torch.tensor([[0.9, -0.4, 0.3], [-1.0, 0.7, 0.2]], device="cuda")
+    out = torch.empty_like(l)
+    moe.moe_route_scores_backward(l, ids, dw, out, score=KIND[kind])
+    want = ref.route_grad(l.double().cpu().numpy(), ids.cpu().numpy(), dw.double().cpu().numpy(), kind, True, 1.0)
+    # each term within W_TOL of itself; of a sigmoid 1 - s is one more (1 / (1 + e^l), 2^-22)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= 3 * (W_TOL + 2.0 ** -22) * np.abs(dw.double().cpu().numpy()).max() *
+                  np.maximum(np.abs(want) / 0.5, 1e-12))
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_gradient_of_the_same_expert_twice_and_of_ids_out_of_range(kind, renorm):
     rng = np.random.default_rng(3)
