@@ -669,7 +669,7 @@ moe_status moe_rmsnorm(const void* x_d, int32_t dtype, int64_t x_stride, const v
 size_t moe_rmsnorm_workspace_size(int32_t T, int32_t H)
 {
     if (check_norm(MOE_BF16, T, H) != MOE_OK) return 0;
-    const int parts = norm_parts(T, H);
+    const int parts = norm_parts(T, H, H <= kNormShort);  // (no fewer than of warps, where those have longer rows)
     return parts > 1 ? (size_t)parts * H * 4 : 0;
 }
 
@@ -711,20 +711,20 @@ moe_status moe_rmsnorm_backward(const void* dy_d, int32_t dtype, int64_t dy_stri
     a.dw = dweight_d;
     a.ws = static_cast<float*>(ws_d);
     const uint64_t some = T > 1 ? es : 0;
-    int piece = largest_unit(addr(dy_d) | addr(dh_d) | addr(h_d) | addr(weight_d) | addr(dx_d) |
+    const int piece = largest_unit(addr(dy_d) | addr(dh_d) | addr(h_d) | addr(weight_d) | addr(dx_d) |
                                    (uint64_t)H * es | dy_stride * some | h_stride * some | dx_stride * some |
                                    (dh_d ? dh_stride * some : 0));
-    if (H <= kNormShort && H % 8) piece = std::min(piece, 8);  // (a warp's eights are whole)
     const int threads = norm_threads(H);
+    const bool one = norm_back_one(H, piece, es);
     const NormBackKernel kern = norm_back_kernel_for(dtype, H, piece, threads);
-    a.parts = norm_parts(T, H);
+    a.parts = norm_parts(T, H, one);
     size_t smem = 0;
-    if (piece == 16 && H > kNormShort) {
-        a.depth = norm_back_depth(threads, es);
-        smem = (size_t)a.depth * norm_row_bytes(threads, es, 3);
+    if (piece == 16) {
+        a.depth = norm_back_depth(H, es, one);
+        smem = (size_t)a.depth * norm_back_row_bytes(H, es, one);
         if (!allow_smem(reinterpret_cast<const void*>(kern), smem, kNormRingMost)) return MOE_ERR_CUDA;
     }
-    const moe_status done = launch(kern, dim3(a.parts), dim3(threads), smem, s, true, a);
+    const moe_status done = launch(kern, dim3(a.parts), dim3(one ? 256 : threads), smem, s, true, a);
     if (done != MOE_OK || !dweight_d || a.parts == 1) return done;
     return launch(norm_parts_kernel, dim3(ceil_div(H, 8)), dim3(256), 0, s, true, a.ws, a.parts, H, dweight_d);
 }

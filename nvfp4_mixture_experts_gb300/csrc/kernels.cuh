@@ -582,20 +582,31 @@ inline int norm_per_sm(int threads, bool back)
     const int most = back ? 608 : threads <= 256 ? 768 : 1024;
     return threads > most / 2 ? 1 : most / threads;
 }
-// Parts of the weight's gradient: the blocks that 152 SMs hold.
-inline int norm_parts(int T, int H)
+// The gradient: whether a row has a warp (16-bit types in 16-byte pieces up to 32 elements a lane), and the parts
+// of the weight's: the blocks that 152 SMs hold.
+inline bool norm_back_one(int H, int piece, int elem_bytes)
 {
-    const int rows = H <= kNormShort ? div_up(T, 8) : T;
-    const int most = 152 * (H <= kNormShort ? 2 : norm_per_sm(norm_threads(H), true));
+    return H <= kNormShort || (piece == 16 && elem_bytes == 2 && H <= 2 * kNormShort);
+}
+inline int norm_parts(int T, int H, bool one)
+{
+    const int rows = one ? div_up(T, 8) : T;
+    const int most = 152 * (one ? 2 : norm_per_sm(norm_threads(H), true));
     return rows < most ? rows : most;
 }
 // Rows of the ring.  The gradient's: up to three of three tensors, in a block's share of an SM's shared memory.
 constexpr int kNormRingMost = 3 * 1024 * 16 * 4;   // bytes of any launch: one row of 1024 threads, fp32
 inline int norm_row_bytes(int threads, int elem_bytes, int tensors) { return tensors * threads * 16 * elem_bytes; }
-inline int norm_back_depth(int threads, int elem_bytes)
+inline int norm_back_row_bytes(int H, int elem_bytes, bool one)
 {
-    const int share = 233472 / norm_per_sm(threads, true) - 1024 - 256;  // (what the system and the sums take)
-    const int d = (share < kNormRingMost ? share : kNormRingMost) / norm_row_bytes(threads, elem_bytes, 3);
+    if (!one) return norm_row_bytes(norm_threads(H), elem_bytes, 3);
+    return norm_row_bytes(256, H <= kNormShort ? elem_bytes : 4, 3);   // of eight warps
+}
+inline int norm_back_depth(int H, int elem_bytes, bool one)
+{
+    // (what the system and the sums take)
+    const int share = 233472 / (one ? 2 : norm_per_sm(norm_threads(H), true)) - 1024 - 256;
+    const int d = (share < kNormRingMost ? share : kNormRingMost) / norm_back_row_bytes(H, elem_bytes, one);
     return d < 1 ? 1 : d > 3 ? 3 : d;
 }
 // The norm's own: as many as keep 48 KB of an SM's loads in flight (8192 x 4096 bf16: with the residual and all

@@ -136,15 +136,20 @@ struct Piece {
     }
 };
 
-// The block's ring: `depth` rows of TENSORS tensors, [depth][TENSORS][kPer][threads] pieces.
-template <typename T, int TENSORS>
+// The block's ring: `depth` rows (ONE: of each of its warps) of TENSORS tensors, [depth][TENSORS][PER][threads]
+// pieces.
+template <typename T, int TENSORS, int PER, bool ONE>
 struct Ring {
-    static constexpr int kPer = Piece<T>::kPer;
     uint4* at;
     int depth, pieces;   // rows; pieces of a row
+    // piece k of this thread
+    static __device__ __forceinline__ int piece(int k)
+    {
+        return ONE ? (int)(threadIdx.x & 31) + 32 * k : (int)threadIdx.x + k * (int)blockDim.x;
+    }
     __device__ __forceinline__ uint4* place(int slot, int x, int k) const
     {
-        return at + ((slot * TENSORS + x) * kPer + k) * blockDim.x + threadIdx.x;
+        return at + ((slot * TENSORS + x) * PER + k) * blockDim.x + threadIdx.x;
     }
     // Copies this thread's pieces of a row (null: of no row), and counts them as one group.
     __device__ __forceinline__ void copy(int slot, const T* const (&from)[TENSORS]) const
@@ -153,8 +158,8 @@ struct Ring {
         for (int x = 0; x < TENSORS; ++x) {
             if (!from[x]) continue;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int c = threadIdx.x + k * blockDim.x;
+            for (int k = 0; k < PER; ++k) {
+                const int c = piece(k);
                 if (c < pieces)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(place(slot, x, k))),
                                  "l"(reinterpret_cast<const uint4*>(from[x]) + c)
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) norm_ring_kernel(NormAr
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
-    const Ring<T, 2> ring{s_ring, a.depth, a.H / kOf};
+    const Ring<T, 2, kPer, false> ring{s_ring, a.depth, a.H / kOf};
     const int blocks = a.H >> 5, KA = (blocks + 3) >> 2;
     auto copy = [&](int slot, int64_t row) {
         const bool in = row < a.T;
@@ -478,94 +483,106 @@ __global__ void __launch_bounds__(NT, NT == 320 ? 2 : 1) norm_back_kernel(NormBa
     }
 }
 
-// The same, a block a row, the rows to come in the ring.
-template <typename T, int NT>
+// The same with the rows to come in the ring, PER pieces a thread.
+template <typename T, int PER, bool ONE, int NT>
 __global__ void __launch_bounds__(NT, NT == 256 ? 2 : 1) norm_back_ring_kernel(NormBackArgs a)
 {
     using P = Piece<T>;
-    constexpr int kPer = P::kPer, kOf = P::kOf;
+    constexpr int kOf = P::kOf;
     extern __shared__ uint4 s_ring[];
     __shared__ float s_part[2][32];
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, nt = blockDim.x, part = blockIdx.x;
-    const Ring<T, 3> ring{s_ring, a.depth, a.H / kOf};
+    const int warp = threadIdx.x >> 5;
+    const int64_t first = ONE ? blockIdx.x * 8 + warp : blockIdx.x, step = ONE ? a.parts * 8 : a.parts;
+    const Ring<T, 3, PER, ONE> ring{s_ring, a.depth, a.H / kOf};
     auto copy = [&](int slot, int64_t row) {
         const bool in = row < a.T;
         ring.copy(slot, {in ? static_cast<const T*>(a.dy) + row * a.dy_stride : nullptr,
                          in ? static_cast<const T*>(a.h) + row * a.h_stride : nullptr,
                          in && a.dh ? static_cast<const T*>(a.dh) + row * a.dh_stride : nullptr});
     };
-    for (int d = 0; d < a.depth; ++d) copy(d, part + (int64_t)d * a.parts);
-    P acc[kPer], w[kPer];
+    for (int d = 0; d < a.depth; ++d) copy(d, first + d * step);
+    P acc[PER];
+    uint4 w[PER] = {};
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
+    for (int k = 0; k < PER; ++k) {
         acc[k].zero();
-        w[k].zero();
-        if (a.w && tid + k * nt < ring.pieces) w[k].from(static_cast<const uint4*>(a.w)[tid + k * nt]);
-        if (!a.w)
-#pragma unroll
-            for (int i = 0; i < kOf / 2; ++i) w[k].v[i] = F2(1.0f);
+        if (a.w && ring.piece(k) < ring.pieces) w[k] = static_cast<const uint4*>(a.w)[ring.piece(k)];
     }
     int buf = 0, slot = 0, at = 0;
-    float rstds = 0.0f;   // of 32 of the block's rows, one a lane (a load a row would be waited for each time)
-    for (int64_t row = part; row < a.T; row += a.parts, at = (at + 1) & 31) {
+    float rstds = 0.0f;   // of 32 of the rows to come, one a lane (a load a row would be waited for each time)
+    for (int64_t row = first; row < a.T; row += step, at = (at + 1) & 31) {
         if (at == 0) {
-            const int64_t mine = row + (int64_t)(tid & 31) * a.parts;
+            const int64_t mine = row + (int64_t)(threadIdx.x & 31) * step;
             rstds = mine < a.T ? a.rstd[mine] : 0.0f;
         }
         const float rstd = __shfl_sync(0xffffffffu, rstds, at);
         ring.wait();
-        P d[kPer], x[kPer];
+        P d[PER], x[PER];
         F2 dot(0.0f);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
+        for (int k = 0; k < PER; ++k) {
             d[k].zero();
             x[k].zero();
-            if (tid + k * nt >= ring.pieces) continue;
+            if (ring.piece(k) >= ring.pieces) continue;
             d[k].from(*ring.place(slot, 0, k));
             x[k].from(*ring.place(slot, 1, k));
+            P q;
+            q.from(w[k]);
 #pragma unroll
             for (int i = 0; i < kOf / 2; ++i) {
                 x[k].v[i] = x[k].v[i] * F2(rstd);
                 acc[k].v[i] = fma2(d[k].v[i], x[k].v[i], acc[k].v[i]);
-                d[k].v[i] = d[k].v[i] * w[k].v[i];
+                if (a.w) d[k].v[i] = d[k].v[i] * q.v[i];
                 dot = fma2(d[k].v[i], x[k].v[i], dot);
             }
         }
         const float2 both = dot.get();
-        const float mean = row_sum<false>(both.x + both.y, s_part, buf) / (float)a.H;
+        const float mean = row_sum<ONE>(both.x + both.y, s_part, buf) / (float)a.H;
         buf ^= 1;
         const F2 less(-mean), r(rstd);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            if (tid + k * nt >= ring.pieces) break;
+        for (int k = 0; k < PER; ++k) {
+            if (ring.piece(k) >= ring.pieces) break;
             P q;
             q.zero();
             if (a.dh) q.from(*ring.place(slot, 2, k));
 #pragma unroll
             for (int i = 0; i < kOf / 2; ++i) q.v[i] = fma2(r, fma2(x[k].v[i], less, d[k].v[i]), q.v[i]);
-            reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.dx_stride)[tid + k * nt] = q.to();
+            reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.dx_stride)[ring.piece(k)] = q.to();
         }
-        copy(slot, row + (int64_t)a.depth * a.parts);   // (over what this thread has read)
+        copy(slot, row + a.depth * step);   // (over what this thread has read)
         slot = slot + 1 == a.depth ? 0 : slot + 1;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!a.dw) return;
-    float* out = a.parts == 1 ? a.dw : a.ws + (int64_t)part * a.H;
+    float* out = a.parts == 1 ? a.dw : a.ws + (int64_t)blockIdx.x * a.H;
+    float* s_dw = reinterpret_cast<float*>(s_ring);   // ONE: [8][H], in the ring's place
+    if constexpr (ONE) __syncthreads();
+    float* to = ONE ? s_dw + warp * a.H : out;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int c = tid + k * nt;
+    for (int k = 0; k < PER; ++k) {
+        const int c = ring.piece(k);
         if (c >= ring.pieces) break;
 #pragma unroll
         for (int i = 0; i < kOf / 2; ++i)   // (dw itself need not be aligned to more than an element)
-            if (a.parts == 1) {
+            if (!ONE && a.parts == 1) {
                 const float2 v = acc[k].v[i].get();
-                out[kOf * c + 2 * i] = v.x;
-                out[kOf * c + 2 * i + 1] = v.y;
+                to[kOf * c + 2 * i] = v.x;
+                to[kOf * c + 2 * i + 1] = v.y;
             } else {
-                reinterpret_cast<uint64_t*>(out)[kOf / 2 * c + i] = acc[k].v[i].v;
+                reinterpret_cast<uint64_t*>(to)[kOf / 2 * c + i] = acc[k].v[i].v;
             }
+    }
+    if constexpr (ONE) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.H; c += 256) {
+            float v = s_dw[c];
+#pragma unroll
+            for (int q = 1; q < 8; ++q) v += s_dw[q * a.H + c];
+            out[c] = v;
+        }
     }
 }
 
@@ -621,7 +638,6 @@ NormKernel norm_kernel_for(int dtype, int H, int piece, bool codes, int threads,
 template <typename T, int PER, bool ONE, int NT>
 static NormBackKernel norm_back_of(int piece)
 {
-    if (ONE && piece == 16) return norm_back_kernel<T, PER, ONE, ONE ? kVec : kApart, NT>;
     if (sizeof(T) == 2 && piece >= 4) return norm_back_kernel<T, PER, ONE, sizeof(T) == 2 ? kPairs : kApart, NT>;
     return norm_back_kernel<T, PER, ONE, kApart, NT>;
 }
@@ -629,11 +645,15 @@ static NormBackKernel norm_back_of(int piece)
 template <typename T>
 static NormBackKernel norm_back_of(int H, int piece, int threads)
 {
+    constexpr int kPer = Piece<T>::kPer;
+    if (piece == 16) {
+        if (H <= kNormShort) return norm_back_ring_kernel<T, kPer, true, 256>;
+        if (sizeof(T) == 2 && H <= 2 * kNormShort) return norm_back_ring_kernel<T, 4, true, 256>;
+        return threads <= 256 ? norm_back_ring_kernel<T, kPer, false, 256>
+             : threads <= 512 ? norm_back_ring_kernel<T, kPer, false, 512> : norm_back_ring_kernel<T, kPer, false, 1024>;
+    }
     if (H <= 256) return norm_back_of<T, 1, true, 256>(piece);
-    if (H <= 512) return norm_back_of<T, 2, true, 256>(piece);
-    if (piece == 16)
-        return threads <= 256 ? norm_back_ring_kernel<T, 256>
-             : threads <= 512 ? norm_back_ring_kernel<T, 512> : norm_back_ring_kernel<T, 1024>;
+    if (H <= kNormShort) return norm_back_of<T, 2, true, 256>(piece);
     return threads <= 320 ? norm_back_of<T, 2, false, 320>(piece) : norm_back_of<T, 2, false, 1024>(piece);
 }
 
