@@ -4,12 +4,12 @@
 // Rows of over 512 elements in 16-byte pieces have a block each at a time (16 elements a thread), and each
 // SM as many blocks as its registers hold: the rows to come are copied into a ring in shared memory, where a
 // thread reads what it copied itself, so that no barrier is needed for them and no registers hold them while
-// the row's sum waits for all of its threads.  Short rows have a warp each; rows that are in no 16-byte
-// pieces are read an element, or two 16-bit ones, a lane at a time.
+// the row's sum waits for all of its threads.  Short rows (the gradient's up to 1024 16-bit elements) have a
+// warp each; rows that are in no 16-byte pieces are read an element, or two 16-bit ones, a lane at a time.
 //
 // All are bound by memory, long rows from 0.8 of the measured copy rate up.  8192 x 4096 bf16 with residual, h,
 // y and MXFP8 50 us (6.0 TB/s; fp32 86), y alone 25 us, its gradient 46 us (5.8 TB/s; fp32 83, 6.5 TB/s); 16384 x
-// 512 15 and 16 us.  What is in no 16 bytes is bound by its instructions: 8192 x 4097 bf16 72 us with residual,
+// 512 15 us each way.  What is in no 16 bytes is bound by its instructions: 8192 x 4097 bf16 72 us with residual,
 // h and y, its gradient 101.
 #include "mx.cuh"
 
