@@ -9,7 +9,7 @@ import torch
 from . import (MOE_GROUP_MAX, MOE_SCORE_SOFTMAX, MOE_SF_TILED, moe_mxfp4_scale_bytes, moe_rmsnorm,
                moe_rmsnorm_backward, moe_rmsnorm_workspace_size, moe_route_scores,
                moe_route_scores_backward)
-from .experts import _FirstOrder
+from .experts import _FirstOrder, as_rows
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, eight=False):
@@ -25,13 +25,13 @@ class _Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, eps, eight):
         T, H = x.shape
-        x = x if x.stride(1) == 1 else x.contiguous()
+        x = as_rows(x)
         y = torch.empty(T, H, dtype=x.dtype, device=x.device)
         rstd = torch.empty(T, dtype=torch.float32, device=x.device)
         w = weight.detach().to(x.dtype).contiguous()
         h = codes = sf = None
         if residual is not None:
-            residual = residual if residual.stride(1) == 1 else residual.contiguous()
+            residual = as_rows(residual)
             h = torch.empty_like(y)
         if eight:
             codes = torch.empty(T, H, dtype=torch.uint8, device=x.device)
@@ -57,7 +57,6 @@ class _Norm(torch.autograd.Function):
     def gradients(ctx, dy, dh):
         h, w, rstd = ctx.saved_tensors
         T, H = h.shape
-        rows = lambda t: t if t is None or t.stride(1) == 1 else t.contiguous()  # noqa: E731
         if dy is None:   # y is not used: its gradient is zero
             dy = torch.zeros(T, H, dtype=h.dtype, device=h.device)
         dx, dw = torch.empty(T, H, dtype=h.dtype, device=h.device), None
@@ -65,7 +64,8 @@ class _Norm(torch.autograd.Function):
         if ctx.needs_input_grad[2]:
             dw = torch.empty(H, dtype=torch.float32, device=h.device)
             ws = torch.empty(moe_rmsnorm_workspace_size(T, H), dtype=torch.uint8, device=h.device)
-        moe_rmsnorm_backward(rows(dy), h, w, rstd, dx, dw, ws, dh=rows(dh))
+        moe_rmsnorm_backward(as_rows(dy), h, w, rstd, dx, dw, ws,
+                             dh=None if dh is None else as_rows(dh))
         return dx, torch.zeros(H, dtype=ctx.weight_dtype, device=h.device) if dw is None else dw.to(ctx.weight_dtype)
 
 
@@ -80,7 +80,7 @@ class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, bias, score, num_groups, topk_groups, group_score, renormalise, scale):
         T = logits.shape[0]
-        logits = logits if logits.stride(1) == 1 else logits.contiguous()
+        logits = as_rows(logits)
         ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
         w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
         moe_route_scores(logits, ids, w, bias=bias, score=score, num_groups=num_groups,
@@ -105,7 +105,8 @@ class MXBlock:
     """h = x + residual; y = rms_norm(h); out = experts(y, route(y router^T)) [+ shared(y)].
 
     norm_weight [H] and router [num_experts, H] are the caller's leaves (any float type); experts: an
-    MXExperts; shared: an MXShared or None; the other arguments are route's."""
+    MXExperts (of a shard: out is its partial sum); shared: an MXShared (of several shards one has it) or
+    None; the other arguments are route's."""
 
     def __init__(self, norm_weight, router, experts, top_k, shared=None, eps=1e-6, **routing):
         self.norm_weight, self.router, self.experts, self.shared = norm_weight, router, experts, shared

@@ -54,6 +54,12 @@ def _empty8(rows, cols, device):
                               device=device)
 
 
+def as_rows(t):
+    """t [rows, cols] itself where its rows are contiguous and apart, else a copy (of a transposed tensor, or of
+    one row that is broadcast)."""
+    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+
+
 def quantise8(x, perm_src=None):
     """(codes, tiled scales) of the rows x [rows, cols] as an MXFP8 matrix."""
     codes, sf = _empty8(*x.shape, x.device)
@@ -271,7 +277,7 @@ class _Shared(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, codes, sf, ex):
         gated = _Gated8(ex)
-        eight = quantise8(x) if codes is None else (codes, sf)
+        eight = quantise8(as_rows(x)) if codes is None else (codes, sf)
         y, ckpt = gated.forward(eight, x.dtype, ctx.needs_input_grad[0])
         ctx.gated, ctx.dtype = gated, x.dtype
         ctx.save_for_backward(*ckpt)

@@ -111,3 +111,31 @@ def test_gradients_of_unused_results(lib):
     assert names(lib)[-1] == "moe_rmsnorm_backward" and x.grad.shape == r.grad.shape == (T, H)
     y, h, codes, sf = rms_norm(x, torch.ones(H), eight=True)
     assert h is x and not codes.requires_grad and not sf.requires_grad
+
+
+def strides(lib, name):
+    """The row strides that the calls of this name were given."""
+    at = {"moe_rmsnorm": (2, 4), "moe_rmsnorm_backward": (2, 4), "moe_route_scores": (2,), "moe_quant_mxfp8": (5,)}
+    return [args[i] for call, args in lib.calls if call == name for i in at[name]]
+
+
+def test_rows_that_repeat_or_are_transposed(lib):
+    """Gradients and inputs that are broadcast over the tokens (row stride 0) or transposed."""
+    x, r = torch.randn(T, H, requires_grad=True), torch.randn(1, H, requires_grad=True)
+    y, h, _, _ = rms_norm(x, torch.ones(H), residual=r.expand(T, H))
+    (y.sum(0) * torch.rand(H)).sum().backward(retain_graph=True)     # dy, dh: one row for all tokens
+    (y.sum(0) * torch.rand(H) + h.sum(0) * torch.rand(H)).sum().backward()
+    assert r.grad.shape == (1, H) and all(s in (0, H) for s in strides(lib, "moe_rmsnorm_backward"))
+    rms_norm(torch.randn(H).expand(T, H), torch.ones(H))
+    rms_norm(torch.randn(H, T).t(), torch.ones(H))
+    route(torch.randn(H).expand(T, H), k)
+    route(torch.randn(H, T).t(), k)
+    sh = shared()
+    for a in (torch.randn(H).expand(T, H), torch.randn(H, T).t(), torch.randn(T, 2 * H)[:, :H]):
+        sh(a)
+    assert strides(lib, "moe_rmsnorm") == [H, H, H, 0, H, 0]
+    assert strides(lib, "moe_route_scores") == [H, H]
+    assert strides(lib, "moe_quant_mxfp8")[-3:] == [H, H, 2 * H]
+    # of dy and dh a row's stride is the rows' own
+    back = [args for call, args in lib.calls if call == "moe_rmsnorm_backward"]
+    assert [a[2] for a in back] == [H, H] and back[1][4] == H

@@ -226,6 +226,29 @@ def test_norm_alone():
         (dx.sum() + dw.sum()).backward()
 
 
+def test_rows_that_repeat_or_are_transposed():
+    """Inputs and gradients that are broadcast over the tokens or transposed: the results of their copies."""
+    g = torch.Generator("cuda").manual_seed(5)
+    T, H = 9, 128
+    w13, w2 = masters(1, H, H, g)
+    sh = MXShared.from_master(w13, w2)
+    one, wide = torch.randn(H, generator=g, device="cuda"), torch.randn(H, T, generator=g, device="cuda")
+    r = torch.randn(1, H, generator=g, device="cuda", requires_grad=True)
+    v = torch.randn(2, H, generator=g, device="cuda")
+    w = torch.rand(H, generator=g, device="cuda")
+    for x in (one.expand(T, H), wide.t()):
+        results = []
+        for copy in (False, True):
+            r.grad = None
+            a = (x.clone(memory_format=torch.contiguous_format) if copy else x.detach()).requires_grad_()
+            res = r.expand(T, H)
+            y, h, _, _ = rms_norm(a, w, residual=res.contiguous() if copy else res)
+            vy, vh = (u.expand(T, H).contiguous() if copy else u.expand(T, H) for u in v)
+            da, dr = torch.autograd.grad((y, h), (a, r), (vy, vh), retain_graph=True)
+            results.append((y, h, da, dr, *route(a, 4), sh(a)))
+        assert all(torch.equal(p, q) for p, q in zip(*results))
+
+
 def test_route_second_derivatives_raise():
     l = torch.randn(3, 8, device="cuda", requires_grad=True)
     _, w = route(l, 2)
