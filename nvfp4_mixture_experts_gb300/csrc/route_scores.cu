@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
 // q (g - r) f with g_j = scale dw_j, q the weight / scale, r = sum_i g_i q_i, f the score's own derivative
 // over it (softmax 1, sigmoid 1 - s); not renormalised g s (1 - s).  Softmax scores that are not
 // renormalised: p_e (sum of the g_j of expert e - sum_j g_j p_j), for every expert e (PL > 0: expert 32 i +
-// lane in the registers of a lane).
+// lane in the registers of a lane).  All of a token's are NaN where its weights are.
 template <int PL, typename T>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackArgs a)
 {
@@ -609,7 +609,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
         for (int i = 0; i < PL; ++i)
             if (32 * i + lane < a.E) from_f32(-l[i] * inv * r, dx[32 * i + lane]);
     } else {
-        for (int e = lane; e < a.E; e += 32) from_f32(0.0f, dx[e]);
+        // the row is read for its token's weights: NaN with a NaN logit, or an infinite one's softmax
+        bool nan = false;
+#pragma unroll 8
+        for (int e = lane; e < a.E; e += 32) {
+            const float l = to_f32(x[e]);
+            nan = nan || l != l || (softmax && l == INFINITY);
+        }
+        nan = __any_sync(kAll, nan);
+        for (int e = lane; e < a.E; e += 32) from_f32(nan ? NAN : 0.0f, dx[e]);
         if (a.renorm) {
             float top = v;
 #pragma unroll
@@ -634,6 +642,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
             const float s = 1.0f / (1.0f + expf(-v));
             g = chosen ? g * s / (1.0f + expf(v)) : 0.0f;
         }
+        if (nan) g = NAN;
     }
     float all = 0.0f;  // of the positions that chose the same expert
     for (int j = 0; j < a.k; ++j) {

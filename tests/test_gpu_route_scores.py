@@ -288,3 +288,27 @@ def test_gradient_of_masked_tokens():
             out = torch.empty(3, 16, device="cuda")
             moe.moe_route_scores_backward(l, ids, dw, out, score=kind, renormalise=renorm)
             assert torch.all(out[0] == 0) and torch.isfinite(out[1]).all() and torch.isnan(out[2, 3])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_a_token_with_nan_weights_has_nan_gradients(kind, renorm, dtype):
+    """Whichever logit it is: one that is not chosen, too."""
+    T, E, k = 5, 70, 4
+    g = torch.Generator("cuda").manual_seed(8)
+    l = torch.randn(T, E, generator=g, device="cuda").to(dtype)
+    l[1, 69] = float("nan")
+    l[2, 3] = float("inf")
+    l[3, 40] = -float("inf")
+    bias = torch.zeros(E, device="cuda")
+    bias[3] = -float("inf")   # (the infinite logit is not chosen)
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    how = dict(score=KIND[kind], renormalise=renorm)
+    moe.moe_route_scores(l, ids, w, bias=bias, **how)
+    assert not torch.any(ids[1] == 69) and not torch.any(ids[2] == 3)
+    d = torch.empty_like(l)
+    moe.moe_route_scores_backward(l, ids, torch.randn(T, k, generator=g, device="cuda"), d, **how)
+    bad = [False, True, kind == "softmax", False, False]
+    for t in range(T):
+        assert bool(torch.isnan(w[t]).all()) == bad[t] == bool(torch.isnan(w[t]).any())
+        assert bool(torch.isnan(d[t]).all()) == bad[t] == bool(torch.isnan(d[t]).any())
