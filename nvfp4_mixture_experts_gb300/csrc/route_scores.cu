@@ -567,9 +567,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
 // A warp per token.  Renormalised scores and sigmoids: the chosen experts' logits alone have gradients,
 // q (g - r) f with g_j = scale dw_j, q the weight / scale, r = sum_i g_i q_i, f the score's own derivative
 // over it (softmax 1, sigmoid 1 - s); not renormalised g s (1 - s).  Softmax scores that are not
-// renormalised: p_e (sum of the g_j of expert e - sum_j g_j p_j), for every expert e (PL > 0: expert 32 i +
-// lane in the registers of a lane).  All of a token's are NaN where its weights are.
-template <int PL, typename T>
+// renormalised: p_e (sum of the g_j of expert e - sum_j g_j p_j), for every expert e (DENSE).  Expert 32 i
+// + lane is in the registers of a lane.  All of a token's are NaN where its weights are.
+template <int PL, bool DENSE, typename T>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackArgs a)
 {
     pdl_wait();
@@ -586,13 +586,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
     const float v = chosen ? to_f32(x[id]) : -INFINITY;
     float g = chosen ? a.dw[t * a.k + lane] * a.scale : 0.0f;
     float p = 0.0f, r = 0.0f;
-    if constexpr (PL > 0) {
-        float l[PL], m = -INFINITY, sum = 0.0f;
+    float l[PL];
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            l[i] = 32 * i + lane < a.E ? to_f32(x[32 * i + lane]) : -INFINITY;
-            m = fmaxf(m, l[i]);
-        }
+    for (int i = 0; i < PL; ++i) l[i] = 32 * i + lane < a.E ? to_f32(x[32 * i + lane]) : -INFINITY;
+    if constexpr (DENSE) {
+        float m = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) m = fmaxf(m, l[i]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
         if (m == -INFINITY) m = 0.0f;
@@ -611,13 +611,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
     } else {
         // the row is read for its token's weights: NaN with a NaN logit, or an infinite one's softmax
         bool nan = false;
-#pragma unroll 8
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = to_f32(x[e]);
-            nan = nan || l != l || (softmax && l == INFINITY);
-        }
+#pragma unroll
+        for (int i = 0; i < PL; ++i) nan = nan || l[i] != l[i] || (softmax && l[i] == INFINITY);
         nan = __any_sync(kAll, nan);
-        for (int e = lane; e < a.E; e += 32) from_f32(nan ? NAN : 0.0f, dx[e]);
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            if (32 * i + lane < a.E) from_f32(nan ? NAN : 0.0f, dx[32 * i + lane]);
         if (a.renorm) {
             float top = v;
 #pragma unroll
@@ -650,7 +649,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
         const float gj = __shfl_sync(kAll, g, j);
         if (other == id) all += gj;
     }
-    if constexpr (PL > 0) all = p * (all - r);
+    if constexpr (DENSE) all = p * (all - r);
     __syncwarp();  // the row is written; its chosen experts' are written again
     if (chosen) from_f32(all, dx[id]);
 }
@@ -669,8 +668,17 @@ struct Forward {
 };
 template <int PL, typename T>
 struct Dense {
-    static RouteBackKernel get() { return route_back_kernel<PL, T>; }
+    static RouteBackKernel get() { return route_back_kernel<PL, true, T>; }
 };
+template <int PL, typename T>
+struct Sparse {
+    static RouteBackKernel get() { return route_back_kernel<PL, false, T>; }
+};
+template <typename T>
+static RouteBackKernel back_of(bool dense, int E)
+{
+    return dense ? with_pl<Dense, T, RouteBackKernel>(E) : with_pl<Sparse, T, RouteBackKernel>(E);
+}
 
 RouteKernel route_scores_kernel_for(int dtype, int E)
 {
@@ -684,10 +692,9 @@ RouteKernel route_scores_kernel_for(int dtype, int E)
 RouteBackKernel route_back_kernel_for(int dtype, bool dense, int E)
 {
     switch (dtype) {
-        case MOE_BF16:
-            return dense ? with_pl<Dense, __nv_bfloat16, RouteBackKernel>(E) : route_back_kernel<0, __nv_bfloat16>;
-        case MOE_FP16: return dense ? with_pl<Dense, __half, RouteBackKernel>(E) : route_back_kernel<0, __half>;
-        default: return dense ? with_pl<Dense, float, RouteBackKernel>(E) : route_back_kernel<0, float>;
+        case MOE_BF16: return back_of<__nv_bfloat16>(dense, E);
+        case MOE_FP16: return back_of<__half>(dense, E);
+        default: return back_of<float>(dense, E);
     }
 }
 
