@@ -113,6 +113,26 @@ def test_shared_expert(T, H, I, dtype):
     assert sh.get_status() == (moe.MOE_OK, 0)
 
 
+def test_weights_of_a_checkpoint():
+    """The same codes with canonical scales."""
+    g = torch.Generator("cuda").manual_seed(2)
+    H, I = 128, 256
+    w13, w2 = masters(3, H, I, g)
+    kept = []
+    for w in (w13, w2):
+        codes = torch.empty(*w.shape[:2], w.shape[2] // 2, dtype=torch.uint8, device="cuda")
+        sf = torch.empty(*w.shape[:2], w.shape[2] // 32, dtype=torch.uint8, device="cuda")
+        moe.moe_quant_mxfp4(w, codes, sf, moe.MOE_SF_CANONICAL, scale_rule=moe.MOE_MX_CEIL)
+        kept += [codes, sf]
+    x = torch.randn(50, H, generator=g, device="cuda").bfloat16()
+    ids = torch.rand(50, 3, generator=g, device="cuda").topk(2, 1).indices.int()
+    w = torch.rand(50, 2, generator=g, device="cuda")
+    a = MXExperts.from_checkpoint(3, 0, *kept, act_bits=8)(x, ids, w)
+    assert torch.equal(a, MXExperts.from_master(3, 0, w13, w2, backward=False, act_bits=8)(x, ids, w))
+    b = MXShared.from_checkpoint(*(t[:1].contiguous() for t in kept))(x)
+    assert torch.equal(b, MXShared.from_master(w13[:1], w2[:1], backward=False)(x))
+
+
 def test_padding_rows_are_not_read_and_results_repeat():
     g = torch.Generator("cuda").manual_seed(0)
     w13, w2 = masters(5, 128, 128, g)

@@ -291,6 +291,35 @@ def test_product_of_all_rows_and_many_tiles():
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("G,most", [(1024, 300), (1024, 3), (619, 300), (618, 300)])
+def test_product_of_many_groups(G, most):
+    """Their starts leave the ring of stages less room (two stages of many rows, or four of few)."""
+    rng = np.random.default_rng(G + most)
+    N, K = 40, 640
+    counts = rng.integers(0, 3, size=G)
+    counts[[0, G // 2, G - 1]] = 0, most, 1
+    offsets = np.concatenate([[0], np.cumsum((counts + 127) // 128 * 128)])
+    cap = int(offsets[-1])
+    w, w_sf, wv = mx_matrices(G, N, K, rng)
+    c, s, v = (np.zeros(z) for z in ((cap, K), (cap, K // 32), (cap, K)))
+    live = np.concatenate([np.arange(o, o + n) for n, o in zip(counts, offsets)])
+    c[live], s[live], v[live] = mx8_rows(len(live), K, rng)
+    c, s = c.astype(np.uint8), s.astype(np.uint8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = torch.full((cap, N), -3.0, device="cuda")
+    d = lambda a: torch.from_numpy(np.asarray(a)).cuda()  # noqa: E731
+    moe.moe_grouped_gemm_mxfp8(d(c), d(ops_ref.tile_scales(s)), d(np.int32(counts)), d(np.int32(offsets)), w, w_sf,
+                               got, status)
+    assert status.item() == 0
+    g64 = f64(got)
+    dead = np.ones(cap, bool)
+    dead[live] = False
+    assert np.all(g64[dead] == -3)
+    for g, (n, o) in enumerate(zip(counts, offsets)):
+        slack = K * 2.0 ** -24 * (np.abs(v[o:o + n]) @ np.abs(wv[g]).T)
+        assert np.all(np.abs(g64[o:o + n] - v[o:o + n] @ wv[g].T) <= slack)
+
+
 def test_product_scales_of_every_block():
     """Rows and weights of ones, block scales of their own: every scale meets its block."""
     N, K, R = 140, 512, 150
