@@ -408,7 +408,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
 {
     extern __shared__ double s_all[];  // [kRouteWarps][E] keys, where there are groups
     __shared__ alignas(16) uint64_t s_key[kRouteWarps][32];
-    __shared__ int s_group[kRouteWarps][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -470,44 +469,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
             if (a.bias) v = s;
         }
         if (a.groups > 1) keys32[e] = top2 ? s : v;
-        else key[i] = ordered(v);
+        key[i] = ordered(v);
     }
     bool again = false;
-    int n = 1, *group = s_group[warp];
     if (a.groups > 1) {
-        n = (int)a.group.d;
         __syncwarp();
         float edge[2];
         float least;
-        const float score = group_score(keys32, a.groups, n, top2, &least);
+        const float score = group_score(keys32, a.groups, (int)a.group.d, top2, &least);
         uint32_t in = best_groups(score, a.groups, a.topk_groups, edge);
         if (summed && near(0.25f * edge[0], 0.25f * edge[1]))
             again = !border_groups(a, x, keys32, score, least, edge, near, reinterpret_cast<int*>(s_key[warp]), in);
-        if (in >> lane & 1) group[__popc(in & ((1u << lane) - 1))] = lane * n;
-        __syncwarp();
-        // the kept groups' experts one after another: position 32 i + lane
-        const int count = a.topk_groups * n;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-            const int p = 32 * i + lane;
-            if (p < count) {
-                const int q = (int)a.group.div(p), e = group[q] + p - q * n;
-                key[i] = ordered(a.bias || !top2 ? keys32[e] : fmaxf(to_f32(x[e]), -INFINITY));
-            }
-        }
+        for (int i = 0; i < PL; ++i)
+            if (!(in >> a.group.div(32 * i + lane) & 1)) key[i] = 0;
+        __syncwarp();
     }
-    auto expert = [&](int p) {
-        if (a.groups == 1) return p;
-        const int q = (int)a.group.div(p);
-        return group[q] + p - q * n;
-    };
     int mine = 0;
     if (!again) {
         // one more than k where the order of sums may need 64 bits
         const int rounds = a.bias && a.k < a.E ? a.k + 1 : a.k;
         uint32_t kept;
         choose_32<PL>(key, rounds, s_key[warp], kept, mine);
-        mine = expert(mine);
         if (a.bias) {
             const uint32_t next = __shfl_down_sync(kAll, kept, 1);
             const int after = __shfl_down_sync(kAll, mine, 1);
@@ -528,7 +511,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
                     if (!more) break;
                     if (c == 32) again = true;
                     if (again) break;
-                    if (lane == c) mine = expert(p);
+                    if (lane == c) mine = p;
                     if (c < a.k) last = unordered(k);
                     ++c;
                 }
