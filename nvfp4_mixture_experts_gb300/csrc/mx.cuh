@@ -176,6 +176,14 @@ struct Eight {
     }
 };
 
+// The largest of m and the magnitudes of a pair (NaN, where one is).
+__device__ __forceinline__ float max_nan(float m, F2 p)
+{
+    const float2 v = p.get();
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(v.x), "f"(v.y));
+    return m;
+}
+
 template <typename T>
 __device__ __forceinline__ void to_pairs(const Eight<T>& e, F2 (&v)[4])
 {

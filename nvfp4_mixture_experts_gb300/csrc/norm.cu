@@ -177,12 +177,6 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ float max_nan(float m, float v)
-{
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v)));
-    return m;
-}
-
 }  // namespace
 
 // A row in the registers of one warp (ONE, eight rows a block) or of one block, PER eights a thread: each
@@ -255,12 +249,7 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) norm_kernel(NormArgs a)
                 if (!a.codes) continue;  // (H % 32 == 0: a block's four lanes are in or out together)
                 float f[8], top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 q = v[p][i].get();
-                    f[2 * i] = q.x;
-                    f[2 * i + 1] = q.y;
-                    top = max_nan(max_nan(top, q.x), q.y);
-                }
+                for (int i = 0; i < 4; ++i) top = max_nan(top, v[p][i]);
                 uint32_t m = __float_as_uint(top);
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -361,10 +350,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) norm_ring_kernel(NormAr
             if (!a.codes) continue;  // (H % 32 == 0: a block's lanes are in or out together)
             float f[kOf], top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kOf / 2; ++i) {
-                const float2 q = v[k].v[i].get();
-                top = max_nan(max_nan(top, q.x), q.y);
-            }
+            for (int i = 0; i < kOf / 2; ++i) top = max_nan(top, v[k].v[i]);
             uint32_t m = __float_as_uint(top);
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -45,11 +45,7 @@ __device__ __forceinline__ uint32_t amax_block(const F2 (&v)[kPairs])
 {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-        const float2 a = v[i].get();
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(a.x)));
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(a.y)));
-    }
+    for (int i = 0; i < kPairs; ++i) m = max_nan(m, v[i]);
     const uint32_t b = __float_as_uint(m);
     return max(b, __shfl_xor_sync(0xffffffffu, b, 1));
 }
