@@ -563,7 +563,8 @@ moe_status moe_route_scores(const void* logits_d, int32_t dtype, int64_t stride,
     a.groups = topk_groups == num_groups ? 1 : num_groups;  // (of all groups: no choice among them)
     a.topk_groups = a.groups == 1 ? 1 : topk_groups;
     a.group_score = group_score;
-    a.group = FastDiv(num_experts / num_groups);
+    a.group = num_experts / num_groups;
+    a.group_mul = ((1u << 20) + a.group - 1) / a.group;
     a.renorm = renormalise;
     a.scale = scale;
     a.ids = topk_ids_d;

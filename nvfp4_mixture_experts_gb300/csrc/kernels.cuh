@@ -501,7 +501,8 @@ struct RouteArgs {
     int T, E, k;
     int score;            // moe_score
     int groups, topk_groups, group_score;
-    FastDiv group;        // by the experts of a group
+    int group;            // experts of a group
+    uint32_t group_mul;   // ceil(2^20 / group): an expert's group is expert * group_mul >> 20 (experts are below 2^10)
     int renorm;
     float scale;
     int32_t* ids;

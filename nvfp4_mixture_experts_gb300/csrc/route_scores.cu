@@ -6,13 +6,14 @@
 // a bias, or a group's two largest) are formed in 32 bits, and a token of which two neighbouring keys lie
 // nearer than their rounding can be is chosen again with keys in 64 bits (about one token in a thousand): of
 // the candidates for the choice alone, or of the largest keys of the groups at the border, a lane each, because
-// 64-bit exponentials take microseconds (all keys of such a token: 43 us where 8192 tokens take 18).
+// 64-bit exponentials take microseconds (all keys of such a token: 43 us where 8192 tokens took 18).
 //
 // A warp has a token, so that a row is read once, in its lanes' registers, and nothing waits for other warps.
-// What bounds it is the work on each token (780 instructions for top-8 of 320 logits, 1480 with sigmoids, a
-// bias and eight groups), not the row's 1280 bytes: 8192 tokens top-8 of 320 9.6 us, with sigmoids and a bias 13,
-// with groups too 18; with softmax scores and a bias 26 (the sum of all exponentials of a few tokens in 64
-// bits); one token 3.3 us.  The gradient is bound by its launch and memory: 4.5 us, 21 MB.
+// What bounds it is the work on each token (780 instructions for top-8 of 320 logits, 1400 with sigmoids, a
+// bias and eight groups), not the row's 1280 bytes: 8192 tokens top-8 of 320 9.4 us, with sigmoids, a bias and
+// groups 16.5, of which the few tokens with 64-bit keys are 2.7; with softmax scores 24, of which they are 10 (the
+// sum of all of a token's exponentials in 64 bits); one token 3.3 us.  The gradient is bound by its launch and memory: 4.5 us, 21 MB;
+// renormalised 5.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -290,7 +291,7 @@ __device__ __noinline__ int choose_64(const RouteArgs& a, const T* x, double* s_
         __syncwarp();
         for (int i = 0; i < PL; ++i) {
             const int e = 32 * i + lane;
-            if (e < a.E && !(in >> a.group.div(e) & 1)) key[i] = 0;
+            if (e < a.E && !(in >> (e * a.group_mul >> 20 & 31) & 1)) key[i] = 0;
         }
     }
     int mine = 0;
@@ -312,7 +313,7 @@ __device__ __noinline__ bool border_groups(const RouteArgs& a, const T* x, const
                                            float least, const float (&edge)[2], Near near, int* s_expert,
                                            uint32_t& in)
 {
-    const int lane = threadIdx.x & 31, n = (int)a.group.d;
+    const int lane = threadIdx.x & 31, n = a.group;
     const bool two = a.group_score == MOE_GROUP_TOP2;
     const bool mine = lane < a.groups;
     // (a group's score is two keys; the border's two scores are near each other)
@@ -476,13 +477,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
         __syncwarp();
         float edge[2];
         float least;
-        const float score = group_score(keys32, a.groups, (int)a.group.d, top2, &least);
+        const float score = group_score(keys32, a.groups, a.group, top2, &least);
         uint32_t in = best_groups(score, a.groups, a.topk_groups, edge);
         if (summed && near(0.25f * edge[0], 0.25f * edge[1]))
             again = !border_groups(a, x, keys32, score, least, edge, near, reinterpret_cast<int*>(s_key[warp]), in);
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            if (!(in >> a.group.div(32 * i + lane) & 1)) key[i] = 0;
+            if (!(in >> ((32 * i + lane) * a.group_mul >> 20 & 31) & 1)) key[i] = 0;
         __syncwarp();
     }
     int mine = 0;
