@@ -5,14 +5,14 @@
 // order of the scores is that of the logits, which are compared as they are; keys that are sums (a score and
 // a bias, or a group's two largest) are formed in 32 bits, and a token of which two neighbouring keys lie
 // nearer than their rounding can be is chosen again with keys in 64 bits (about one token in a thousand): of
-// the candidates for the choice alone, or of the largest keys of the groups at the border, a lane each, because
+// the chosen ones where the next is apart, of the candidates for the choice, or of the largest keys of the groups at the border, a lane each, because
 // 64-bit exponentials take microseconds (all keys of such a token: 43 us where 8192 tokens took 18).
 //
 // A warp has a token, so that a row is read once, in its lanes' registers, and nothing waits for other warps.
 // What bounds it is the work on each token (780 instructions for top-8 of 320 logits, 1400 with sigmoids, a
 // bias and eight groups), not the row's 1280 bytes: 8192 tokens top-8 of 320 9.4 us, with sigmoids, a bias and
-// groups 16.5, of which the few tokens with 64-bit keys are 2.7; with softmax scores 24, of which they are 10 (the
-// sum of all of a token's exponentials in 64 bits); one token 3.3 us.  The gradient is bound by its launch and memory: 4.5 us, 21 MB;
+// groups 15.6, of which the few tokens with 64-bit keys are 1.5; with softmax scores 23, of which they are 9 (the sum
+// of all of a token's exponentials in 64 bits); one token 3.3 us.  The gradient is bound by its launch and memory: 4.5 us, 21 MB;
 // renormalised 5.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -497,11 +497,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
             const int after = __shfl_down_sync(kAll, mine, 1);
             bool apart = lane >= rounds - 1 || lane == 31 || !next || !near(unordered(kept), unordered(next));
             bool all = __all_sync(kAll, apart);
+            // the k are known where the next key is apart from the k-th, and so from all of them (not where the two
+            // are equal: a near one above them may be below both)
+            const bool known = rounds <= 32 && (__ballot_sync(kAll, apart) >> (a.k - 1) & 1);
             if (!all) {   // (the sums of equal terms are equal)
                 apart = apart || (to_f32(x[mine]) == to_f32(x[after]) && a.bias[mine] == a.bias[after]);
                 all = __all_sync(kAll, apart);
             }
-            if (!all || rounds > 32) {
+            if (!all && known) {
+                mine = order_64(a, x, mine, a.k);
+            } else if (!all || rounds > 32) {
                 // every expert that may be among the k: those with keys near the k-th, or before it
                 int c = 0;
                 float last = 0.0f;

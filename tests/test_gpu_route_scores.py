@@ -312,3 +312,32 @@ def test_a_token_with_nan_weights_has_nan_gradients(kind, renorm, dtype):
     for t in range(T):
         assert bool(torch.isnan(w[t]).all()) == bad[t] == bool(torch.isnan(w[t]).any())
         assert bool(torch.isnan(d[t]).all()) == bad[t] == bool(torch.isnan(d[t]).any())
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 2])
+def test_equal_keys_at_the_border_below_a_near_one(kind, groups):
+    """Each token has three experts, the others are masked: a first one whose key lies within a rounding
+    of two equal ones.  Of k = 2 the pair is chosen where it is larger, else the first and the lower one."""
+    T, k = 300, 2
+    rng = np.random.default_rng(groups)
+    E = 1024
+    l = np.full((T, E), -np.inf, np.float32)
+    bias = rng.normal(size=E).astype(np.float32)
+    a = 3 * np.arange(T) + 1
+    row = np.arange(T)
+    la, lb = rng.normal(size=(2, T)).astype(np.float32)
+    l[row, a], l[row, a + 1], l[row, a + 2] = la, lb, lb
+    bias[a + 2] = bias[a + 1]
+    sa, sb = (1 / (1 + np.exp(-x.astype(np.float64))) for x in (la, lb))
+    if kind == "softmax":
+        ea, eb = np.exp(la.astype(np.float64)), np.exp(lb.astype(np.float64))
+        sa, sb = ea / (ea + 2 * eb), eb / (ea + 2 * eb)
+    bias[a] = sb + bias[a + 1].astype(np.float64) - sa     # (rounded: the keys differ by that)
+    first = sa + bias[a] > sb + bias[a + 1]
+    assert 100 < first.sum() < 200
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    moe.moe_route_scores(torch.from_numpy(l).cuda(), ids, w, bias=torch.from_numpy(bias).cuda(), score=KIND[kind],
+                         num_groups=groups, topk_groups=groups)
+    want = np.where(first[:, None], np.stack([a, a + 1], 1), np.stack([a + 1, a + 2], 1))
+    assert np.array_equal(ids.cpu().numpy(), want)
