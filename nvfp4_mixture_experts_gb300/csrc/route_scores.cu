@@ -5,15 +5,16 @@
 // order of the scores is that of the logits, which are compared as they are; keys that are sums (a score and
 // a bias, or a group's two largest) are formed in 32 bits, and a token of which two neighbouring keys lie
 // nearer than their rounding can be is chosen again with keys in 64 bits (about one token in a thousand): of
-// the chosen ones where the next is apart, of the candidates for the choice, or of the largest keys of the groups at the border, a lane each, because
-// 64-bit exponentials take microseconds (all keys of such a token: 43 us where 8192 tokens took 18).
+// the chosen experts where the next one is apart, else of the candidates for the choice, or of the largest
+// keys of the groups at the border, a lane each, because 64-bit exponentials take microseconds (all keys of
+// such a token: 43 us where 8192 tokens took 18).
 //
 // A warp has a token, so that a row is read once, in its lanes' registers, and nothing waits for other warps.
-// What bounds it is the work on each token (780 instructions for top-8 of 320 logits, 1400 with sigmoids, a
+// What bounds it is the work on each token (800 instructions for top-8 of 320 logits, 1380 with sigmoids, a
 // bias and eight groups), not the row's 1280 bytes: 8192 tokens top-8 of 320 9.4 us, with sigmoids, a bias and
-// groups 15.6, of which the few tokens with 64-bit keys are 1.5; with softmax scores 23, of which they are 9 (the sum
-// of all of a token's exponentials in 64 bits); one token 3.3 us.  The gradient is bound by its launch and memory: 4.5 us, 21 MB;
-// renormalised 5.4.
+// groups 15.8, of which the few tokens with 64-bit keys are 1.5; with softmax scores 18, of which they are 3
+// (23 with all of such a token's exponentials in 64 bits, which are now for what 32-bit ones do not settle); one
+// token 3.3 us.  The gradient is bound by its launch and memory: 4.5 us, 21 MB; renormalised 5.4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -227,17 +228,20 @@ __device__ __forceinline__ F group_score(const F* keys, int groups, int n, bool 
 }
 
 // A token's scores in 64 bits.  (What follows is out of line and reads the logits again: few tokens need it.)
+// `quick`: a softmax's sum is one of 32-bit exponentials, added in 64 bits.  Each term is within 2^-22 + 2^-24
+// of itself (expf by two units at most; what the rounding of l - m left out is multiplied back in, which is
+// rounded once), so the scores are all off by one factor, within 2^-21 of 1.
 template <typename T>
 struct Scores64 {
     const RouteArgs& a;
     const T* x;
-    double m, sum;
+    double m, sum, off;
     __device__ __forceinline__ float logit(int e) const
     {
         const float l = to_f32(x[e]);
         return l != l ? -INFINITY : l;
     }
-    __device__ Scores64(const RouteArgs& a, const T* x) : a(a), x(x), m(0.0), sum(1.0)
+    __device__ Scores64(const RouteArgs& a, const T* x, bool quick) : a(a), x(x), m(0.0), sum(1.0), off(0.0)
     {
         if (a.score != MOE_SCORE_SOFTMAX) return;
         const int lane = threadIdx.x & 31;
@@ -247,6 +251,19 @@ struct Scores64 {
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
         m = top;
         sum = 0.0;
+        if (quick && fabsf(top) <= FLT_MAX) {
+            off = 0x1p-21;
+            for (int e = lane; e < a.E; e += 32) {
+                const float l = logit(e), d = l - top;
+                if (!(d >= -FLT_MAX)) continue;   // (e^d is 0 in 64 bits, too)
+                // l - top is d + rest (two numbers' difference and what its rounding left out: Knuth's)
+                const float back = d + top, rest = (l - back) + ((back - d) - top);
+                const float p = expf(d);
+                sum += (double)fmaf(p, rest, p);
+            }
+            sum = warp_sum(sum);
+            return;
+        }
         double part[4] = {};   // (four exponentials at a time: 64-bit instructions take long)
         for (int e0 = lane; e0 < a.E; e0 += 128)
 #pragma unroll
@@ -256,14 +273,15 @@ struct Scores64 {
             }
         sum = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
     }
-    // the key of a sum: score and bias
-    __device__ double key(int e) const
+    // the key of a sum: score (of which `score` receives what may be off) and bias
+    __device__ double key(int e, double& score) const
     {
+        score = 0.0;
         const float l = logit(e);
         if (l == -INFINITY) return -INFINITY;
-        double v = a.score == MOE_SCORE_SOFTMAX ? (l == m ? 1.0 : exp((double)l - m)) / sum
-                                                : 1.0 / (1.0 + exp(-(double)l));
-        if (a.bias) v += (double)a.bias[e];
+        score = a.score == MOE_SCORE_SOFTMAX ? (l == m ? 1.0 : exp((double)l - m)) / sum
+                                             : 1.0 / (1.0 + exp(-(double)l));
+        const double v = a.bias ? score + (double)a.bias[e] : score;
         return v >= -DBL_MAX ? v : -INFINITY;  // a bias of -infinity or NaN
     }
 };
@@ -273,13 +291,14 @@ template <int PL, typename T>
 __device__ __noinline__ int choose_64(const RouteArgs& a, const T* x, double* s_keys)
 {
     const int lane = threadIdx.x & 31;
-    const Scores64<T> sc(a, x);
+    const Scores64<T> sc(a, x, false);
     uint64_t key[PL];
     for (int i = 0; i < PL; ++i) {
         const int e = 32 * i + lane;
         key[i] = 0;
         if (e >= a.E) continue;
-        const double v = sc.key(e);
+        double score;
+        const double v = sc.key(e, score);
         if (a.groups > 1) s_keys[e] = v;
         key[i] = ordered(a.bias ? v : (double)sc.logit(e));
     }
@@ -343,25 +362,36 @@ __device__ __noinline__ bool border_groups(const RouteArgs& a, const T* x, const
     }
     __syncwarp();
     e = s_expert[lane];
-    const Scores64<T> sc(a, x);
-    const double v = e >= 0 ? sc.key(e) : -INFINITY;
-    const int rank = __popc(borders & ((1u << lane) - 1));
-    double p = -INFINITY, q = -INFINITY;
+    for (bool quick = a.score == MOE_SCORE_SOFTMAX;; quick = false) {
+        const Scores64<T> sc(a, x, quick);
+        double score;
+        const double v = e >= 0 ? sc.key(e, score) : -INFINITY;
+        if (e < 0) score = 0.0;
+        const int rank = __popc(borders & ((1u << lane) - 1));
+        double p = -INFINITY, q = -INFINITY, most = 0.0;   // most: of the candidates' scores
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const double c = __shfl_sync(kAll, v, (4 * rank + i) & 31);
-        q = larger(q, smaller(p, c));
-        p = larger(p, c);
+        for (int i = 0; i < 4; ++i) {
+            const double c = __shfl_sync(kAll, v, (4 * rank + i) & 31);
+            most = larger(most, __shfl_sync(kAll, score, (4 * rank + i) & 31));
+            q = larger(q, smaller(p, c));
+            p = larger(p, c);
+        }
+        const double exact = two && q > -INFINITY ? p + q : p;
+        // a group's score is off by what two of its keys are (and 2^-50 of rounding), the border's order known
+        // where the scores are further apart
+        const double mine_off = 2.0 * sc.off * most + 0x1p-50 * fabs(exact);
+        bool known = true;
+        int before = __popc(above);
+        for (uint32_t left = borders; left; left &= left - 1) {
+            const int g = __ffs(left) - 1;
+            const double o = __shfl_sync(kAll, exact, g), off = __shfl_sync(kAll, mine_off, g);
+            before += o > exact || (o == exact && g < lane);
+            known = known && (g == lane || fabs(o - exact) > off + mine_off);
+        }
+        if (quick && !__all_sync(kAll, known || !border)) continue;
+        in = above | __ballot_sync(kAll, border && before < a.topk_groups);
+        return true;
     }
-    const double exact = two && q > -INFINITY ? p + q : p;
-    int before = __popc(above);
-    for (uint32_t left = borders; left; left &= left - 1) {
-        const int g = __ffs(left) - 1;
-        const double o = __shfl_sync(kAll, exact, g);
-        before += o > exact || (o == exact && g < lane);
-    }
-    in = above | __ballot_sync(kAll, border && before < a.topk_groups);
-    return true;
 }
 
 // The order of n candidates, one a lane, by their keys in 64 bits: expert j of lane j.
@@ -369,20 +399,34 @@ template <typename T>
 __device__ __noinline__ int order_64(const RouteArgs& a, const T* x, int mine, int n)
 {
     const int lane = threadIdx.x & 31;
-    const Scores64<T> sc(a, x);
-    const double k = lane < n ? sc.key(mine) : -INFINITY;
-    int rank = 0;
-    for (int j = 0; j < n; ++j) {
-        const double o = __shfl_sync(kAll, k, j);
-        const int e = __shfl_sync(kAll, mine, j);
-        rank += o > k || (o == k && e < mine);
+    for (bool quick = a.score == MOE_SCORE_SOFTMAX;; quick = false) {
+        const Scores64<T> sc(a, x, quick);
+        double score = 0.0;
+        const double k = lane < n ? sc.key(mine, score) : -INFINITY;
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const double o = __shfl_sync(kAll, k, j);
+            const int e = __shfl_sync(kAll, mine, j);
+            rank += o > k || (o == k && e < mine);
+        }
+        // what of a key may be off; the order is known where neighbours are further apart, or of equal terms
+        const double off = sc.off * score + 0x1p-50 * fabs(k);
+        int out = 0, from = 0;
+        for (int j = 0; j < n; ++j) {
+            const int r = __shfl_sync(kAll, rank, j), e = __shfl_sync(kAll, mine, j);
+            if (r == lane) {
+                out = e;
+                from = j;
+            }
+        }
+        if (!quick) return out;
+        const int next = __shfl_down_sync(kAll, from, 1), after = __shfl_down_sync(kAll, out, 1);
+        const double hi = __shfl_sync(kAll, k, from), lo = __shfl_sync(kAll, k, next);
+        const double offs = __shfl_sync(kAll, off, from) + __shfl_sync(kAll, off, next);
+        const bool known = lane >= n - 1 || hi - lo > offs || lo == -INFINITY ||
+                           (sc.logit(out) == sc.logit(after) && a.bias[out] == a.bias[after]);
+        if (__all_sync(kAll, known)) return out;
     }
-    int out = 0;
-    for (int j = 0; j < n; ++j) {
-        const int r = __shfl_sync(kAll, rank, j), e = __shfl_sync(kAll, mine, j);
-        if (r == lane) out = e;
-    }
-    return out;
 }
 
 __device__ __forceinline__ float ex2_approx(float x)

@@ -341,3 +341,22 @@ def test_equal_keys_at_the_border_below_a_near_one(kind, groups):
                          num_groups=groups, topk_groups=groups)
     want = np.where(first[:, None], np.stack([a, a + 1], 1), np.stack([a + 1, a + 2], 1))
     assert np.array_equal(ids.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("k,groups,topg", [(1, 1, 1), (2, 1, 1), (3, 1, 1), (1, 32, 1), (2, 32, 2), (40 // 8, 32, 2)])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_keys_near_by_every_measure(kind, k, groups, topg):
+    """Each token has two experts far above the others, in two groups, with keys from 2^-29 to 2^-14 apart."""
+    rng = np.random.default_rng(k + groups)
+    T, E = 500, 1024
+    a, row = np.arange(T), np.arange(T)
+    b = a + 512
+    l = rng.normal(size=(T, E)).astype(np.float32) - 8
+    l[row, a], l[row, b] = 1 + 0.1 * rng.normal(size=(2, T))
+    e = np.exp(l.astype(np.float64))
+    s = e / e.sum(1, keepdims=True) if kind == "softmax" else 1 / (1 + np.exp(-l.astype(np.float64)))
+    apart = 2.0 ** rng.uniform(-29, -14, size=T) * rng.choice([-1, 1], size=T)
+    bias = np.zeros(E, np.float32)
+    bias[a] = s[row, b] - s[row, a] + apart
+    assert 100 < (s[row, a] + bias[a] > s[row, b] + bias[b]).sum() < 400
+    check(dev(l), dev(bias), k, kind, groups, topg)
