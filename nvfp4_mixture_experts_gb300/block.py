@@ -2,7 +2,9 @@
 backward -- the norm with the residual's addition, routing, the experts and the shared expert.
 
 rms_norm and route are the block's own operators for autograd; their gradients, like the experts',
-have none of their own (second derivatives raise).
+have none of their own (second derivatives raise).  A step with its backward pass can be captured into a
+CUDA graph, as with torch's own operators once nothing holds an eager step's results: autograd ties the
+leaves' gradients to the stream of the oldest graph of theirs that is alive, which must not be another one.
 """
 import torch
 
