@@ -12,7 +12,7 @@
 // A warp has a token, so that a row is read once, in its lanes' registers, and nothing waits for other warps.
 // What bounds it is the work on each token (800 instructions for top-8 of 320 logits, 1380 with sigmoids, a
 // bias and eight groups), not the row's 1280 bytes: 8192 tokens top-8 of 320 9.4 us, with sigmoids, a bias and
-// groups 15.8, of which the few tokens with 64-bit keys are 1.5; with softmax scores 18, of which they are 3
+// groups 16.0, of which the few tokens with 64-bit keys are 1.5; with softmax scores 18, of which they are 3
 // (23 with all of such a token's exponentials in 64 bits, which are now for what 32-bit ones do not settle); one
 // token 3.3 us.  The gradient is bound by its launch and memory: 4.5 us, 21 MB; renormalised 5.4.
 #include <cuda_bf16.h>
@@ -445,6 +445,36 @@ __device__ __forceinline__ float rcp_approx(float x)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The 32-bit key of a sum: of a logit v's score and a bias (m, inv: the softmax's largest logit and the inverse
+// of its sum).
+__device__ __forceinline__ float sum_key(bool softmax, float v, float m, float inv, float bias)
+{
+    const float s = softmax ? ex2_approx(kLog2e * (v == m ? 0.0f : v - m)) * inv
+                            : rcp_approx(1.0f + ex2_approx(-kLog2e * v));
+    const float key = s + bias;
+    return v == -INFINITY || !(key >= -FLT_MAX) ? -INFINITY : key;  // masked; a bias of -infinity or NaN
+}
+
+// Whether two keys may be in the other order in exact arithmetic.
+__device__ __forceinline__ bool near_keys(float hi, float lo, float slack)
+{
+    return hi - lo <= slack + 0x1p-22f * fminf(fmaxf(fabsf(hi), fabsf(lo)), FLT_MAX);
+}
+
+// Whether all experts with keys near that of expert `kth` have its logit and its bias.
+template <typename T>
+__device__ __noinline__ bool near_are_equal(const RouteArgs& a, const T* x, float m, float inv, float slack, int kth)
+{
+    const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+    const float l = to_f32(x[kth]), b = a.bias[kth], at = sum_key(softmax, l, m, inv, b);
+    bool same = true;
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+        const float v = fmaxf(to_f32(x[e]), -INFINITY), o = sum_key(softmax, v, m, inv, a.bias[e]);
+        if (near_keys(fmaxf(at, o), fminf(at, o), slack)) same = same && v == l && a.bias[e] == b;
+    }
+    return __all_sync(kAll, same);
+}
+
 }  // namespace
 
 // A warp per token, expert 32 i + lane in the registers of a lane.
@@ -496,9 +526,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
     // |l| 2^-24), of a softmax score 2^-18 of the largest (a lane's sum of up to 32 terms), and 2^-24 of
     // the sum with the bias.
     const float slack = softmax ? inv * 0x1p-17f : 0x1p-20f;
-    auto near = [&](float hi, float lo) {
-        return hi - lo <= slack + 0x1p-22f * fminf(fmaxf(fabsf(hi), fabsf(lo)), FLT_MAX);
-    };
+    auto near = [&](float hi, float lo) { return near_keys(hi, lo, slack); };
     float* keys32 = reinterpret_cast<float*>(s_keys);
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
@@ -507,10 +535,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
         if (e >= a.E) continue;
         float v = l[i], s = v;  // the expert's key, and what its group's score is made of
         if (summed) {
-            s = softmax ? ex2_approx(kLog2e * (v == m ? 0.0f : v - m)) * inv
-                        : rcp_approx(1.0f + ex2_approx(-kLog2e * v));
-            s += bias[i];
-            if (v == -INFINITY || !(s >= -FLT_MAX)) s = -INFINITY;  // masked; a bias of -infinity or NaN
+            s = sum_key(softmax, v, m, inv, bias[i]);
             if (a.bias) v = s;
         }
         if (a.groups > 1) keys32[e] = top2 ? s : v;
@@ -539,33 +564,37 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
         if (a.bias) {
             const uint32_t next = __shfl_down_sync(kAll, kept, 1);
             const int after = __shfl_down_sync(kAll, mine, 1);
-            bool apart = lane >= rounds - 1 || lane == 31 || !next || !near(unordered(kept), unordered(next));
+            const bool apart = lane >= rounds - 1 || lane == 31 || !next || !near(unordered(kept), unordered(next));
             bool all = __all_sync(kAll, apart);
-            // the k are known where the next key is apart from the k-th, and so from all of them (not where the two
-            // are equal: a near one above them may be below both)
-            const bool known = rounds <= 32 && (__ballot_sync(kAll, apart) >> (a.k - 1) & 1);
-            if (!all) {   // (the sums of equal terms are equal)
-                apart = apart || (to_f32(x[mine]) == to_f32(x[after]) && a.bias[mine] == a.bias[after]);
-                all = __all_sync(kAll, apart);
-            }
-            if (!all && known) {
-                mine = order_64(a, x, mine, a.k);
-            } else if (!all || rounds > 32) {
-                // every expert that may be among the k: those with keys near the k-th, or before it
-                int c = 0;
-                float last = 0.0f;
-                for (bool more = true; more;) {
-                    int p;
-                    const uint32_t k = take_max<PL>(key, p);
-                    more = k && (c < a.k || near(last, unordered(k)));
-                    if (!more) break;
-                    if (c == 32) again = true;
-                    if (again) break;
-                    if (lane == c) mine = p;
-                    if (c < a.k) last = unordered(k);
-                    ++c;
+            if (!all || rounds > 32) {
+                // the k are known where the next key is apart from the k-th, and so from all of them; or where the two
+                // are of equal terms (whose sums are equal), if all keys near them are
+                const bool equal = to_f32(x[mine]) == to_f32(x[after]) && a.bias[mine] == a.bias[after];
+                const bool clear = __ballot_sync(kAll, apart) >> (a.k - 1) & 1;
+                const bool even = __ballot_sync(kAll, equal) >> (a.k - 1) & 1;
+                if (rounds <= 32 && (clear || even)) {
+                    all = __all_sync(kAll, apart || equal || lane >= a.k - 1);
+                    if (!clear && !near_are_equal(a, x, m, inv, slack, __shfl_sync(kAll, mine, a.k - 1)))
+                        again = true;   // (the loop below would have the keys live across the call: 17.3 us where 16.0)
+                    else if (!all)
+                        mine = order_64(a, x, mine, a.k);
+                } else {
+                    // every expert that may be among the k: those with keys near the k-th, or before it
+                    int c = 0;
+                    float last = 0.0f;
+                    for (bool more = true; more;) {
+                        int p;
+                        const uint32_t k = take_max<PL>(key, p);
+                        more = k && (c < a.k || near(last, unordered(k)));
+                        if (!more) break;
+                        if (c == 32) again = true;
+                        if (again) break;
+                        if (lane == c) mine = p;
+                        if (c < a.k) last = unordered(k);
+                        ++c;
+                    }
+                    if (!again) mine = order_64(a, x, mine, c);
                 }
-                if (!again) mine = order_64(a, x, mine, c);
             }
         }
     }

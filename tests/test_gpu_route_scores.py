@@ -360,3 +360,19 @@ def test_keys_near_by_every_measure(kind, k, groups, topg):
     bias[a] = s[row, b] - s[row, a] + apart
     assert 100 < (s[row, a] + bias[a] > s[row, b] + bias[b]).sum() < 400
     check(dev(l), dev(bias), k, kind, groups, topg)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+def test_equal_keys_at_the_border_and_larger_ones_behind(dtype):
+    """Experts of equal terms before others whose keys differ from theirs in 64 bits alone."""
+    l = torch.tensor([[-34.5, 22.75, -37.25, -5.25, -5.0, -31.5, 22.75, 31.75, 84.25],
+                      [22.75, 22.75, 22.75, 22.75, 22.75, 22.75, 22.75, 22.75, 24.0],
+                      [22.75] * 9, [0.0] * 9])
+    for bias in (torch.zeros(9), torch.full((9,), 0.25)):
+        for k in range(1, 9):
+            check(dev(l, DT[dtype]), dev(bias), k, "sigmoid")
+    many = torch.full((3, 400), 22.75)
+    many[0, 399] = 30.0
+    many[1, 200:] = 23.0
+    for k in (1, 8, 31, 32):
+        check(dev(many, DT[dtype]), dev(torch.zeros(400)), k, "sigmoid")
