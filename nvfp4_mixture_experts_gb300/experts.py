@@ -67,6 +67,14 @@ def quantise8(x, perm_src=None):
     return codes, sf
 
 
+def _held(dtype):
+    """The type in which gate and up, and the gradient of their product, lie between a product and the gate, for
+    tokens of a type.  It is theirs (the gate rounds to 8 bits with a scale for 32 elements, so 16 bits lose
+    nothing that counts), but for fp16: its range would make an infinity of a value past 65504, and the gate NaN
+    of the row."""
+    return torch.float32 if dtype == torch.float16 else dtype
+
+
 class _Gated8:
     """silu(gate) * up between two products of MXFP8 rows with MXFP4 weights, and its gradient.  counts,
     offsets, perm: the rows' groups (None: one group, of all rows)."""
@@ -82,7 +90,7 @@ class _Gated8:
     def forward(self, a, dtype, keep):
         """a: the rows' codes and tiled scales; (rows of the down product, checkpoint or None)."""
         ex, rows, dev = self.ex, a[0].shape[0], a[0].device
-        gu = self.product(a, ex.w13, 2 * ex.inter, dtype)
+        gu = self.product(a, ex.w13, 2 * ex.inter, _held(dtype))
         s, ckpt = _empty8(rows, ex.inter, dev), (None, None)
         if keep:
             ckpt = (torch.empty(rows, 2 * ex.inter, dtype=torch.uint8, device=dev),
@@ -95,7 +103,7 @@ class _Gated8:
         ex = self.ex
         if ex.w13_t is None:
             raise RuntimeError("%s without transposed weights has no backward" % type(ex).__name__)
-        ds = self.product(quantise8(dy, self.perm), ex.w2_t, ex.inter, dy.dtype)
+        ds = self.product(quantise8(dy, self.perm), ex.w2_t, ex.inter, _held(dy.dtype))
         dgu = _empty8(dy.shape[0], 2 * ex.inter, dy.device)
         moe_swiglu_mxfp8_backward(ds, *ckpt, *dgu, MOE_SF_TILED, perm_src=self.perm)
         return self.product(dgu, ex.w13_t, ex.hidden, dy.dtype)

@@ -1,6 +1,5 @@
 """The experts and the shared expert with 8-bit activations and fp16 tokens: gate, up and the gradient of their
 product may be past fp16's largest number, or below its steps, where the results are not."""
-import numpy as np
 import pytest
 import torch
 
@@ -61,4 +60,4 @@ def test_experts(T, H, I, E, k, off, El, up):
     assert rel(out, want) < TOL and rel(x.grad, dx) < TOL and rel(w.grad, dw) < TOL
     assert ex.get_status() == (moe.MOE_OK, 0)
     # what 4 bits give is finite, too
-    assert np.isfinite(MXExperts.from_master(E, off, w13, w2, backward=False)(x.detach(), ids, w.detach()).float().cpu()).all()
+    assert torch.isfinite(MXExperts.from_master(E, off, w13, w2, backward=False)(x.detach(), ids, w.detach())).all()
