@@ -344,7 +344,9 @@ class _Dtypes(dict):
 _DTYPES = _Dtypes({torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_FP16,
                    torch.float32: MOE_FP32})
 _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
-_MOST = 0x7fffffff  # sizes are 32-bit numbers on the C side; an or of sizes passes it if one does
+# Integers are 32-bit numbers on the C side, to which a larger one would be cut: an or of them is negative or
+# passes this if one is or does.
+_MOST = 0x7fffffff
 
 
 def _refuse(where):
@@ -352,14 +354,14 @@ def _refuse(where):
 
 
 def _sf_bytes(batch, rows, blocks, sf_layout):
-    """moe_mxfp4_scale_bytes for `blocks` scales a row."""
+    """moe_mxfp4_scale_bytes for `blocks` scales a row (-1, no tensor's, for another layout)."""
     if sf_layout == MOE_SF_TILED:
         return batch * ((rows + 127) >> 7) * ((blocks + 3) >> 2) * 512
-    return batch * rows * blocks
+    return batch * rows * blocks if sf_layout == MOE_SF_CANONICAL else -1
 
 
 def moe_dispatch_rows_capacity(T, k, num_local, row_align):
-    if not 0 <= T <= _MOST:
+    if not 0 <= (T | k | num_local | row_align) <= _MOST:
         return 0
     return load().moe_dispatch_rows_capacity(T, k, num_local, row_align)
 
@@ -371,7 +373,8 @@ def moe_dispatch(x, topk_ids, num_experts, local_off, num_local, row_align, coun
     [rows_cap, H]; status: an int32 word that errors found on the device are or-ed into."""
     T, k = topk_ids.shape
     cap = perm_src.numel()
-    if not ((T | k | cap) <= _MOST and topk_ids.dtype is _I32 and topk_ids.is_contiguous() and
+    if not (0 <= (T | k | cap | num_experts | local_off | num_local | row_align) <= _MOST and
+            topk_ids.dtype is _I32 and topk_ids.is_contiguous() and
             inv.dtype is _I32 and inv.numel() == T * k and inv.is_contiguous() and
             counts.dtype is _I32 and counts.numel() == num_local and counts.is_contiguous() and
             offsets.dtype is _I32 and offsets.numel() == num_local + 1 and
@@ -409,8 +412,8 @@ def moe_dispatch_backward(drows, inv, k, dx, stream=None):
     cap, Hr = drows.shape
     xs, one = dx.stride()
     dt = _DTYPES[dx.dtype]
-    if not (Hr == H and (T | H | cap) <= _MOST and (one == 1 or H == 1 or T == 0) and drows.is_contiguous() and
-            _DTYPES[drows.dtype] == dt and inv.dtype is _I32 and inv.numel() == T * k and
+    if not (Hr == H and 0 <= (T | H | cap | k) <= _MOST and (one == 1 or H == 1 or T == 0) and
+            drows.is_contiguous() and _DTYPES[drows.dtype] == dt and inv.dtype is _I32 and inv.numel() == T * k and
             inv.is_contiguous()):
         _refuse("moe_dispatch_backward")
     dev, handle = _place(stream)
@@ -429,7 +432,7 @@ def moe_combine_weighted(y, inv, w, out, stream=None):
     cap, Hy = y.shape
     xs, one = out.stride()
     dt = _DTYPES[y.dtype]
-    if not (To == T and Hy == H and (T | H | cap) <= _MOST and (one == 1 or H == 1 or T == 0) and
+    if not (To == T and Hy == H and (T | k | H | cap) <= _MOST and (one == 1 or H == 1 or T == 0) and
             y.is_contiguous() and
             _DTYPES[out.dtype] == dt and inv.dtype is _I32 and inv.numel() == T * k and
             inv.is_contiguous() and w.is_contiguous() and w.dtype is _F32):
@@ -452,7 +455,7 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
     dt = _DTYPES[dout.dtype]
     ok = (To == T and (one == 1 or H == 1 or T == 0) and inv.dtype is _I32 and inv.numel() == T * k and
           inv.is_contiguous() and w.is_contiguous() and w.dtype is _F32)
-    ok = ok and not (dy is None and dw is None) and (T | H) <= _MOST
+    ok = ok and not (dy is None and dw is None) and (T | k | H) <= _MOST
     cap = None
     for t in (y, dy):
         if t is not None:
@@ -478,12 +481,12 @@ def moe_combine_backward(dout, y, inv, w, dy, dw, stream=None):
 
 
 def moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout):
-    if not 0 <= (batch | rows | cols) <= _MOST:
+    if not 0 <= (batch | rows | cols | sf_layout) <= _MOST:
         return 0
     return load().moe_mxfp4_scale_bytes(batch, rows, cols, sf_layout)
 
 
-def _quant(where, per, x, codes, sf, sf_layout, transpose, perm_src, values, stream):
+def _quant(where, per, x, codes, sf, sf_layout, transpose, scale_rule, perm_src, values, stream):
     """The arguments that moe_quant_mxfp4 (per: two codes a byte) and moe_quant_mxfp8 (one) begin with,
     checked: x's, and the stream's handle."""
     shape, stride = x.shape, x.stride()
@@ -496,7 +499,7 @@ def _quant(where, per, x, codes, sf, sf_layout, transpose, perm_src, values, str
         _refuse(where)
     n, dt = B * R * Cc, _DTYPES[x.dtype]
     scales = _sf_bytes(B, Cc, R >> 5, sf_layout) if transpose else _sf_bytes(B, R, Cc >> 5, sf_layout)
-    if not ((B | R | Cc) <= _MOST and (one == 1 or Cc == 1 or n == 0) and codes.dtype is _U8 and
+    if not (0 <= (B | R | Cc | scale_rule) <= _MOST and (one == 1 or Cc == 1 or n == 0) and codes.dtype is _U8 and
             codes.numel() * per == n and codes.is_contiguous() and sf.dtype is _U8 and
             sf.numel() == scales and sf.is_contiguous() and
             (perm_src is None or (perm_src.dtype is _I32 and perm_src.numel() == R and
@@ -516,8 +519,8 @@ def moe_quant_mxfp4(x, codes, sf, sf_layout, transpose=False, scale_rule=MOE_MX_
                     perm_src=None, values=None, stream=None):
     """x [rows, cols] or [batch, rows, cols] (columns contiguous); codes uint8, sf uint8 and values
     (x's type) hold the MXFP4 matrix, or with transpose that of each matrix's transpose."""
-    args, handle = _quant("moe_quant_mxfp4", 2, x, codes, sf, sf_layout, transpose, perm_src, values,
-                          stream)
+    args, handle = _quant("moe_quant_mxfp4", 2, x, codes, sf, sf_layout, transpose, scale_rule, perm_src,
+                          values, stream)
     st = (_lib or load()).moe_quant_mxfp4(*args, 1 if transpose else 0, scale_rule, _p(perm_src),
                                           codes.data_ptr(), sf.data_ptr(), sf_layout, _p(values), handle)
     if st:
@@ -528,7 +531,8 @@ def moe_quant_mxfp8(x, codes, sf, sf_layout, scale_rule=MOE_MX_CEIL, perm_src=No
                     stream=None):
     """x [rows, cols] or [batch, rows, cols] (columns contiguous) -> codes uint8 of x's shape and sf
     uint8, its MXFP8 matrix, and values (x's type; None)."""
-    args, handle = _quant("moe_quant_mxfp8", 1, x, codes, sf, sf_layout, False, perm_src, values, stream)
+    args, handle = _quant("moe_quant_mxfp8", 1, x, codes, sf, sf_layout, False, scale_rule, perm_src, values,
+                          stream)
     st = (_lib or load()).moe_quant_mxfp8(*args, scale_rule, _p(perm_src), codes.data_ptr(),
                                           sf.data_ptr(), sf_layout, _p(values), handle)
     if st:
@@ -536,7 +540,7 @@ def moe_quant_mxfp8(x, codes, sf, sf_layout, scale_rule=MOE_MX_CEIL, perm_src=No
 
 
 def moe_mxfp4_tile_scales(sf, batch, rows, cols, sf_tiled, stream=None):
-    if not ((batch | rows | cols) <= _MOST and
+    if not (0 <= (batch | rows | cols) <= _MOST and
             sf.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_CANONICAL) and
             sf_tiled.numel() == _sf_bytes(batch, rows, cols >> 5, MOE_SF_TILED) and
             sf.is_contiguous() and sf_tiled.is_contiguous() and sf.dtype is _U8 and
@@ -551,6 +555,8 @@ def moe_mxfp4_tile_scales(sf, batch, rows, cols, sf_tiled, stream=None):
 
 
 def moe_mxfp4_workspace_size(rows_cap, num_groups, N, K):
+    if not 0 <= (rows_cap | num_groups | N | K) <= _MOST:
+        return 0
     return load().moe_mxfp4_workspace_size(rows_cap, num_groups, N, K)
 
 
@@ -628,7 +634,8 @@ def moe_route_scores(logits, topk_ids, topk_w, bias=None, score=MOE_SCORE_SOFTMA
     T, E = logits.shape
     Tk, k = topk_ids.shape
     stride, one = logits.stride()
-    if not (Tk == T and (T | E | k) <= _MOST and (one == 1 or E == 1 or T == 0) and
+    if not (Tk == T and 0 <= (T | E | k | score | num_groups | topk_groups | group_score) <= _MOST and
+            (one == 1 or E == 1 or T == 0) and
             topk_ids.dtype is _I32 and topk_ids.is_contiguous() and _flat(topk_w, T * k, _F32) and
             (bias is None or _flat(bias, E, _F32))):
         _refuse("moe_route_scores")
@@ -652,7 +659,7 @@ def moe_route_scores_backward(logits, topk_ids, dtopk_w, dlogits, score=MOE_SCOR
     Tk, k = topk_ids.shape
     stride, one = logits.stride()
     dt = _DTYPES[logits.dtype]
-    if not (Tk == T and (T | E | k) <= _MOST and (one == 1 or E == 1 or T == 0) and
+    if not (Tk == T and 0 <= (T | E | k | score) <= _MOST and (one == 1 or E == 1 or T == 0) and
             topk_ids.dtype is _I32 and topk_ids.is_contiguous() and _flat(dtopk_w, T * k, _F32)):
         _refuse("moe_route_scores_backward")
     dev, handle = _place(stream)
@@ -675,7 +682,8 @@ def moe_rmsnorm(x, weight, eps, residual=None, h=None, y=None, rstd=None, codes=
     xs, one = x.stride()
     dt = _DTYPES[xt]
     dev, handle = _place(stream)
-    ok = (T | H) <= _MOST and (one == 1 or H == 1 or T == 0) and x.get_device() == dev
+    ok = (0 <= (T | H | sf_layout | scale_rule) <= _MOST and (one == 1 or H == 1 or T == 0) and
+          x.get_device() == dev)
     pr = ph = py = pw = ps = pc = pf = None
     rs = hs = ys = 0
     if weight is not None:
@@ -741,7 +749,8 @@ def moe_swiglu_mxfp8(gate_up, codes, sf, sf_layout, ckpt=None, ckpt_sf=None, per
     R, I2 = gate_up.shape
     stride, one = gate_up.stride()
     I = I2 >> 1
-    if not ((R | I2) <= _MOST and not I2 & 1 and (one == 1 or R == 0) and _flat(codes, R * I, _U8) and
+    if not (0 <= (R | I2 | sf_layout | scale_rule) <= _MOST and not I2 & 1 and (one == 1 or R == 0) and
+            _flat(codes, R * I, _U8) and
             _flat(sf, _sf_bytes(1, R, I >> 5, sf_layout), _U8) and (ckpt is None) == (ckpt_sf is None) and
             (ckpt is None or (_flat(ckpt, R * I2, _U8) and _flat(ckpt_sf, R * (I2 >> 5), _U8))) and
             (perm_src is None or _flat(perm_src, R, _I32))):
@@ -765,7 +774,8 @@ def moe_swiglu_mxfp8_backward(ds, ckpt, ckpt_sf, codes=None, sf=None, sf_layout=
     R, I = ds.shape
     stride, one = ds.stride()
     dt = _DTYPES[ds.dtype]
-    if not ((R | 2 * I) <= _MOST and (one == 1 or I == 1 or R == 0) and _flat(ckpt, 2 * R * I, _U8) and
+    if not (0 <= (R | 2 * I | sf_layout | scale_rule) <= _MOST and (one == 1 or I == 1 or R == 0) and
+            _flat(ckpt, 2 * R * I, _U8) and
             _flat(ckpt_sf, R * (2 * I >> 5), _U8) and (codes is None) == (sf is None) and
             (codes is None or (_flat(codes, 2 * R * I, _U8) and
                                _flat(sf, _sf_bytes(1, R, 2 * I >> 5, sf_layout), _U8))) and
