@@ -51,7 +51,7 @@ class _Norm(torch.autograd.Function):
         with torch.no_grad():
             dx, dw = _Norm.gradients(ctx, dy, dh)
         if torch.is_grad_enabled():
-            dx, dw = _FirstOrder.apply(dx.requires_grad_(), dw.requires_grad_())
+            dx, dw = _FirstOrder.apply("rms_norm", dx.requires_grad_(), dw.requires_grad_())
         need = ctx.needs_input_grad
         return dx, dx if need[1] else None, dw if need[2] else None, None, None
 
@@ -99,7 +99,7 @@ class _Route(torch.autograd.Function):
             d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
             moe_route_scores_backward(logits, ids, dw.float().contiguous(), d, **ctx.how)
         if torch.is_grad_enabled():
-            d, = _FirstOrder.apply(d.requires_grad_())
+            d, = _FirstOrder.apply("route", d.requires_grad_())
         return (d,) + (None,) * 8
 
 

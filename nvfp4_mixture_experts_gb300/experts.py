@@ -195,15 +195,16 @@ class MXShared(MXExperts):
 
 
 class _FirstOrder(torch.autograd.Function):
-    """Gradients that are part of a graph (create_graph) and have no gradient of their own."""
+    """Gradients that are part of a graph (create_graph) and have no gradient of their own; name: whose."""
 
     @staticmethod
-    def forward(ctx, *grads):
+    def forward(ctx, name, *grads):
+        ctx.name = name
         return tuple(g.clone() for g in grads)
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("MXExperts has no second derivatives")
+        raise RuntimeError("%s has no second derivatives" % ctx.name)
 
 
 class _Experts(torch.autograd.Function):
@@ -251,7 +252,7 @@ class _Experts(torch.autograd.Function):
         # Under create_graph the gradients depend on x, topk_w and dout, but the kernels leave no
         # graph: a second derivative must not be taken for zero.
         if torch.is_grad_enabled():
-            grads = _FirstOrder.apply(*(g.requires_grad_() for g in grads))
+            grads = _FirstOrder.apply("MXExperts", *(g.requires_grad_() for g in grads))
         return (*grads, None, None)
 
     @staticmethod
@@ -296,5 +297,5 @@ class _Shared(torch.autograd.Function):
         with torch.no_grad():
             dx = ctx.gated.backward(dout.to(ctx.dtype).contiguous(), ctx.saved_tensors)
         if torch.is_grad_enabled():
-            dx, = _FirstOrder.apply(dx.requires_grad_())
+            dx, = _FirstOrder.apply("MXShared", dx.requires_grad_())
         return dx, None, None, None
