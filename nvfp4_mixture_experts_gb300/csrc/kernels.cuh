@@ -612,8 +612,8 @@ inline int norm_back_depth(int H, int elem_bytes, bool one)
 }
 // The norm's own: as many as keep 48 KB of an SM's loads in flight (8192 x 4096 bf16: with the residual and all
 // results one row 50.5 us, two 57.6, y alone one row 28.8, two 24.7, three 26.5).  0, where one row of each
-// block is over 64 KB: the kernel that loads a row into registers, one block a row (the first with fp32: 86.3 us,
-// with the ring 98.4; of bf16 53.1 and 34.8).
+// block is over 64 KB, which is so of fp32 with a residual alone: the kernel that loads a row into registers, one
+// block a row (the first with fp32: 86.3 us, with the ring 98.4; of bf16 53.1 and 34.8).
 inline int norm_depth(int threads, int elem_bytes, int tensors)
 {
     const int row = norm_row_bytes(threads, elem_bytes, tensors) * norm_per_sm(threads, false);

@@ -593,11 +593,13 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(const float* ws, int pa
     if (lane == 0 && blockIdx.x * 8 + warp < H) dw[blockIdx.x * 8 + warp] = v;
 }
 
-// (MXFP8 results of rows that are in no 16 bytes: one by one)
+// (MXFP8 results of rows that are in no 16 bytes: one by one.  Long rows in 16-byte pieces get here in fp32 with
+// a residual alone, all others go through the ring.)
 template <typename T, int PER, bool ONE>
 static NormKernel norm_of(int piece, bool codes)
 {
-    if (piece == 16) return norm_kernel<T, PER, ONE, kVec>;
+    if constexpr (ONE || sizeof(T) == 4)
+        if (piece == 16) return norm_kernel<T, PER, ONE, kVec>;
     if (codes) return norm_kernel<T, PER, ONE, kEach>;
     if (sizeof(T) == 2 && piece >= 4) return norm_kernel<T, PER, ONE, sizeof(T) == 2 ? kPairs : kApart>;
     return norm_kernel<T, PER, ONE, kApart>;
