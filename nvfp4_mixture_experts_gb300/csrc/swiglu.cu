@@ -28,8 +28,10 @@ __device__ __forceinline__ float rcp_approx(float x)
     return r;
 }
 
-// 1 / (1 + e^-g), within 2^-20 of it for |g| < 80 (0 below -87): both instructions are within 2^-22, and the
-// exponent's rounding adds |g| 2^-23.  (Results are rounded to four bits.)
+// 1 / (1 + e^-g), within 2^-21 + 1.25 |g| 2^-24 of itself down to g = -87 (2^-17.3 at -80), 0 below: the two
+// instructions are within 2^-22 and 2^-23, the sum within 2^-24; the exponent's rounding is |g| 2^-24 and that of
+// log2 e as a 32-bit number |g| 2^-26, of which a positive g's small e^-g takes little.  (MXFP8 results are rounded
+// to four bits.)
 __device__ __forceinline__ F2 sigmoid(F2 g)
 {
     const float2 x = (g * F2(-1.4426950408889634f)).get();
