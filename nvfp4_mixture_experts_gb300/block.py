@@ -18,7 +18,8 @@ def rms_norm(x, weight, eps=1e-6, residual=None, eight=False):
     """(y, h, codes, scales) for rows x [T, H]: h = x + residual (x where there is none), y = h /
     sqrt(mean h^2 + eps) * weight, and with eight y's MXFP8 matrix with tiled scales (None without; it
     has no gradient of its own: what reads it passes its gradient to y).  Differentiable in x, residual
-    and weight, through y and h."""
+    and weight, through y and h.  The weight may be of any float type; it is rounded to x's for the product,
+    and its gradient to the weight's."""
     y, h, codes, sf = _Norm.apply(x, residual, weight, eps, eight)
     return y, x if residual is None else h, codes, sf
 
@@ -106,9 +107,10 @@ class _Route(torch.autograd.Function):
 class MXBlock:
     """h = x + residual; y = rms_norm(h); out = experts(y, route(y router^T)) [+ shared(y)].
 
-    norm_weight [H] and router [num_experts, H] are the caller's leaves (any float type); experts: an
-    MXExperts (of a shard: out is its partial sum); shared: an MXShared (of several shards one has it) or
-    None; the other arguments are route's."""
+    norm_weight [H] and router [num_experts, H] are the caller's leaves, of any float type: the norm's weight is
+    rounded to x's on every call, y to the router's for the logits, which are torch's matrix product in that
+    type.  experts: an MXExperts (of a shard: out is its partial sum); shared: an MXShared (of several shards
+    one has it) or None; the other arguments are route's."""
 
     def __init__(self, norm_weight, router, experts, top_k, shared=None, eps=1e-6, **routing):
         self.norm_weight, self.router, self.experts, self.shared = norm_weight, router, experts, shared

@@ -7,10 +7,12 @@
 // the row's sum waits for all of its threads.  Short rows (the gradient's up to 1024 16-bit elements) have a
 // warp each; rows that are in no 16-byte pieces are read an element, or two 16-bit ones, a lane at a time.
 //
-// All are bound by memory, long rows from 0.8 of the measured copy rate up.  8192 x 4096 bf16 with residual, h,
-// y and MXFP8 50 us (6.0 TB/s; fp32 86), y alone 25 us, its gradient 46 us (5.8 TB/s; fp32 83, 6.5 TB/s); 16384 x
-// 512 15 us each way.  What is in no 16 bytes is bound by its instructions: 8192 x 4097 bf16 72 us with residual,
-// h and y, its gradient 101.
+// Rows of 4096 and 8192 elements are bound by memory, from 0.8 of the measured copy rate up: 8192 x 4096 bf16 with
+// residual, h, y and MXFP8 50 us (6.0 TB/s; fp32 86), y alone 25 us, its gradient 46 us (5.8 TB/s; fp32 83, 6.5
+// TB/s).  Others come to 0.5 to 0.7 of it: 16384 x 512 15 us each way; the gradient of 8192 x 1024 20 us and of
+// x 2048 32 us, with few rows a warp or block before the parts of the weight's gradient are added up; that of
+// 2048 x 16384 68 us, where a block of 1024 threads is alone on its SM and nothing hides its barrier.  What is in
+// no 16 bytes is bound by its instructions: 8192 x 4097 bf16 72 us with residual, h and y, its gradient 101.
 #include "mx.cuh"
 
 namespace moe {
