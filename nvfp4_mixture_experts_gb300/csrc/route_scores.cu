@@ -628,8 +628,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, PL <= 12 ? 7 : 1) route_scor
 }
 
 // A warp per token.  Renormalised scores and sigmoids: the chosen experts' logits alone have gradients,
-// q (g - r) f with g_j = scale dw_j, q the weight / scale, r = sum_i g_i q_i, f the score's own derivative
-// over it (softmax 1, sigmoid 1 - s); not renormalised g s (1 - s).  Softmax scores that are not
+// q (g - r) f with g the weights' gradients, q the weight / scale, r = sum_i g_i q_i, f the score's own derivative
+// over it (softmax 1, sigmoid 1 - s); not renormalised g s (1 - s); each times scale.  Softmax scores that are not
 // renormalised: p_e (sum of the g_j of expert e - sum_j g_j p_j), for every expert e (DENSE); of a chosen
 // one the difference as a sum of differences.  Expert 32 i + lane is in the registers of a lane.  All of a
 // token's are NaN where its weights are.
@@ -648,7 +648,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
     if (id >= a.E) id = -1;  // (an id out of range has no gradient)
     const bool chosen = id >= 0;
     const float v = chosen ? to_f32(x[id]) : -INFINITY;
-    float g = chosen ? a.dw[t * a.k + lane] * a.scale : 0.0f;
+    // (the scale comes last: it would round the gradients whose differences count)
+    float g = chosen ? a.dw[t * a.k + lane] : 0.0f;
     float p = 0.0f, r = 0.0f, inv = 0.0f, mass = 0.0f;   // mass: the positions' scores together
     float l[PL];
 #pragma unroll
@@ -675,9 +676,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
             mass += __shfl_xor_sync(kAll, mass, o);
             r += __shfl_xor_sync(kAll, r, o);
         }
+        const float less = -(inv * r) * a.scale;
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            if (32 * i + lane < a.E) from_f32(-l[i] * inv * r, dx[32 * i + lane]);
+            if (32 * i + lane < a.E) from_f32(l[i] * less, dx[32 * i + lane]);
     } else {
         // the row is read for its token's weights: NaN with a NaN logit, or an infinite one's softmax
         bool nan = false;
@@ -748,7 +750,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_back_kernel(RouteBackA
         }
     }
     __syncwarp();  // the row is written; its chosen experts' are written again
-    if (chosen) from_f32(all, dx[id]);
+    if (chosen) from_f32(all * a.scale, dx[id]);
 }
 
 // Registers of a lane for a token's experts: powers of two and steps between them (320 experts in 10, not 16).

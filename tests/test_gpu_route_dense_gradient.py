@@ -65,3 +65,27 @@ def test_the_same_expert_twice_and_ids_out_of_range(dtype):
     ids = np.array([[3, 3, 8, 3], [8, 8, 3, -1], [40, 3, 2000000000, 3], [-1, -1, 41, 50]] * 3)
     check(l, ids, rng.normal(size=(T, 4)), dtype)
     check(l, ids, np.ones((T, 4)), dtype)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradients_of_weights_next_to_each_other(renorm):
+    """An expert of a small score whose weight's gradient is the nearly certain expert's up to 1e-5: their difference
+    is exact before the scale, and rounded by it after."""
+    T, E = 64, 24
+    rng = np.random.default_rng(5)
+    l = np.float32(rng.normal(size=(T, E)))
+    l[:, 2] += 18
+    ids = np.tile([2, 7, 11], (T, 1))
+    dw = np.float32(rng.normal(size=(T, 3)))
+    dw[:, 1] = dw[:, 0] * (1 + np.float32(2e-5) * np.float32(rng.uniform(-1, 1, size=T)))
+    scale = 1.7
+    out = torch.empty(T, E, device="cuda")
+    moe.moe_route_scores_backward(dev(l), dev(ids, torch.int32), dev(dw), out, score=moe.MOE_SCORE_SOFTMAX,
+                                  renormalise=renorm, scale=scale)
+    got = out.double().cpu().numpy()
+    for t in range(T):
+        row = l[t].astype(np.float64)
+        if renorm:
+            row = np.where(np.isin(np.arange(E), ids[t]), row, -np.inf)   # the same as scores of the chosen alone
+        want, mag = dense_grad(row, ids[t], dw[t].astype(np.float64), float(np.float32(scale)))
+        assert np.all(np.abs(got[t] - want) <= 5 * W_TOL * mag + 2.0 ** -140)
